@@ -499,6 +499,136 @@ int moe_residency_plan(const moe_dims* dims, const moe_residency* r, const int32
 int moe_expert_copy(const moe_dims* dims, int bits, const moe_qweights* src, const moe_qweights* dst, int32_t n_dst,
                     const int32_t* copies, const int32_t* n_copy, int32_t max_copies, void* stream);
 
+/* -------------------------------------------- dense quantised products
+ * Products with one quantised matrix outside the experts (projections around
+ * the layer, output logits) and the gradient past it, the matrix frozen.  The
+ * codes, scales and biases are one expert's matrix of moe_qweights:
+ *   w[n][k] = code[n][k] * scale[n][k/G] + bias[n][k/G]
+ *   q      uint8 [K/128][N][16*bits], group-major as in moe_qweights
+ *   scale  fp16 bits [N][K/G], bias likewise; G = group_size (128, 64 or 32)
+ * The "Strata" page, sec. 2.2 and 3.4 (INT4 g128 and its matvec), and the
+ * "Flash-MoE" page, sec. 2 and 3 (the FMA form, 4 and 2 bits).
+ * Limits: 1 <= N <= 1048576; K a multiple of 128, 128 <= K <= 32768; bits 4
+ * or 2; 0 <= T <= 65536.  q, scale and bias are 16-byte aligned.  The struct
+ * is a host object, read during the call only. */
+typedef struct moe_qmatrix {
+    const uint8_t* q;
+    const uint16_t* scale;
+    const uint16_t* bias;
+    int32_t N;
+    int32_t K;
+    int32_t group_size;
+    int32_t bits;
+} moe_qmatrix;
+
+/* Element types of y and dy below. */
+#define MOE_BF16 0
+#define MOE_F32 1
+
+/* Device workspace of moe_linear (grad = 0) or moe_linear_grad (grad = 1) for T
+ * tokens and this element type of y or dy (host-only; the matrix' pointers are
+ * not used).  It is 0 for moe_linear's decode kernels.  A workspace serves calls
+ * of one stream at a time; what it holds between calls is scratch. */
+int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int grad, size_t* bytes);
+
+/* y[t][n] = sum_k x[t][k] w[n][k] (+ row_bias[n]) (+ residual[t][n]), sums in
+ * float32, rounded once to y's type (nearest, ties to even).
+ *   x          bf16 [T] rows of K elements, ldx elements apart; 16-byte aligned,
+ *              ldx >= K a multiple of 8
+ *   row_bias   float32 [N] or NULL
+ *   residual   bf16 [T] rows of N elements, ldr >= N apart, or NULL; may be y
+ *              itself (bf16, ldr == ldy), else y overlaps no input
+ *   y          bf16 or float32 (y_type) [T] rows of N elements, ldy >= N apart
+ *   workspace  moe_linear_workspace_bytes(w, T, y_type, 0), 256-byte aligned
+ *              (NULL where that is 0)
+ * A row of x with an infinity or NaN gives a row of y of NaNs and infinities,
+ * and changes no other row. */
+int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, const float* row_bias,
+               const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int y_type, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/* The gradient of moe_linear's x: dx[t][k] = sum_n dy[t][n] w[n][k], sums in
+ * float32, rounded once to bf16.  (The row bias' gradient is dy's sum over the
+ * tokens and the residual's is dy; the quantised matrix is frozen.)
+ *   dy         bf16 or float32 (dy_type) [T] rows of N elements, lddy >= N
+ *              elements apart, aligned to its element
+ *   dx         bf16 [T] rows of K elements, lddx apart; 16-byte aligned, lddx >=
+ *              K a multiple of 8; overlaps no input
+ *   workspace  moe_linear_workspace_bytes(w, T, dy_type, 1), 256-byte aligned
+ *   sync       int32 [MOE_LINEAR_SYNC_INTS] device memory, 256-byte aligned,
+ *              holding zeros before the first call; each call leaves it zero.
+ *              Calls that share a workspace or sync must be ordered (one stream).
+ * Rows of dy with infinities or NaNs as for moe_linear's x. */
+#define MOE_LINEAR_SYNC_INTS 4096
+int moe_linear_grad(const moe_qmatrix* w, int32_t T, const void* dy, int64_t lddy, int dy_type, uint16_t* dx,
+                    int64_t lddx, void* workspace, size_t workspace_bytes, int32_t* sync, void* stream);
+
+/* ------------------------------------------------- the router's training pass
+ * What a user needs to tune the router over the frozen quantised experts: the
+ * losses that keep the experts' load even, and the gradients from the layer's
+ * output back to the logits (step 6 and step 2 in reverse).  The router weight's
+ * gradient is then a plain product of d logits and x. */
+
+/* Per-expert counts, mean probabilities and the router's losses, from the
+ * float32 logits [T][E] and picks [T][k] of steps 1-2.  With
+ *   V      the tokens that take part: valid[t] != 0 (valid NULL: all), and
+ *          some logit of t other than -inf,
+ *   p_t    softmax of token t's logits, lse_t the logarithm of its sum,
+ *   c_e    picks of expert e by tokens of V,   P_e = sum_{t in V} p_t[e] / |V|,
+ * the call writes
+ *   expert_counts  int32 [E]    c_e
+ *   prob_mean      float32 [E]  P_e
+ *   n_valid        int32 [1]    |V|
+ *   losses         float32 [2]  [0] balance = E sum_e c_e / (|V| k) P_e
+ *                               [1] z = sum_{t in V} lse_t^2 / |V|
+ * With |V| = 0 (or T = 0) all of them are 0.  Picks out of range are not
+ * counted.  Sums are taken in a fixed order: equal calls give equal bits.
+ *   valid      uint8 [T] or NULL
+ *   workspace  moe_balance_workspace_bytes(dims), 256-byte aligned
+ *   sync       int32 [MOE_BALANCE_SYNC_INTS] device memory, 256-byte aligned,
+ *              holding zeros before the first call; each call leaves it zero.
+ *              Calls that share a workspace or sync must be ordered (one stream).
+ * Only T, E and k of dims are used (and checked with group_size), here and in
+ * moe_route_backward. */
+#define MOE_BALANCE_SYNC_INTS 1088
+int moe_balance_workspace_bytes(const moe_dims* dims, size_t* bytes);
+int moe_balance_loss(const moe_dims* dims, const float* logits, const int32_t* topk_ids, const uint8_t* valid,
+                     int32_t* expert_counts, float* prob_mean, int32_t* n_valid, float* losses, void* workspace,
+                     size_t workspace_bytes, int32_t* sync, void* stream);
+
+/* d logits [T][E] (every element written): the sum of
+ *   the gates' part (topk_w_grad not NULL: float32 [T][k], the gradient dg of
+ *   topk_w, as moe_combine_backward writes it), for every token,
+ *     renormalize != 0:  at e = topk_ids[t][j]:  g_j (dg_j - sum_i g_i dg_i)
+ *     renormalize == 0:  at e = topk_ids[t][j]:  g_j dg_j;  everywhere
+ *                        - p_t[e] sum_i g_i dg_i
+ *   with g = topk_w [T][k] of steps 1-2 (the same renormalize); and
+ *   the losses' part (losses_grad not NULL: device float32 [2], the gradients a
+ *   and z of moe_balance_loss' two losses), for tokens of V,
+ *     a E / |V| p_t[e] (f_e - sum_i p_t[i] f_i) + z 2 / |V| lse_t p_t[e],
+ *     f_e = expert_counts[e] / (|V| k),  |V| = *n_valid (taken as 1 if less).
+ * The counts are constants of the balance loss.  expert_counts and n_valid are
+ * moe_balance_loss' (or their sums over several ranks); they and valid are read
+ * for the losses' part only.  A token whose logits are all -inf has p = 0, and
+ * picks out of range add nothing.  An expert picked twice by a token gets the
+ * sum of both picks. */
+int moe_route_backward(const moe_dims* dims, const float* logits, const int32_t* topk_ids, const float* topk_w,
+                       int renormalize, const float* topk_w_grad, const float* losses_grad,
+                       const int32_t* expert_counts, const int32_t* n_valid, const uint8_t* valid, float* logits_grad,
+                       void* stream);
+
+/* Step 6 in reverse, from out_grad = d out [T][H] (bf16):
+ *   topk_w_grad[t][j]           = sum_n out_grad[t][n] y_rows[r][n]   (float32)
+ *   y_rows_grad[r][n]           = bf16(topk_w[t][j] out_grad[t][n])
+ * with r = pair_to_row[t*k+j]; the residual's gradient is out_grad itself.
+ * y_rows_grad (bf16 [T*k][H]) may be NULL: not written, and topk_w is then not
+ * used.  A pair whose row is out of range gets topk_w_grad 0 and no y_rows_grad;
+ * rows of y_rows_grad that no pair names stay as they were.  No two pairs may
+ * name one row.  Alignment as for moe_combine. */
+int moe_combine_backward(const moe_dims* dims, const uint16_t* out_grad, const uint16_t* y_rows,
+                         const int32_t* pair_to_row, const float* topk_w, float* topk_w_grad, uint16_t* y_rows_grad,
+                         void* stream);
+
 /* Measurement aid, not a step of the layer: reads `bytes` of device memory at
  * `src` once, with 16-byte loads spread over every compute unit, and writes
  * the XOR of what each workgroup read into sink[0 .. MOE_STREAM_SINK_INTS),

@@ -33,6 +33,8 @@ EXPORTS = (
     "moe_combine", "moe_combine_shared",
     "moe_zero_point_bias", "moe_stream_read",
     "moe_route_counts", "moe_hot_set", "moe_residency_plan", "moe_expert_copy",
+    "moe_linear_workspace_bytes", "moe_linear", "moe_linear_grad",
+    "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward", "moe_combine_backward",
 )
 
 
@@ -67,6 +69,12 @@ class ResidencyC(ctypes.Structure):
     """struct moe_residency (include/moe.h)."""
     _fields_ = [("n_hot", ctypes.c_int32), ("n_slots", ctypes.c_int32), ("slot_of_expert", ctypes.c_void_p),
                 ("expert_of_slot", ctypes.c_void_p), ("last_use", ctypes.c_void_p)]
+
+
+class QMatrixC(ctypes.Structure):
+    """struct moe_qmatrix (include/moe.h)."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group_size", ctypes.c_int32), ("bits", ctypes.c_int32)]
 
 
 _lib = None
@@ -108,6 +116,14 @@ def lib() -> ctypes.CDLL:
     L.moe_hot_set.argtypes = [Dp, P, i32, P, P]
     L.moe_residency_plan.argtypes = [Dp, ctypes.POINTER(ResidencyC), P, P, u32, P, P, P, P, P, P, P]
     L.moe_expert_copy.argtypes = [Dp, ctypes.c_int, Wp, Wp, i32, P, P, i32, P]
+    Mp, i64 = ctypes.POINTER(QMatrixC), ctypes.c_int64
+    L.moe_linear_workspace_bytes.argtypes = [Mp, i32, ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)]
+    L.moe_linear.argtypes = [Mp, i32, P, i64, P, P, i64, P, i64, ctypes.c_int, P, sz, P]
+    L.moe_linear_grad.argtypes = [Mp, i32, P, i64, ctypes.c_int, P, i64, P, sz, P, P]
+    L.moe_balance_workspace_bytes.argtypes = [Dp, ctypes.POINTER(sz)]
+    L.moe_balance_loss.argtypes = [Dp, P, P, P, P, P, P, P, P, sz, P, P]
+    L.moe_route_backward.argtypes = [Dp, P, P, P, ctypes.c_int, P, P, P, P, P, P, P]
+    L.moe_combine_backward.argtypes = [Dp, P, P, P, P, P, P, P]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -366,8 +382,261 @@ def expert_copy(d: Dims, bits: int, src: "QWeights", dst: "QWeights", n_dst: int
                                  _ptr(copies), _ptr(n_copy), int(max_copies), _stream(stream)))
 
 
-from .layer import (LayerBuffers, ResidentExperts, SharedBuffers, SharedExpert, StackLayer, layer_forward,  # noqa: E402
-                    resident_layer_forward, stack_forward)  # (orchestration of the calls above)
+# ----------------------------------------- operators around frozen weights
+
+BF16, F32 = 0, 1                             # MOE_BF16, MOE_F32
+LINEAR_SYNC_INTS = 4096                      # MOE_LINEAR_SYNC_INTS
+BALANCE_SYNC_INTS = 1088                     # MOE_BALANCE_SYNC_INTS
+
+
+def _element_type(dtype) -> int:
+    import torch
+    if dtype == torch.bfloat16 or dtype == torch.int16:
+        return BF16
+    if dtype == torch.float32:
+        return F32
+    raise ValueError(f"elements of type {dtype}: bfloat16 (or its bits as int16) or float32 needed")
+
+
+def _want(name: str, t, device, dtypes, shape=None) -> None:
+    """A contiguous tensor on `device` of one of these types (and this shape)."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} holds {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {shape} needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _want_rows(name: str, t, device, dtypes, rows: int, cols: int) -> int:
+    """A [rows, cols] tensor whose rows are contiguous; returns their stride."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} holds {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {(rows, cols)} needed")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows are not contiguous")
+    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+
+
+def _enqueue(fn, device, stream, *args) -> None:
+    """fn(*args, stream) on `device`: the given stream, or that device's current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}: the library runs on the GPU")
+    if stream is None:
+        s = torch.cuda.current_stream(device).cuda_stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, s))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s))
+
+
+@dataclass(frozen=True, eq=False)
+class QMatrix:
+    """One quantised matrix [N, K] (struct moe_qmatrix): codes in the layout of
+    an expert's matrix, uint8 [K/128, N, 16*bits] (group_major()), scale and
+    bias fp16 (or their bits as int16) [N, K/group_size]."""
+    bits: int
+    group_size: int
+    q: "torch.Tensor"
+    scale: "torch.Tensor"
+    bias: "torch.Tensor"
+
+    def __post_init__(self):
+        import torch
+        if self.bits not in (2, 4) or self.group_size not in (32, 64, 128):
+            raise ValueError(f"{self.bits}-bit codes in groups of {self.group_size}: bits 4 or 2, groups 128, 64 or 32")
+        if self.q.dim() != 3 or self.q.shape[2] != 16 * self.bits:
+            raise ValueError(f"q has shape {tuple(self.q.shape)}, [K/128, N, {16 * self.bits}] needed")
+        _want("q", self.q, self.q.device, (torch.uint8,))
+        half = (torch.float16, torch.int16)
+        shape = (self.N, self.K // self.group_size)
+        _want("scale", self.scale, self.q.device, half, shape)
+        _want("bias", self.bias, self.q.device, half, shape)
+        c = QMatrixC(_ptr(self.q), _ptr(self.scale), _ptr(self.bias), self.N, self.K, self.group_size, self.bits)
+        object.__setattr__(self, "_c", c)
+
+    @property
+    def N(self) -> int:
+        return self.q.shape[1]
+
+    @property
+    def K(self) -> int:
+        return 128 * self.q.shape[0]
+
+
+def linear_workspace_bytes(w: QMatrix, T: int, dtype, grad: bool = False) -> int:
+    """moe_linear_workspace_bytes; dtype: the type of y, or of dy with grad."""
+    out = ctypes.c_size_t(0)
+    _check(lib().moe_linear_workspace_bytes(ctypes.byref(w._c), int(T), _element_type(dtype), int(bool(grad)),
+                                            ctypes.byref(out)))
+    return int(out.value)
+
+
+@dataclass
+class LinearBuffers:
+    """What linear() or linear_grad() need beside their operands, for calls of up
+    to the sizes they were allocated for, one at a time on one stream."""
+    workspace: "torch.Tensor"     # uint8
+    sync: "torch.Tensor"          # int32 [LINEAR_SYNC_INTS], zeros (every call leaves them zero)
+
+    @staticmethod
+    def allocate(w: QMatrix, T: int, dtype, grad: bool = False) -> "LinearBuffers":
+        import torch
+        dev = w.q.device
+        return LinearBuffers(
+            workspace=torch.empty(max(linear_workspace_bytes(w, T, dtype, grad), 256), dtype=torch.uint8, device=dev),
+            sync=torch.zeros(LINEAR_SYNC_INTS if grad else 1, dtype=torch.int32, device=dev))
+
+
+def linear(w: QMatrix, x, y, buffers: Optional[LinearBuffers] = None, row_bias=None, residual=None, stream=None):
+    """moe_linear: y = x W^T (+ row_bias) (+ residual).  x bfloat16 [T, K] and y
+    bfloat16 or float32 [T, N], rows contiguous (any row stride; x's a multiple of
+    8 elements); row_bias float32 [N]; residual bfloat16 [T, N] (may be y itself).
+    buffers: LinearBuffers.allocate(w, T, y.dtype), or None where no workspace is
+    needed."""
+    import torch
+    dev, b16 = w.q.device, (torch.bfloat16, torch.int16)
+    T = x.shape[0]
+    ldx = _want_rows("x", x, dev, b16, T, w.K)
+    ldy = _want_rows("y", y, dev, b16 + (torch.float32,), T, w.N)
+    ldr = 0
+    if residual is not None:
+        ldr = _want_rows("residual", residual, dev, b16, T, w.N)
+    if row_bias is not None:
+        _want("row_bias", row_bias, dev, (torch.float32,), (w.N,))
+    ws = None if buffers is None else buffers.workspace
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"the buffers are on {ws.device}, not on {dev}")
+    _enqueue(lib().moe_linear, dev, stream, ctypes.byref(w._c), T, _ptr(x), ldx, _ptr(row_bias), _ptr(residual), ldr,
+             _ptr(y), ldy, _element_type(y.dtype), _ptr(ws), _nbytes(ws))
+
+
+def linear_grad(w: QMatrix, dy, dx, buffers: LinearBuffers, stream=None):
+    """moe_linear_grad: dx = dy W.  dy bfloat16 or float32 [T, N] and dx bfloat16
+    [T, K], rows contiguous (dx's row stride a multiple of 8 elements).  buffers:
+    LinearBuffers.allocate(w, T, dy.dtype, grad=True)."""
+    import torch
+    dev, b16 = w.q.device, (torch.bfloat16, torch.int16)
+    T = dy.shape[0]
+    lddy = _want_rows("dy", dy, dev, b16 + (torch.float32,), T, w.N)
+    lddx = _want_rows("dx", dx, dev, b16, T, w.K)
+    _want("buffers.sync", buffers.sync, dev, (torch.int32,), (LINEAR_SYNC_INTS,))
+    ws = buffers.workspace
+    if ws.device != dev:
+        raise ValueError(f"the buffers are on {ws.device}, not on {dev}")
+    _enqueue(lib().moe_linear_grad, dev, stream, ctypes.byref(w._c), T, _ptr(dy), lddy, _element_type(dy.dtype),
+             _ptr(dx), lddx, _ptr(ws), _nbytes(ws), _ptr(buffers.sync))
+
+
+def balance_workspace_bytes(d: Dims) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().moe_balance_workspace_bytes(ctypes.byref(d), ctypes.byref(out)))
+    return int(out.value)
+
+
+@dataclass
+class BalanceBuffers:
+    """balance_loss()'s scratch, for calls of these dims' E, one at a time on one stream."""
+    workspace: "torch.Tensor"     # uint8
+    sync: "torch.Tensor"          # int32 [BALANCE_SYNC_INTS], zeros (every call leaves them zero)
+
+    @staticmethod
+    def allocate(d: Dims, device="cuda") -> "BalanceBuffers":
+        import torch
+        return BalanceBuffers(workspace=torch.empty(balance_workspace_bytes(d), dtype=torch.uint8, device=device),
+                              sync=torch.zeros(BALANCE_SYNC_INTS, dtype=torch.int32, device=device))
+
+
+def _want_valid(valid, dev, T: int) -> None:
+    import torch
+    if valid is not None:
+        _want("valid", valid, dev, (torch.uint8, torch.bool), (T,))
+
+
+def balance_loss(d: Dims, logits, topk_ids, expert_counts, prob_mean, n_valid, losses, buffers: BalanceBuffers,
+                 valid=None, stream=None):
+    """moe_balance_loss: per-expert counts int32 [E], mean probabilities float32
+    [E], tokens that take part int32 [1] and the losses float32 [2] (balance, z)
+    of logits float32 [T, E] and picks int32 [T, k]; valid: None or uint8/bool [T]."""
+    import torch
+    dev = logits.device
+    _want("logits", logits, dev, (torch.float32,), (d.T, d.E))
+    _want("topk_ids", topk_ids, dev, (torch.int32,), (d.T, d.k))
+    _want_valid(valid, dev, d.T)
+    _want("expert_counts", expert_counts, dev, (torch.int32,), (d.E,))
+    _want("prob_mean", prob_mean, dev, (torch.float32,), (d.E,))
+    _want("n_valid", n_valid, dev, (torch.int32,), (1,))
+    _want("losses", losses, dev, (torch.float32,), (2,))
+    _want("buffers.sync", buffers.sync, dev, (torch.int32,), (BALANCE_SYNC_INTS,))
+    ws = buffers.workspace
+    if ws.device != dev:
+        raise ValueError(f"the buffers are on {ws.device}, not on {dev}")
+    _enqueue(lib().moe_balance_loss, dev, stream, ctypes.byref(d), _ptr(logits), _ptr(topk_ids), _ptr(valid),
+             _ptr(expert_counts), _ptr(prob_mean), _ptr(n_valid), _ptr(losses), _ptr(ws), _nbytes(ws),
+             _ptr(buffers.sync))
+
+
+def route_backward(d: Dims, logits, topk_ids, topk_w, renormalize: bool, logits_grad, topk_w_grad=None,
+                   losses_grad=None, expert_counts=None, n_valid=None, valid=None, stream=None):
+    """moe_route_backward: logits_grad float32 [T, E] from the gates' gradient
+    topk_w_grad float32 [T, k] (None: no such part) and the losses' gradients
+    losses_grad float32 [2] on the GPU (None: no such part; else with
+    balance_loss()'s expert_counts and n_valid)."""
+    import torch
+    dev, f32, i32 = logits.device, (torch.float32,), (torch.int32,)
+    _want("logits", logits, dev, f32, (d.T, d.E))
+    _want("logits_grad", logits_grad, dev, f32, (d.T, d.E))
+    if topk_w_grad is not None:
+        _want("topk_w_grad", topk_w_grad, dev, f32, (d.T, d.k))
+        _want("topk_w", topk_w, dev, f32, (d.T, d.k))
+        _want("topk_ids", topk_ids, dev, i32, (d.T, d.k))
+    if losses_grad is not None:
+        if expert_counts is None or n_valid is None:
+            raise ValueError("the losses' gradient needs expert_counts and n_valid")
+        _want("losses_grad", losses_grad, dev, f32, (2,))
+        _want("expert_counts", expert_counts, dev, i32, (d.E,))
+        _want("n_valid", n_valid, dev, i32, (1,))
+    _want_valid(valid, dev, d.T)
+    _enqueue(lib().moe_route_backward, dev, stream, ctypes.byref(d), _ptr(logits), _ptr(topk_ids), _ptr(topk_w),
+             int(bool(renormalize)), _ptr(topk_w_grad), _ptr(losses_grad), _ptr(expert_counts), _ptr(n_valid),
+             _ptr(valid), _ptr(logits_grad))
+
+
+def combine_backward(d: Dims, out_grad, y_rows, pair_to_row, topk_w, topk_w_grad, y_rows_grad=None, stream=None):
+    """moe_combine_backward: the gates' gradient topk_w_grad float32 [T, k] and, if
+    given, the expert rows' gradient y_rows_grad bfloat16 [T*k, H] from out_grad
+    bfloat16 [T, H] (the residual's gradient is out_grad itself).  y_rows may hold
+    more rows than T*k (a shared expert's); y_rows_grad's first T*k are written."""
+    import torch
+    dev, b16 = out_grad.device, (torch.bfloat16, torch.int16)
+    P = d.T * d.k
+    _want("out_grad", out_grad, dev, b16, (d.T, d.H))
+    for name, t in (("y_rows", y_rows), ("y_rows_grad", y_rows_grad)):
+        if t is None:
+            continue
+        _want(name, t, dev, b16)
+        if t.dim() != 2 or t.shape[0] < P or t.shape[1] != d.H:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, at least {(P, d.H)} needed")
+    _want("pair_to_row", pair_to_row, dev, (torch.int32,))
+    if pair_to_row.numel() < P:
+        raise ValueError(f"pair_to_row has {pair_to_row.numel()} entries, {P} needed")
+    _want("topk_w", topk_w, dev, (torch.float32,), (d.T, d.k))
+    _want("topk_w_grad", topk_w_grad, dev, (torch.float32,), (d.T, d.k))
+    _enqueue(lib().moe_combine_backward, dev, stream, ctypes.byref(d), _ptr(out_grad), _ptr(y_rows), _ptr(pair_to_row),
+             _ptr(topk_w), _ptr(topk_w_grad), _ptr(y_rows_grad))
+
+
+from .layer import (LayerBuffers, ResidentExperts, RouterGradBuffers, SharedBuffers, SharedExpert, StackLayer,  # noqa: E402
+                    layer_forward, resident_layer_forward, router_backward, router_losses, stack_forward)  # (orchestration of the calls above)
 
 __all__ = [
     "lib", "abi_version", "status_string", "last_error", "MoeError", "Dims", "dims", "QWeights",
@@ -375,5 +644,8 @@ __all__ = [
     "topk_from_logits", "slot_lookup", "permute", "expert_ffn_q4",
     "expert_ffn_q2", "expert_gateup", "expert_down", "expert_ffn_fused", "expert_ffn_fused_shared", "expert_ffn_fused_noalloc", "NOALLOC_WORKSPACE_BYTES", "combine", "combine_shared", "zero_point_bias", "stream_read", "STREAM_SINK_INTS", "route_counts", "hot_set", "residency_plan",
     "expert_copy", "RESIDENCY_LISTS", "ResidencyC", "LayerBuffers", "ResidentExperts", "resident_layer_forward", "SharedBuffers", "SharedExpert", "layer_forward", "StackLayer", "stack_forward", "EXPORTS",
+    "QMatrix", "LinearBuffers", "linear", "linear_grad", "linear_workspace_bytes", "LINEAR_SYNC_INTS", "BF16", "F32",
+    "BalanceBuffers", "balance_loss", "balance_workspace_bytes", "BALANCE_SYNC_INTS", "route_backward", "combine_backward",
+    "RouterGradBuffers", "router_losses", "router_backward",
     "group_major", "ALGO_AUTO", "ALGO_GEMV", "ALGO_MFMA", "ALGO_GEMM", "OP_ROUTE", "OP_LOOKUP", "OP_PERMUTE", "OP_FFN", "OP_COMBINE",
 ]

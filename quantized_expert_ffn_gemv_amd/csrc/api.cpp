@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "common.h"
+#include "linear.h"
 #include "moe.h"
 
 namespace {
@@ -147,6 +148,36 @@ int ffn_common(const char* fn, int bits, const moe_dims* d, const uint16_t* x,
     return ok();
 }
 
+// Checks shared by the dense quantised products; the pointers too if `pointers`.
+int check_qmatrix(const char* fn, const moe_qmatrix* w, int32_t T, int type, bool pointers) {
+    if (w == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: w is NULL", fn);
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T = %d is negative", fn, T);
+    if (T > 65536) return fail(MOE_ERR_UNSUPPORTED, "%s: T = %d exceeds 65536", fn, T);
+    if (w->bits != 2 && w->bits != 4) return fail(MOE_ERR_UNSUPPORTED, "%s: bits = %d (2 or 4)", fn, w->bits);
+    if (w->group_size != 128 && w->group_size != 64 && w->group_size != 32)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: group_size = %d (32, 64 or 128)", fn, w->group_size);
+    if (w->N < 1 || w->N > 1048576) return fail(MOE_ERR_UNSUPPORTED, "%s: N = %d outside [1, 1048576]", fn, w->N);
+    if (w->K < 128 || w->K > 32768 || w->K % 128 != 0)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 128 in [128, 32768]", fn, w->K);
+    if (type != MOE_BF16 && type != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: element type %d (MOE_BF16 or MOE_F32)", fn, type);
+    if (!pointers) return MOE_OK;
+    REQUIRE_PTR(w->q, 16);
+    REQUIRE_PTR(w->scale, 16);
+    REQUIRE_PTR(w->bias, 16);
+    return MOE_OK;
+}
+
+int check_linear_workspace(const char* fn, const moe_qmatrix* w, int32_t T, int type, bool grad, const void* ws,
+                           size_t ws_bytes) {
+    const size_t need = moe::linear_workspace_bytes(*w, T, type, grad);
+    if (need == 0) return MOE_OK;
+    if (ws == nullptr || ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                    ws == nullptr ? (size_t)0 : ws_bytes);
+    if (!aligned(ws, 256)) return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
+    return MOE_OK;
+}
 
 }  // namespace
 
@@ -609,6 +640,149 @@ int moe_expert_copy(const moe_dims* d, int bits, const moe_qweights* src, const 
             return fail(MOE_ERR_INVALID_ARG, "%s: matrix %d is not 16-byte aligned", fn, m);
     }
     st = moe::launch_expert_copy(*d, bits, *src, *dst, n_dst, copies, n_copy, max_copies, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int grad, size_t* bytes) {
+    const char* fn = "moe_linear_workspace_bytes";
+    if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+    const int st = check_qmatrix(fn, w, T, type, false);
+    if (st) return st;
+    *bytes = T == 0 ? 0 : moe::linear_workspace_bytes(*w, T, type, grad != 0);
+    return ok();
+}
+
+int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, const float* row_bias,
+               const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int y_type, void* ws, size_t ws_bytes,
+               void* stream) {
+    const char* fn = "moe_linear";
+    int st = check_qmatrix(fn, w, T, y_type, T != 0);
+    if (st) return st;
+    if (T == 0) return ok();
+    REQUIRE_PTR(x, 16);
+    if (ldx < w->K || ldx % 8 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: ldx = %lld must be a multiple of 8, at least K = %d", fn, (long long)ldx, w->K);
+    REQUIRE_PTR(y, y_type == MOE_F32 ? 4 : 2);
+    if (ldy < w->N) return fail(MOE_ERR_INVALID_ARG, "%s: ldy = %lld is less than N = %d", fn, (long long)ldy, w->N);
+    if (row_bias && !aligned(row_bias, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: row_bias is not 4-byte aligned", fn);
+    if (residual && !aligned(residual, 2)) return fail(MOE_ERR_INVALID_ARG, "%s: residual is not 2-byte aligned", fn);
+    if (residual && ldr < w->N)
+        return fail(MOE_ERR_INVALID_ARG, "%s: ldr = %lld is less than N = %d", fn, (long long)ldr, w->N);
+    if (residual && residual == y && (y_type != MOE_BF16 || ldr != ldy))
+        return fail(MOE_ERR_INVALID_ARG, "%s: y is the residual but differs from it in type or row stride", fn);
+    st = check_linear_workspace(fn, w, T, y_type, false, ws, ws_bytes);
+    if (st) return st;
+    moe::LinearArgs a{};
+    a.w = *w; a.T = T; a.x = x; a.ldx = ldx; a.row_bias = row_bias; a.residual = residual; a.ldr = ldr;
+    a.y = y; a.ldy = ldy; a.y_type = y_type; a.ws = ws;
+    st = moe::launch_linear(a, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_linear_grad(const moe_qmatrix* w, int32_t T, const void* dy, int64_t lddy, int dy_type, uint16_t* dx,
+                    int64_t lddx, void* ws, size_t ws_bytes, int32_t* sync, void* stream) {
+    const char* fn = "moe_linear_grad";
+    int st = check_qmatrix(fn, w, T, dy_type, T != 0);
+    if (st) return st;
+    if (T == 0) return ok();
+    REQUIRE_PTR(dy, dy_type == MOE_F32 ? 4 : 2);
+    if (lddy < w->N) return fail(MOE_ERR_INVALID_ARG, "%s: lddy = %lld is less than N = %d", fn, (long long)lddy, w->N);
+    REQUIRE_PTR(dx, 16);
+    if (lddx < w->K || lddx % 8 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: lddx = %lld must be a multiple of 8, at least K = %d", fn, (long long)lddx, w->K);
+    REQUIRE_PTR(sync, 256);
+    st = check_linear_workspace(fn, w, T, dy_type, true, ws, ws_bytes);
+    if (st) return st;
+    moe::LinearGradArgs a{};
+    a.w = *w; a.T = T; a.dy = dy; a.lddy = lddy; a.dy_type = dy_type; a.dx = dx; a.lddx = lddx; a.ws = ws; a.sync = sync;
+    st = moe::launch_linear_grad(a, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_balance_workspace_bytes(const moe_dims* d, size_t* bytes) {
+    const char* fn = "moe_balance_workspace_bytes";
+    if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+    const int st = check_dims(fn, d, false, false);
+    if (st) return st;
+    *bytes = moe::balance_workspace_bytes(*d);
+    return ok();
+}
+
+int moe_balance_loss(const moe_dims* d, const float* logits, const int32_t* topk_ids, const uint8_t* valid,
+                     int32_t* expert_counts, float* prob_mean, int32_t* n_valid, float* losses, void* ws,
+                     size_t ws_bytes, int32_t* sync, void* stream) {
+    const char* fn = "moe_balance_loss";
+    int st = check_dims(fn, d, false, false);
+    if (st) return st;
+    if (d->T > 0) {
+        REQUIRE_PTR(logits, 4);
+        REQUIRE_PTR(topk_ids, 4);
+    }
+    REQUIRE_PTR(expert_counts, 4);
+    REQUIRE_PTR(prob_mean, 4);
+    REQUIRE_PTR(n_valid, 4);
+    REQUIRE_PTR(losses, 4);
+    REQUIRE_PTR(sync, 256);
+    const size_t need = moe::balance_workspace_bytes(*d);
+    if (ws == nullptr || ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                    ws == nullptr ? (size_t)0 : ws_bytes);
+    if (!aligned(ws, 256)) return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
+    st = moe::launch_balance_loss(*d, logits, topk_ids, valid, expert_counts, prob_mean, n_valid, losses, ws, sync,
+                                  as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_route_backward(const moe_dims* d, const float* logits, const int32_t* topk_ids, const float* topk_w,
+                       int renormalize, const float* topk_w_grad, const float* losses_grad,
+                       const int32_t* expert_counts, const int32_t* n_valid, const uint8_t* valid, float* logits_grad,
+                       void* stream) {
+    const char* fn = "moe_route_backward";
+    int st = check_dims(fn, d, false, false);
+    if (st) return st;
+    if (d->T == 0) return ok();
+    REQUIRE_PTR(logits, 4);
+    REQUIRE_PTR(logits_grad, 4);
+    if (logits_grad == logits) return fail(MOE_ERR_INVALID_ARG, "%s: logits_grad is logits", fn);
+    if (topk_w_grad) {
+        REQUIRE_PTR(topk_w_grad, 4);
+        REQUIRE_PTR(topk_ids, 4);
+        REQUIRE_PTR(topk_w, 4);
+    }
+    if (losses_grad) {
+        REQUIRE_PTR(losses_grad, 4);
+        REQUIRE_PTR(expert_counts, 4);
+        REQUIRE_PTR(n_valid, 4);
+    }
+    st = moe::launch_route_backward(*d, logits, topk_ids, topk_w, renormalize, topk_w_grad, losses_grad, expert_counts,
+                                    n_valid, valid, logits_grad, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_combine_backward(const moe_dims* d, const uint16_t* out_grad, const uint16_t* y_rows,
+                         const int32_t* pair_to_row, const float* topk_w, float* topk_w_grad, uint16_t* y_rows_grad,
+                         void* stream) {
+    const char* fn = "moe_combine_backward";
+    int st = check_dims(fn, d, true, false);
+    if (st) return st;
+    if (d->T == 0) return ok();
+    REQUIRE_PTR(out_grad, 16);
+    REQUIRE_PTR(y_rows, 16);
+    REQUIRE_PTR(pair_to_row, 4);
+    REQUIRE_PTR(topk_w_grad, 4);
+    if (y_rows_grad) {
+        REQUIRE_PTR(y_rows_grad, 16);
+        REQUIRE_PTR(topk_w, 4);
+        if (y_rows_grad == y_rows || y_rows_grad == out_grad)
+            return fail(MOE_ERR_INVALID_ARG, "%s: y_rows_grad is one of the inputs", fn);
+    }
+    st = moe::launch_combine_backward(*d, out_grad, y_rows, pair_to_row, topk_w, topk_w_grad, y_rows_grad,
+                                      as_stream(stream));
     if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
     return ok();
 }

@@ -232,6 +232,17 @@ int launch_combine(const moe_dims& d, const uint16_t* y, const int32_t* p2r, con
 int launch_combine_shared(const moe_dims& d, const uint16_t* y, const int32_t* p2r, const float* gates,
                           const uint16_t* ys, const uint16_t* x, const float* w, const uint16_t* residual,
                           uint16_t* out, float* gate_out, hipStream_t s);
+// The combine in reverse (combine_backward.hip); dy may be NULL.
+int launch_combine_backward(const moe_dims& d, const uint16_t* dout, const uint16_t* y, const int32_t* p2r,
+                            const float* gates, float* dgates, uint16_t* dy, hipStream_t s);
+// The router's losses and backward pass (router_grad.hip).
+size_t balance_workspace_bytes(const moe_dims& d);
+int launch_balance_loss(const moe_dims& d, const float* logits, const int32_t* ids, const uint8_t* valid,
+                        int32_t* counts, float* prob_mean, int32_t* n_valid, float* losses, void* ws, int32_t* sync,
+                        hipStream_t s);
+int launch_route_backward(const moe_dims& d, const float* logits, const int32_t* ids, const float* gates, int renorm,
+                          const float* dgates, const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                          const uint8_t* valid, float* dlogits, hipStream_t s);
 int launch_zero_point_bias(long n, const uint16_t* scale, const uint8_t* zeros, uint16_t* bias, hipStream_t s);
 int launch_stream_read(const void* src, size_t bytes, uint32_t* sink, hipStream_t s);
 

@@ -1,0 +1,38 @@
+// Arguments and launchers of the dense quantised products.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+struct LinearArgs {
+    moe_qmatrix w;
+    int T;
+    const uint16_t* x;
+    int64_t ldx;
+    const float* row_bias;        // or NULL
+    const uint16_t* residual;     // or NULL
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+    int y_type;                   // MOE_BF16, MOE_F32
+    void* ws;
+};
+
+struct LinearGradArgs {
+    moe_qmatrix w;
+    int T;
+    const void* dy;
+    int64_t lddy;
+    int dy_type;
+    uint16_t* dx;
+    int64_t lddx;
+    void* ws;
+    int32_t* sync;
+};
+
+size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
+int launch_linear(const LinearArgs& a, hipStream_t s);
+int launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
+
+}  // namespace moe

@@ -30,6 +30,10 @@ already resident runs, then the FFN of the rest and the combine.
 layers back to back (each layer's output is the next one's input), the unit
 that is captured once in a HIP graph and replayed per token.
 
+``RouterGradBuffers``, ``router_losses`` and ``router_backward`` are the training
+side of a step with the quantised experts frozen: the router's losses after the
+routing, and the way back from the layer's output to the logits.
+
 This module only orders the calls; the arithmetic is in the HIP kernels.
 """
 from __future__ import annotations
@@ -40,9 +44,10 @@ from typing import Optional, Sequence
 import torch
 
 from . import (ALGO_AUTO, DISPATCH_SYNC_INTS, FFN_SYNC_INTS, OP_FFN, RESIDENCY_LISTS, WORK_ENTRY_INTS, Dims,
-               QWeights, combine, combine_shared, dims, expert_copy, expert_ffn_fused, expert_ffn_fused_shared,
-               expert_ffn_q2, expert_ffn_q4, permute, residency_plan, route_counts, route_dispatch, route_topk,
-               slot_lookup, work_list_capacity, workspace_bytes)
+               BalanceBuffers, QWeights, balance_loss, combine, combine_backward, combine_shared, dims, expert_copy,
+               expert_ffn_fused, expert_ffn_fused_shared, expert_ffn_q2, expert_ffn_q4, permute, residency_plan,
+               route_backward, route_counts, route_dispatch, route_topk, slot_lookup, work_list_capacity,
+               workspace_bytes)
 
 
 @dataclass
@@ -197,6 +202,54 @@ def layer_forward(buf: LayerBuffers, x: torch.Tensor, w_router: torch.Tensor,
         ys, gate_out = sb.buf.y_rows, sb.gate_out
     combine_shared(d, buf.y_rows, buf.pair_to_row, buf.topk_w, ys, x, shared.gate_w, residual, out, gate_out,
                    stream)
+
+
+@dataclass
+class RouterGradBuffers:
+    """What a layer's router training pass writes, and its scratch."""
+    d: Dims
+    counts: torch.Tensor          # int32 [E]: picks of the tokens that take part
+    prob_mean: torch.Tensor       # float32 [E]
+    n_valid: torch.Tensor         # int32 [1]
+    losses: torch.Tensor          # float32 [2]: balance, z
+    topk_w_grad: torch.Tensor     # float32 [T, k]
+    logits_grad: torch.Tensor     # float32 [T, E]
+    scratch: BalanceBuffers
+
+    @staticmethod
+    def allocate(d: Dims, device="cuda") -> "RouterGradBuffers":
+        f32 = dict(dtype=torch.float32, device=device)
+        return RouterGradBuffers(
+            d=d, counts=torch.empty((d.E,), dtype=torch.int32, device=device), prob_mean=torch.empty((d.E,), **f32),
+            n_valid=torch.empty((1,), dtype=torch.int32, device=device), losses=torch.empty((2,), **f32),
+            topk_w_grad=torch.empty((d.T, d.k), **f32), logits_grad=torch.empty((d.T, d.E), **f32),
+            scratch=BalanceBuffers.allocate(d, device))
+
+
+def router_losses(buf: LayerBuffers, grads: RouterGradBuffers, valid: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """After a layer step on `buf`: the per-expert counts, mean probabilities and
+    the balance and z losses of its routing.  valid: None, or uint8/bool [T], 0 for
+    padded tokens.  Returns grads.losses (on the GPU)."""
+    balance_loss(buf.d, buf.logits, buf.topk_ids, grads.counts, grads.prob_mean, grads.n_valid, grads.losses,
+                 grads.scratch, valid, stream)
+    return grads.losses
+
+
+def router_backward(buf: LayerBuffers, grads: RouterGradBuffers, out_grad: torch.Tensor,
+                    losses_grad: Optional[torch.Tensor] = None, valid: Optional[torch.Tensor] = None,
+                    y_rows_grad: Optional[torch.Tensor] = None, renormalize: bool = True, stream=None) -> torch.Tensor:
+    """The way back through a layer step on `buf` to its logits, from out_grad
+    (bf16 [T, H]; also the residual's gradient) and losses_grad (float32 [2] on
+    the GPU, the gradients of router_losses()'s two losses, with the same valid).
+    The gates of a shared expert's step are unchanged by it, so this holds for
+    such a step too.  y_rows_grad: None, or bf16 [T*k, H] for the gradient of the
+    expert rows.  Returns grads.logits_grad; the router weight's gradient is
+    logits_grad^T x and its bias' the sum of logits_grad over the tokens."""
+    combine_backward(buf.d, out_grad, buf.y_rows, buf.pair_to_row, buf.topk_w, grads.topk_w_grad, y_rows_grad, stream)
+    route_backward(buf.d, buf.logits, buf.topk_ids, buf.topk_w, renormalize, grads.logits_grad, grads.topk_w_grad,
+                   losses_grad, grads.counts, grads.n_valid, valid, stream)
+    return grads.logits_grad
 
 
 @dataclass

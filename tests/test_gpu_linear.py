@@ -1,0 +1,282 @@
+"""Dense quantised products and their input gradient on the GPU against the
+64-bit forms of weights_ref.py, with its bounds."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_expert_ffn_gemv_amd as moe
+import weights_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+NAN = float("nan")
+
+
+class Matrix:
+    def __init__(self, seed, N, K, bits=4, group=128, scale=(0.005, 0.02), parts=None):
+        rng = np.random.default_rng(seed)
+        q, s, b = ref.make_matrix(rng, N, K, bits, group, scale) if parts is None else parts
+        self.N, self.K, self.rng = N, K, rng
+        self.W, self.mag = ref.weights(q, s, b, bits, group)
+        self.q = moe.QMatrix(bits, group, torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV),
+                             torch.from_numpy(b).to(DEV))
+
+    def rows(self, T, C, size=1.0):
+        return ref.bf16_round(size * self.rng.standard_normal((T, C)).astype(np.float32))
+
+
+def dev(a, dtype=torch.bfloat16):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV, dtype)
+
+
+def wide(a, pad, dtype=torch.bfloat16):
+    """a's values as the first columns of a wider buffer of NaNs."""
+    buf = torch.full((a.shape[0], a.shape[1] + pad), NAN, dtype=dtype, device=DEV)
+    buf[:, :a.shape[1]] = dev(a, dtype)
+    return buf[:, :a.shape[1]]
+
+
+def check(got, want, bound, what):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all(), what
+    worst = float(np.max(np.abs(got - want) / bound)) if want.size else 0.0
+    assert worst <= 1.0, f"{what}: {worst:.3g} times the bound"
+
+
+def run_linear(m, T, f32=False, row_bias=False, residual=False, pad=0, x=None):
+    dt = torch.float32 if f32 else torch.bfloat16
+    x = m.rows(T, m.K) if x is None else x
+    rb = (0.5 * m.rng.standard_normal(m.N)).astype(np.float32) if row_bias else None
+    res = m.rows(T, m.N) if residual else None
+    ybuf = torch.full((T + 1, m.N + pad + 1), 7.0, dtype=dt, device=DEV)
+    y = ybuf[:T, :m.N]
+    y.fill_(NAN)
+    buf = moe.LinearBuffers.allocate(m.q, T, dt)
+    moe.linear(m.q, wide(x, 8 * pad), y, buf, row_bias=None if rb is None else dev(rb, torch.float32),
+               residual=None if res is None else wide(res, pad))
+    torch.cuda.synchronize()
+    assert bool((ybuf[T:] == 7.0).all()) and bool((ybuf[:, m.N:] == 7.0).all()), "wrote outside y"
+    want = ref.linear(x, m.W, rb, res)
+    extra = (0 if rb is None else np.abs(rb)) + (0 if res is None else np.abs(res))
+    check(y, want, ref.linear_bound(x, m.W, m.mag, want, f32, extra), f"T={T} N={m.N} K={m.K}")
+    return y
+
+
+def run_grad(m, T, f32=False, pad=0, dy=None):
+    dt = torch.float32 if f32 else torch.bfloat16
+    if dy is None:
+        dy = 1e-3 * np.exp(2 * m.rng.standard_normal((T, 1))) * m.rng.standard_normal((T, m.N))
+        dy = dy.astype(np.float32) if f32 else ref.bf16_round(dy.astype(np.float32))
+        dy[::5] = 0.0
+    dxbuf = torch.full((T + 1, m.K + 8 * pad + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    dx = dxbuf[:T, :m.K]
+    dx.fill_(NAN)
+    buf = moe.LinearBuffers.allocate(m.q, T, dt, grad=True)
+    buf.workspace.fill_(0xFF)
+    moe.linear_grad(m.q, wide(dy, pad, dt), dx, buf)
+    torch.cuda.synchronize()
+    assert bool((dxbuf[T:] == 7.0).all()) and bool((dxbuf[:, m.K:] == 7.0).all()), "wrote outside dx"
+    assert int(buf.sync.abs().sum()) == 0
+    want = dy.astype(np.float64) @ m.W
+    check(dx, want, ref.linear_grad_bound(dy, m.W, m.mag, want), f"T={T} N={m.N} K={m.K}")
+    return dx
+
+
+SHAPES = [(1, 1, 128), (1, 2048, 2048), (2, 15, 256), (3, 16, 384), (5, 17, 128), (8, 100, 1152), (16, 333, 640),
+          (17, 128, 256), (31, 65, 512), (33, 47, 2048), (48, 200, 384), (64, 129, 256), (65, 64, 128), (97, 300, 512),
+          (128, 256, 256), (129, 130, 384), (200, 77, 1024), (257, 513, 640), (400, 1, 256), (513, 384, 1152)]
+
+
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 64), (4, 32), (2, 128), (2, 64), (2, 32)])
+def test_linear_shapes(bits, group):
+    for i, (T, N, K) in enumerate(SHAPES):
+        m = Matrix(100 * i + bits + group, N, K, bits, group)
+        run_linear(m, T, f32=i % 3 == 1, row_bias=i % 2 == 0, residual=i % 4 < 2, pad=i % 3)
+
+
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 64), (4, 32), (2, 128), (2, 64), (2, 32)])
+def test_linear_grad_shapes(bits, group):
+    for i, (T, N, K) in enumerate(SHAPES):
+        m = Matrix(100 * i + bits + group + 1, N, K, bits, group)
+        run_grad(m, T, f32=i % 3 == 1, pad=i % 3)
+
+
+@pytest.mark.parametrize("T", [1, 4, 16, 60])
+def test_linear_tall_and_wide(T):
+    """Many output rows (a vocabulary) and a long K, with partial last tiles."""
+    run_linear(Matrix(T, 20011, 512), T, f32=True)
+    run_grad(Matrix(T + 1, 20011, 256), T)
+    run_linear(Matrix(T + 2, 40, 16384, 2), T, row_bias=True)
+    run_grad(Matrix(T + 3, 40, 16384, 2, 32), T, f32=True)
+
+
+@pytest.mark.parametrize("T", [1024, 1500])
+@pytest.mark.parametrize("f32", [False, True])
+def test_linear_prompt(T, f32):
+    m = Matrix(T, 1030, 1280, 4, 128)
+    run_linear(m, T, f32=f32, row_bias=True, residual=True, pad=1)
+    run_grad(m, T, f32=f32, pad=1)
+
+
+@pytest.mark.parametrize("T", [1, 9, 64, 300])
+def test_residual_in_place(T):
+    m = Matrix(T, 96, 256)
+    x, res = m.rows(T, m.K), m.rows(T, m.N)
+    y = dev(res)
+    moe.linear(m.q, dev(x), y, moe.LinearBuffers.allocate(m.q, T, y.dtype), residual=y)
+    want = ref.linear(x, m.W, None, res)
+    check(y, want, ref.linear_bound(x, m.W, m.mag, want, False, np.abs(res)), "in place")
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_a_bad_row_stays_in_its_row(T, bad):
+    m = Matrix(T, 80, 256)
+    x = m.rows(T, m.K)
+    clean = run_linear(m, T, x=x).clone()
+    xb = x.copy()
+    xb[1, 70] = bad
+    y = torch.empty_like(clean)
+    moe.linear(m.q, dev(xb), y, moe.LinearBuffers.allocate(m.q, T, y.dtype))
+    assert not bool(torch.isfinite(y[1]).any())
+    keep = torch.arange(T, device=DEV) != 1
+    assert torch.equal(y[keep], clean[keep])
+    dy = m.rows(T, m.N)
+    clean = run_grad(m, T, dy=dy).clone()
+    db = dy.copy()
+    db[1, 7] = bad
+    dx = torch.empty_like(clean)
+    moe.linear_grad(m.q, dev(db), dx, moe.LinearBuffers.allocate(m.q, T, dx.dtype, grad=True))
+    assert not bool(torch.isfinite(dx[1]).any())
+    assert torch.equal(dx[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [1, 20, 200])
+@pytest.mark.parametrize("kind", ["zero", "large", "tiny", "mixed"])
+def test_extreme_scales(T, kind):
+    """Zero scales, the largest and smallest fp16 scales, and both in one matrix."""
+    rng = np.random.default_rng(5)
+    N, K, group = 50, 512, 64
+    q, s, b = ref.make_matrix(rng, N, K, 4, group)
+    if kind == "zero":
+        s[rng.random(s.shape) < 0.3] = 0
+    elif kind == "large":
+        s[:] = np.float16(60000)
+        b[:] = np.float16(-65504)
+    elif kind == "tiny":
+        s[:] = np.float16(6e-8)
+        b[:] = np.float16(-6e-8)
+    else:
+        s[:] = np.exp(rng.uniform(np.log(1e-4), np.log(1.0), s.shape)).astype(np.float16)
+        b[:] = -s
+    m = Matrix(1, N, K, 4, group, parts=(q, s, b))
+    run_linear(m, T)
+    run_linear(m, T, f32=True)
+    run_grad(m, T)
+
+
+@pytest.mark.parametrize("T", [7, 150])
+def test_gradient_of_zeros_and_of_very_different_rows(T):
+    m = Matrix(T, 130, 256)
+    assert bool((run_grad(m, T, dy=np.zeros((T, m.N), np.float32)) == 0).all())
+    dy = m.rows(T, m.N) * np.float32(2.0) ** m.rng.integers(-90, 90, (T, 1)).astype(np.float32)
+    run_grad(m, T, dy=ref.bf16_round(dy))
+    x = m.rows(T, m.K) * np.float32(2.0) ** m.rng.integers(-90, 90, (T, 1)).astype(np.float32)
+    run_linear(m, T, x=ref.bf16_round(x))
+
+
+@pytest.mark.parametrize("T", [2, 40, 300])
+def test_grad_is_the_transpose_of_linear(T):
+    """<dy, W x> = <dx, x>: both sides by the kernels, each within its own bound."""
+    m = Matrix(T, 120, 384)
+    x, dy = m.rows(T, m.K), m.rows(T, m.N)
+    y = run_linear(m, T, f32=True, x=x).double().cpu().numpy()
+    dx = run_grad(m, T, dy=dy).double().cpu().numpy()
+    for t in range(T):
+        left, right = float(y[t] @ dy[t]), float(dx[t] @ x[t])
+        by = ref.linear_bound(x, m.W, m.mag, y, True)[t]
+        bx = ref.linear_grad_bound(dy, m.W, m.mag, dx)[t]
+        assert abs(left - right) <= float(by @ np.abs(dy[t]) + bx @ np.abs(x[t]))
+
+
+@pytest.mark.parametrize("T", [1, 24, 260])
+def test_other_streams_and_two_calls_at_once(T):
+    a, b = Matrix(1, 500, 512), Matrix(2, 300, 1024, 2, 64)
+    jobs = []
+    for m in (a, b):
+        x, dy = dev(m.rows(T, m.K)), dev(m.rows(T, m.N))
+        y, dx = torch.empty(T, m.N, dtype=torch.float32, device=DEV), torch.empty(T, m.K, dtype=torch.bfloat16, device=DEV)
+        fb, gb = moe.LinearBuffers.allocate(m.q, T, y.dtype), moe.LinearBuffers.allocate(m.q, T, dy.dtype, grad=True)
+        moe.linear(m.q, x, y, fb)
+        moe.linear_grad(m.q, dy, dx, gb)
+        jobs.append((m, x, dy, y, dx, fb, gb, y.clone(), dx.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for m, x, dy, y, dx, *_ in jobs:
+        y.fill_(NAN)
+        dx.fill_(NAN)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for m, x, dy, y, dx, fb, gb, _, _, s in jobs:
+            moe.linear(m.q, x, y, fb, stream=s)
+            with torch.cuda.stream(s):
+                moe.linear_grad(m.q, dy, dx, gb)
+    torch.cuda.synchronize()
+    for m, x, dy, y, dx, fb, gb, y0, dx0, s in jobs:
+        assert torch.equal(y, y0) and torch.equal(dx, dx0)
+
+
+@pytest.mark.parametrize("T", [1, 12, 70, 300])
+def test_graph_replay(T):
+    m = Matrix(T, 700, 768)
+    x, dy = dev(m.rows(T, m.K)), dev(m.rows(T, m.N))
+    y, dx = torch.empty(T, m.N, dtype=torch.bfloat16, device=DEV), torch.empty(T, m.K, dtype=torch.bfloat16, device=DEV)
+    fb, gb = moe.LinearBuffers.allocate(m.q, T, y.dtype), moe.LinearBuffers.allocate(m.q, T, dy.dtype, grad=True)
+
+    def step():
+        moe.linear(m.q, x, y, fb)
+        moe.linear_grad(m.q, dy, dx, gb)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        x.copy_(dev(m.rows(T, m.K)))
+        dy.copy_(dev(m.rows(T, m.N)))
+        step()
+        torch.cuda.synchronize()
+        want = (y.clone(), dx.clone())
+        y.fill_(NAN)
+        dx.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(dx, want[1]), f"replay {i}"
+    # two graphs that share the buffers, one after the other
+    other = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(other):
+        step()
+    for g in (graph, other, graph):
+        y.fill_(NAN)
+        dx.fill_(NAN)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+
+
+def test_no_tokens():
+    m = Matrix(0, 64, 128)
+    y, dx = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), torch.empty(0, 128, dtype=torch.bfloat16, device=DEV)
+    moe.linear(m.q, torch.empty(0, 128, dtype=torch.bfloat16, device=DEV), y)
+    moe.linear_grad(m.q, y, dx, moe.LinearBuffers.allocate(m.q, 0, y.dtype, grad=True))
+
+
+def test_bits_as_int16_are_the_same_call():
+    m = Matrix(3, 48, 256)
+    x = dev(m.rows(5, m.K))
+    y = torch.empty(5, m.N, dtype=torch.bfloat16, device=DEV)
+    moe.linear(m.q, x, y)
+    q16 = moe.QMatrix(4, 128, m.q.q, m.q.scale.view(torch.int16), m.q.bias.view(torch.int16))
+    y16 = torch.empty(5, m.N, dtype=torch.int16, device=DEV)
+    moe.linear(q16, x.view(torch.int16), y16)
+    assert torch.equal(y16, y.view(torch.int16))
