@@ -389,17 +389,24 @@ LINEAR_SYNC_INTS = 4096                      # MOE_LINEAR_SYNC_INTS
 BALANCE_SYNC_INTS = 1088                     # MOE_BALANCE_SYNC_INTS
 
 
+import torch  # noqa: E402
+
+_BITS16 = (torch.bfloat16, torch.int16)      # bf16, or its bits
+_HALF16 = (torch.float16, torch.int16)
+_VALUES = (torch.bfloat16, torch.int16, torch.float32)
+_F32S, _I32S, _BYTES, _FLAGS = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.uint8, torch.bool)
+
+
 def _element_type(dtype) -> int:
-    import torch
-    if dtype == torch.bfloat16 or dtype == torch.int16:
+    if dtype in _BITS16:
         return BF16
     if dtype == torch.float32:
         return F32
     raise ValueError(f"elements of type {dtype}: bfloat16 (or its bits as int16) or float32 needed")
 
 
-def _want(name: str, t, device, dtypes, shape=None) -> None:
-    """A contiguous tensor on `device` of one of these types (and this shape)."""
+def _want(name: str, t, device, dtypes, shape=None) -> int:
+    """The address of a contiguous tensor on `device` of one of these types (and this shape)."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype not in dtypes:
@@ -408,35 +415,38 @@ def _want(name: str, t, device, dtypes, shape=None) -> None:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {shape} needed")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
+    return t.data_ptr()
 
 
 def _want_rows(name: str, t, device, dtypes, rows: int, cols: int) -> int:
-    """A [rows, cols] tensor whose rows are contiguous; returns their stride."""
+    """The row stride of a [rows, cols] tensor whose rows are contiguous."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} holds {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {(rows, cols)} needed")
-    if cols > 1 and t.stride(1) != 1:
+    to_row, to_col = t.stride()
+    if to_col != 1 and cols > 1:
         raise ValueError(f"{name}'s rows are not contiguous")
-    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    return to_row if rows > 1 else cols
 
 
 def _enqueue(fn, device, stream, *args) -> None:
     """fn(*args, stream) on `device`: the given stream, or that device's current one."""
-    import torch
     if device.type != "cuda":
         raise ValueError(f"tensors on {device}: the library runs on the GPU")
     if stream is None:
-        s = torch.cuda.current_stream(device).cuda_stream
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without its object
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, s))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s))
+            status = fn(*args, stream)
+    if status != OK:
+        _check(status)
 
 
 @dataclass(frozen=True, eq=False)
@@ -446,37 +456,27 @@ class QMatrix:
     bias fp16 (or their bits as int16) [N, K/group_size]."""
     bits: int
     group_size: int
-    q: "torch.Tensor"
-    scale: "torch.Tensor"
-    bias: "torch.Tensor"
+    q: torch.Tensor
+    scale: torch.Tensor
+    bias: torch.Tensor
 
     def __post_init__(self):
-        import torch
         if self.bits not in (2, 4) or self.group_size not in (32, 64, 128):
             raise ValueError(f"{self.bits}-bit codes in groups of {self.group_size}: bits 4 or 2, groups 128, 64 or 32")
         if self.q.dim() != 3 or self.q.shape[2] != 16 * self.bits:
             raise ValueError(f"q has shape {tuple(self.q.shape)}, [K/128, N, {16 * self.bits}] needed")
-        _want("q", self.q, self.q.device, (torch.uint8,))
-        half = (torch.float16, torch.int16)
-        shape = (self.N, self.K // self.group_size)
-        _want("scale", self.scale, self.q.device, half, shape)
-        _want("bias", self.bias, self.q.device, half, shape)
-        c = QMatrixC(_ptr(self.q), _ptr(self.scale), _ptr(self.bias), self.N, self.K, self.group_size, self.bits)
-        object.__setattr__(self, "_c", c)
-
-    @property
-    def N(self) -> int:
-        return self.q.shape[1]
-
-    @property
-    def K(self) -> int:
-        return 128 * self.q.shape[0]
+        N, K, dev = self.q.shape[1], 128 * self.q.shape[0], self.q.device
+        shape = (N, K // self.group_size)
+        c = QMatrixC(_want("q", self.q, dev, _BYTES), _want("scale", self.scale, dev, _HALF16, shape),
+                     _want("bias", self.bias, dev, _HALF16, shape), N, K, self.group_size, self.bits)
+        for name, v in (("N", N), ("K", K), ("_c", c), ("_ref", ctypes.byref(c))):
+            object.__setattr__(self, name, v)
 
 
 def linear_workspace_bytes(w: QMatrix, T: int, dtype, grad: bool = False) -> int:
     """moe_linear_workspace_bytes; dtype: the type of y, or of dy with grad."""
     out = ctypes.c_size_t(0)
-    _check(lib().moe_linear_workspace_bytes(ctypes.byref(w._c), int(T), _element_type(dtype), int(bool(grad)),
+    _check(lib().moe_linear_workspace_bytes(w._ref, int(T), _element_type(dtype), int(bool(grad)),
                                             ctypes.byref(out)))
     return int(out.value)
 
@@ -485,16 +485,23 @@ def linear_workspace_bytes(w: QMatrix, T: int, dtype, grad: bool = False) -> int
 class LinearBuffers:
     """What linear() or linear_grad() need beside their operands, for calls of up
     to the sizes they were allocated for, one at a time on one stream."""
-    workspace: "torch.Tensor"     # uint8
-    sync: "torch.Tensor"          # int32 [LINEAR_SYNC_INTS], zeros (every call leaves them zero)
+    workspace: torch.Tensor       # uint8
+    sync: torch.Tensor            # int32 [LINEAR_SYNC_INTS], zeros (every call leaves them zero)
 
     @staticmethod
     def allocate(w: QMatrix, T: int, dtype, grad: bool = False) -> "LinearBuffers":
-        import torch
         dev = w.q.device
         return LinearBuffers(
             workspace=torch.empty(max(linear_workspace_bytes(w, T, dtype, grad), 256), dtype=torch.uint8, device=dev),
             sync=torch.zeros(LINEAR_SYNC_INTS if grad else 1, dtype=torch.int32, device=dev))
+
+
+def _scratch(buffers, device):
+    """(address, bytes) of a call's workspace."""
+    if buffers is None:
+        return None, 0
+    ws = buffers.workspace
+    return _want("buffers.workspace", ws, device, _BYTES), ws.numel()
 
 
 def linear(w: QMatrix, x, y, buffers: Optional[LinearBuffers] = None, row_bias=None, residual=None, stream=None):
@@ -503,38 +510,29 @@ def linear(w: QMatrix, x, y, buffers: Optional[LinearBuffers] = None, row_bias=N
     8 elements); row_bias float32 [N]; residual bfloat16 [T, N] (may be y itself).
     buffers: LinearBuffers.allocate(w, T, y.dtype), or None where no workspace is
     needed."""
-    import torch
-    dev, b16 = w.q.device, (torch.bfloat16, torch.int16)
+    dev, N = w.q.device, w.N
     T = x.shape[0]
-    ldx = _want_rows("x", x, dev, b16, T, w.K)
-    ldy = _want_rows("y", y, dev, b16 + (torch.float32,), T, w.N)
-    ldr = 0
-    if residual is not None:
-        ldr = _want_rows("residual", residual, dev, b16, T, w.N)
-    if row_bias is not None:
-        _want("row_bias", row_bias, dev, (torch.float32,), (w.N,))
-    ws = None if buffers is None else buffers.workspace
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"the buffers are on {ws.device}, not on {dev}")
-    _enqueue(lib().moe_linear, dev, stream, ctypes.byref(w._c), T, _ptr(x), ldx, _ptr(row_bias), _ptr(residual), ldr,
-             _ptr(y), ldy, _element_type(y.dtype), _ptr(ws), _nbytes(ws))
+    ldx = _want_rows("x", x, dev, _BITS16, T, w.K)
+    ldy = _want_rows("y", y, dev, _VALUES, T, N)
+    ldr = 0 if residual is None else _want_rows("residual", residual, dev, _BITS16, T, N)
+    rb = None if row_bias is None else _want("row_bias", row_bias, dev, _F32S, (N,))
+    ws, nbytes = _scratch(buffers, dev)
+    _enqueue(lib().moe_linear, dev, stream, w._ref, T, x.data_ptr(), ldx, rb,
+             None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, _element_type(y.dtype), ws, nbytes)
 
 
 def linear_grad(w: QMatrix, dy, dx, buffers: LinearBuffers, stream=None):
     """moe_linear_grad: dx = dy W.  dy bfloat16 or float32 [T, N] and dx bfloat16
     [T, K], rows contiguous (dx's row stride a multiple of 8 elements).  buffers:
     LinearBuffers.allocate(w, T, dy.dtype, grad=True)."""
-    import torch
-    dev, b16 = w.q.device, (torch.bfloat16, torch.int16)
+    dev = w.q.device
     T = dy.shape[0]
-    lddy = _want_rows("dy", dy, dev, b16 + (torch.float32,), T, w.N)
-    lddx = _want_rows("dx", dx, dev, b16, T, w.K)
-    _want("buffers.sync", buffers.sync, dev, (torch.int32,), (LINEAR_SYNC_INTS,))
-    ws = buffers.workspace
-    if ws.device != dev:
-        raise ValueError(f"the buffers are on {ws.device}, not on {dev}")
-    _enqueue(lib().moe_linear_grad, dev, stream, ctypes.byref(w._c), T, _ptr(dy), lddy, _element_type(dy.dtype),
-             _ptr(dx), lddx, _ptr(ws), _nbytes(ws), _ptr(buffers.sync))
+    lddy = _want_rows("dy", dy, dev, _VALUES, T, w.N)
+    lddx = _want_rows("dx", dx, dev, _BITS16, T, w.K)
+    ws, nbytes = _scratch(buffers, dev)
+    sync = _want("buffers.sync", buffers.sync, dev, _I32S, (LINEAR_SYNC_INTS,))
+    _enqueue(lib().moe_linear_grad, dev, stream, w._ref, T, dy.data_ptr(), lddy, _element_type(dy.dtype),
+             dx.data_ptr(), lddx, ws, nbytes, sync)
 
 
 def balance_workspace_bytes(d: Dims) -> int:
@@ -546,20 +544,17 @@ def balance_workspace_bytes(d: Dims) -> int:
 @dataclass
 class BalanceBuffers:
     """balance_loss()'s scratch, for calls of these dims' E, one at a time on one stream."""
-    workspace: "torch.Tensor"     # uint8
-    sync: "torch.Tensor"          # int32 [BALANCE_SYNC_INTS], zeros (every call leaves them zero)
+    workspace: torch.Tensor       # uint8
+    sync: torch.Tensor            # int32 [BALANCE_SYNC_INTS], zeros (every call leaves them zero)
 
     @staticmethod
     def allocate(d: Dims, device="cuda") -> "BalanceBuffers":
-        import torch
         return BalanceBuffers(workspace=torch.empty(balance_workspace_bytes(d), dtype=torch.uint8, device=device),
                               sync=torch.zeros(BALANCE_SYNC_INTS, dtype=torch.int32, device=device))
 
 
-def _want_valid(valid, dev, T: int) -> None:
-    import torch
-    if valid is not None:
-        _want("valid", valid, dev, (torch.uint8, torch.bool), (T,))
+def _want_valid(valid, dev, T: int) -> Optional[int]:
+    return None if valid is None else _want("valid", valid, dev, _FLAGS, (T,))
 
 
 def balance_loss(d: Dims, logits, topk_ids, expert_counts, prob_mean, n_valid, losses, buffers: BalanceBuffers,
@@ -567,22 +562,13 @@ def balance_loss(d: Dims, logits, topk_ids, expert_counts, prob_mean, n_valid, l
     """moe_balance_loss: per-expert counts int32 [E], mean probabilities float32
     [E], tokens that take part int32 [1] and the losses float32 [2] (balance, z)
     of logits float32 [T, E] and picks int32 [T, k]; valid: None or uint8/bool [T]."""
-    import torch
-    dev = logits.device
-    _want("logits", logits, dev, (torch.float32,), (d.T, d.E))
-    _want("topk_ids", topk_ids, dev, (torch.int32,), (d.T, d.k))
-    _want_valid(valid, dev, d.T)
-    _want("expert_counts", expert_counts, dev, (torch.int32,), (d.E,))
-    _want("prob_mean", prob_mean, dev, (torch.float32,), (d.E,))
-    _want("n_valid", n_valid, dev, (torch.int32,), (1,))
-    _want("losses", losses, dev, (torch.float32,), (2,))
-    _want("buffers.sync", buffers.sync, dev, (torch.int32,), (BALANCE_SYNC_INTS,))
-    ws = buffers.workspace
-    if ws.device != dev:
-        raise ValueError(f"the buffers are on {ws.device}, not on {dev}")
-    _enqueue(lib().moe_balance_loss, dev, stream, ctypes.byref(d), _ptr(logits), _ptr(topk_ids), _ptr(valid),
-             _ptr(expert_counts), _ptr(prob_mean), _ptr(n_valid), _ptr(losses), _ptr(ws), _nbytes(ws),
-             _ptr(buffers.sync))
+    dev, T, E = logits.device, d.T, d.E
+    ws, nbytes = _scratch(buffers, dev)
+    _enqueue(lib().moe_balance_loss, dev, stream, ctypes.byref(d), _want("logits", logits, dev, _F32S, (T, E)),
+             _want("topk_ids", topk_ids, dev, _I32S, (T, d.k)), _want_valid(valid, dev, T),
+             _want("expert_counts", expert_counts, dev, _I32S, (E,)), _want("prob_mean", prob_mean, dev, _F32S, (E,)),
+             _want("n_valid", n_valid, dev, _I32S, (1,)), _want("losses", losses, dev, _F32S, (2,)), ws, nbytes,
+             _want("buffers.sync", buffers.sync, dev, _I32S, (BALANCE_SYNC_INTS,)))
 
 
 def route_backward(d: Dims, logits, topk_ids, topk_w, renormalize: bool, logits_grad, topk_w_grad=None,
@@ -591,24 +577,28 @@ def route_backward(d: Dims, logits, topk_ids, topk_w, renormalize: bool, logits_
     topk_w_grad float32 [T, k] (None: no such part) and the losses' gradients
     losses_grad float32 [2] on the GPU (None: no such part; else with
     balance_loss()'s expert_counts and n_valid)."""
-    import torch
-    dev, f32, i32 = logits.device, (torch.float32,), (torch.int32,)
-    _want("logits", logits, dev, f32, (d.T, d.E))
-    _want("logits_grad", logits_grad, dev, f32, (d.T, d.E))
+    dev, T, E = logits.device, d.T, d.E
+    ids = g = dg = dl = counts = n = None
     if topk_w_grad is not None:
-        _want("topk_w_grad", topk_w_grad, dev, f32, (d.T, d.k))
-        _want("topk_w", topk_w, dev, f32, (d.T, d.k))
-        _want("topk_ids", topk_ids, dev, i32, (d.T, d.k))
+        picks = (T, d.k)
+        dg = _want("topk_w_grad", topk_w_grad, dev, _F32S, picks)
+        g = _want("topk_w", topk_w, dev, _F32S, picks)
+        ids = _want("topk_ids", topk_ids, dev, _I32S, picks)
     if losses_grad is not None:
         if expert_counts is None or n_valid is None:
             raise ValueError("the losses' gradient needs expert_counts and n_valid")
-        _want("losses_grad", losses_grad, dev, f32, (2,))
-        _want("expert_counts", expert_counts, dev, i32, (d.E,))
-        _want("n_valid", n_valid, dev, i32, (1,))
-    _want_valid(valid, dev, d.T)
-    _enqueue(lib().moe_route_backward, dev, stream, ctypes.byref(d), _ptr(logits), _ptr(topk_ids), _ptr(topk_w),
-             int(bool(renormalize)), _ptr(topk_w_grad), _ptr(losses_grad), _ptr(expert_counts), _ptr(n_valid),
-             _ptr(valid), _ptr(logits_grad))
+        dl = _want("losses_grad", losses_grad, dev, _F32S, (2,))
+        counts = _want("expert_counts", expert_counts, dev, _I32S, (E,))
+        n = _want("n_valid", n_valid, dev, _I32S, (1,))
+    _enqueue(lib().moe_route_backward, dev, stream, ctypes.byref(d), _want("logits", logits, dev, _F32S, (T, E)), ids, g,
+             1 if renormalize else 0, dg, dl, counts, n, _want_valid(valid, dev, T),
+             _want("logits_grad", logits_grad, dev, _F32S, (T, E)))
+
+
+def _want_pair_rows(name: str, t, device, P: int, H: int) -> int:
+    if t.dim() != 2 or t.shape[0] < P or t.shape[1] != H:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, at least {(P, H)} needed")
+    return _want(name, t, device, _BITS16)
 
 
 def combine_backward(d: Dims, out_grad, y_rows, pair_to_row, topk_w, topk_w_grad, y_rows_grad=None, stream=None):
@@ -616,23 +606,14 @@ def combine_backward(d: Dims, out_grad, y_rows, pair_to_row, topk_w, topk_w_grad
     given, the expert rows' gradient y_rows_grad bfloat16 [T*k, H] from out_grad
     bfloat16 [T, H] (the residual's gradient is out_grad itself).  y_rows may hold
     more rows than T*k (a shared expert's); y_rows_grad's first T*k are written."""
-    import torch
-    dev, b16 = out_grad.device, (torch.bfloat16, torch.int16)
-    P = d.T * d.k
-    _want("out_grad", out_grad, dev, b16, (d.T, d.H))
-    for name, t in (("y_rows", y_rows), ("y_rows_grad", y_rows_grad)):
-        if t is None:
-            continue
-        _want(name, t, dev, b16)
-        if t.dim() != 2 or t.shape[0] < P or t.shape[1] != d.H:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, at least {(P, d.H)} needed")
-    _want("pair_to_row", pair_to_row, dev, (torch.int32,))
+    dev, T, H, k = out_grad.device, d.T, d.H, d.k
+    P = T * k
     if pair_to_row.numel() < P:
         raise ValueError(f"pair_to_row has {pair_to_row.numel()} entries, {P} needed")
-    _want("topk_w", topk_w, dev, (torch.float32,), (d.T, d.k))
-    _want("topk_w_grad", topk_w_grad, dev, (torch.float32,), (d.T, d.k))
-    _enqueue(lib().moe_combine_backward, dev, stream, ctypes.byref(d), _ptr(out_grad), _ptr(y_rows), _ptr(pair_to_row),
-             _ptr(topk_w), _ptr(topk_w_grad), _ptr(y_rows_grad))
+    _enqueue(lib().moe_combine_backward, dev, stream, ctypes.byref(d), _want("out_grad", out_grad, dev, _BITS16, (T, H)),
+             _want_pair_rows("y_rows", y_rows, dev, P, H), _want("pair_to_row", pair_to_row, dev, _I32S),
+             _want("topk_w", topk_w, dev, _F32S, (T, k)), _want("topk_w_grad", topk_w_grad, dev, _F32S, (T, k)),
+             None if y_rows_grad is None else _want_pair_rows("y_rows_grad", y_rows_grad, dev, P, H))
 
 
 from .layer import (LayerBuffers, ResidentExperts, RouterGradBuffers, SharedBuffers, SharedExpert, StackLayer,  # noqa: E402

@@ -25,36 +25,6 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i, int type) {
 }  // namespace
 
 template <int BITS>
-__global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int n = (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
-    const int t0 = (int)blockIdx.y * kTok;
-    if (n >= a.w.N) return;
-    const int ngs = a.w.K / a.w.group_size;
-    float acc[kTok] = {};
-    for (int k = lane; k < a.w.K; k += kWave) {
-        const uint8_t* piece = a.w.q + ((size_t)(k >> 7) * a.w.N + n) * (16 * BITS);
-        const size_t gi = (size_t)n * ngs + k / a.w.group_size;
-        const float w = fmaf(code_at<BITS>(piece, k & 127), f16_bits_to_f32(a.w.scale[gi]), f16_bits_to_f32(a.w.bias[gi]));
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            const int t = min(t0 + i, a.T - 1);
-            acc[i] = fmaf(bf16_bits_to_f32(a.x[(size_t)t * a.ldx + k]), w, acc[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        float v = wave_sum_xor(acc[i], kWave);
-        const int t = t0 + i;
-        if (lane != 0 || t >= a.T) continue;
-        if (a.row_bias) v += a.row_bias[n];
-        if (a.residual) v += bf16_bits_to_f32(a.residual[(size_t)t * a.ldr + n]);
-        if (a.y_type == MOE_F32) static_cast<float*>(a.y)[(size_t)t * a.ldy + n] = v;
-        else static_cast<uint16_t*>(a.y)[(size_t)t * a.ldy + n] = (uint16_t)f32_to_bf16_bits(v);
-    }
-}
-
-template <int BITS>
 __global__ __launch_bounds__(128) void linear_grad_simple_kernel(LinearGradArgs a) {
     const int k = (int)blockIdx.x * 128 + (int)threadIdx.x, t0 = (int)blockIdx.y * kTok;
     const int ngs = a.w.K / a.w.group_size;
@@ -74,16 +44,11 @@ __global__ __launch_bounds__(128) void linear_grad_simple_kernel(LinearGradArgs 
 }
 
 size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad) {
-    (void)w; (void)T; (void)type; (void)grad;
-    return 0;
+    (void)type;
+    return grad ? 0 : linear_dec_workspace_bytes(w, T);
 }
 
-int launch_linear(const LinearArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.w.N + 3) / 4), (unsigned)((a.T + kTok - 1) / kTok));
-    if (a.w.bits == 4) hipLaunchKernelGGL(linear_simple_kernel<4>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(linear_simple_kernel<2>, grid, dim3(256), 0, s, a);
-    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-}
+int launch_linear(const LinearArgs& a, hipStream_t s) { return launch_linear_dec(a, s); }
 
 int launch_linear_grad(const LinearGradArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.w.K / 128), (unsigned)((a.T + kTok - 1) / kTok));

@@ -110,6 +110,14 @@ def test_linear_tall_and_wide(T):
     run_grad(Matrix(T + 3, 40, 16384, 2, 32), T, f32=True)
 
 
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 64), (4, 32), (2, 128), (2, 64), (2, 32)])
+def test_linear_every_share_of_k(bits, group):
+    """K from one group to more than one launch's registers hold, odd counts of groups among them."""
+    for NG in (1, 3, 8, 9, 13, 16, 17, 23, 32, 33, 41, 48, 49, 55, 64, 65, 79, 96, 131):
+        for T, N in ((1, 33), (16, 47)) if NG % 2 else ((19, 31), (5, 4099)):
+            run_linear(Matrix(NG + T, N, 128 * NG, bits, group), T, f32=NG % 3 == 0, row_bias=True, residual=True)
+
+
 @pytest.mark.parametrize("T", [1024, 1500])
 @pytest.mark.parametrize("f32", [False, True])
 def test_linear_prompt(T, f32):
