@@ -36,6 +36,10 @@ int launch_linear(const LinearArgs& a, hipStream_t s);
 // Few tokens (linear_dec.hip): any T, the matrix read once per 16 or 32 tokens.
 size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_dec(const LinearArgs& a, hipStream_t s);
+// Many tokens (linear_gemm.hip).
+size_t linear_gemm_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
+int launch_linear_gemm(const LinearArgs& a, hipStream_t s);
+int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s);
 int launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
 
 }  // namespace moe

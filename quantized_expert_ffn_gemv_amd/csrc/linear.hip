@@ -9,6 +9,8 @@ namespace moe {
 namespace {
 
 constexpr int kTok = 8;            // tokens per pass
+constexpr int kDecTokens = 128;
+constexpr int kGradDecTokens = 64;
 
 // Code k (0..127) of row n's piece of a 128-wide run.
 template <int BITS>
@@ -44,13 +46,16 @@ __global__ __launch_bounds__(128) void linear_grad_simple_kernel(LinearGradArgs 
 }
 
 size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad) {
-    (void)type;
+    if (T > (grad ? kGradDecTokens : kDecTokens)) return linear_gemm_workspace_bytes(w, T, type, grad);
     return grad ? 0 : linear_dec_workspace_bytes(w, T);
 }
 
-int launch_linear(const LinearArgs& a, hipStream_t s) { return launch_linear_dec(a, s); }
+int launch_linear(const LinearArgs& a, hipStream_t s) {
+    return a.T > kDecTokens ? launch_linear_gemm(a, s) : launch_linear_dec(a, s);
+}
 
 int launch_linear_grad(const LinearGradArgs& a, hipStream_t s) {
+    if (a.T > kGradDecTokens) return launch_linear_grad_gemm(a, s);
     const dim3 grid((unsigned)(a.w.K / 128), (unsigned)((a.T + kTok - 1) / kTok));
     if (a.w.bits == 4) hipLaunchKernelGGL(linear_grad_simple_kernel<4>, grid, dim3(128), 0, s, a);
     else hipLaunchKernelGGL(linear_grad_simple_kernel<2>, grid, dim3(128), 0, s, a);

@@ -6,8 +6,10 @@ bf16 result is 2^-8 of it.  A float32 sum of K products in any order is off by a
 most K U32 times the sum of the terms' absolute values; the code operands carry an
 offset of 16 code units (32 quarter units at 2 bits), which is subtracted again, so
 a term counts |x| (|s| (q + 16) + |b|) here.  Products of many tokens go through a
-half-precision copy of the weights (2^-11 of each), only where the result is bf16.
-The input gradient splits dy s into two bf16 parts (2^-16 of it left out).
+half-precision copy of the weights (2^-11 of each), only where the result is bf16,
+and the input gradient's through one of a float32 dy too (2^-11 of each; bf16
+values keep their bits).  The input gradient of few tokens splits dy s into two
+bf16 parts (2^-16 of it left out).
 """
 import numpy as np
 
@@ -69,7 +71,8 @@ def linear_bound(x, W, mag, y, f32, extra=0.0):
 def linear_grad_bound(dy, W, mag, dx):
     N = W.shape[0]
     ad = np.abs(dy).astype(np.float64)
-    bound = ((N + 16) * U32 + 2.0 ** -16) * (ad @ mag) + 2.0 ** -11 * (ad @ np.abs(W))
+    halves = 1 if np.array_equal(bf16_round(dy), dy) else 2
+    bound = ((N + 16) * U32 + 2.0 ** -16) * (ad @ mag) + halves * 2.0 ** -11 * (ad @ np.abs(W))
     return bound + HALF_BF16 * (np.abs(dx) + bound) + 1e-37
 
 
