@@ -2,8 +2,10 @@
 // as a dense half-precision GEMM on the matrix cores:
 //   forward    y[t][n]  = sum_k x[t][k]  w[n][k]
 //   gradient   dx[t][k] = sum_n dy[t][n] w[n][k]
-// Both operands are laid out once per call with the summed index contiguous:
-//   B  the weights as fp16, [n][k] forward and transposed [k][n] for the gradient,
+// Both operands are laid out once per call in blocks of 32 along the summed index,
+// [block][row][32], so that a stage of a tile is one contiguous run (rows a power
+// of two apart met in one L2 channel and made the product 1.3 to 1.9 times slower):
+//   B  the weights as fp16, rows n forward and, transposed, rows k for the gradient,
 //      each weight row n scaled by a power of two 2^en so that its largest possible
 //      |w| lies in [2^14, 2^15): no overflow, and 29 binades of full fp16 precision
 //      below a row's largest weight;
@@ -31,8 +33,9 @@ typedef float floatx16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kTop = 14;                               // scaled rows' largest exponent
 constexpr int kMid = 16;                               // en of weights below 1/4: dy takes 2^(kMid - en), near 1
-constexpr int kStep = 32;                              // summed elements per LDS stage
-constexpr int kStages = 4;
+constexpr int kStep = 32;                              // summed elements per block
+constexpr int kBlocks = 4;                             // rows are whole runs of this many blocks (zeros behind)
+constexpr int kPrepGroups = 8;                         // 128-runs of K a workgroup lays out
 constexpr size_t kChunkBytes = (size_t)128 << 20;      // laid-out weights per chunk
 
 __host__ __device__ inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
@@ -63,11 +66,15 @@ __device__ __forceinline__ float row_bound(const moe_qmatrix& w, size_t n, int f
     return top;
 }
 
-// Code k (0 .. 31 of a quarter of a 128-run) from the quarter's words.
+// Word wi (0 .. 15) of a row's piece of a 128-run: eight codes, k = 8 wi ..
 template <int BITS>
-__device__ __forceinline__ float quarter_code(const uint32_t (&c)[BITS], int k) {
-    constexpr int PER = 32 / BITS;
-    return (float)((c[k / PER] >> (BITS * (k % PER))) & ((1u << BITS) - 1));
+__device__ __forceinline__ uint32_t code_word(const uint8_t* piece, int wi) {
+    return BITS == 4 ? reinterpret_cast<const uint32_t*>(piece)[wi] : reinterpret_cast<const uint16_t*>(piece)[wi];
+}
+
+template <int BITS>
+__device__ __forceinline__ float word_code(uint32_t w, int j) {
+    return (float)((w >> (BITS * j)) & ((1u << BITS) - 1));
 }
 
 struct PrepArgs {
@@ -76,96 +83,169 @@ struct PrepArgs {
     int64_t lda;
     int a_type;
     int T, len, kd;           // rows; elements of a row; kd: len rounded up (zeros behind)
-    uint16_t* ah;             // fp16 [T][kd]
+    uint16_t* ah;             // fp16 [kd / 32][T][32]
     int32_t* et;              // [T]
     int32_t* en;              // [N]
-    uint16_t* wh;             // fp16: forward [planes][rows][K], gradient [columns][kd]
+    uint16_t* wh;             // fp16: forward [planes][K / 32][rows][32], gradient [kd / 32][columns][32]
     int c0, cn;               // this chunk's weight rows (forward) or 128-runs of K (gradient)
     int planes;
     int a_blocks;             // workgroups that lay out A (the first ones); 0 in later chunks
 };
 
-// One row of A by a workgroup of 256.
-__device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t, bool grad) {
+// Eight consecutive values of a row from element i (zeros at or past len), dy's
+// times 2^(kMid - en).  VEC: 16-byte loads (the row and i allow them).
+template <bool GRAD, bool VEC>
+__device__ __forceinline__ void a_values(const PrepArgs& p, int64_t row, int i, float (&v)[8]) {
+    if (p.a_type == MOE_F32) {
+        const float* src = static_cast<const float*>(p.a) + row + i;
+        if (VEC && i + 8 <= p.len) {
+            const float4 x = reinterpret_cast<const float4*>(src)[0], y = reinterpret_cast<const float4*>(src)[1];
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = i + j < p.len ? src[j] : 0.f;
+        }
+    } else {
+        const uint16_t* src = static_cast<const uint16_t*>(p.a) + row + i;
+        if (VEC && i + 8 <= p.len) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = i + j < p.len ? bf16_bits_to_f32(src[j]) : 0.f;
+        }
+    }
+    if constexpr (GRAD) {
+        int e[8];
+        if (i + 8 <= p.len) {                                      // (en and i are aligned)
+            const int4 x = reinterpret_cast<const int4*>(p.en + i)[0], y = reinterpret_cast<const int4*>(p.en + i)[1];
+            e[0] = x.x; e[1] = x.y; e[2] = x.z; e[3] = x.w; e[4] = y.x; e[5] = y.y; e[6] = y.z; e[7] = y.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = i + j < p.len ? p.en[i + j] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < p.len) v[j] = ldexpf(v[j], kMid - e[j]);
+    }
+}
+
+// One row of A by a workgroup of 256: its first 256 * 8 * KEEP values stay in
+// registers between the maximum and the rounding, the rest is read twice.
+template <bool GRAD, bool VEC>
+__device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
+    constexpr int KEEP = 4;
     __shared__ float tops[4];
     const int tid = threadIdx.x;
     const int64_t row = (int64_t)t * p.lda;
-    const uint16_t* ab = static_cast<const uint16_t*>(p.a) + row;
-    const float* af = static_cast<const float*>(p.a) + row;
-    auto value = [&](int i) {
-        const float v = p.a_type == MOE_F32 ? af[i] : bf16_bits_to_f32(ab[i]);
-        return grad ? ldexpf(v, kMid - p.en[i]) : v;
-    };
-    float top = 0.f;
+    float v[KEEP][8], top = 0.f;
     bool bad = false;
-    for (int i = tid; i < p.len; i += 256) {
-        const float v = value(i);
-        top = fmaxf(top, fabsf(v));
-        bad |= v != v;
+    auto look = [&](const float (&x)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            top = fmaxf(top, fabsf(x[j]));
+            bad |= x[j] != x[j];
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c) {
+        const int i = 8 * (tid + 256 * c);
+        if (i < p.kd) {
+            a_values<GRAD, VEC>(p, row, i, v[c]);
+            look(v[c]);
+        }
+    }
+    for (int i = 8 * (tid + 256 * KEEP); i < p.kd; i += 2048) {
+        float x[8];
+        a_values<GRAD, VEC>(p, row, i, x);
+        look(x);
     }
     top = row_max<kWave>(bad ? INFINITY : top);
     if ((tid & 63) == 0) tops[tid >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     const int e = scale_exponent(top);
-    if (tid == 0) p.et[t] = grad ? e + kMid : e;
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.ah + (size_t)t * p.kd);
-    for (int i = 2 * tid; i < p.kd; i += 512) {
-        const float v0 = i < p.len ? ldexpf(value(i), e) : 0.f, v1 = i + 1 < p.len ? ldexpf(value(i + 1), e) : 0.f;
-        out[i >> 1] = pack_half(v0, v1);
+    if (tid == 0) p.et[t] = GRAD ? e + kMid : e;
+    auto put = [&](const float (&x)[8], int i) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack_half(ldexpf(x[2 * j], e), ldexpf(x[2 * j + 1], e));
+        *reinterpret_cast<uint4*>(p.ah + ((size_t)(i / kStep) * p.T + t) * kStep + (i & (kStep - 1))) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+    };
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c) {
+        const int i = 8 * (tid + 256 * c);
+        if (i < p.kd) put(v[c], i);
     }
+    for (int i = 8 * (tid + 256 * KEEP); i < p.kd; i += 2048) {
+        float x[8];
+        a_values<GRAD, VEC>(p, row, i, x);
+        put(x, i);
+    }
+}
+
+// The rows of A or dy may be read 16 bytes at a time.
+__device__ __forceinline__ bool a_rows_aligned(const PrepArgs& p) {
+    return (reinterpret_cast<uintptr_t>(p.a) & 15) == 0 && p.lda % 8 == 0;
 }
 
 }  // namespace
 
-// Forward: workgroups [0, a_blocks) lay out rows of x, the others 16 weight rows each.
+// Forward: workgroups [0, a_blocks) lay out rows of x, the others 16 weight rows times
+// kPrepGroups 128-runs of K each.
 template <int BITS>
 __global__ __launch_bounds__(256) void linear_prep_kernel(PrepArgs p) {
     if ((int)blockIdx.x < p.a_blocks) {
-        prep_a_row(p, blockIdx.x, false);
+        prep_a_row<false, true>(p, blockIdx.x);
         return;
     }
     __shared__ int ens[16];
     const int tid = threadIdx.x;
-    const int r0 = ((int)blockIdx.x - p.a_blocks) * 16;            // within the chunk
-    const int ngs = p.w.K / p.w.group_size, gshift = __builtin_ctz(p.w.group_size), NG = p.w.K / 128;
+    const int NG = p.w.K / 128, parts = (NG + kPrepGroups - 1) / kPrepGroups;
+    const int blk = (int)blockIdx.x - p.a_blocks, part = blk % parts;
+    const int r0 = blk / parts * 16;                               // within the chunk
+    const int ngs = p.w.K / p.w.group_size, gshift = __builtin_ctz(p.w.group_size);
     {
         const int r = r0 + (tid >> 4);
         const float top = row_max<16>(r < p.cn ? row_bound<BITS>(p.w, (size_t)(p.c0 + r), tid & 15, 16) : 0.f);
         if ((tid & 15) == 0) {
             ens[tid >> 4] = scale_exponent(top);
-            if (r < p.cn) p.en[p.c0 + r] = ens[tid >> 4];
+            if (r < p.cn && part == 0) p.en[p.c0 + r] = ens[tid >> 4];
         }
     }
     __syncthreads();
-    const int rr = (tid >> 2) & 15, q = tid & 3, r = r0 + rr;      // 4 threads a row and group, 4 groups at once
+    // 16 threads a row and group, each one word of eight codes: four neighbours fill the 64
+    // bytes of a row in a block
+    const int rr = tid >> 4, wi = tid & 15, r = r0 + rr;
     if (r >= p.cn) return;
     const size_t n = (size_t)(p.c0 + r);
     const int e = ens[rr];
     const size_t plane = (size_t)p.cn * p.w.K;
-    for (int g = tid >> 6; g < NG; g += 4) {
-        uint32_t c[BITS];
-        const uint8_t* src = p.w.q + ((size_t)g * p.w.N + n) * (16 * BITS) + 4 * BITS * q;
-#pragma unroll
-        for (int i = 0; i < BITS; ++i) c[i] = reinterpret_cast<const uint32_t*>(src)[i];
-        const int k0 = 128 * g + 32 * q;                           // 32 consecutive k share a scale group
+    const uint8_t* src = p.w.q + n * (16 * BITS);
+    const size_t step = (size_t)p.w.N * (16 * BITS);
+#pragma unroll 4
+    for (int g = part * kPrepGroups; g < min(NG, (part + 1) * kPrepGroups); ++g) {
+        const uint32_t c = code_word<BITS>(src + g * step, wi);
+        const int k0 = 128 * g + 8 * wi;
         const size_t at = n * ngs + (k0 >> gshift);
         const float s = ldexpf(f16_bits_to_f32(p.w.scale[at]), e), b = ldexpf(f16_bits_to_f32(p.w.bias[at]), e);
-        uint16_t* dst = p.wh + (size_t)r * p.w.K + k0;
+        uint16_t* dst = p.wh + ((size_t)(k0 / kStep) * p.cn + r) * kStep + (k0 & (kStep - 1));
+        uint32_t o[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t o[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float w0 = fmaf(quarter_code<BITS>(c, 8 * i + 2 * j), s, b);
-                const float w1 = fmaf(quarter_code<BITS>(c, 8 * i + 2 * j + 1), s, b);
-                o[j] = pack_half(w0, w1);
-                const half2_t h = __builtin_bit_cast(half2_t, o[j]);
-                lo[j] = pack_half(w0 - (float)h[0], w1 - (float)h[1]);
-            }
-            reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[0], o[1], o[2], o[3]);
-            if (p.planes == 2) reinterpret_cast<uint4*>(dst + plane)[i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int j = 0; j < 4; ++j) {
+            const float w0 = fmaf(word_code<BITS>(c, 2 * j), s, b), w1 = fmaf(word_code<BITS>(c, 2 * j + 1), s, b);
+            o[j] = pack_half(w0, w1);
+            const half2_t h = __builtin_bit_cast(half2_t, o[j]);
+            lo[j] = pack_half(w0 - (float)h[0], w1 - (float)h[1]);
         }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (p.planes == 2) *reinterpret_cast<uint4*>(dst + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -178,50 +258,51 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(PrepArgs p) {
 }
 
 // Gradient: workgroups [0, a_blocks) lay out rows of dy, the others one 128-run of
-// K times 64 weight rows each, transposed through LDS.
+// K times 128 weight rows each.  A thread takes one word of eight rows: its 8 x 8
+// codes are eight 16-byte pieces of the transposed matrix, and four neighbours
+// (32 weight rows) fill the 64 bytes of a row in a block.
 template <int BITS>
 __global__ __launch_bounds__(256) void linear_grad_prep_kernel(PrepArgs p) {
     if ((int)blockIdx.x < p.a_blocks) {
-        prep_a_row(p, blockIdx.x, true);
+        if (a_rows_aligned(p)) prep_a_row<true, true>(p, blockIdx.x);
+        else prep_a_row<true, false>(p, blockIdx.x);
         return;
     }
-    constexpr int PITCH = 64 + 8;                                  // halves a k row in LDS
-    __shared__ __attribute__((aligned(16))) uint16_t tile[128 * PITCH];
     const int tid = threadIdx.x, blk = (int)blockIdx.x - p.a_blocks;
-    const int nblocks = (p.kd + 63) / 64;
-    const int gl = blk / nblocks, n0 = (blk % nblocks) * 64, g = p.c0 + gl;
+    const int nblocks = (p.kd + 127) / 128;
+    const int gl = blk / nblocks, g = p.c0 + gl;
+    const int n0 = (blk % nblocks) * 128 + 32 * (tid >> 6) + 8 * (tid & 3), wi = (tid >> 2) & 15;
+    if (n0 >= p.kd) return;
     const int ngs = p.w.K / p.w.group_size, gshift = __builtin_ctz(p.w.group_size);
-    {
-        const int rr = tid >> 2, q = tid & 3, n = n0 + rr;
-        const bool in = n < p.w.N;
-        const size_t nn = in ? n : 0;
-        uint32_t c[BITS];
-        const uint8_t* src = p.w.q + ((size_t)g * p.w.N + nn) * (16 * BITS) + 4 * BITS * q;
+    uint32_t c[8];
+    float s[8], b[8];
 #pragma unroll
-        for (int i = 0; i < BITS; ++i) c[i] = reinterpret_cast<const uint32_t*>(src)[i];
-        const int k0 = 128 * g + 32 * q;
-        const size_t at = nn * ngs + (k0 >> gshift);
-        const int e = p.en[nn];
-        const float s = in ? ldexpf(f16_bits_to_f32(p.w.scale[at]), e) : 0.f;
-        const float b = in ? ldexpf(f16_bits_to_f32(p.w.bias[at]), e) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            tile[(32 * q + i) * PITCH + rr] = (uint16_t)(pack_half(fmaf(quarter_code<BITS>(c, i), s, b), 0.f) & 0xFFFFu);
+    for (int i = 0; i < 8; ++i) {
+        const int n = min(n0 + i, p.w.N - 1);
+        c[i] = code_word<BITS>(p.w.q + ((size_t)g * p.w.N + n) * (16 * BITS), wi);
+        const size_t at = (size_t)n * ngs + ((128 * g + 8 * wi) >> gshift);
+        const int e = p.en[n];
+        const bool in = n0 + i < p.w.N;
+        s[i] = in ? ldexpf(f16_bits_to_f32(p.w.scale[at]), e) : 0.f;
+        b[i] = in ? ldexpf(f16_bits_to_f32(p.w.bias[at]), e) : 0.f;
     }
-    __syncthreads();
-    for (int o = tid; o < 128 * 8; o += 256) {                     // 16-byte pieces, 8 a k row
-        const int k = o >> 3, piece = o & 7;
-        if (n0 + 8 * piece < p.kd)
-            *reinterpret_cast<uint4*>(p.wh + ((size_t)gl * 128 + k) * p.kd + n0 + 8 * piece) =
-                *reinterpret_cast<const uint4*>(tile + k * PITCH + 8 * piece);
+    uint16_t* dst = p.wh + ((size_t)(n0 / kStep) * (128 * p.cn) + 128 * gl + 8 * wi) * kStep + (n0 & (kStep - 1));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = pack_half(fmaf(word_code<BITS>(c[2 * i], j), s[2 * i], b[2 * i]),
+                             fmaf(word_code<BITS>(c[2 * i + 1], j), s[2 * i + 1], b[2 * i + 1]));
+        *reinterpret_cast<uint4*>(dst + j * kStep) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
 namespace {
 
 struct GemmArgs {
-    const uint16_t* A;        // fp16 [M][kd]
-    const uint16_t* B;        // fp16 [planes][N][kd]
+    const uint16_t* A;        // fp16 [kd / 32][M][32]
+    const uint16_t* B;        // fp16 [planes][kd / 32][N][32]
     int M, N, kd, planes;
     const int32_t* et;        // [M]
     const int32_t* en;        // [N], or NULL (folded into A)
@@ -238,17 +319,17 @@ struct GemmArgs {
 // C = A B^T in tiles of 64 WM x 64 WN by four waves (2 x 2, each 32 WM x 32 WN on
 // v_mfma_f32_32x32x16_f16: A lane l holds row l % 32 and k = 8 (l / 32) + i, B the
 // same of a column; accumulator 4 j + i is row 8 j + 4 (l / 32) + i of column
-// l % 32).  Stages of 32 summed elements pass through a ring of four LDS slots,
-// three ahead, by direct-to-LDS loads waited for by count; one barrier a stage.
-// A row's 64 bytes of a stage are four 16-byte pieces, piece c of row r at place
+// l % 32).  Stages of KB blocks of 32 summed elements pass through a ring of STAGES
+// LDS slots by direct-to-LDS loads waited for by count; one barrier a stage.
+// A row's 64 bytes of a block are four 16-byte pieces, piece c of row r at place
 // c ^ ((r >> 2) & 3): 16 rows read at one piece hit all banks once.  Workgroups
 // on one XCD take neighbouring tiles (8 rows of tiles at a time), which share
 // their operands in its L2.
-template <int WM, int WN>
-__global__ __launch_bounds__(256) void linear_gemm_kernel(GemmArgs p) {
-    constexpr int BM = 64 * WM, BN = 64 * WN;
-    constexpr int SLOT = (BM + BN) * 2 * kStep;                    // bytes
-    constexpr int LOADS = SLOT / kDma / 4;                         // a wave's loads per stage
+template <int WM, int WN, int WR, int WC, int STAGES, int KB>
+__global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_gemm_kernel(GemmArgs p) {
+    constexpr int BM = 32 * WM * WR, BN = 32 * WN * WC, WAVES = WR * WC;
+    constexpr int BLOCK = (BM + BN) * 2 * kStep, SLOT = KB * BLOCK;   // bytes
+    constexpr int LOADS = BLOCK / kDma / WAVES;                         // a wave's loads per stage
     extern __shared__ __attribute__((aligned(16))) uint8_t slots[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN, tiles = tm * tn;
@@ -262,30 +343,33 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(GemmArgs p) {
     const int band = tile / (8 * tn), rows = min(8, tm - 8 * band), in = tile - band * 8 * tn;
     const int m0 = (8 * band + in % rows) * BM, n0 = (in / rows) * BN;
 
-    // this lane's part of the wave's loads: chunk i (1 KB, 16 rows of A's or B's tile)
+    // this wave's loads of a stage: LOADS chunks of 1 KB (16 rows) of A's rows, then B's
     uint32_t off[LOADS];
-    const uint8_t* base[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int row = 16 * (LOADS * wid + i) + (lane >> 2);      // of the slot: A's rows, then B's
-        const bool isA = 16 * (LOADS * wid + i) < BM;
-        const int r = isA ? min(m0 + row, p.M - 1) - m0 : min(n0 + row - BM, p.N - 1) - n0;
-        const int piece = (lane & 3) ^ ((row >> 2) & 3);
-        base[i] = reinterpret_cast<const uint8_t*>(isA ? p.A + (size_t)m0 * p.kd : p.B + (size_t)n0 * p.kd);
-        off[i] = (uint32_t)r * (uint32_t)(2 * p.kd) + 16u * piece;
+        const int chunk = LOADS * wid + i, row = 16 * chunk + (lane >> 2);
+        const int r = 16 * chunk < BM ? min(m0 + row, p.M - 1) - m0 : min(n0 + row - BM, p.N - 1) - n0;
+        off[i] = (uint32_t)r * (2 * kStep) + 16u * ((lane & 3) ^ ((row >> 2) & 3));
     }
-    const int steps1 = p.kd / kStep, steps = steps1 * p.planes;
-    const size_t plane = (size_t)p.N * p.kd * 2;
-    auto stage = [&](int s) {
-        const int sc = min(s, steps - 1);
-        const int pl = sc >= steps1 ? 1 : 0, ks = sc - pl * steps1;
-        uint8_t* slot = slots + (s & (kStages - 1)) * SLOT;
+    const int blocks1 = p.kd / kStep, blocks = blocks1 * p.planes, steps = blocks / KB;   // (kd: whole stages)
+    const size_t strideA = (size_t)p.M * (2 * kStep), strideB = (size_t)p.N * (2 * kStep);   // bytes from block to block
+    const uint8_t* firstA = reinterpret_cast<const uint8_t*>(p.A + (size_t)m0 * kStep);
+    const uint8_t* srcA = firstA;
+    const uint8_t* srcB = reinterpret_cast<const uint8_t*>(p.B + (size_t)n0 * kStep);
+    int staged = 0, slot_in = 0;                                             // blocks staged
+    auto stage = [&] {                                                       // (past the end: the last block again)
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const bool isA = 16 * (LOADS * wid + i) < BM;
-            const uint8_t* b = base[i] + (size_t)ks * (2 * kStep) + (isA ? 0 : pl * plane);
-            dma16_sv(b, off[i], slot + (LOADS * wid + i) * kDma);
+        for (int kb = 0; kb < KB; ++kb) {
+            uint8_t* slot = slots + slot_in * SLOT + kb * BLOCK + LOADS * wid * kDma;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) dma16_sv(16 * (LOADS * wid + i) < BM ? srcA : srcB, off[i], slot + i * kDma);
+            ++staged;
+            if (staged < blocks) {
+                srcA = staged == blocks1 ? firstA : srcA + strideA;
+                srcB += strideB;
+            }
         }
+        slot_in = slot_in + 1 < STAGES ? slot_in + 1 : 0;
     };
     floatx16_t acc[WM][WN];
 #pragma unroll
@@ -294,68 +378,144 @@ __global__ __launch_bounds__(256) void linear_gemm_kernel(GemmArgs p) {
         for (int j = 0; j < WN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-    for (int s = 0; s < kStages - 1; ++s) stage(s);
-
-    const int wm = wid >> 1, wn = wid & 1, m = lane & 31, h = lane >> 5;
+    const int wm = wid / WC, wn = wid % WC, m = lane & 31, h = lane >> 5;
     const int arow = 32 * WM * wm + m, brow = BM + 32 * WN * wn + m;
-    for (int s = 0; s < steps; ++s) {
-        wait_vmem<(kStages - 2) * LOADS>();                        // stage s has arrived
-        lds_barrier();                                             // for every wave; stage s - 1 is used up
-        stage(s + kStages - 1);
-        const uint8_t* slot = slots + (s & (kStages - 1)) * SLOT;
+    half8_t a[2][WM], b[2][WN];
+    auto read = [&](int half, int at) {                            // half a block of the stage in slot `at`
+        const uint8_t* slot = slots + at * SLOT + (half >> 1) * BLOCK;
+        const int kk = half & 1;
+        // rows r, r + 32, ... swap pieces alike: (r >> 2) & 3 is the same
+        const int place = 16 * ((2 * kk + h) ^ ((m >> 2) & 3));
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            half8_t a[WM], b[WN];
-            // rows r, r + 32, ... swap pieces alike: (r >> 2) & 3 is the same
-            const int place = 16 * ((2 * kk + h) ^ ((m >> 2) & 3));
+        for (int i = 0; i < WM; ++i) a[kk][i] = *reinterpret_cast<const half8_t*>(slot + (arow + 32 * i) * 64 + place);
 #pragma unroll
-            for (int i = 0; i < WM; ++i) a[i] = *reinterpret_cast<const half8_t*>(slot + (arow + 32 * i) * 64 + place);
-#pragma unroll
-            for (int j = 0; j < WN; ++j) b[j] = *reinterpret_cast<const half8_t*>(slot + (brow + 32 * j) * 64 + place);
-#pragma unroll
-            for (int i = 0; i < WM; ++i)
-#pragma unroll
-                for (int j = 0; j < WN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i], b[j], acc[i][j], 0, 0, 0);
-        }
-    }
-    wait_vmem<0>();                                                // loads past the last stage, before the LDS is given up
-#pragma unroll
-    for (int j = 0; j < WN; ++j) {
-        const int n = n0 + 32 * WN * wn + 32 * j + m;
-        if (n >= p.N) continue;
-        const int en = p.en ? p.en[n] : 0;
-        const float rb = p.row_bias ? p.row_bias[n] : 0.f;
+        for (int j = 0; j < WN; ++j) b[kk][j] = *reinterpret_cast<const half8_t*>(slot + (brow + 32 * j) * 64 + place);
+        asm volatile("" ::: "memory");                             // the reads stay here, ahead of the products
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](int kk) {
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int t = m0 + 32 * WM * wm + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3);
-                if (t >= p.M) continue;
-                float v = ldexpf(acc[i][j][e], -(p.et[t] + en)) + rb;
-                if (p.residual) v += bf16_bits_to_f32(p.residual[(size_t)t * p.ldr + n]);
-                if (p.y_type == MOE_F32) static_cast<float*>(p.y)[(size_t)t * p.ldy + n] = v;
-                else static_cast<uint16_t*>(p.y)[(size_t)t * p.ldy + n] = (uint16_t)(pack_bf16(v, 0.f) & 0xFFFFu);
+            for (int j = 0; j < WN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[kk][i], b[kk][j], acc[i][j], 0, 0, 0);
+    };
+    // One half of a stage is read from LDS while the other is multiplied: read together
+    // behind the barrier, the waves' reads (three quarters of a stage's time at LDS
+    // rate) left the matrix cores idle.
+    for (int s = 0; s < STAGES; ++s) stage();
+    wait_vmem<(STAGES - 1) * KB * LOADS>();
+    lds_barrier();
+    int at = 0;
+    read(0, 0);
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+        for (int half = 0; half + 1 < 2 * KB; ++half) {
+            read(half + 1, at);
+            multiply(half & 1);
+        }
+        wait_vmem<(STAGES - 2) * KB * LOADS>();                         // this wave's part of stage s + 1 has arrived
+        lds_barrier();                                             // every wave's; stage s is read
+        stage();                                                   // stage s + STAGES, into stage s's slot
+        at = at + 1 < STAGES ? at + 1 : 0;
+        read(0, at);                                               // (past the end: a stage never used)
+        multiply(1);
+    }
+    wait_vmem<0>();                                                // loads past the last stage, before their LDS is used again
+    lds_barrier();
+    // each wave turns its sums around in LDS, 32 rows at a time: rows of 32 WN results
+    constexpr int COLS = 32 * WN, PITCH = COLS + 4;
+    static_assert(WAVES * 32 * PITCH * 4 <= STAGES * SLOT, "the results fit the slots");
+    float* turn = reinterpret_cast<float*>(slots) + wid * 32 * PITCH;
+    const int c0 = n0 + COLS * wn;
+    int en[WN];
+#pragma unroll
+    for (int j = 0; j < WN; ++j) en[j] = p.en ? p.en[min(c0 + 32 * j + m, p.N - 1)] : 0;
+    const bool wide = p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0 &&
+                      (p.residual == nullptr || (p.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.residual) & 15) == 0));
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+        const int r0 = m0 + 32 * (WM * wm + i);
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 8 * e4 + 4 * h + e, et = p.et[min(r0 + r, p.M - 1)];
+#pragma unroll
+                for (int j = 0; j < WN; ++j) turn[r * PITCH + 32 * j + m] = ldexpf(acc[i][j][4 * e4 + e], -(et + en[j]));
             }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        constexpr int PER_ROW = COLS / 8;                          // lanes a row, eight results each
+#pragma unroll
+        for (int rr = 0; rr < 32; rr += 64 / PER_ROW) {
+            const int r = rr + lane / PER_ROW, cc = 8 * (lane % PER_ROW), t = r0 + r, n = c0 + cc;
+            if (t >= p.M || n >= p.N) continue;
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 8; x += 4) {
+                const floatx4_t f = *reinterpret_cast<const floatx4_t*>(turn + r * PITCH + cc + x);
+                v[x] = f[0]; v[x + 1] = f[1]; v[x + 2] = f[2]; v[x + 3] = f[3];
+            }
+            if (wide && n + 8 <= p.N) {
+                if (p.row_bias)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) v[x] += p.row_bias[n + x];
+                if (p.residual) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(p.residual + (size_t)t * p.ldr + n);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        v[2 * x] += __uint_as_float(w[x] << 16);
+                        v[2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
+                    }
+                }
+                if (p.y_type == MOE_F32) {
+                    float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + (size_t)t * p.ldy + n);
+                    y[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    y[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + n) =
+                        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                }
+            } else {
+                for (int x = 0; x < 8 && n + x < p.N; ++x) {
+                    float u = turn[r * PITCH + cc + x];
+                    if (p.row_bias) u += p.row_bias[n + x];
+                    if (p.residual) u += bf16_bits_to_f32(p.residual[(size_t)t * p.ldr + n + x]);
+                    if (p.y_type == MOE_F32) static_cast<float*>(p.y)[(size_t)t * p.ldy + n + x] = u;
+                    else static_cast<uint16_t*>(p.y)[(size_t)t * p.ldy + n + x] = (uint16_t)(pack_bf16(u, 0.f) & 0xFFFFu);
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     }
 }
 
 namespace {
 
-template <int WM, int WN>
+template <int WM, int WN, int WR, int WC, int STAGES, int KB>
 void gemm_go(const GemmArgs& p, hipStream_t s) {
-    const int tm = (p.M + 64 * WM - 1) / (64 * WM), tn = (p.N + 64 * WN - 1) / (64 * WN);
+    constexpr int BM = 32 * WM * WR, BN = 32 * WN * WC;
+    static_assert(kBlocks % KB == 0, "stages are whole");
+    const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
     const int blocks = ((tm * tn + 7) / 8) * 8;
-    const size_t lds = (size_t)kStages * (64 * WM + 64 * WN) * 2 * kStep;
-    hipLaunchKernelGGL((linear_gemm_kernel<WM, WN>), dim3((unsigned)blocks), dim3(256), lds, s, p);
+    const size_t lds = (size_t)STAGES * KB * (BM + BN) * 2 * kStep;
+    hipLaunchKernelGGL((linear_gemm_kernel<WM, WN, WR, WC, STAGES, KB>), dim3((unsigned)blocks), dim3(64 * WR * WC), lds,
+                       s, p);
 }
 
+// The largest tiles that give every CU one (4096 x 8192 x 2048: 256-wide 130 us,
+// 128-wide 145; 4096 x 2048 x 8192, 128 256-wide tiles: 207, 136; 1024 x 4096 x 4096:
+// 128-wide 45, 64-wide 55; 512 x 4096 x 4096, 128 128-wide tiles: 45, 29); 64-wide
+// tiles with one workgroup a CU take all its LDS (256 x 4096 x 4096: 20 us against 25
+// with two slots, 512: 37 against 29).
 void gemm(const GemmArgs& p, hipStream_t s) {
     const int cus = device_cus();
     auto tiles = [&](int b) { return (long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
-    if (tiles(256) >= cus) gemm_go<4, 4>(p, s);
-    else if (tiles(128) >= cus) gemm_go<2, 2>(p, s);
-    else gemm_go<1, 1>(p, s);
+    if (tiles(256) >= cus) gemm_go<4, 2, 2, 4, 2, 2>(p, s);
+    else if (tiles(128) >= cus) gemm_go<2, 2, 2, 2, 4, 1>(p, s);
+    else if (tiles(64) > cus) gemm_go<1, 1, 2, 2, 2, 4>(p, s);
+    else gemm_go<1, 1, 2, 2, 4, 4>(p, s);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -368,7 +528,7 @@ struct Plan {
 
 Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
     Plan p{};
-    p.kd = grad ? round_up(w.N, kStep) : w.K;
+    p.kd = grad ? round_up(w.N, kStep * kBlocks) : w.K;
     p.planes = !grad && type == MOE_F32 ? 2 : 1;
     p.total = grad ? w.K / 128 : w.N;
     const size_t unit = grad ? (size_t)256 * p.kd : (size_t)2 * p.kd * p.planes;       // bytes
@@ -403,7 +563,8 @@ int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
         p.c0 = c0;
         p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
         p.a_blocks = c0 == 0 ? a.T : 0;
-        const dim3 grid((unsigned)(p.a_blocks + (p.cn + 15) / 16));
+        const int parts = (a.w.K / 128 + kPrepGroups - 1) / kPrepGroups;
+        const dim3 grid((unsigned)(p.a_blocks + (p.cn + 15) / 16 * parts));
         if (a.w.bits == 4) hipLaunchKernelGGL(linear_prep_kernel<4>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(linear_prep_kernel<2>, grid, dim3(256), 0, s, p);
         GemmArgs g{};
@@ -435,7 +596,7 @@ int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
         p.c0 = c0;
         p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
         p.a_blocks = c0 == 0 ? a.T : 0;
-        const dim3 grid((unsigned)(p.a_blocks + p.cn * ((pl.kd + 63) / 64)));
+        const dim3 grid((unsigned)(p.a_blocks + p.cn * ((pl.kd + 127) / 128)));
         if (a.w.bits == 4) hipLaunchKernelGGL(linear_grad_prep_kernel<4>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(linear_grad_prep_kernel<2>, grid, dim3(256), 0, s, p);
         GemmArgs g{};

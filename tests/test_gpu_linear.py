@@ -118,6 +118,14 @@ def test_linear_every_share_of_k(bits, group):
             run_linear(Matrix(NG + T, N, 128 * NG, bits, group), T, f32=NG % 3 == 0, row_bias=True, residual=True)
 
 
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 64), (4, 32), (2, 128), (2, 64), (2, 32)])
+def test_linear_grad_every_share_of_rows(bits, group):
+    """Weight rows from one to many rounds of a workgroup, several workgroups a run, partial last units."""
+    for N, K, T in ((1, 128, 3), (31, 256, 17), (32, 128, 33), (33, 384, 1), (255, 128, 16), (256, 256, 20), (257, 128, 15),
+                    (513, 384, 49), (2000, 128, 4), (4100, 256, 31), (9001, 128, 64), (3000, 1024, 100), (700, 4096, 2)):
+        run_grad(Matrix(N + T, N, K, bits, group), T, f32=N % 2 == 0, pad=T % 4)
+
+
 @pytest.mark.parametrize("T", [1024, 1500])
 @pytest.mark.parametrize("f32", [False, True])
 def test_linear_prompt(T, f32):
