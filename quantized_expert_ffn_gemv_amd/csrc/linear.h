@@ -36,7 +36,7 @@ int launch_linear(const LinearArgs& a, hipStream_t s);
 // Few tokens (linear_dec.hip): any T, the matrix read once per 16 or 32 tokens.
 size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_dec(const LinearArgs& a, hipStream_t s);
-// Input gradient of few tokens (linear_grad_dec.hip): at most kLinearDecTokens.
+// Input gradient of few tokens (linear_grad_dec.hip).
 size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_grad_dec(const LinearGradArgs& a, hipStream_t s);
 // Many tokens (linear_gemm.hip).

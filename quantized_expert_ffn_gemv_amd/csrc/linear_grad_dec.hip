@@ -19,6 +19,8 @@
 // A workgroup owns one 128-run of K and a share of the weight rows, its waves 32
 // rows at a time in turn; their sums meet in LDS, those of several workgroups in
 // the workspace, where the last to arrive adds them in order.
+#include <type_traits>
+
 #include "launch_util.h"
 #include "linear.h"
 #include "mfma_ops.h"
@@ -31,30 +33,31 @@ namespace {
 constexpr int kGradWaves = 8;
 constexpr int kUnit = 32;                              // weight rows per wave and step
 constexpr int kRound = kGradWaves * kUnit;             // per workgroup
-constexpr int kCounterStride = 2;                      // ints
+constexpr int kTok = 16;                               // tokens per workgroup
+constexpr int kCounters = 256, kCounterStride = MOE_LINEAR_SYNC_INTS / kCounters;   // ints
 
 struct GradArgs {
     LinearGradArgs l;
     int splits, rows;        // workgroups that share a run's weight rows, rows each (a multiple of kRound)
-    float* part;             // [token block][run][split][16 NT][128]
+    float* part;             // [token block][run][split][16][128]
 };
 
-template <int BITS, int SPG, int NT, bool F32>
+template <int SPG, bool F32>
 struct GradFrag {
     uint32_t c[8];                                     // this lane's word of rows 8 h + i
-    uint32_t dy[NT][F32 ? 8 : 4];                      // token l % 16 of each tile, rows 8 h ..
+    uint32_t dy[F32 ? 8 : 4];                          // token l % 16, rows 8 h ..
     uint32_t sb[(SPG + 1) / 2];                        // scales (lanes 0-31) or biases (32-63) of row l % 32
 };
 
 }  // namespace
 
-template <int BITS, int SPG, int NT, bool F32>
+template <int BITS, int SPG, bool F32>
 __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradArgs ga) {
-    using Frag = GradFrag<BITS, SPG, NT, F32>;
-    constexpr int TOK = 16 * NT, SW = (SPG + 1) / 2;
+    using Frag = GradFrag<SPG, F32>;
+    constexpr int SW = (SPG + 1) / 2, STEP = 2 * 64 * kGradWaves;
     const LinearGradArgs& a = ga.l;
-    __shared__ __attribute__((aligned(16))) float sums[kGradWaves][16][128];
-    __shared__ float zs[kGradWaves][SPG][TOK];
+    __shared__ __attribute__((aligned(16))) float sums[kGradWaves][kTok][128];
+    __shared__ float zs[kGradWaves][SPG][kTok];
     __shared__ __attribute__((aligned(16))) float srow[kGradWaves][SPG][64];   // scales, biases of a unit's rows
     __shared__ int flag;
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -65,17 +68,24 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
     const int id = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
     if (((int)blockIdx.x >> 3) >= per || id >= all) return;
     const int split = id / runs, run = id % runs;
-    const int t0 = (int)blockIdx.y * TOK;
+    const int t0 = (int)blockIdx.y * kTok;
     const int first = split * ga.rows, last = min(first + ga.rows, N);
 
-    const uint8_t* codes = a.w.q + (size_t)run * N * (16 * BITS);
-    auto load = [&](Frag& f, int n0) {
+    const gbytes_t codes = uniform_gptr(a.w.q + (size_t)run * N * (16 * BITS));
+    const int64_t dyrow = (int64_t)min(t0 + c, a.T - 1) * a.lddy;
+    // Rows n0 .. n0 + 31; with TAIL some of them past N: their dy reads as 0 and they count
+    // nothing.  (dy rows have any alignment.)
+    auto load = [&](Frag& f, int n0, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint8_t* row = codes + (size_t)min(n0 + 8 * h + i, N - 1) * (16 * BITS);
-            f.c[i] = BITS == 4 ? reinterpret_cast<const uint32_t*>(row)[c] : reinterpret_cast<const uint16_t*>(row)[c];
+            const int n = TAIL ? min(n0 + 8 * h + i, N - 1) : n0 + 8 * h + i;
+            const uint32_t at = (uint32_t)n * (16 * BITS) + BITS * c;
+            f.c[i] = BITS == 4 ? *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(codes + at)
+                               : *reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(codes + at);
         }
-        const uint16_t* sb = (lane < 32 ? a.w.scale : a.w.bias) + (size_t)min(n0 + (lane & 31), N - 1) * ngs + run * SPG;
+        const int nr = TAIL ? min(n0 + (lane & 31), N - 1) : n0 + (lane & 31);
+        const uint16_t* sb = (lane < 32 ? a.w.scale : a.w.bias) + (size_t)nr * ngs + run * SPG;
         if constexpr (SPG == 1) {
             f.sb[0] = *sb;
         } else if constexpr (SPG == 2) {
@@ -85,42 +95,45 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
             f.sb[0] = v.x;
             f.sb[SW - 1] = v.y;
         }
-        // dy rows have any alignment; the last rows' unit stops at N
+        const int64_t at = dyrow + n0 + 8 * h;
+        if constexpr (!TAIL) {
+            if constexpr (F32) __builtin_memcpy(f.dy, static_cast<const float*>(a.dy) + at, 32);
+            else __builtin_memcpy(f.dy, static_cast<const uint16_t*>(a.dy) + at, 16);
+        } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int64_t at = (int64_t)min(t0 + 16 * t + c, a.T - 1) * a.lddy + n0 + 8 * h;
-            constexpr int W = F32 ? 8 : 4;
-            if (n0 + kUnit <= N) {
-                if constexpr (F32) __builtin_memcpy(f.dy[t], static_cast<const float*>(a.dy) + at, 32);
-                else __builtin_memcpy(f.dy[t], static_cast<const uint16_t*>(a.dy) + at, 16);
-            } else {
-                for (int i = 0; i < W; ++i) f.dy[t][i] = 0u;
+            for (int i = 0; i < (F32 ? 8 : 4); ++i) f.dy[i] = 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (n0 + 8 * h + i >= N) continue;
-                    if constexpr (F32) f.dy[t][i] = static_cast<const uint32_t*>(a.dy)[at + i];
-                    else f.dy[t][i >> 1] |= (uint32_t)static_cast<const uint16_t*>(a.dy)[at + i] << (16 * (i & 1));
-                }
+            for (int i = 0; i < 8; ++i) {
+                if (n0 + 8 * h + i >= N) continue;
+                if constexpr (F32) f.dy[i] = static_cast<const uint32_t*>(a.dy)[at + i];
+                else f.dy[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(a.dy)[at + i] << (16 * (i & 1));
             }
         }
     };
 
-    floatx4_t acc[SPG][NT][8];
-    float z[SPG][NT];
+    floatx4_t acc[SPG][8];
+    float z[SPG];
 #pragma unroll
-    for (int u = 0; u < SPG; ++u)
+    for (int u = 0; u < SPG; ++u) {
+        z[u] = 0.f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            z[u][t] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[u][t][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-        }
-    auto compute = [&](const Frag& f, int n0) {
-        // rows past N have dy = 0 and count nothing
+        for (int j = 0; j < 8; ++j) acc[u][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    auto compute = [&](const Frag& f) {
 #pragma unroll
         for (int u = 0; u < SPG; ++u) srow[wid][u][lane] = f16_bits_to_f32((f.sb[u >> 1] >> (16 * (u & 1))) & 0xFFFFu);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-        uint32_t hi[SPG][NT][4], lo[SPG][NT][4];
+        const uint32_t base = vreg_const(0x43004300u), mask = vreg_const(BITS == 4 ? 0x00780078u : 0x00300030u);
+        uint32_t B[8][4];
+#pragma unroll
+        for (int half = 0; half < (BITS == 4 ? 2 : 1); ++half)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t p = __builtin_amdgcn_perm(f.c[i + 4], f.c[i], half ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                for (int jj = 0; jj < (BITS == 4 ? 4 : 8); ++jj)
+                    B[4 * half + jj][i] = and_or(shift_to(p, BITS == 4 ? 4 * jj - 3 : 2 * jj - 4), mask, base);
+            }
 #pragma unroll
         for (int u = 0; u < SPG; ++u) {
             float s[8], be[8];
@@ -134,133 +147,135 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
                     be[i + e] = fmaf(-kOffset<BITS>, vs[e], vb[e]);
                 }
             }
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float d[8];
+            for (int i = 0; i < 4; ++i) {
+                float d[2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int x = 0; x < 2; ++x) {
+                    const int r = i + 4 * x;
                     float g;
-                    if constexpr (F32) g = __uint_as_float(f.dy[t][i]);
-                    else g = (i & 1) ? __uint_as_float(f.dy[t][i >> 1] & 0xFFFF0000u) : __uint_as_float(f.dy[t][i >> 1] << 16);
-                    d[i] = g * s[i];
-                    z[u][t] = fmaf(g, be[i], z[u][t]);
+                    if constexpr (F32) g = __uint_as_float(f.dy[r]);
+                    else g = (r & 1) ? __uint_as_float(f.dy[r >> 1] & 0xFFFF0000u) : __uint_as_float(f.dy[r >> 1] << 16);
+                    d[x] = g * s[r];
+                    z[u] = fmaf(g, be[r], z[u]);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    hi[u][t][i] = pack_bf16(d[i], d[i + 4]);
-                    lo[u][t][i] = pack_bf16(d[i] - __uint_as_float(hi[u][t][i] << 16),
-                                            d[i + 4] - __uint_as_float(hi[u][t][i] & 0xFFFF0000u));
-                }
+                hi[i] = pack_bf16(d[0], d[1]);
+                lo[i] = pack_bf16(d[0] - __uint_as_float(hi[i] << 16), d[1] - __uint_as_float(hi[i] & 0xFFFF0000u));
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[u][j] = mfma16(hi, B[j], acc[u][j]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[u][j] = mfma16(lo, B[j], acc[u][j]);
+            // one scale group's products after another: together their operands would not fit the registers
+            if (SPG > 1) __builtin_amdgcn_sched_barrier(0);
         }
-        const uint32_t base = vreg_const(0x43004300u), mask = vreg_const(BITS == 4 ? 0x00780078u : 0x00300030u);
-#pragma unroll
-        for (int half = 0; half < (BITS == 4 ? 2 : 1); ++half) {
-            uint32_t p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                p[i] = __builtin_amdgcn_perm(f.c[i + 4], f.c[i], half ? 0x07060302u : 0x05040100u);
-#pragma unroll
-            for (int jj = 0; jj < (BITS == 4 ? 4 : 8); ++jj) {
-                const int j = 4 * half + jj;
-                uint32_t B[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) B[i] = and_or(shift_to(p[i], BITS == 4 ? 4 * jj - 3 : 2 * jj - 4), mask, base);
-#pragma unroll
-                for (int u = 0; u < SPG; ++u)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        acc[u][t][j] = mfma16(hi[u][t], B, acc[u][t][j]);
-                        acc[u][t][j] = mfma16(lo[u][t], B, acc[u][t][j]);
-                    }
-            }
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     };
     {
+        // this wave's whole units: unit wid + 8 i of the share; the next one's loads are always
+        // made (the last again at the end), so that no branch waits for them
+        const int whole = (last - first) / kUnit, mine = whole > wid ? (whole - wid + kGradWaves - 1) / kGradWaves : 0;
+        const std::false_type full{};
         Frag f0, f1;
-        int n = first + kUnit * wid;
-        if (n < last) load(f0, n);
-        while (n < last) {
-            if (n + kRound < last) load(f1, n + kRound);
-            compute(f0, n);
-            n += kRound;
-            if (n >= last) break;
-            if (n + kRound < last) load(f0, n + kRound);
-            compute(f1, n);
-            n += kRound;
+        if (mine > 0) {
+            auto at = [&](int i) { return first + kUnit * (wid + kGradWaves * min(i, mine - 1)); };
+            load(f0, at(0), full);
+            for (int i = 0; i < mine; i += 2) {
+                load(f1, at(i + 1), full);
+                compute(f0);
+                if (i + 1 >= mine) break;
+                load(f0, at(i + 2), full);
+                compute(f1);
+            }
+        }
+        if (whole * kUnit < last - first && whole % kGradWaves == wid) {
+            load(f0, first + kUnit * whole, std::true_type{});
+            compute(f0);
         }
     }
     // second sums: over the quarters here, over the waves below
 #pragma unroll
-    for (int u = 0; u < SPG; ++u)
+    for (int u = 0; u < SPG; ++u) {
+        float v = z[u];
+        v += __shfl_xor(v, 16, kWave);
+        v += __shfl_xor(v, 32, kWave);
+        if (h == 0) zs[wid][u][c] = v;
+    }
+    const int end = min(kTok, a.T - t0) * 128;                     // results
+    float* part = ga.part + (((size_t)blockIdx.y * runs + run) * ga.splits + split) * (kTok * 128);
+    // this lane's columns 8 c .. 8 c + 7, of its own scale group
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float v = z[u][t];
-            v += __shfl_xor(v, 16, kWave);
-            v += __shfl_xor(v, 32, kWave);
-            if (h == 0) zs[wid][u][16 * t + c] = v;
+    for (int i = 0; i < 4; ++i) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = acc[0][j][i];
+#pragma unroll
+            for (int u = 1; u < SPG; ++u) v[j] = c / (16 / SPG) == u ? acc[u][j][i] : v[j];
         }
-    const int tokens = min(TOK, a.T - t0);
-    float* part = ga.part + (((size_t)blockIdx.y * runs + run) * ga.splits + split) * (TOK * 128);
+        floatx4_t* dst = reinterpret_cast<floatx4_t*>(&sums[wid][4 * h + i][8 * c]);
+        dst[0] = floatx4_t{v[0], v[1], v[2], v[3]};
+        dst[1] = floatx4_t{v[4], v[5], v[6], v[7]};
+    }
+    __syncthreads();
+    for (int o = 2 * tid; o < end; o += STEP) {
+        const int tt = o >> 7, k = o & 127;
+        float2v_t v = {0.f, 0.f};
+        float zz = 0.f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        if (t > 0) __syncthreads();
-        // this lane's columns 8 c .. 8 c + 7, of its own scale group
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = acc[0][t][j][i];
-#pragma unroll
-                for (int u = 1; u < SPG; ++u) v[j] = c / (16 / SPG) == u ? acc[u][t][j][i] : v[j];
-            }
-            floatx4_t* dst = reinterpret_cast<floatx4_t*>(&sums[wid][4 * h + i][8 * c]);
-            dst[0] = floatx4_t{v[0], v[1], v[2], v[3]};
-            dst[1] = floatx4_t{v[4], v[5], v[6], v[7]};
+        for (int w = 0; w < kGradWaves; ++w) {
+            v += *reinterpret_cast<const float2v_t*>(&sums[w][tt][k]);
+            zz += zs[w][k / (128 / SPG)][tt];
         }
-        __syncthreads();
-        for (int o = tid; o < min(16, tokens - 16 * t) * 128; o += 64 * kGradWaves) {
-            const int tt = o >> 7, k = o & 127;
-            float v = 0.f, zz = 0.f;
-#pragma unroll
-            for (int w = 0; w < kGradWaves; ++w) {
-                v += sums[w][tt][k];
-                zz += zs[w][k / (128 / SPG)][16 * t + tt];
-            }
-            v = fmaf(v, kInvLever<BITS>, zz);
-            if (ga.splits == 1)
-                a.dx[(size_t)(t0 + 16 * t + tt) * a.lddx + 128 * run + k] = (uint16_t)(pack_bf16(v, 0.f) & 0xFFFFu);
-            else
-                put_device(part + (16 * t + tt) * 128 + k, v);
-        }
+        v = v * kInvLever<BITS> + zz;
+        if (ga.splits == 1) *reinterpret_cast<uint32_t*>(a.dx + (size_t)(t0 + tt) * a.lddx + 128 * run + k) = pack_bf16(v[0], v[1]);
+        else put_device(reinterpret_cast<uint64_t*>(part + o), __builtin_bit_cast(uint64_t, v));
     }
     if (ga.splits == 1) return;
     if (!arrive_last(a.sync + kCounterStride * ((int)blockIdx.y * runs + run), ga.splits, &flag)) return;
-    const float* from = ga.part + ((size_t)blockIdx.y * runs + run) * ga.splits * (TOK * 128);
-    for (int o = tid; o < tokens * 128; o += 64 * kGradWaves) {
-        float v = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < ga.splits; ++s) v += get_device(from + (size_t)s * (TOK * 128) + o);
-        a.dx[(size_t)(t0 + (o >> 7)) * a.lddx + 128 * run + (o & 127)] = (uint16_t)(pack_bf16(v, 0.f) & 0xFFFFu);
+    // pairs of results, AT a thread side by side and several splits at once, so that the
+    // loads overlap (every one is made, past the tokens the last pair's again: none waits
+    // behind a branch)
+    const float* from = ga.part + ((size_t)blockIdx.y * runs + run) * ga.splits * (kTok * 128);
+    constexpr int AT = 2;
+    static_assert(AT * STEP == kTok * 128, "all of them at once");
+    float2v_t v[AT];
+#pragma unroll
+    for (int x = 0; x < AT; ++x) v[x] = float2v_t{0.f, 0.f};
+    auto add = [&](auto n) {
+#pragma unroll 4
+        for (int s = 0; s < ga.splits; ++s)
+#pragma unroll
+            for (int x = 0; x < decltype(n)::value; ++x) {
+                const int o = min(2 * tid + x * STEP, end - 2);
+                v[x] += __builtin_bit_cast(float2v_t, get_device(reinterpret_cast<const uint64_t*>(from + (size_t)s * (kTok * 128) + o)));
+            }
+    };
+    if (end <= STEP) add(std::integral_constant<int, 1>{});
+    else add(std::integral_constant<int, AT>{});
+#pragma unroll
+    for (int x = 0; x < AT; ++x) {
+        const int o = 2 * tid + x * STEP;
+        if (o < end)
+            *reinterpret_cast<uint32_t*>(a.dx + (size_t)(t0 + (o >> 7)) * a.lddx + 128 * run + (o & 127)) = pack_bf16(v[x][0], v[x][1]);
     }
 }
 
 namespace {
 
-// Token tiles per workgroup: two where the sums fit the registers.
-inline int grad_tiles(const moe_qmatrix& w, int T) { return T > 16 && w.group_size >= 64 ? 2 : 1; }
-
-// Splits of the weight rows: enough workgroups for two on every CU, whole rounds
-// of rows each, and partial sums of at most half the codes' bytes.
+// Splits of the weight rows, whole rounds of rows each: one workgroup a CU (4096 x
+// 4096, 1 token: 7.6 us; half as many 7.9, twice 9.2; 49999 x 4096, 8 tokens: 36, 58,
+// 39), rounded up where a CU holds two (SPG = 1), else down (3 x 96 workgroups took
+// a second turn: 21 us against 11); and partial sums, written and read, of at most
+// twice the codes' bytes.
 int grad_splits(const moe_qmatrix& w, int T) {
-    const int runs = w.K / 128, tok = 16 * grad_tiles(w, T), blocks = (T + tok - 1) / tok;
+    // (more than one split only where runs times token blocks are fewer than the counters)
+    const int runs = w.K / 128, blocks = (T + kTok - 1) / kTok, cus = device_cus() < kCounters ? device_cus() : kCounters;
     const int rounds = (w.N + kRound - 1) / kRound;
-    const int fill = (2 * device_cus() + runs * blocks - 1) / (runs * blocks);
-    const int bytes = w.N * 16 * w.bits / (2 * 512 * 2 * (T < tok ? T : tok));
+    const int fill = (cus + (w.group_size == 128 ? runs * blocks - 1 : 0)) / (runs * blocks);
+    const long bytes = (long)w.N * 16 * w.bits * 2 / (512 * 2 * (T < kTok ? T : kTok));
     int s = fill < rounds ? fill : rounds;
-    s = s < bytes ? s : bytes;
+    s = s < bytes ? s : (int)bytes;
     s = s < 1 ? 1 : s;
     const int per = (rounds + s - 1) / s;                      // rounds a split
     return (rounds + per - 1) / per;
@@ -269,33 +284,28 @@ int grad_splits(const moe_qmatrix& w, int T) {
 }  // namespace
 
 size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T) {
-    const int tok = 16 * grad_tiles(w, T), blocks = (T + tok - 1) / tok, s = grad_splits(w, T);
-    return s == 1 ? 0 : (size_t)blocks * (w.K / 128) * s * tok * 128 * sizeof(float);
+    const int s = grad_splits(w, T);
+    return s == 1 ? 0 : (size_t)((T + kTok - 1) / kTok) * (w.K / 128) * s * kTok * 128 * sizeof(float);
 }
 
 namespace {
 
-template <int BITS, int SPG, int NT>
+template <int BITS, int SPG>
 void grad_go(const GradArgs& g, hipStream_t s) {
     const int all = g.l.w.K / 128 * g.splits;
-    const dim3 grid((unsigned)((all + 7) / 8 * 8), (unsigned)((g.l.T + 16 * NT - 1) / (16 * NT)));
+    const dim3 grid((unsigned)((all + 7) / 8 * 8), (unsigned)((g.l.T + kTok - 1) / kTok));
     if (g.l.dy_type == MOE_F32)
-        hipLaunchKernelGGL((linear_grad_dec_kernel<BITS, SPG, NT, true>), grid, dim3(64 * kGradWaves), 0, s, g);
+        hipLaunchKernelGGL((linear_grad_dec_kernel<BITS, SPG, true>), grid, dim3(64 * kGradWaves), 0, s, g);
     else
-        hipLaunchKernelGGL((linear_grad_dec_kernel<BITS, SPG, NT, false>), grid, dim3(64 * kGradWaves), 0, s, g);
+        hipLaunchKernelGGL((linear_grad_dec_kernel<BITS, SPG, false>), grid, dim3(64 * kGradWaves), 0, s, g);
 }
 
 template <int BITS>
 void grad_groups(const GradArgs& g, hipStream_t s) {
     const int spg = 128 / g.l.w.group_size;
-    if (grad_tiles(g.l.w, g.l.T) == 2) {
-        if (spg == 1) grad_go<BITS, 1, 2>(g, s);
-        else grad_go<BITS, 2, 2>(g, s);
-    } else {
-        if (spg == 1) grad_go<BITS, 1, 1>(g, s);
-        else if (spg == 2) grad_go<BITS, 2, 1>(g, s);
-        else grad_go<BITS, 4, 1>(g, s);
-    }
+    if (spg == 1) grad_go<BITS, 1>(g, s);
+    else if (spg == 2) grad_go<BITS, 2>(g, s);
+    else grad_go<BITS, 4>(g, s);
 }
 
 }  // namespace
