@@ -15,7 +15,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBalThreads = 512;
 constexpr int kBalTree = 16;                              // workgroups joined by one ticket
 constexpr int kBalBlocks = kBalTree * kBalTree;           // at most this many workgroups
 constexpr int kBalSyncStride = 64;                        // counters 256 bytes apart
@@ -47,7 +47,10 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     }
 }
 
-// v (logits) -> p in place; returns whether the row has a logit, and lse.
+// v (logits) -> p in place; returns whether the row has a logit, and lse.  The
+// exponential is the hardware's of (L - m) log2 e: rounding the product leaves a
+// relative |L - m| 2^-24 in p, no more than rounding the logits themselves did,
+// and below 2^-126 of the row's largest p is 0.
 template <int LPT, int PER>
 __device__ __forceinline__ bool softmax_row(float (&v)[PER], float& lse) {
     float m = v[0];
@@ -63,7 +66,7 @@ __device__ __forceinline__ bool softmax_row(float (&v)[PER], float& lse) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        v[i] = expf(v[i] - base);
+        v[i] = __builtin_amdgcn_exp2f((v[i] - base) * 1.44269504f);
         s += v[i];
     }
     s = row_sum<LPT>(s);
@@ -82,49 +85,36 @@ struct BalanceArgs {
     float* prob_mean;
     int32_t* n_valid;
     float* losses;
-    float* part;              // [blocks + kBalTree][stride]: E sums of p, E counts, z, n
+    uint64_t* part;           // [blocks + kBalTree][E + 1]: (sum of p, picks) per expert, then (z, tokens)
     int32_t* sync;
-    int T, E, k, stride;
+    int T, E, k;
 };
 
-// Sum of partial rows [first, first + n) of `part` into the workgroup's LDS.
-__device__ __forceinline__ void join_parts(const BalanceArgs& a, int first, int n, float* sp, int* sc, float* sz, int* sn) {
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+__device__ __forceinline__ uint64_t pair_of(float x, int n) { return (uint64_t)__float_as_uint(x) | ((uint64_t)(uint32_t)n << 32); }
+
+// The sum of partial rows [first, first + n), n <= kBalTree, into the workgroup's
+// LDS, in index order.  Every row's load is made (past n the last again), so that
+// they overlap.
+__device__ __forceinline__ void join_parts(const BalanceArgs& a, int first, int n, float* sp, int* sc) {
+    for (int e = threadIdx.x; e <= a.E; e += kBalThreads) {
+        uint64_t v[kBalTree];
+#pragma unroll
+        for (int b = 0; b < kBalTree; ++b) v[b] = get_device(a.part + (size_t)(first + min(b, n - 1)) * (a.E + 1) + e);
         float p = 0.f;
         int c = 0;
-#pragma unroll 4
-        for (int b = 0; b < n; ++b) {
-            const float* row = a.part + (size_t)(first + b) * a.stride;
-            p += get_device(row + e);
-            c += get_device(reinterpret_cast<const int*>(row) + a.E + e);
+#pragma unroll
+        for (int b = 0; b < kBalTree; ++b) {
+            p += b < n ? __uint_as_float((uint32_t)v[b]) : 0.f;
+            c += b < n ? (int)(v[b] >> 32) : 0;
         }
         sp[e] = p;
         sc[e] = c;
     }
-    if (threadIdx.x == 0) {
-        float z = 0.f;
-        int cnt = 0;
-        for (int b = 0; b < n; ++b) {
-            const float* row = a.part + (size_t)(first + b) * a.stride + 2 * a.E;
-            z += get_device(row);
-            cnt += get_device(reinterpret_cast<const int*>(row) + 1);
-        }
-        *sz = z;
-        *sn = cnt;
-    }
     __syncthreads();
 }
 
-__device__ __forceinline__ void put_part(const BalanceArgs& a, int slot, const float* sp, const int* sc, float z, int n) {
-    float* row = a.part + (size_t)slot * a.stride;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        put_device(row + e, sp[e]);
-        put_device(reinterpret_cast<int*>(row) + a.E + e, sc[e]);
-    }
-    if (threadIdx.x == 0) {
-        put_device(row + 2 * a.E, z);
-        put_device(reinterpret_cast<int*>(row) + 2 * a.E + 1, n);
-    }
+__device__ __forceinline__ void put_part(const BalanceArgs& a, int slot, const float* sp, const int* sc) {
+    for (int e = threadIdx.x; e <= a.E; e += kBalThreads) put_device(a.part + (size_t)slot * (a.E + 1) + e, pair_of(sp[e], sc[e]));
 }
 
 }  // namespace
@@ -132,28 +122,37 @@ __device__ __forceinline__ void put_part(const BalanceArgs& a, int slot, const f
 // Sums of p, picks, lse^2 and tokens per workgroup, joined by a tree of arrival
 // tickets: the last of each 16 workgroups sums their 16 partial rows, the last
 // of those sums the groups' rows and writes the results, all in index order.
+// Eight waves a workgroup, one token per LPT lanes at a time with the next one's
+// logits in flight.
 template <int LPT, int PER, bool VEC>
-__global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
-    constexpr int TPW = kWave / LPT;                      // tokens per wave at once
-    __shared__ float sp[1024];
-    __shared__ int sc[1024];
-    __shared__ float wp[4][1024];
-    __shared__ float sz;
-    __shared__ int sn;
-    __shared__ float wz[4];
-    __shared__ int wn[4], flag;
+__global__ __launch_bounds__(kBalThreads) void balance_kernel(BalanceArgs a) {
+    constexpr int TPW = kWave / LPT, WAVES = kBalThreads / kWave;  // tokens per wave at once
+    constexpr int ROW = LPT * PER;                        // experts a row of LDS holds
+    __shared__ float sp[ROW + 1];                         // [E]: z, tokens
+    __shared__ int sc[ROW + 1];
+    __shared__ float wp[WAVES][ROW];
+    __shared__ float wz[WAVES];
+    __shared__ int wn[WAVES], flag;
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sub = lane % LPT;
-    for (int e = tid; e < a.E; e += kThreads) sc[e] = 0;
+    for (int e = tid; e <= a.E; e += kBalThreads) sc[e] = 0;
     __syncthreads();
-    float acc[PER], z = 0.f;
+    float acc[PER], z = 0.f, next[PER];
     int n = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    const int step = (int)gridDim.x * 4 * TPW;
-    for (int t = ((int)blockIdx.x * 4 + wid) * TPW + lane / LPT; t - lane / LPT < a.T; t += step) {
-        const bool live = t < a.T && (a.valid == nullptr || a.valid[t] != 0);
+    const int step = (int)gridDim.x * WAVES * TPW, first_t = ((int)blockIdx.x * WAVES + wid) * TPW + lane / LPT;
+    bool live = false;
+    auto load = [&](int t) {
+        live = t < a.T && (a.valid == nullptr || a.valid[t] != 0);
+        load_row<LPT, PER, VEC>(a.logits + (size_t)(t < a.T ? t : 0) * a.E, a.T > 0 ? a.E : 0, sub, -INFINITY, next);
+    };
+    if (first_t - lane / LPT < a.T) load(first_t);
+    for (int t = first_t; t - lane / LPT < a.T; t += step) {
         float v[PER], lse;
-        load_row<LPT, PER, VEC>(a.logits + (size_t)(live ? t : 0) * a.E, live ? a.E : 0, sub, -INFINITY, v);
+        const bool mine = live;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = mine ? next[i] : -INFINITY;
+        if (t - lane / LPT + step < a.T) load(t + step);
         const bool part = softmax_row<LPT, PER>(v, lse);
         if (part) {
 #pragma unroll
@@ -173,17 +172,22 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
     for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, kWave);
     if (lane < LPT) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = slot_expert<LPT, VEC>(sub, i);
-            if (e < a.E) wp[wid][e] = acc[i];
-        }
+        for (int i = 0; i < PER; ++i) wp[wid][slot_expert<LPT, VEC>(sub, i)] = acc[i];
     }
     if (lane == 0) { wz[wid] = z; wn[wid] = n; }
     __syncthreads();
-    for (int e = tid; e < a.E; e += kThreads) sp[e] = (wp[0][e] + wp[1][e]) + (wp[2][e] + wp[3][e]);
+    for (int e = tid; e < a.E; e += kBalThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) s += wp[w][e];
+        sp[e] = s;
+    }
     if (tid == 0) {
-        sz = (wz[0] + wz[1]) + (wz[2] + wz[3]);
-        sn = (wn[0] + wn[1]) + (wn[2] + wn[3]);
+        float s = 0.f;
+        int c = 0;
+        for (int w = 0; w < WAVES; ++w) { s += wz[w]; c += wn[w]; }
+        sp[a.E] = s;
+        sc[a.E] = c;
     }
     __syncthreads();
 
@@ -191,20 +195,20 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
     if (blocks > 1) {
         const int group = (int)blockIdx.x / kBalTree, first = group * kBalTree;
         const int members = min(kBalTree, blocks - first), groups = (blocks + kBalTree - 1) / kBalTree;
-        put_part(a, (int)blockIdx.x, sp, sc, sz, sn);
+        put_part(a, (int)blockIdx.x, sp, sc);
         if (!arrive_last(a.sync + kBalSyncStride * (1 + group), members, &flag)) return;
-        join_parts(a, first, members, sp, sc, &sz, &sn);
+        join_parts(a, first, members, sp, sc);
         if (groups > 1) {
-            put_part(a, blocks + group, sp, sc, sz, sn);
+            put_part(a, blocks + group, sp, sc);
             if (!arrive_last(a.sync, groups, &flag)) return;
-            join_parts(a, blocks, groups, sp, sc, &sz, &sn);
+            join_parts(a, blocks, groups, sp, sc);
         }
     }
     // results: |V| tokens take part
-    const float inv = sn > 0 ? 1.f / (float)sn : 0.f;
+    const int nv = sc[a.E];
     float bal = 0.f;
-    for (int e = tid; e < a.E; e += kThreads) {
-        const float P = sn > 0 ? sp[e] / (float)sn : 0.f;
+    for (int e = tid; e < a.E; e += kBalThreads) {
+        const float P = nv > 0 ? sp[e] / (float)nv : 0.f;
         a.counts[e] = sc[e];
         a.prob_mean[e] = P;
         bal = fmaf((float)sc[e], P, bal);
@@ -214,9 +218,11 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
     if (lane == 0) wz[wid] = bal;
     __syncthreads();
     if (tid == 0) {
-        *a.n_valid = sn;
-        a.losses[0] = ((wz[0] + wz[1]) + (wz[2] + wz[3])) * ((float)a.E / (float)a.k) * inv;
-        a.losses[1] = sn > 0 ? sz / (float)sn : 0.f;
+        float s = 0.f;
+        for (int w = 0; w < WAVES; ++w) s += wz[w];
+        *a.n_valid = nv;
+        a.losses[0] = nv > 0 ? s * ((float)a.E / (float)a.k) / (float)nv : 0.f;
+        a.losses[1] = nv > 0 ? sp[a.E] / (float)nv : 0.f;
     }
 }
 
@@ -233,66 +239,94 @@ struct RouteGradArgs {
     int T, E, k, renorm;
 };
 
-// One wave walks its tokens; the experts' f (from the counts) stay in registers.
+// A token per LPT lanes.  The experts' f (from the counts) stand in LDS; a token's
+// picks are read once, pick p by lane p % LPT, and handed round by lane reads.
 template <int LPT, int PER, bool VEC>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteGradArgs a) {
-    constexpr int TPW = kWave / LPT;
-    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sub = lane % LPT;
-    float f[PER], ca = 0.f, cz = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) f[i] = 0.f;
+    constexpr int TPW = kWave / LPT, KP = LPT >= 32 ? 1 : LPT == 16 ? 2 : 4;   // picks a lane (k <= min(E, 32))
+    __shared__ float fs[LPT * PER];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sub = lane % LPT, base = lane - sub;
+    float ca = 0.f, cz = 0.f;
     if (a.dlosses) {
         const int nv = *a.n_valid;
         const float V = (float)(nv > 1 ? nv : 1);
         ca = a.dlosses[0] * (float)a.E / V;
         cz = a.dlosses[1] * 2.f / V;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = slot_expert<LPT, VEC>(sub, i);
-            if (e < a.E) f[i] = (float)a.counts[e] / (V * (float)a.k);
-        }
+        for (int e = tid; e < LPT * PER; e += kThreads) fs[e] = e < a.E ? (float)a.counts[e] / (V * (float)a.k) : 0.f;
+        __syncthreads();
     }
     const bool soft = a.dlosses != nullptr || (a.dgates != nullptr && !a.renorm);
     const int step = (int)gridDim.x * 4 * TPW;
     for (int t = ((int)blockIdx.x * 4 + wid) * TPW + lane / LPT; t - lane / LPT < a.T; t += step) {
         const bool in = t < a.T;
         const size_t row = (size_t)(in ? t : 0);
-        float d[PER];
+        float v[PER], g[KP], dg[KP];
+        int id[KP];
+        if (soft) load_row<LPT, PER, VEC>(a.logits + row * a.E, a.E, sub, -INFINITY, v);
+        if (a.dgates) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) d[i] = 0.f;
-        const float* g = a.gates + row * a.k;
-        const float* dg = a.dgates + row * a.k;
+            for (int p = 0; p < KP; ++p) {
+                const int j = sub + p * LPT;
+                const size_t at = row * a.k + (j < a.k ? j : 0);
+                id[p] = a.ids[at];
+                g[p] = j < a.k ? a.gates[at] : 0.f;
+                dg[p] = j < a.k ? a.dgates[at] : 0.f;
+            }
+        }
+        const bool losses = a.dlosses && in && (a.valid == nullptr || a.valid[t] != 0);
         float inner = 0.f;
-        if (a.dgates && in)
-            for (int j = 0; j < a.k; ++j) inner = fmaf(g[j], dg[j], inner);
-        if (soft) {
-            float v[PER], lse;
-            load_row<LPT, PER, VEC>(a.logits + row * a.E, in ? a.E : 0, sub, -INFINITY, v);
-            const bool some = softmax_row<LPT, PER>(v, lse);
-            const bool part = some && a.dlosses && in && (a.valid == nullptr || a.valid[t] != 0);
-            float pf = 0.f;
+        if (a.dgates) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) pf = fmaf(v[i], f[i], pf);
+            for (int p = 0; p < KP; ++p) inner = fmaf(g[p], dg[p], inner);
+            inner = row_sum<LPT>(inner);
+        }
+        typedef float row_t __attribute__((ext_vector_type(PER)));
+        row_t d = 0.f;
+        if (soft) {
+            float lse;
+            const bool some = softmax_row<LPT, PER>(v, lse);
+            float f[PER], pf = 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                f[i] = a.dlosses ? fs[slot_expert<LPT, VEC>(sub, i)] : 0.f;
+                pf = fmaf(v[i], f[i], pf);
+            }
             pf = row_sum<LPT>(pf);
             const float zl = cz * lse, all = a.renorm ? 0.f : inner;
             if (some) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const float loss = part ? fmaf(ca, f[i] - pf, zl) : 0.f;
+                    const float loss = losses ? fmaf(ca, f[i] - pf, zl) : 0.f;
                     d[i] = v[i] * (loss - all);
                 }
             }
         }
-        if (!in) continue;
         if (a.dgates) {
-            const int32_t* id = a.ids + row * a.k;
-            for (int j = 0; j < a.k; ++j) {
-                const int e = id[j];
-                const float add = g[j] * (a.renorm ? dg[j] - inner : dg[j]);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) d[i] += slot_expert<LPT, VEC>(sub, i) == e ? add : 0.f;
+            for (int p = 0; p < KP; ++p) {
+                const float mine = g[p] * (a.renorm ? dg[p] - inner : dg[p]);
+                for (int j = 0; j < min(LPT, a.k - p * LPT); ++j) {
+                    int e;
+                    float add;
+                    if constexpr (LPT == kWave) {
+                        e = __builtin_amdgcn_readlane(id[p], j);
+                        add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));
+                    } else {
+                        e = __shfl(id[p], base + j, kWave);
+                        add = __shfl(mine, base + j, kWave);
+                    }
+                    if constexpr (LPT == kWave && PER > 4) {               // e is uniform: its slot by register index
+                        if (e < 0 || e >= a.E) continue;
+                        const int i = VEC ? 4 * (e / (4 * LPT)) + (e & 3) : e / LPT;
+                        d[i] += (VEC ? (e >> 2) % LPT : e % LPT) == sub ? add : 0.f;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) d[i] += slot_expert<LPT, VEC>(sub, i) == e ? add : 0.f;
+                    }
+                }
             }
         }
+        if (!in) continue;
         float* out = a.dlogits + row * a.E;
         if constexpr (VEC) {
 #pragma unroll
@@ -328,22 +362,22 @@ void by_experts(int E, GO go) {
 }  // namespace
 
 size_t balance_workspace_bytes(const moe_dims& d) {
-    return (size_t)(kBalBlocks + kBalTree) * (2 * (size_t)d.E + 2) * sizeof(float);
+    return (size_t)(kBalBlocks + kBalTree) * ((size_t)d.E + 1) * sizeof(uint64_t);
 }
 
 int launch_balance_loss(const moe_dims& d, const float* logits, const int32_t* ids, const uint8_t* valid,
                         int32_t* counts, float* prob_mean, int32_t* n_valid, float* losses, void* ws, int32_t* sync,
                         hipStream_t s) {
-    const BalanceArgs a{logits, ids, valid, counts, prob_mean, n_valid, losses, static_cast<float*>(ws), sync,
-                        d.T, d.E, d.k, 2 * d.E + 2};
+    const BalanceArgs a{logits, ids, valid, counts, prob_mean, n_valid, losses, static_cast<uint64_t*>(ws), sync,
+                        d.T, d.E, d.k};
     const bool vec = d.E % 4 == 0 && aligned16(logits);
     by_experts(d.E, [&](auto lpt, auto per) {
         constexpr int L = lpt.value, P = per.value;
-        const long tpb = 4 * (kWave / L);                 // tokens per workgroup and step
+        const long tpb = kBalThreads / L;                 // tokens per workgroup and step
         long blocks = ((long)d.T + tpb - 1) / tpb;
         blocks = blocks < 1 ? 1 : blocks > kBalBlocks ? kBalBlocks : blocks;
-        if (vec) hipLaunchKernelGGL((balance_kernel<L, P, true>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
-        else hipLaunchKernelGGL((balance_kernel<L, P, false>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+        if (vec) hipLaunchKernelGGL((balance_kernel<L, P, true>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a);
+        else hipLaunchKernelGGL((balance_kernel<L, P, false>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a);
     });
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
