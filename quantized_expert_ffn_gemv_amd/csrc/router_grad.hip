@@ -17,9 +17,9 @@ namespace {
 
 constexpr int kThreads = 256, kBalThreads = 512;
 constexpr int kBalTree = 16;                              // workgroups joined by one ticket
-constexpr int kBalBlocks = kBalTree * kBalTree;           // at most this many workgroups
+constexpr int kBalBlocks = 256;                           // at most this many workgroups
 constexpr int kBalSyncStride = 64;                        // counters 256 bytes apart
-static_assert(MOE_BALANCE_SYNC_INTS == kBalSyncStride * (1 + kBalTree), "sync buffer layout");
+static_assert(MOE_BALANCE_SYNC_INTS >= kBalSyncStride * (1 + kBalBlocks / kBalTree), "sync buffer layout");
 
 // Expert of slot i of lane `sub`: VEC rows are read 16 bytes a lane.
 template <int LPT, bool VEC>
@@ -85,25 +85,26 @@ struct BalanceArgs {
     float* prob_mean;
     int32_t* n_valid;
     float* losses;
-    uint64_t* part;           // [blocks + kBalTree][E + 1]: (sum of p, picks) per expert, then (z, tokens)
+    uint64_t* part;           // [blocks + groups of kBalTree][E + 1]: (sum of p, picks) per expert, then (z, tokens)
     int32_t* sync;
     int T, E, k;
 };
 
 __device__ __forceinline__ uint64_t pair_of(float x, int n) { return (uint64_t)__float_as_uint(x) | ((uint64_t)(uint32_t)n << 32); }
 
-// The sum of partial rows [first, first + n), n <= kBalTree, into the workgroup's
-// LDS, in index order.  Every row's load is made (past n the last again), so that
-// they overlap.
-__device__ __forceinline__ void join_parts(const BalanceArgs& a, int first, int n, float* sp, int* sc) {
+// The sum of partial rows [first, first + n), n <= N, into the workgroup's LDS, in
+// index order.  Every row's load is made (past n the last again), so that they
+// overlap; they pass the caches by and cost their number, hence the two sizes.
+template <int N>
+__device__ __forceinline__ void join_rows(const BalanceArgs& a, int first, int n, float* sp, int* sc) {
     for (int e = threadIdx.x; e <= a.E; e += kBalThreads) {
-        uint64_t v[kBalTree];
+        uint64_t v[N];
 #pragma unroll
-        for (int b = 0; b < kBalTree; ++b) v[b] = get_device(a.part + (size_t)(first + min(b, n - 1)) * (a.E + 1) + e);
+        for (int b = 0; b < N; ++b) v[b] = get_device(a.part + (size_t)(first + min(b, n - 1)) * (a.E + 1) + e);
         float p = 0.f;
         int c = 0;
 #pragma unroll
-        for (int b = 0; b < kBalTree; ++b) {
+        for (int b = 0; b < N; ++b) {
             p += b < n ? __uint_as_float((uint32_t)v[b]) : 0.f;
             c += b < n ? (int)(v[b] >> 32) : 0;
         }
@@ -111,6 +112,11 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int first, int 
         sc[e] = c;
     }
     __syncthreads();
+}
+
+__device__ __forceinline__ void join_parts(const BalanceArgs& a, int first, int n, float* sp, int* sc) {
+    if (n <= 4) join_rows<4>(a, first, n, sp, sc);
+    else join_rows<kBalTree>(a, first, n, sp, sc);
 }
 
 __device__ __forceinline__ void put_part(const BalanceArgs& a, int slot, const float* sp, const int* sc) {
@@ -362,7 +368,7 @@ void by_experts(int E, GO go) {
 }  // namespace
 
 size_t balance_workspace_bytes(const moe_dims& d) {
-    return (size_t)(kBalBlocks + kBalTree) * ((size_t)d.E + 1) * sizeof(uint64_t);
+    return (size_t)(kBalBlocks + kBalBlocks / kBalTree) * ((size_t)d.E + 1) * sizeof(uint64_t);
 }
 
 int launch_balance_loss(const moe_dims& d, const float* logits, const int32_t* ids, const uint8_t* valid,
@@ -375,7 +381,8 @@ int launch_balance_loss(const moe_dims& d, const float* logits, const int32_t* i
         constexpr int L = lpt.value, P = per.value;
         const long tpb = kBalThreads / L;                 // tokens per workgroup and step
         long blocks = ((long)d.T + tpb - 1) / tpb;
-        blocks = blocks < 1 ? 1 : blocks > kBalBlocks ? kBalBlocks : blocks;
+        // up to four tokens in a row a lane group rather than a second level of joins
+        blocks = blocks < 1 ? 1 : blocks > kBalBlocks ? kBalBlocks : blocks <= 4 * kBalTree ? (blocks < kBalTree ? blocks : kBalTree) : blocks;
         if (vec) hipLaunchKernelGGL((balance_kernel<L, P, true>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a);
         else hipLaunchKernelGGL((balance_kernel<L, P, false>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a);
     });
