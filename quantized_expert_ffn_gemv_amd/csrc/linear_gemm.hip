@@ -33,6 +33,7 @@ typedef float floatx16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kTop = 14;                               // scaled rows' largest exponent
 constexpr int kMid = 16;                               // en of weights below 1/4: dy takes 2^(kMid - en), near 1
+constexpr int kNone = 400;                             // exponent of zero rows: 2^-400 leaves no finite dy above 0
 constexpr int kStep = 32;                              // summed elements per block
 constexpr int kBlocks = 4;                             // rows are whole runs of this many blocks (zeros behind)
 constexpr int kPrepGroups = 8;                         // 128-runs of K a workgroup lays out
@@ -41,9 +42,10 @@ constexpr size_t kChunkBytes = (size_t)128 << 20;      // laid-out weights per c
 __host__ __device__ inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
 // Exponent that brings a row whose largest magnitude is `top` into [2^14, 2^15):
-// 0 for zero rows; infinities and NaNs count as the largest exponent.
+// kNone for zero rows (dy at such a weight row must not set the scale of its
+// token); infinities and NaNs count as the largest exponent.
 __device__ __forceinline__ int scale_exponent(float top) {
-    if (top == 0.f) return 0;
+    if (top == 0.f) return kNone;
     const uint32_t u = __float_as_uint(top) & 0x7FFFFFFFu;
     const int e = u >= 0x7F800000u ? 128 : __builtin_amdgcn_frexp_expf(top) - 1;
     return kTop - e;

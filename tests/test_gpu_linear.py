@@ -297,3 +297,67 @@ def test_bits_as_int16_are_the_same_call():
     y16 = torch.empty(5, m.N, dtype=torch.int16, device=DEV)
     moe.linear(q16, x.view(torch.int16), y16)
     assert torch.equal(y16, y.view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [5, 40, 400])
+@pytest.mark.parametrize("f32", [False, True])
+def test_zero_weight_rows_do_not_weigh(T, f32):
+    """Rows of zeros (the padding of a vocabulary) count nothing in dx, whatever their dy."""
+    q, s, b = ref.make_matrix(np.random.default_rng(6), 90, 256, 4, 128)
+    s[::2] = 0
+    b[::2] = 0
+    m = Matrix(2, 90, 256, 4, 128, parts=(q, s, b))
+    dy = m.rows(T, m.N)
+    dy[:, ::2] *= np.float32(2.0) ** 40
+    run_grad(m, T, f32=f32, dy=dy)
+    dy[::3, 1::2] = 0.0
+    dx = run_grad(m, T, f32=f32, dy=dy)
+    assert bool((dx[::3] == 0).all())
+
+
+@pytest.mark.parametrize("T,N,K,bits,group", [(2, 1048576, 128, 4, 128), (3, 40, 32768, 4, 32), (400, 24, 32768, 2, 128),
+                                              (65536, 24, 128, 2, 64), (1, 1, 32768, 4, 64)])
+def test_largest_sizes(T, N, K, bits, group):
+    m = Matrix(N + K, N, K, bits, group)
+    run_linear(m, T, f32=T % 2 == 0, row_bias=True)
+    run_grad(m, T, f32=T % 2 == 0)
+
+
+@pytest.mark.parametrize("T,step", [(3, (1 << 30) + 8), (400, (1 << 23) + 8)])
+def test_rows_far_apart(T, step):
+    """Row strides that carry offsets past 32 bits."""
+    m = Matrix(T, 70, 256)
+    far = torch.zeros((T - 1) * step + 256, dtype=torch.bfloat16, device=DEV)
+
+    def rows(C):
+        return far.as_strided((T, C), (step, 1))
+
+    x, dy = m.rows(T, m.K), m.rows(T, m.N)
+    y, dx = run_linear(m, T, x=x), run_grad(m, T, dy=dy)
+    fb, gb = (moe.LinearBuffers.allocate(m.q, T, torch.bfloat16, grad=g) for g in (False, True))
+    near = torch.empty_like(y)
+    rows(m.K).copy_(dev(x))
+    moe.linear(m.q, rows(m.K), near, fb)
+    assert torch.equal(near, y)
+    moe.linear(m.q, dev(x), rows(m.N), fb)
+    assert torch.equal(rows(m.N), y)
+    rows(m.N).copy_(dev(dy))
+    near = torch.empty_like(dx)
+    moe.linear_grad(m.q, rows(m.N), near, gb)
+    assert torch.equal(near, dx)
+    moe.linear_grad(m.q, dev(dy), rows(m.K), gb)
+    assert torch.equal(rows(m.K), dx)
+
+
+@pytest.mark.parametrize("bits,group,K", [(4, 128, 512), (2, 32, 16384)])
+def test_buffers_serve_fewer_tokens(bits, group, K):
+    m = Matrix(K, 600, K, bits, group)
+    most = 700
+    fb, gb = (moe.LinearBuffers.allocate(m.q, most, torch.bfloat16, grad=g) for g in (False, True))
+    for T in (most, 300, 129, 90, 17, 16, 3, 1):
+        x, dy = m.rows(T, m.K), m.rows(T, m.N)
+        y, dx = run_linear(m, T, x=x), run_grad(m, T, dy=dy)
+        y2, dx2 = torch.empty_like(y), torch.empty_like(dx)
+        moe.linear(m.q, dev(x), y2, fb)
+        moe.linear_grad(m.q, dev(dy), dx2, gb)
+        assert torch.equal(y, y2) and torch.equal(dx, dx2)
