@@ -525,10 +525,11 @@ typedef struct moe_qmatrix {
 #define MOE_BF16 0
 #define MOE_F32 1
 
-/* Device workspace of moe_linear (grad = 0) or moe_linear_grad (grad = 1) for T
- * tokens and this element type of y or dy (host-only; the matrix' pointers are
- * not used).  It is 0 for moe_linear's decode kernels.  A workspace serves calls
- * of one stream at a time; what it holds between calls is scratch. */
+/* Device workspace of moe_linear (grad = 0) or moe_linear_grad (grad = 1) for any
+ * call of up to T tokens with this element type of y or dy (host-only; the
+ * matrix' pointers are not used).  It is 0 for moe_linear of few tokens with K up
+ * to 8192.  A workspace serves calls of one stream at a time; what it holds
+ * between calls is scratch. */
 int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int grad, size_t* bytes);
 
 /* y[t][n] = sum_k x[t][k] w[n][k] (+ row_bias[n]) (+ residual[t][n]), sums in
@@ -541,6 +542,9 @@ int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int gr
  *   y          bf16 or float32 (y_type) [T] rows of N elements, ldy >= N apart
  *   workspace  moe_linear_workspace_bytes(w, T, y_type, 0), 256-byte aligned
  *              (NULL where that is 0)
+ * Many tokens: x and w enter the product as half-precision values scaled by a
+ * power of two per row, which carry 2^-11 of a w (2^-22 where y is float32) and
+ * values down to 2^-28 of their row's largest; few tokens: without rounding.
  * A row of x with an infinity or NaN gives a row of y of NaNs and infinities,
  * and changes no other row. */
 int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, const float* row_bias,
@@ -558,6 +562,8 @@ int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, 
  *   sync       int32 [MOE_LINEAR_SYNC_INTS] device memory, 256-byte aligned,
  *              holding zeros before the first call; each call leaves it zero.
  *              Calls that share a workspace or sync must be ordered (one stream).
+ * Few tokens: dy times the scales enters as two bf16 parts (2^-16); many: as
+ * moe_linear's operands (a float32 dy with 2^-11 too).
  * Rows of dy with infinities or NaNs as for moe_linear's x. */
 #define MOE_LINEAR_SYNC_INTS 4096
 int moe_linear_grad(const moe_qmatrix* w, int32_t T, const void* dy, int64_t lddy, int dy_type, uint16_t* dx,

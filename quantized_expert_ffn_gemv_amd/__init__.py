@@ -483,8 +483,8 @@ def linear_workspace_bytes(w: QMatrix, T: int, dtype, grad: bool = False) -> int
 
 @dataclass
 class LinearBuffers:
-    """What linear() or linear_grad() need beside their operands, for calls of up
-    to the sizes they were allocated for, one at a time on one stream."""
+    """What linear() or linear_grad() need beside their operands, for calls with
+    this matrix (or one of its sizes) of up to T tokens, one at a time on one stream."""
     workspace: torch.Tensor       # uint8
     sync: torch.Tensor            # int32 [LINEAR_SYNC_INTS], zeros (every call leaves them zero)
 

@@ -649,7 +649,7 @@ int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int gr
     if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
     const int st = check_qmatrix(fn, w, T, type, false);
     if (st) return st;
-    *bytes = T == 0 ? 0 : moe::linear_workspace_bytes(*w, T, type, grad != 0);
+    *bytes = T == 0 ? 0 : moe::linear_workspace_bytes_up_to(*w, T, type, grad != 0);
     return ok();
 }
 

@@ -31,8 +31,11 @@ struct LinearGradArgs {
     int32_t* sync;
 };
 
+// Workspace of a call of T tokens, and of all calls of 1 .. T tokens.
 size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
+size_t linear_workspace_bytes_up_to(const moe_qmatrix& w, int T, int type, bool grad);
 int launch_linear(const LinearArgs& a, hipStream_t s);
+int launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
 // Few tokens (linear_dec.hip): any T, the matrix read once per 16 or 32 tokens.
 size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_dec(const LinearArgs& a, hipStream_t s);
@@ -43,6 +46,5 @@ int launch_linear_grad_dec(const LinearGradArgs& a, hipStream_t s);
 size_t linear_gemm_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
 int launch_linear_gemm(const LinearArgs& a, hipStream_t s);
 int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s);
-int launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
 
 }  // namespace moe

@@ -30,6 +30,18 @@ size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad) 
     return grad ? linear_grad_dec_workspace_bytes(w, T) : linear_dec_workspace_bytes(w, T);
 }
 
+// The streaming kernels' needs do not grow with T alone: the splits of the summed
+// axis fall as tokens rise.  (The GEMM's do.)
+size_t linear_workspace_bytes_up_to(const moe_qmatrix& w, int T, int type, bool grad) {
+    const int streamed = most_streamed(w, type, grad);
+    size_t most = linear_workspace_bytes(w, T, type, grad);
+    for (int t = 1; t <= streamed && t < T; ++t) {
+        const size_t n = linear_workspace_bytes(w, t, type, grad);
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
 int launch_linear(const LinearArgs& a, hipStream_t s) {
     return a.T > most_streamed(a.w, a.y_type, false) ? launch_linear_gemm(a, s) : launch_linear_dec(a, s);
 }

@@ -51,6 +51,14 @@ def test_workspace_sizes():
     assert L.moe_linear_workspace_bytes(None, 1, 0, 0, ctypes.byref(ctypes.c_size_t(0))) == moe.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("grad", [0, 1])
+@pytest.mark.parametrize("kw", [dict(), dict(N=4099, K=16384), dict(N=20000, K=1024, group=32), dict(N=5000, K=8320, bits=2)])
+def test_workspace_serves_fewer_tokens(kw, grad):
+    for t in (moe.BF16, moe.F32):
+        sizes = [_ws(_w(**kw), T, t, grad)[1] for T in range(1, 800)] + [_ws(_w(**kw), T, t, grad)[1] for T in (4096, 65536)]
+        assert sizes == sorted(sizes)
+
+
 def _linear(w=None, T=4, x=FAKE, ldx=256, rb=None, res=None, ldr=64, y=FAKE, ldy=64, t=moe.BF16, ws=FAKE, n=1 << 40):
     return moe.lib().moe_linear(ctypes.byref(w or _w()), T, x, ldx, rb, res, ldr, y, ldy, t, ws, n, None)
 
