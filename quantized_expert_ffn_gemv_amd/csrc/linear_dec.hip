@@ -334,31 +334,50 @@ void stream_launch(const StreamArgs& sa, hipStream_t s) {
     const int blocks = (a.T + 16 * NT - 1) / (16 * NT);        // of tokens
     const int tiles = (a.w.N + 16 * RT - 1) / (16 * RT);
     const int all = device_cus() * (kStreamMaxWaves / waves), resident = all > blocks ? all / blocks : 1;
-    // one tile per workgroup: nothing to request ahead
+    // one tile per workgroup: nothing to request ahead (1 token, 2048 x 1024: 3.4 us against 3.9)
     if (RBU > 1 && tiles <= resident) stream_go<BITS, SPG, NT, RT, GPW, 1>(sa, waves, resident, blocks, s);
     else stream_go<BITS, SPG, NT, RT, GPW, RBU>(sa, waves, resident, blocks, s);
 }
 
-// Two token tiles where their operands fit the registers (K <= 4096), else one.
-template <int BITS, int SPG>
+// Two token tiles where their operands fit the registers (K <= 4096) and every CU has
+// more than two weight tiles to share its start among: 32 tokens, 4096 outputs, K =
+// 4096: 12.7 us against 10.2 with one, 8192: 16.5 and 14.5, 16384: 21.6 and 21.2,
+// 49999: 41 and 48; K = 2048: 8.2 and 7.4, 10.3 and 10.1, 14.1 and 15.4; 64 tokens,
+// 28672 outputs: 43 and 51.  A second ring entry per slot pays only where a slot is
+// one group (8 tokens, 49999 outputs, K = 1024: 16.6 us against 18.1; K = 2048: 21.3 and
+// 21.0; K = 4096: 30.0 and 29.2).
+template <int BITS, int SPG, int RT>
 void stream_groups(const StreamArgs& sa, hipStream_t s) {
-    constexpr int RT = BITS == 2 && SPG == 1 ? 2 : 1;          // units of 1 KB
     const int ng = sa.ng;
-    if (sa.l.T > 16 && ng <= 32) {
-        if (ng <= 8) stream_launch<BITS, SPG, 2, RT, 1, 4>(sa, s);
-        else if (ng <= 16) stream_launch<BITS, SPG, 2, RT, 2, 2>(sa, s);
+    const long work = (long)((sa.l.w.N + 16 * RT - 1) / (16 * RT)) * ((sa.l.T + 31) / 32);
+    if (sa.l.T > 16 && ng <= 32 && work > 2 * device_cus()) {
+        if (ng <= 8) stream_launch<BITS, SPG, 2, RT, 1, 2>(sa, s);
+        else if (ng <= 16) stream_launch<BITS, SPG, 2, RT, 2, 1>(sa, s);
         else stream_launch<BITS, SPG, 2, RT, 4, 1>(sa, s);
     } else if (ng <= 8) {
-        stream_launch<BITS, SPG, 1, RT, 1, 8>(sa, s);
+        stream_launch<BITS, SPG, 1, RT, 1, 2>(sa, s);
     } else if (ng <= 16) {
-        stream_launch<BITS, SPG, 1, RT, 2, 4>(sa, s);
+        stream_launch<BITS, SPG, 1, RT, 2, 1>(sa, s);
     } else if (ng <= 32) {
-        stream_launch<BITS, SPG, 1, RT, 4, 2>(sa, s);
+        stream_launch<BITS, SPG, 1, RT, 4, 1>(sa, s);
     } else if (ng <= 48) {
         stream_launch<BITS, SPG, 1, RT, 6, 1>(sa, s);
     } else {
         stream_launch<BITS, SPG, 1, RT, 8, 1>(sa, s);
     }
+}
+
+// Tiles of 32 weight rows (units of 1 KB) for 2-bit codes of groups of 128 where they
+// still give every CU one (8 tokens, K = 4096: 4096 outputs 7.7 us against 6.9 with 16
+// rows, 8192 8.2 and 8.6, 49999 24.8 and 27.1; K = 1024: 8192 outputs 4.5 and 5.4, 28672
+// 8.5 and 9.8); 4-bit codes gain nothing (49999 outputs: 30.0 and 29.4), nor do 2-bit
+// ones of finer groups (28672 outputs: 21.3 and 20.7).
+template <int BITS, int SPG>
+void stream_rows(const StreamArgs& sa, hipStream_t s) {
+    if constexpr (BITS == 2 && SPG == 1) {
+        if ((sa.l.w.N + 31) / 32 >= device_cus()) return stream_groups<BITS, SPG, 2>(sa, s);
+    }
+    stream_groups<BITS, SPG, 1>(sa, s);
 }
 
 }  // namespace
@@ -382,13 +401,13 @@ int launch_linear_dec(const LinearArgs& a, hipStream_t s) {
             sa.l.residual = nullptr;
         }
         if (a.w.bits == 4) {
-            if (spg == 1) stream_groups<4, 1>(sa, s);
-            else if (spg == 2) stream_groups<4, 2>(sa, s);
-            else stream_groups<4, 4>(sa, s);
+            if (spg == 1) stream_rows<4, 1>(sa, s);
+            else if (spg == 2) stream_rows<4, 2>(sa, s);
+            else stream_rows<4, 4>(sa, s);
         } else {
-            if (spg == 1) stream_groups<2, 1>(sa, s);
-            else if (spg == 2) stream_groups<2, 2>(sa, s);
-            else stream_groups<2, 4>(sa, s);
+            if (spg == 1) stream_rows<2, 1>(sa, s);
+            else if (spg == 2) stream_rows<2, 2>(sa, s);
+            else stream_rows<2, 4>(sa, s);
         }
     }
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;

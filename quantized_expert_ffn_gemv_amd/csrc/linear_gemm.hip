@@ -4,7 +4,8 @@
 //   gradient   dx[t][k] = sum_n dy[t][n] w[n][k]
 // Both operands are laid out once per call in blocks of 32 along the summed index,
 // [block][row][32], so that a stage of a tile is one contiguous run (rows a power
-// of two apart met in one L2 channel and made the product 1.3 to 1.9 times slower):
+// of two apart met in one L2 channel: 4096 x 8192 x 2048 took 1.08 times as long with
+// 256-wide tiles, 1.27 times with 128-wide ones):
 //   B  the weights as fp16, rows n forward and, transposed, rows k for the gradient,
 //      each weight row n scaled by a power of two 2^en so that its largest possible
 //      |w| lies in [2^14, 2^15): no overflow, and 29 binades of full fp16 precision
@@ -15,9 +16,9 @@
 // Powers of two leave the significands alone, so the roundings are fp16's of the
 // weights (2^-11 of each, an eighth of the bf16 result's own step; fp32 results
 // take the weights as two fp16 parts, 2^-22), float32's in the sums, and the
-// result's.  Laying the weights out costs one pass over the codes and 2 bytes a
-// weight; a matrix is taken in chunks of output columns that stay in the 256 MB
-// cache between the two kernels.
+// result's; a float32 dy takes fp16's too (2^-11).  Laying the weights out costs one
+// pass over the codes and 2 bytes a weight written and read; a matrix is taken in
+// chunks of output columns, which bound the workspace.
 #include "launch_util.h"
 #include "linear.h"
 #include "mfma_ops.h"
@@ -37,7 +38,10 @@ constexpr int kNone = 400;                             // exponent of zero rows:
 constexpr int kStep = 32;                              // summed elements per block
 constexpr int kBlocks = 4;                             // rows are whole runs of this many blocks (zeros behind)
 constexpr int kPrepGroups = 8;                         // 128-runs of K a workgroup lays out
-constexpr size_t kChunkBytes = (size_t)128 << 20;      // laid-out weights per chunk
+// Laid-out weights per chunk: past the 256 MB cache, for enough tiles in a chunk's GEMM
+// (1024 tokens, 28672 x 8192: 128 MB 680 us, 256 MB 626, 512 MB 601, 1 GB 610; gradient,
+// 49999 x 4096: 1257, 1299, 777, 782; 4096 tokens, 49999 x 4096 forward: 1847, 1872, 1875, 1874).
+constexpr size_t kChunkBytes = (size_t)512 << 20;
 
 __host__ __device__ inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
 

@@ -15,9 +15,12 @@ namespace moe {
 
 namespace {
 
+// Workgroups of the losses: 512 threads (1024: 16384 x 512 15.3 us against 16.8, but 32 x
+// 256 and 1024 x 128 slower), at most 256 (half as many: 16384 x 512 23.4 us against 16.9,
+// 8191 x 128 10.1 and 8.8), 16 joined by one ticket (32: slower at every size).
 constexpr int kThreads = 256, kBalThreads = 512;
-constexpr int kBalTree = 16;                              // workgroups joined by one ticket
-constexpr int kBalBlocks = 256;                           // at most this many workgroups
+constexpr int kBalTree = 16;
+constexpr int kBalBlocks = 256;
 constexpr int kBalSyncStride = 64;                        // counters 256 bytes apart
 static_assert(MOE_BALANCE_SYNC_INTS >= kBalSyncStride * (1 + kBalBlocks / kBalTree), "sync buffer layout");
 
@@ -381,8 +384,11 @@ int launch_balance_loss(const moe_dims& d, const float* logits, const int32_t* i
         constexpr int L = lpt.value, P = per.value;
         const long tpb = kBalThreads / L;                 // tokens per workgroup and step
         long blocks = ((long)d.T + tpb - 1) / tpb;
-        // up to four tokens in a row a lane group rather than a second level of joins
-        blocks = blocks < 1 ? 1 : blocks > kBalBlocks ? kBalBlocks : blocks <= 4 * kBalTree ? (blocks < kBalTree ? blocks : kBalTree) : blocks;
+        // up to two tokens in a row a lane group rather than a second level of joins (256 tokens
+        // x 1024: 9.4 us against 10.7, 512 x 128: 6.6 and 7.3; four in a row for 1024 x 128: 7.8 and 7.3)
+        blocks = blocks < 1 ? 1 : blocks;
+        if (blocks > kBalTree && blocks <= 2 * kBalTree) blocks = kBalTree;
+        if (blocks > kBalBlocks) blocks = kBalBlocks;
         if (vec) hipLaunchKernelGGL((balance_kernel<L, P, true>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a);
         else hipLaunchKernelGGL((balance_kernel<L, P, false>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a);
     });
@@ -400,7 +406,7 @@ int launch_route_backward(const moe_dims& d, const float* logits, const int32_t*
         constexpr int L = lpt.value, P = per.value;
         const long tpb = 4 * (kWave / L);
         long blocks = ((long)d.T + tpb - 1) / tpb;
-        blocks = blocks > 2048 ? 2048 : blocks;
+        blocks = blocks > 2048 ? 2048 : blocks;           // (16384 x 512: 16.8 us; 1024 18.3, 8192 18.6)
         if (vec) hipLaunchKernelGGL((route_backward_kernel<L, P, true>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
         else hipLaunchKernelGGL((route_backward_kernel<L, P, false>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
     });
