@@ -19,6 +19,8 @@
 // result's; a float32 dy takes fp16's too (2^-11).  Laying the weights out costs one
 // pass over the codes and 2 bytes a weight written and read; a matrix is taken in
 // chunks of output columns, which bound the workspace.
+#include <algorithm>
+
 #include "launch_util.h"
 #include "linear.h"
 #include "mfma_ops.h"
@@ -91,66 +93,52 @@ struct PrepArgs {
     int T, len, kd;           // rows; elements of a row; kd: len rounded up (zeros behind)
     uint16_t* ah;             // fp16 [kd / 32][T][32]
     int32_t* et;              // [T]
-    int32_t* en;              // [N]
+    int16_t* en;              // [N]
     uint16_t* wh;             // fp16: forward [planes][K / 32][rows][32], gradient [kd / 32][columns][32]
     int c0, cn;               // this chunk's weight rows (forward) or 128-runs of K (gradient)
     int planes;
     int a_blocks;             // workgroups that lay out A (the first ones); 0 in later chunks
 };
 
-// Eight consecutive values of a row from element i (zeros at or past len), dy's
-// times 2^(kMid - en).  VEC: 16-byte loads (the row and i allow them).
-template <bool GRAD, bool VEC>
-__device__ __forceinline__ void a_values(const PrepArgs& p, int64_t row, int i, float (&v)[8]) {
-    if (p.a_type == MOE_F32) {
-        const float* src = static_cast<const float*>(p.a) + row + i;
-        if (VEC && i + 8 <= p.len) {
-            const float4 x = reinterpret_cast<const float4*>(src)[0], y = reinterpret_cast<const float4*>(src)[1];
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = i + j < p.len ? src[j] : 0.f;
-        }
-    } else {
-        const uint16_t* src = static_cast<const uint16_t*>(p.a) + row + i;
-        if (VEC && i + 8 <= p.len) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(w[j] << 16);
-                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = i + j < p.len ? bf16_bits_to_f32(src[j]) : 0.f;
-        }
-    }
-    if constexpr (GRAD) {
-        int e[8];
-        if (i + 8 <= p.len) {                                      // (en and i are aligned)
-            const int4 x = reinterpret_cast<const int4*>(p.en + i)[0], y = reinterpret_cast<const int4*>(p.en + i)[1];
-            e[0] = x.x; e[1] = x.y; e[2] = x.z; e[3] = x.w; e[4] = y.x; e[5] = y.y; e[6] = y.z; e[7] = y.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = i + j < p.len ? p.en[i + j] : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (i + j < p.len) v[j] = ldexpf(v[j], kMid - e[j]);
-    }
-}
-
-// One row of A by a workgroup of 256: its first 256 * 8 * KEEP values stay in
-// registers between the maximum and the rounding, the rest is read twice.
-template <bool GRAD, bool VEC>
+// One row of A by a workgroup of 256, in pieces of eight values: the first 256 KEEP
+// pieces stay in registers between the maximum and the rounding, the rest is read
+// twice.  dy's values take 2^(kMid - en) of their weight row.  Every thread's KEEP
+// loads are made whatever the row's length (past its whole pieces the last one again):
+// behind a branch each waited for the one before (4096 x 8192 of dy with its weights: 54 us against 46).
+template <bool GRAD, bool F32>
 __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
-    constexpr int KEEP = 4;
+    constexpr int KEEP = 4, GROUP = 256 * KEEP, SIZE = F32 ? 4 : 2;
     __shared__ float tops[4];
     const int tid = threadIdx.x;
-    const int64_t row = (int64_t)t * p.lda;
-    float v[KEEP][8], top = 0.f;
+    const uint8_t* src = static_cast<const uint8_t*>(p.a) + (size_t)t * p.lda * SIZE;
+    const int whole = p.len / 8, rest = p.len % 8, pieces = p.kd / 8, groups = (pieces + GROUP - 1) / GROUP;
+    float v[KEEP][8], tail[8], top = 0.f;
     bool bad = false;
+    auto get = [&](int first) {                                    // pieces first + tid + 256 c (zeros past the whole ones)
+        uint32_t x[KEEP][F32 ? 8 : 4];
+        uint4 e[KEEP];
+        if (whole > 0) {
+#pragma unroll
+            for (int c = 0; c < KEEP; ++c) {
+                const int i = min(first + tid + 256 * c, whole - 1);
+                __builtin_memcpy(x[c], src + (size_t)i * (8 * SIZE), 8 * SIZE);   // (rows of dy have any alignment)
+                if constexpr (GRAD) e[c] = *reinterpret_cast<const uint4*>(p.en + 8 * i);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c) {
+            const bool in = first + tid + 256 * c < whole;
+            const uint32_t ew[4] = {e[c].x, e[c].y, e[c].z, e[c].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float f;
+                if constexpr (F32) f = __uint_as_float(x[c][j]);
+                else f = __uint_as_float((j & 1) ? x[c][j >> 1] & 0xFFFF0000u : x[c][j >> 1] << 16);
+                if constexpr (GRAD) f = ldexpf(f, kMid - (int)(int16_t)(ew[j >> 1] >> (16 * (j & 1))));
+                v[c][j] = in ? f : 0.f;
+            }
+        }
+    };
     auto look = [&](const float (&x)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -158,18 +146,23 @@ __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
             bad |= x[j] != x[j];
         }
     };
+    if (rest != 0 && tid == 0) {                                   // the piece that the row ends in
 #pragma unroll
-    for (int c = 0; c < KEEP; ++c) {
-        const int i = 8 * (tid + 256 * c);
-        if (i < p.kd) {
-            a_values<GRAD, VEC>(p, row, i, v[c]);
-            look(v[c]);
+        for (int j = 0; j < 8; ++j) {
+            const int i = 8 * whole + j;
+            tail[j] = 0.f;
+            if (j < rest) {
+                if constexpr (F32) tail[j] = reinterpret_cast<const float*>(src)[i];
+                else tail[j] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(src)[i]);
+                if constexpr (GRAD) tail[j] = ldexpf(tail[j], kMid - p.en[i]);
+            }
         }
+        look(tail);
     }
-    for (int i = 8 * (tid + 256 * KEEP); i < p.kd; i += 2048) {
-        float x[8];
-        a_values<GRAD, VEC>(p, row, i, x);
-        look(x);
+    for (int g = groups - 1; g >= 0; --g) {
+        get(g * GROUP);
+#pragma unroll
+        for (int c = 0; c < KEEP; ++c) look(v[c]);
     }
     top = row_max<kWave>(bad ? INFINITY : top);
     if ((tid & 63) == 0) tops[tid >> 6] = top;
@@ -181,24 +174,18 @@ __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = pack_half(ldexpf(x[2 * j], e), ldexpf(x[2 * j + 1], e));
-        *reinterpret_cast<uint4*>(p.ah + ((size_t)(i / kStep) * p.T + t) * kStep + (i & (kStep - 1))) =
+        *reinterpret_cast<uint4*>(p.ah + ((size_t)(8 * i / kStep) * p.T + t) * kStep + (8 * i & (kStep - 1))) =
             make_uint4(o[0], o[1], o[2], o[3]);
     };
+    if (rest != 0 && tid == 0) put(tail, whole);
+    for (int g = 0; g < groups; ++g) {
+        if (g > 0) get(g * GROUP);
 #pragma unroll
-    for (int c = 0; c < KEEP; ++c) {
-        const int i = 8 * (tid + 256 * c);
-        if (i < p.kd) put(v[c], i);
+        for (int c = 0; c < KEEP; ++c) {
+            const int i = g * GROUP + tid + 256 * c;
+            if (i < pieces && !(rest != 0 && i == whole)) put(v[c], i);
+        }
     }
-    for (int i = 8 * (tid + 256 * KEEP); i < p.kd; i += 2048) {
-        float x[8];
-        a_values<GRAD, VEC>(p, row, i, x);
-        put(x, i);
-    }
-}
-
-// The rows of A or dy may be read 16 bytes at a time.
-__device__ __forceinline__ bool a_rows_aligned(const PrepArgs& p) {
-    return (reinterpret_cast<uintptr_t>(p.a) & 15) == 0 && p.lda % 8 == 0;
 }
 
 }  // namespace
@@ -208,7 +195,7 @@ __device__ __forceinline__ bool a_rows_aligned(const PrepArgs& p) {
 template <int BITS>
 __global__ __launch_bounds__(256) void linear_prep_kernel(PrepArgs p) {
     if ((int)blockIdx.x < p.a_blocks) {
-        prep_a_row<false, true>(p, blockIdx.x);
+        prep_a_row<false, false>(p, blockIdx.x);
         return;
     }
     __shared__ int ens[16];
@@ -222,7 +209,7 @@ __global__ __launch_bounds__(256) void linear_prep_kernel(PrepArgs p) {
         const float top = row_max<16>(r < p.cn ? row_bound<BITS>(p.w, (size_t)(p.c0 + r), tid & 15, 16) : 0.f);
         if ((tid & 15) == 0) {
             ens[tid >> 4] = scale_exponent(top);
-            if (r < p.cn && part == 0) p.en[p.c0 + r] = ens[tid >> 4];
+            if (r < p.cn && part == 0) p.en[p.c0 + r] = (int16_t)ens[tid >> 4];
         }
     }
     __syncthreads();
@@ -260,7 +247,7 @@ template <int BITS>
 __global__ __launch_bounds__(256) void linear_rows_kernel(PrepArgs p) {
     const int n = (int)blockIdx.x * 16 + (int)(threadIdx.x >> 4);
     const float top = row_max<16>(n < p.w.N ? row_bound<BITS>(p.w, (size_t)n, threadIdx.x & 15, 16) : 0.f);
-    if (n < p.w.N && (threadIdx.x & 15) == 0) p.en[n] = scale_exponent(top);
+    if (n < p.w.N && (threadIdx.x & 15) == 0) p.en[n] = (int16_t)scale_exponent(top);
 }
 
 // Gradient: workgroups [0, a_blocks) lay out rows of dy, the others one 128-run of
@@ -270,7 +257,7 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(PrepArgs p) {
 template <int BITS>
 __global__ __launch_bounds__(256) void linear_grad_prep_kernel(PrepArgs p) {
     if ((int)blockIdx.x < p.a_blocks) {
-        if (a_rows_aligned(p)) prep_a_row<true, true>(p, blockIdx.x);
+        if (p.a_type == MOE_F32) prep_a_row<true, true>(p, blockIdx.x);
         else prep_a_row<true, false>(p, blockIdx.x);
         return;
     }
@@ -311,7 +298,7 @@ struct GemmArgs {
     const uint16_t* B;        // fp16 [planes][kd / 32][N][32]
     int M, N, kd, planes;
     const int32_t* et;        // [M]
-    const int32_t* en;        // [N], or NULL (folded into A)
+    const int16_t* en;        // [N], or NULL (folded into A)
     const float* row_bias;    // [N] or NULL
     const uint16_t* residual; // or NULL
     int64_t ldr;
@@ -322,7 +309,7 @@ struct GemmArgs {
 
 }  // namespace
 
-// C = A B^T in tiles of 64 WM x 64 WN by four waves (2 x 2, each 32 WM x 32 WN on
+// C = A B^T in tiles of 32 WM WR x 32 WN WC by WR x WC waves (each 32 WM x 32 WN on
 // v_mfma_f32_32x32x16_f16: A lane l holds row l % 32 and k = 8 (l / 32) + i, B the
 // same of a column; accumulator 4 j + i is row 8 j + 4 (l / 32) + i of column
 // l % 32).  Stages of KB blocks of 32 summed elements pass through a ring of STAGES
@@ -330,12 +317,15 @@ struct GemmArgs {
 // A row's 64 bytes of a block are four 16-byte pieces, piece c of row r at place
 // c ^ ((r >> 2) & 3): 16 rows read at one piece hit all banks once.  Workgroups
 // on one XCD take neighbouring tiles (8 rows of tiles at a time), which share
-// their operands in its L2.
+// their operands in its L2.  4096 x 8192 x 2048 takes 123 us (1.12 PF; a library half
+// product 105), of which a tile's first loads and its stores, with nothing to multiply,
+// are 8.5 us a round: tiles taken in turn by one workgroup, the loads running on into the
+// next, took 131.
 template <int WM, int WN, int WR, int WC, int STAGES, int KB>
 __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_gemm_kernel(GemmArgs p) {
     constexpr int BM = 32 * WM * WR, BN = 32 * WN * WC, WAVES = WR * WC;
     constexpr int BLOCK = (BM + BN) * 2 * kStep, SLOT = KB * BLOCK;   // bytes
-    constexpr int LOADS = BLOCK / kDma / WAVES;                         // a wave's loads per stage
+    constexpr int LOADS = BLOCK / kDma / WAVES;                         // a wave's loads per block
     extern __shared__ __attribute__((aligned(16))) uint8_t slots[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN, tiles = tm * tn;
@@ -349,7 +339,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const int band = tile / (8 * tn), rows = min(8, tm - 8 * band), in = tile - band * 8 * tn;
     const int m0 = (8 * band + in % rows) * BM, n0 = (in / rows) * BN;
 
-    // this wave's loads of a stage: LOADS chunks of 1 KB (16 rows) of A's rows, then B's
+    // this wave's loads of a block: LOADS chunks of 1 KB (16 rows) of A's rows, then B's
     uint32_t off[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -362,20 +352,25 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const uint8_t* firstA = reinterpret_cast<const uint8_t*>(p.A + (size_t)m0 * kStep);
     const uint8_t* srcA = firstA;
     const uint8_t* srcB = reinterpret_cast<const uint8_t*>(p.B + (size_t)n0 * kStep);
-    int staged = 0, slot_in = 0;                                             // blocks staged
-    auto stage = [&] {                                                       // (past the end: the last block again)
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            uint8_t* slot = slots + slot_in * SLOT + kb * BLOCK + LOADS * wid * kDma;
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) dma16_sv(16 * (LOADS * wid + i) < BM ? srcA : srcB, off[i], slot + i * kDma);
+    // The loads of a stage are made in its PARTS = 2 KB halves of a block, half of a block's
+    // LOADS each; the sources then move on to the next block (past the end: the last again).
+    constexpr int PARTS = 2 * KB, EACH = LOADS / 2;
+    static_assert(LOADS % 2 == 0, "halves");
+    int staged = 0, slot_in = 0;                                   // blocks staged, slot they go to
+    auto put = [&](int part, int i) {                              // load i of a half
+        uint8_t* slot = slots + slot_in * SLOT + (part >> 1) * BLOCK + LOADS * wid * kDma;
+        const int c = EACH * (part & 1) + i;
+        dma16_sv(16 * (LOADS * wid + c) < BM ? srcA : srcB, off[c], slot + c * kDma);
+    };
+    auto put_done = [&](int part) {
+        if (part & 1) {
             ++staged;
             if (staged < blocks) {
                 srcA = staged == blocks1 ? firstA : srcA + strideA;
                 srcB += strideB;
             }
         }
-        slot_in = slot_in + 1 < STAGES ? slot_in + 1 : 0;
+        if (part == PARTS - 1) slot_in = slot_in + 1 < STAGES ? slot_in + 1 : 0;
     };
     floatx16_t acc[WM][WN];
 #pragma unroll
@@ -399,33 +394,54 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
         asm volatile("" ::: "memory");                             // the reads stay here, ahead of the products
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto multiply = [&](int kk) {
+    // Half a block's products, a load of a later stage after every few of them: the loads issue
+    // while the matrix cores work (made together behind the barrier, they left them idle).
+    auto multiply = [&](int part) {
+        constexpr int N = WM * WN;
+        const int kk = part & 1;
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
-            for (int j = 0; j < WN; ++j)
+            for (int j = 0; j < WN; ++j) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[kk][i], b[kk][j], acc[i][j], 0, 0, 0);
+                const int n = i * WN + j;
+#pragma unroll
+                for (int c = 0; c < EACH; ++c)
+                    if (n == (N * c + N / 2) / EACH) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        put(part, c);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
+        put_done(part);
     };
-    // One half of a stage is read from LDS while the other is multiplied: read together
-    // behind the barrier, the waves' reads (three quarters of a stage's time at LDS
-    // rate) left the matrix cores idle.
-    for (int s = 0; s < STAGES; ++s) stage();
-    wait_vmem<(STAGES - 1) * KB * LOADS>();
+    // During stage s the loads of stage s + STAGES - 1 are made, into the slot that stage
+    // s - 1 left at the barrier; one half of a block is read from LDS while the other is
+    // multiplied: read together behind the barrier, the waves' reads left the matrix cores idle.
+    static_assert(STAGES >= 3, "a stage in flight behind the next one");
+    for (int s = 0; s + 1 < STAGES; ++s)
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+#pragma unroll
+            for (int c = 0; c < EACH; ++c) put(part, c);
+            put_done(part);
+        }
+    wait_vmem<(STAGES - 2) * PARTS * EACH>();
     lds_barrier();
     int at = 0;
     read(0, 0);
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
-        for (int half = 0; half + 1 < 2 * KB; ++half) {
-            read(half + 1, at);
-            multiply(half & 1);
+        for (int part = 0; part + 1 < PARTS; ++part) {
+            read(part + 1, at);
+            multiply(part);
         }
-        wait_vmem<(STAGES - 2) * KB * LOADS>();                         // this wave's part of stage s + 1 has arrived
-        lds_barrier();                                             // every wave's; stage s is read
-        stage();                                                   // stage s + STAGES, into stage s's slot
+        // this wave's part of stage s + 1 has arrived; then every wave's, and stage s is read
+        wait_vmem<((STAGES - 3) * PARTS + PARTS - 1) * EACH>();
+        lds_barrier();
         at = at + 1 < STAGES ? at + 1 : 0;
         read(0, at);                                               // (past the end: a stage never used)
-        multiply(1);
+        multiply(PARTS - 1);
     }
     wait_vmem<0>();                                                // loads past the last stage, before their LDS is used again
     lds_barrier();
@@ -434,38 +450,41 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     static_assert(WAVES * 32 * PITCH * 4 <= STAGES * SLOT, "the results fit the slots");
     float* turn = reinterpret_cast<float*>(slots) + wid * 32 * PITCH;
     const int c0 = n0 + COLS * wn;
-    int en[WN];
+    constexpr int PER_ROW = COLS / 8, PASS = 64 / PER_ROW;         // lanes a row, eight results each; rows at once
+    const int cc = 8 * (lane % PER_ROW), n = c0 + cc;
+    int en[8], et[WM][32 / PASS];
+    float rb[8];
 #pragma unroll
-    for (int j = 0; j < WN; ++j) en[j] = p.en ? p.en[min(c0 + 32 * j + m, p.N - 1)] : 0;
+    for (int x = 0; x < 8; ++x) {
+        en[x] = p.en ? p.en[min(n + x, p.N - 1)] : 0;
+        rb[x] = p.row_bias ? p.row_bias[min(n + x, p.N - 1)] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int rr = 0; rr < 32 / PASS; ++rr) et[i][rr] = p.et[min(m0 + 32 * (WM * wm + i) + PASS * rr + lane / PER_ROW, p.M - 1)];
     const bool wide = p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0 &&
                       (p.residual == nullptr || (p.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.residual) & 15) == 0));
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
         const int r0 = m0 + 32 * (WM * wm + i);
 #pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4)
+        for (int e = 0; e < 16; ++e)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 8 * e4 + 4 * h + e, et = p.et[min(r0 + r, p.M - 1)];
-#pragma unroll
-                for (int j = 0; j < WN; ++j) turn[r * PITCH + 32 * j + m] = ldexpf(acc[i][j][4 * e4 + e], -(et + en[j]));
-            }
+            for (int j = 0; j < WN; ++j) turn[(8 * (e >> 2) + 4 * h + (e & 3)) * PITCH + 32 * j + m] = acc[i][j][e];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-        constexpr int PER_ROW = COLS / 8;                          // lanes a row, eight results each
 #pragma unroll
-        for (int rr = 0; rr < 32; rr += 64 / PER_ROW) {
-            const int r = rr + lane / PER_ROW, cc = 8 * (lane % PER_ROW), t = r0 + r, n = c0 + cc;
+        for (int rr = 0; rr < 32 / PASS; ++rr) {
+            const int r = PASS * rr + lane / PER_ROW, t = r0 + r;
             if (t >= p.M || n >= p.N) continue;
             float v[8];
 #pragma unroll
             for (int x = 0; x < 8; x += 4) {
                 const floatx4_t f = *reinterpret_cast<const floatx4_t*>(turn + r * PITCH + cc + x);
-                v[x] = f[0]; v[x + 1] = f[1]; v[x + 2] = f[2]; v[x + 3] = f[3];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[x + u] = ldexpf(f[u], -(et[i][rr] + en[x + u])) + rb[x + u];
             }
             if (wide && n + 8 <= p.N) {
-                if (p.row_bias)
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) v[x] += p.row_bias[n + x];
                 if (p.residual) {
                     const uint4 q = *reinterpret_cast<const uint4*>(p.residual + (size_t)t * p.ldr + n);
                     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -484,9 +503,10 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
                         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
                 }
             } else {
-                for (int x = 0; x < 8 && n + x < p.N; ++x) {
-                    float u = turn[r * PITCH + cc + x];
-                    if (p.row_bias) u += p.row_bias[n + x];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    if (n + x >= p.N) continue;
+                    float u = v[x];
                     if (p.residual) u += bf16_bits_to_f32(p.residual[(size_t)t * p.ldr + n + x]);
                     if (p.y_type == MOE_F32) static_cast<float*>(p.y)[(size_t)t * p.ldy + n + x] = u;
                     else static_cast<uint16_t*>(p.y)[(size_t)t * p.ldy + n + x] = (uint16_t)(pack_bf16(u, 0.f) & 0xFFFFu);
@@ -510,17 +530,30 @@ void gemm_go(const GemmArgs& p, hipStream_t s) {
                        s, p);
 }
 
-// The largest tiles that give every CU one (4096 x 8192 x 2048: 256-wide 130 us,
-// 128-wide 145; 4096 x 2048 x 8192, 128 256-wide tiles: 207, 136; 1024 x 4096 x 4096:
-// 128-wide 45, 64-wide 55; 512 x 4096 x 4096, 128 128-wide tiles: 45, 29); 64-wide
-// tiles with one workgroup a CU take all its LDS (256 x 4096 x 4096: 20 us against 25
-// with two slots, 512: 37 against 29).
+// Tiles by the time their rounds over the CUs take, in hundredths of one round of 256 x
+// 256 tiles (K = 4096: about 115 us):
+//   256 x 256  100, one a CU;              256 x 128  56, one a CU;
+//   128 x 128  60, two a CU, 42 with one;  64 x 64  28, two a CU, 19 with one, whose ring
+//   takes all of the LDS (330 x 2048 x 4096: 28.0 us against 30.1 with half of it).
+// Whole calls with each of the four, us:
+//   4096 x 8192 x 2048  141 165 167 236    3000 x 4096 x 4096  121 134 124 178
+//   4096 x 5120 x 2048  121 116 106 154    4096 x 2048 x 8192  193 158 167 234
+//   1500 x 4096 x 4096  101  73  75  92     700 x 4096 x 4096   98  65  52  55
+//   1024 x 2048 x 2048   58  42  34  32     512 x 4096 x 4096    -   -  50  42
 void gemm(const GemmArgs& p, hipStream_t s) {
-    const int cus = device_cus();
-    auto tiles = [&](int b) { return (long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
-    if (tiles(256) >= cus) gemm_go<4, 2, 2, 4, 2, 2>(p, s);
-    else if (tiles(128) >= cus) gemm_go<2, 2, 2, 2, 4, 1>(p, s);
-    else if (tiles(64) > cus) gemm_go<1, 1, 2, 2, 2, 4>(p, s);
+    const long cus = device_cus();
+    auto tiles = [&](int rows, int cols) { return (long)((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols); };
+    auto two_a_cu = [&](long t, int one, int two) {
+        const long rest = t % (2 * cus);
+        return t / (2 * cus) * two + (rest == 0 ? 0 : rest <= cus ? one : two);
+    };
+    const long large = (tiles(256, 256) + cus - 1) / cus * 100, tall = (tiles(256, 128) + cus - 1) / cus * 56;
+    const long mid = two_a_cu(tiles(128, 128), 42, 60), small = two_a_cu(tiles(64, 64), 19, 28);
+    const long least = std::min(std::min(large, tall), std::min(mid, small));
+    if (large == least) gemm_go<4, 2, 2, 4, 3, 1>(p, s);
+    else if (tall == least) gemm_go<4, 2, 2, 2, 6, 1>(p, s);
+    else if (mid == least) gemm_go<2, 2, 2, 2, 4, 1>(p, s);
+    else if (tiles(64, 64) > cus) gemm_go<1, 1, 2, 2, 4, 2>(p, s);
     else gemm_go<1, 1, 2, 2, 4, 4>(p, s);
 }
 
@@ -544,7 +577,7 @@ Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
     p.chunk = (size_t)p.total < c ? p.total : (int)c;
     p.et = align256((size_t)T * p.kd * 2);
     p.en = p.et + align256((size_t)T * 4);
-    p.wh = p.en + align256((size_t)w.N * 4);
+    p.wh = p.en + align256((size_t)w.N * 2);
     p.bytes = p.wh + align256(unit * p.chunk);
     return p;
 }
@@ -562,7 +595,7 @@ int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
     p.w = a.w; p.a = a.x; p.lda = a.ldx; p.a_type = MOE_BF16; p.T = a.T; p.len = a.w.K; p.kd = pl.kd;
     p.ah = reinterpret_cast<uint16_t*>(ws);
     p.et = reinterpret_cast<int32_t*>(ws + pl.et);
-    p.en = reinterpret_cast<int32_t*>(ws + pl.en);
+    p.en = reinterpret_cast<int16_t*>(ws + pl.en);
     p.wh = reinterpret_cast<uint16_t*>(ws + pl.wh);
     p.planes = pl.planes;
     for (int c0 = 0; c0 < pl.total; c0 += pl.chunk) {
@@ -592,7 +625,7 @@ int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
     p.w = a.w; p.a = a.dy; p.lda = a.lddy; p.a_type = a.dy_type; p.T = a.T; p.len = a.w.N; p.kd = pl.kd;
     p.ah = reinterpret_cast<uint16_t*>(ws);
     p.et = reinterpret_cast<int32_t*>(ws + pl.et);
-    p.en = reinterpret_cast<int32_t*>(ws + pl.en);
+    p.en = reinterpret_cast<int16_t*>(ws + pl.en);
     p.wh = reinterpret_cast<uint16_t*>(ws + pl.wh);
     p.planes = 1;
     const dim3 rows((unsigned)((a.w.N + 15) / 16));
