@@ -463,8 +463,6 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     for (int i = 0; i < WM; ++i)
 #pragma unroll
         for (int rr = 0; rr < 32 / PASS; ++rr) et[i][rr] = p.et[min(m0 + 32 * (WM * wm + i) + PASS * rr + lane / PER_ROW, p.M - 1)];
-    const bool wide = p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0 &&
-                      (p.residual == nullptr || (p.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.residual) & 15) == 0));
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
         const int r0 = m0 + 32 * (WM * wm + i);
@@ -484,10 +482,10 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
                 for (int u = 0; u < 4; ++u) v[x + u] = ldexpf(f[u], -(et[i][rr] + en[x + u])) + rb[x + u];
             }
-            if (wide && n + 8 <= p.N) {
+            if (n + 8 <= p.N) {                                    // (16 bytes at any alignment)
                 if (p.residual) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(p.residual + (size_t)t * p.ldr + n);
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    uint32_t w[4];
+                    __builtin_memcpy(w, p.residual + (size_t)t * p.ldr + n, 16);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         v[2 * x] += __uint_as_float(w[x] << 16);
@@ -495,12 +493,10 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
                     }
                 }
                 if (p.y_type == MOE_F32) {
-                    float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + (size_t)t * p.ldy + n);
-                    y[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    y[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    __builtin_memcpy(static_cast<float*>(p.y) + (size_t)t * p.ldy + n, v, 32);
                 } else {
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + n) =
-                        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                    const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+                    __builtin_memcpy(static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + n, w, 16);
                 }
             } else {
 #pragma unroll

@@ -63,12 +63,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, h = lane >> 4, N = a.w.N;
     const int runs = a.w.K / 128, ngs = runs * SPG;
-    // workgroups on one XCD share weight rows (and the lines of their scales)
-    const int all = runs * ga.splits, per = (all + 7) / 8;
+    // workgroups on one XCD share weight rows: the token blocks of a run their codes, its
+    // runs the lines of their scales
+    const int blocks = (a.T + kTok - 1) / kTok, all = runs * ga.splits * blocks, per = (all + 7) / 8;
     const int id = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= per || id >= all) return;
-    const int split = id / runs, run = id % runs;
-    const int t0 = (int)blockIdx.y * kTok;
+    if (id >= all) return;
+    const int block = id % blocks, run = id / blocks % runs, split = id / blocks / runs;
+    const int t0 = block * kTok;
     const int first = split * ga.rows, last = min(first + ga.rows, N);
 
     const gbytes_t codes = uniform_gptr(a.w.q + (size_t)run * N * (16 * BITS));
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
         if (h == 0) zs[wid][u][c] = v;
     }
     const int end = min(kTok, a.T - t0) * 128;                     // results
-    float* part = ga.part + (((size_t)blockIdx.y * runs + run) * ga.splits + split) * (kTok * 128);
+    float* part = ga.part + (((size_t)block * runs + run) * ga.splits + split) * (kTok * 128);
     // this lane's columns 8 c .. 8 c + 7, of its own scale group
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -232,11 +233,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
         else put_device(reinterpret_cast<uint64_t*>(part + o), __builtin_bit_cast(uint64_t, v));
     }
     if (ga.splits == 1) return;
-    if (!arrive_last(a.sync + kCounterStride * ((int)blockIdx.y * runs + run), ga.splits, &flag)) return;
+    if (!arrive_last(a.sync + kCounterStride * (block * runs + run), ga.splits, &flag)) return;
     // pairs of results, AT a thread side by side and several splits at once, so that the
     // loads overlap (every one is made, past the tokens the last pair's again: none waits
     // behind a branch)
-    const float* from = ga.part + ((size_t)blockIdx.y * runs + run) * ga.splits * (kTok * 128);
+    const float* from = ga.part + ((size_t)block * runs + run) * ga.splits * (kTok * 128);
     constexpr int AT = 2;
     static_assert(AT * STEP == kTok * 128, "all of them at once");
     float2v_t v[AT];
@@ -292,8 +293,8 @@ namespace {
 
 template <int BITS, int SPG>
 void grad_go(const GradArgs& g, hipStream_t s) {
-    const int all = g.l.w.K / 128 * g.splits;
-    const dim3 grid((unsigned)((all + 7) / 8 * 8), (unsigned)((g.l.T + kTok - 1) / kTok));
+    const long all = (long)(g.l.w.K / 128) * g.splits * ((g.l.T + kTok - 1) / kTok);
+    const dim3 grid((unsigned)((all + 7) / 8 * 8));
     if (g.l.dy_type == MOE_F32)
         hipLaunchKernelGGL((linear_grad_dec_kernel<BITS, SPG, true>), grid, dim3(64 * kGradWaves), 0, s, g);
     else
