@@ -67,23 +67,24 @@ __device__ __forceinline__ float combine_grad_row(const uint16_t* dout, const ui
 
 }  // namespace
 
-// One wave per pair, the workgroup's four pairs consecutive.
-template <bool DY>
+// LP lanes per pair, a workgroup's 256 / LP pairs consecutive.
+template <bool DY, int LP>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradArgs a) {
     const int lane = threadIdx.x & 63;
-    const int p = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
-    if (p >= a.P) return;
-    const int t = p / a.k;
-    const int row = ld_scalar(a.p2r, (size_t)p);
-    const bool ok = row >= 0 && row < a.P;
+    const int wave = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
+    const int p = LP == kWave ? wave : wave * (kWave / LP) + lane / LP;
+    const bool in = p < a.P;
+    const size_t pc = in ? p : a.P - 1;
+    const int t = (int)pc / a.k;
+    const int row = LP == kWave ? ld_scalar(a.p2r, pc) : a.p2r[pc];
     float dot = 0.f;
-    if (ok) {
-        const float g = DY ? ld_scalar(a.gates, (size_t)p) : 0.f;
+    if (in && row >= 0 && row < a.P) {
+        const float g = !DY ? 0.f : LP == kWave ? ld_scalar(a.gates, pc) : a.gates[pc];
         dot = combine_grad_row<DY>(a.dout + (size_t)t * a.H, a.y + (size_t)row * a.H,
-                                   DY ? a.dy + (size_t)row * a.H : nullptr, g, a.H / 8, lane, kWave);
+                                   DY ? a.dy + (size_t)row * a.H : nullptr, g, a.H / 8, lane % LP, LP);
     }
-    dot = wave_sum_xor(dot, kWave);
-    if (lane == 0) a.dgates[p] = dot;
+    dot = row_sum<LP>(dot);
+    if (in && lane % LP == 0) a.dgates[p] = dot;
 }
 
 // One workgroup per pair: for calls with few pairs, whose time is one row's latency.
@@ -105,6 +106,17 @@ __global__ __launch_bounds__(256) void combine_backward_few_kernel(CombineGradAr
     if (threadIdx.x == 0) a.dgates[p] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
+namespace {
+
+template <int LP>
+void combine_go(const CombineGradArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.P + 256 / LP - 1) / (256 / LP)));
+    if (a.dy) hipLaunchKernelGGL((combine_backward_kernel<true, LP>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((combine_backward_kernel<false, LP>), grid, dim3(256), 0, s, a);
+}
+
+}  // namespace
+
 int launch_combine_backward(const moe_dims& d, const uint16_t* dout, const uint16_t* y, const int32_t* p2r,
                             const float* gates, float* dgates, uint16_t* dy, hipStream_t s) {
     const CombineGradArgs a{dout, y, p2r, gates, dgates, dy, d.T * d.k, d.H, d.k};
@@ -113,9 +125,12 @@ int launch_combine_backward(const moe_dims& d, const uint16_t* dout, const uint1
         if (dy) hipLaunchKernelGGL(combine_backward_few_kernel<true>, dim3((unsigned)a.P), dim3(256), 0, s, a);
         else hipLaunchKernelGGL(combine_backward_few_kernel<false>, dim3((unsigned)a.P), dim3(256), 0, s, a);
     } else {
-        const unsigned blocks = (unsigned)((a.P + 3) / 4);
-        if (dy) hipLaunchKernelGGL(combine_backward_kernel<true>, dim3(blocks), dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(combine_backward_kernel<false>, dim3(blocks), dim3(256), 0, s, a);
+        // a wave per pair, or half or a quarter of one where a row has no more 16-byte pieces (H =
+        // 128: 5652 tokens, 9 picks 8.4 us against 17.4 by waves; H = 256: 8000 tokens, 8
+        // picks 15.2 and 21.4)
+        if (a.H <= 128) combine_go<16>(a, s);
+        else if (a.H <= 256) combine_go<32>(a, s);
+        else combine_go<kWave>(a, s);
     }
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -7,6 +7,10 @@
 //
 // Activations are the A operand (rows = tokens) and codes the B operand (columns
 // = weight rows), so a lane's four sums share one weight row's scale.
+//
+// Bound by the weight stream: 8 tokens x 49999 x 4096 at 4 bits, float32 out, take 26 us
+// (4.2 TB/s of the bytes that have to move), 28672 x 8192 32 us (3.9 TB/s); 4096 x 4096,
+// one or two tiles a CU, 7.5 us, most of it launch, start and the last tile.
 #include "launch_util.h"
 #include "linear.h"
 #include "mfma_ops.h"
@@ -77,8 +81,8 @@ __device__ __forceinline__ uint4 load16_any(const uint16_t* p) {
 // soon as its codes are used, so the stream does not stop at tile borders.  A
 // tile's scales and biases are read by the workgroup's threads 16 bytes each and
 // passed on through LDS (read by each lane where it needs them they took eight
-// times the codes' cache cycles: 16 rows' cache lines for two bytes each).  The
-// waves' sums meet in LDS, one barrier a tile.
+// times the codes' cache cycles: 16 rows' cache lines for two bytes each; 49999 x
+// 4096 38 us against 28).  The waves' sums meet in LDS, one barrier a tile.
 template <int BITS, int SPG, int NT, int RT, int GPW, int RBU>
 __global__ __launch_bounds__(64 * kStreamMaxWaves) void linear_stream_kernel(StreamArgs sa) {
     const LinearArgs& a = sa.l;

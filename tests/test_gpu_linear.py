@@ -361,3 +361,81 @@ def test_buffers_serve_fewer_tokens(bits, group, K):
         moe.linear(m.q, dev(x), y2, fb)
         moe.linear_grad(m.q, dev(dy), dx2, gb)
         assert torch.equal(y, y2) and torch.equal(dx, dx2)
+
+
+class LargeMatrix:
+    """A matrix of weights drawn, and multiplied in 64 bits, on the GPU."""
+
+    def __init__(self, seed, N, K, bits, group):
+        gen = torch.Generator(DEV).manual_seed(seed)
+        q = torch.randint(0, 256, (K // 128, N, 16 * bits), dtype=torch.uint8, device=DEV, generator=gen)
+        s = (0.005 + 0.015 * torch.rand(N, K // group, device=DEV, generator=gen)).half()
+        b = (-torch.randint(0, 1 << bits, (N, K // group), device=DEV, generator=gen) * s.float()).half()
+        self.N, self.K, self.gen, self.q = N, K, gen, moe.QMatrix(bits, group, q, s, b)
+        c = torch.stack([(q >> (bits * i)) & ((1 << bits) - 1) for i in range(8 // bits)], -1)
+        c = c.permute(1, 0, 2, 3).reshape(N, K).double()
+        S, B = (a.double().repeat_interleave(group, 1) for a in (s, b))
+        self.W, self.mag = c * S + B, S.abs() * (c + 16) + B.abs()
+
+    def rows(self, T, C, size=1.0):
+        return (size * torch.randn(T, C, device=DEV, generator=self.gen)).bfloat16()
+
+    def linear(self, T, f32, row_bias, residual, pad):
+        """weights_ref.linear_bound, on the GPU"""
+        x = self.rows(T, self.K)
+        rb = torch.randn(self.N, device=DEV, generator=self.gen) if row_bias else None
+        res = self.rows(T, self.N) if residual else None
+        dt = torch.float32 if f32 else torch.bfloat16
+        y = torch.full((T, self.N + pad), 7.0, dtype=dt, device=DEV)
+        moe.linear(self.q, x, y[:, :self.N], moe.LinearBuffers.allocate(self.q, T, dt), row_bias=rb, residual=res)
+        assert bool((y[:, self.N:] == 7.0).all())
+        ax = x.double().abs()
+        want, bound = x.double() @ self.W.t(), (self.K + 16) * ref.U32 * (ax @ self.mag.t())
+        for a in (rb, res):
+            if a is not None:
+                want, bound = want + a.double(), bound + (self.K + 16) * ref.U32 * a.double().abs()
+        if not f32:
+            bound = bound + 2.0 ** -11 * (ax @ self.W.abs().t())
+            bound = bound + ref.HALF_BF16 * (want.abs() + bound)
+        worst = float(((y[:, :self.N].double() - want).abs() / (bound + 1e-37)).max())
+        assert worst <= 1.0, f"{worst:.3g} times the bound"
+
+    def grad(self, T, f32, pad):
+        """weights_ref.linear_grad_bound, on the GPU"""
+        dt = torch.float32 if f32 else torch.bfloat16
+        dy = self.rows(T, self.N + pad, 1e-3).to(dt)[:, :self.N]
+        if f32:
+            dy = dy * 1.001
+        dx = torch.full((T, self.K + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+        moe.linear_grad(self.q, dy, dx[:, :self.K], moe.LinearBuffers.allocate(self.q, T, dt, grad=True))
+        assert bool((dx[:, self.K:] == 7.0).all())
+        ad = dy.double().abs()
+        want = dy.double() @ self.W
+        bound = ((self.N + 16) * ref.U32 + 2.0 ** -16) * (ad @ self.mag) + (2 if f32 else 1) * 2.0 ** -11 * (ad @ self.W.abs())
+        bound = bound + ref.HALF_BF16 * (want.abs() + bound) + 1e-37
+        worst = float(((dx[:, :self.K].double() - want).abs() / bound).max())
+        assert worst <= 1.0, f"{worst:.3g} times the bound"
+
+
+@pytest.mark.parametrize("T,N,K,bits,group", [(4100, 4300, 128, 4, 128), (4000, 2100, 640, 4, 64), (1030, 4001, 384, 2, 32),
+                                              (2100, 9000, 256, 4, 128), (600, 1000, 4096, 4, 32), (3000, 4096, 1152, 2, 128)])
+def test_every_tile(T, N, K, bits, group):
+    m = LargeMatrix(T, N, K, bits, group)
+    m.linear(T, f32=False, row_bias=True, residual=True, pad=3)
+    m.linear(T, f32=True, row_bias=bits == 4, residual=False, pad=0)
+    m.grad(T, f32=bits == 4, pad=5)
+
+
+@pytest.mark.parametrize("T,N,K,bits,group", [(4000, 16, 512, 4, 128), (3001, 130, 8192, 4, 64), (2500, 40, 16384, 2, 32),
+                                              (4000, 417, 128, 4, 32), (1000, 30001, 256, 4, 128), (5000, 1, 256, 2, 128)])
+def test_many_tokens_and_a_narrow_matrix(T, N, K, bits, group):
+    m = LargeMatrix(T + N, N, K, bits, group)
+    m.linear(T, f32=False, row_bias=False, residual=True, pad=1)
+    m.grad(T, f32=False, pad=N % 2)
+
+
+def test_a_matrix_in_chunks():
+    """Laid-out weights past one chunk's bytes, forward and gradient."""
+    LargeMatrix(1, 5000, 32768, 4, 128).linear(1500, f32=True, row_bias=True, residual=True, pad=0)
+    LargeMatrix(2, 40000, 8192, 2, 64).linear(600, f32=False, row_bias=True, residual=False, pad=1)
+    LargeMatrix(3, 300001, 1024, 4, 128).grad(1000, f32=False, pad=1)

@@ -296,3 +296,12 @@ def test_graph_replay_and_streams():
         step(s)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), f"stream {i}"
+
+
+@pytest.mark.parametrize("T,H,k", [(171, 128, 3), (700, 256, 3), (5001, 128, 5), (65536, 128, 1), (900, 384, 1)])
+def test_combine_backward_short_rows(T, H, k):
+    """Several pairs a wave, a partial last wave, and rows out of range among them."""
+    run_combine(T, T, H, k)
+    rows = np.random.default_rng(T).permutation(T * k).astype(np.int32)
+    rows[::11], rows[-1] = -1, T * k
+    run_combine(T + 1, T, H, k, rows=rows, extra_rows=1)
