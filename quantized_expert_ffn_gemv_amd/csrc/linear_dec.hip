@@ -45,6 +45,11 @@ __device__ __forceinline__ void quarter_transpose(const uint32_t* c, uint32_t (&
 // read at one group hit distinct banks.
 __host__ __device__ inline int scale_pitch(int n) { return 8 * ((n + 7) / 8) + 8; }
 
+// Kernels of which two workgroups fit a CU's registers (128 a lane; with twice the
+// operands the bound made them spill: 8 tokens, 28672 x 4096, groups of 32 27 us against 23).
+template <int NT, int GPW>
+constexpr bool kTwoFit = NT * GPW <= 2;
+
 struct StreamArgs {
     LinearArgs l;
     int g0, ng;              // the launch's groups of K: [g0, g0 + ng)
@@ -84,7 +89,7 @@ __device__ __forceinline__ uint4 load16_any(const uint16_t* p) {
 // times the codes' cache cycles: 16 rows' cache lines for two bytes each; 49999 x
 // 4096 38 us against 28).  The waves' sums meet in LDS, one barrier a tile.
 template <int BITS, int SPG, int NT, int RT, int GPW, int RBU>
-__global__ __launch_bounds__(64 * kStreamMaxWaves) void linear_stream_kernel(StreamArgs sa) {
+__global__ __launch_bounds__(64 * kStreamMaxWaves, (kTwoFit<NT, GPW> ? 4 : 2)) void linear_stream_kernel(StreamArgs sa) {
     const LinearArgs& a = sa.l;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int RB = 16 * RT, STEPS = 4 / SPG, SW = (SPG + 1) / 2;
@@ -337,7 +342,11 @@ void stream_launch(const StreamArgs& sa, hipStream_t s) {
     const int waves = for_groups > for_pieces ? for_groups : for_pieces;
     const int blocks = (a.T + 16 * NT - 1) / (16 * NT);        // of tokens
     const int tiles = (a.w.N + 16 * RT - 1) / (16 * RT);
-    const int all = device_cus() * (kStreamMaxWaves / waves), resident = all > blocks ? all / blocks : 1;
+    // two workgroups a CU, one multiplying while the other's waves meet, where each still has
+    // four tiles of 16 rows (8 tokens, 4 bits: 49999 x 1024 12.7 us against 16.6, 49999 x 2048
+    // 17.7 and 20.8; with fewer tiles 8192 x 2048 7.7 and 6.6, 16384 x 512 6.9 and 6.6)
+    const bool two = kTwoFit<NT, GPW> && (long)tiles * RT * blocks >= 8L * device_cus();
+    const int all = device_cus() * ((two ? 2 : 1) * kStreamMaxWaves / waves), resident = all > blocks ? all / blocks : 1;
     // one tile per workgroup: nothing to request ahead (1 token, 2048 x 1024: 3.4 us against 3.9)
     if (RBU > 1 && tiles <= resident) stream_go<BITS, SPG, NT, RT, GPW, 1>(sa, waves, resident, blocks, s);
     else stream_go<BITS, SPG, NT, RT, GPW, RBU>(sa, waves, resident, blocks, s);
