@@ -305,7 +305,39 @@ struct GemmArgs {
     void* y;
     int64_t ldy;
     int y_type;
+    int splits;               // of the sum; more than one: unscaled sums to part
+    float* part;              // float32 [splits][M][N]
 };
+
+// Results [t][n .. n + 7] from scaled sums: the row bias, the residual, the rounding.
+__device__ __forceinline__ void put_results(const GemmArgs& p, int t, int n, float (&v)[8]) {
+    if (n + 8 <= p.N) {                                            // (16 bytes at any alignment)
+        if (p.residual) {
+            uint32_t w[4];
+            __builtin_memcpy(w, p.residual + (size_t)t * p.ldr + n, 16);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                v[2 * x] += __uint_as_float(w[x] << 16);
+                v[2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
+            }
+        }
+        if (p.y_type == MOE_F32) {
+            __builtin_memcpy(static_cast<float*>(p.y) + (size_t)t * p.ldy + n, v, 32);
+        } else {
+            const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            __builtin_memcpy(static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + n, w, 16);
+        }
+    } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            if (n + x >= p.N) continue;
+            float u = v[x];
+            if (p.residual) u += bf16_bits_to_f32(p.residual[(size_t)t * p.ldr + n + x]);
+            if (p.y_type == MOE_F32) static_cast<float*>(p.y)[(size_t)t * p.ldy + n + x] = u;
+            else static_cast<uint16_t*>(p.y)[(size_t)t * p.ldy + n + x] = (uint16_t)(pack_bf16(u, 0.f) & 0xFFFFu);
+        }
+    }
+}
 
 }  // namespace
 
@@ -347,16 +379,18 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
         const int r = 16 * chunk < BM ? min(m0 + row, p.M - 1) - m0 : min(n0 + row - BM, p.N - 1) - n0;
         off[i] = (uint32_t)r * (2 * kStep) + 16u * ((lane & 3) ^ ((row >> 2) & 3));
     }
-    const int blocks1 = p.kd / kStep, blocks = blocks1 * p.planes, steps = blocks / KB;   // (kd: whole stages)
+    // blocks [first, last) of the sum, of blocks1 a plane, in whole stages (kd is whole stages)
+    const int blocks1 = p.kd / kStep, stages = blocks1 * p.planes / KB, each = (stages + p.splits - 1) / p.splits;
+    const int steps = min(each, stages - (int)blockIdx.y * each), first = (int)blockIdx.y * each * KB, last = first + steps * KB;
     const size_t strideA = (size_t)p.M * (2 * kStep), strideB = (size_t)p.N * (2 * kStep);   // bytes from block to block
     const uint8_t* firstA = reinterpret_cast<const uint8_t*>(p.A + (size_t)m0 * kStep);
-    const uint8_t* srcA = firstA;
-    const uint8_t* srcB = reinterpret_cast<const uint8_t*>(p.B + (size_t)n0 * kStep);
+    const uint8_t* srcA = firstA + (size_t)(first < blocks1 ? first : first - blocks1) * strideA;
+    const uint8_t* srcB = reinterpret_cast<const uint8_t*>(p.B + (size_t)n0 * kStep) + (size_t)first * strideB;
     // The loads of a stage are made in its PARTS = 2 KB halves of a block, half of a block's
     // LOADS each; the sources then move on to the next block (past the end: the last again).
     constexpr int PARTS = 2 * KB, EACH = LOADS / 2;
     static_assert(LOADS % 2 == 0, "halves");
-    int staged = 0, slot_in = 0;                                   // blocks staged, slot they go to
+    int staged = first, slot_in = 0;                               // next block, slot it goes to
     auto put = [&](int part, int i) {                              // load i of a half
         uint8_t* slot = slots + slot_in * SLOT + (part >> 1) * BLOCK + LOADS * wid * kDma;
         const int c = EACH * (part & 1) + i;
@@ -365,7 +399,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     auto put_done = [&](int part) {
         if (part & 1) {
             ++staged;
-            if (staged < blocks) {
+            if (staged < last) {
                 srcA = staged == blocks1 ? firstA : srcA + strideA;
                 srcB += strideB;
             }
@@ -456,13 +490,14 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     float rb[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-        en[x] = p.en ? p.en[min(n + x, p.N - 1)] : 0;
-        rb[x] = p.row_bias ? p.row_bias[min(n + x, p.N - 1)] : 0.f;
+        en[x] = p.en && p.splits == 1 ? p.en[min(n + x, p.N - 1)] : 0;
+        rb[x] = p.row_bias && p.splits == 1 ? p.row_bias[min(n + x, p.N - 1)] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < WM; ++i)
 #pragma unroll
-        for (int rr = 0; rr < 32 / PASS; ++rr) et[i][rr] = p.et[min(m0 + 32 * (WM * wm + i) + PASS * rr + lane / PER_ROW, p.M - 1)];
+        for (int rr = 0; rr < 32 / PASS; ++rr)
+            et[i][rr] = p.splits == 1 ? p.et[min(m0 + 32 * (WM * wm + i) + PASS * rr + lane / PER_ROW, p.M - 1)] : 0;
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
         const int r0 = m0 + 32 * (WM * wm + i);
@@ -482,35 +517,52 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
                 for (int u = 0; u < 4; ++u) v[x + u] = ldexpf(f[u], -(et[i][rr] + en[x + u])) + rb[x + u];
             }
-            if (n + 8 <= p.N) {                                    // (16 bytes at any alignment)
-                if (p.residual) {
-                    uint32_t w[4];
-                    __builtin_memcpy(w, p.residual + (size_t)t * p.ldr + n, 16);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        v[2 * x] += __uint_as_float(w[x] << 16);
-                        v[2 * x + 1] += __uint_as_float(w[x] & 0xFFFF0000u);
-                    }
-                }
-                if (p.y_type == MOE_F32) {
-                    __builtin_memcpy(static_cast<float*>(p.y) + (size_t)t * p.ldy + n, v, 32);
-                } else {
-                    const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-                    __builtin_memcpy(static_cast<uint16_t*>(p.y) + (size_t)t * p.ldy + n, w, 16);
-                }
+            if (p.splits == 1) {
+                put_results(p, t, n, v);
             } else {
+                float* part = p.part + ((size_t)blockIdx.y * p.M + t) * p.N + n;
+                if (n + 8 <= p.N) __builtin_memcpy(part, v, 32);
+                else
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    if (n + x >= p.N) continue;
-                    float u = v[x];
-                    if (p.residual) u += bf16_bits_to_f32(p.residual[(size_t)t * p.ldr + n + x]);
-                    if (p.y_type == MOE_F32) static_cast<float*>(p.y)[(size_t)t * p.ldy + n + x] = u;
-                    else static_cast<uint16_t*>(p.y)[(size_t)t * p.ldy + n + x] = (uint16_t)(pack_bf16(u, 0.f) & 0xFFFFu);
-                }
+                    for (int x = 0; x < 8; ++x)
+                        if (n + x < p.N) part[x] = v[x];
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     }
+}
+
+// The splits' sums joined in order, scaled back and finished; a thread eight results.
+__global__ __launch_bounds__(256) void linear_join_kernel(GemmArgs p) {
+    const int cols = (p.N + 7) / 8;
+    const long id = (long)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (long)cols * p.M) return;
+    const int t = (int)(id / cols), n = (int)(id % cols) * 8;
+    const size_t step = (size_t)p.M * p.N;
+    const float* src = p.part + (size_t)t * p.N + n;
+    float v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = 0.f;
+    if (n + 8 <= p.N) {
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            float u[8];
+            __builtin_memcpy(u, src + s * step, 32);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] += u[x];
+        }
+    } else {
+        for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] += n + x < p.N ? src[s * step + x] : 0.f;
+    }
+    const int et = p.et[t];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const int c = min(n + x, p.N - 1);
+        v[x] = ldexpf(v[x], -(et + (p.en ? p.en[c] : 0))) + (p.row_bias ? p.row_bias[c] : 0.f);
+    }
+    put_results(p, t, n, v);
 }
 
 namespace {
@@ -522,12 +574,24 @@ void gemm_go(const GemmArgs& p, hipStream_t s) {
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
     const int blocks = ((tm * tn + 7) / 8) * 8;
     const size_t lds = (size_t)STAGES * KB * (BM + BN) * 2 * kStep;
-    hipLaunchKernelGGL((linear_gemm_kernel<WM, WN, WR, WC, STAGES, KB>), dim3((unsigned)blocks), dim3(64 * WR * WC), lds,
-                       s, p);
+    hipLaunchKernelGGL((linear_gemm_kernel<WM, WN, WR, WC, STAGES, KB>), dim3((unsigned)blocks, (unsigned)p.splits),
+                       dim3(64 * WR * WC), lds, s, p);
 }
 
+enum Tile { k256x256, k256x128, k128, k64, k64One };
+
+constexpr int kMaxSplits = 16;
+
+// The splits' sums are at most what fills the card with the largest tiles.
+long split_results() { return 65536L * device_cus(); }
+
+struct Choice {
+    Tile tile;
+    int splits;               // of the sum
+};
+
 // Tiles by the time their rounds over the CUs take, in hundredths of one round of 256 x
-// 256 tiles (K = 4096: about 115 us):
+// 256 tiles (about 115 us for a sum of 4096):
 //   256 x 256  100, one a CU;              256 x 128  56, one a CU;
 //   128 x 128  60, two a CU, 42 with one;  64 x 64  28, two a CU, 19 with one, whose ring
 //   takes all of the LDS (330 x 2048 x 4096: 28.0 us against 30.1 with half of it).
@@ -536,29 +600,61 @@ void gemm_go(const GemmArgs& p, hipStream_t s) {
 //   4096 x 5120 x 2048  121 116 106 154    4096 x 2048 x 8192  193 158 167 234
 //   1500 x 4096 x 4096  101  73  75  92     700 x 4096 x 4096   98  65  52  55
 //   1024 x 2048 x 2048   58  42  34  32     512 x 4096 x 4096    -   -  50  42
-void gemm(const GemmArgs& p, hipStream_t s) {
+// Long sums over few tiles are split, where the shorter sums gain more than the join takes
+// (a launch, and the partial sums written and read); without and with: gradient, 253 x
+// 24471 x 4736 286 187, 1024 x 49999 x 4096 764 655, 64 x 30000 x 256 100 30; forward
+// 64 x 128 x 8192 33 17, 4000 x 512 x 8192 80 82.
+Choice gemm_choice(int M, int N, int kd, int planes) {
     const long cus = device_cus();
-    auto tiles = [&](int rows, int cols) { return (long)((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols); };
+    const int sum = kd * planes;
+    auto tiles = [&](int rows, int cols) { return (long)((M + rows - 1) / rows) * ((N + cols - 1) / cols); };
     auto two_a_cu = [&](long t, int one, int two) {
         const long rest = t % (2 * cus);
         return t / (2 * cus) * two + (rest == 0 ? 0 : rest <= cus ? one : two);
     };
-    const long large = (tiles(256, 256) + cus - 1) / cus * 100, tall = (tiles(256, 128) + cus - 1) / cus * 56;
-    const long mid = two_a_cu(tiles(128, 128), 42, 60), small = two_a_cu(tiles(64, 64), 19, 28);
-    const long least = std::min(std::min(large, tall), std::min(mid, small));
-    if (large == least) gemm_go<4, 2, 2, 4, 3, 1>(p, s);
-    else if (tall == least) gemm_go<4, 2, 2, 2, 6, 1>(p, s);
-    else if (mid == least) gemm_go<2, 2, 2, 2, 4, 1>(p, s);
-    else if (tiles(64, 64) > cus) gemm_go<1, 1, 2, 2, 4, 2>(p, s);
-    else gemm_go<1, 1, 2, 2, 4, 4>(p, s);
+    const long t[4] = {tiles(256, 256), tiles(256, 128), tiles(128, 128), tiles(64, 64)};
+    const int stage[4] = {1, 1, 1, 2};                             // blocks
+    Choice best{k256x256, 1};
+    double least = 0.;
+    for (int s = 1; s == 1 || (s <= kMaxSplits && s * 512 <= sum && t[2] < 2 * cus && (long)s * M * N <= split_results()); ++s) {
+        const double join = s == 1 ? 0. : 3.5 + 2.3e-6 * s * M * N;
+        const long cost[4] = {(t[0] * s + cus - 1) / cus * 100, (t[1] * s + cus - 1) / cus * 56, two_a_cu(t[2] * s, 42, 60),
+                              two_a_cu(t[3] * s, 19, 28)};
+        for (int i = 0; i < 4; ++i) {
+            // (fewer tiles than CUs run faster than their rounds say: a split has to promise a fifth)
+            const double us = (1.15 / 4096 * sum / s * (double)cost[i] + join) * (s == 1 ? 1. : 1.25);
+            if ((s > 1 || i > 0) && us >= least) continue;
+            least = us;
+            const bool one = i == 3 && t[3] * s <= cus;
+            const int stages = sum / kStep / (one ? 4 : stage[i]), each = (stages + s - 1) / s;
+            best = Choice{one ? k64One : (Tile)i, (stages + each - 1) / each};   // (no split without a stage)
+        }
+    }
+    return best;
+}
+
+void gemm(GemmArgs p, hipStream_t s) {
+    const Choice c = gemm_choice(p.M, p.N, p.kd, p.planes);
+    p.splits = c.splits;
+    switch (c.tile) {
+    case k256x256: gemm_go<4, 2, 2, 4, 3, 1>(p, s); break;
+    case k256x128: gemm_go<4, 2, 2, 2, 6, 1>(p, s); break;
+    case k128: gemm_go<2, 2, 2, 2, 4, 1>(p, s); break;
+    case k64: gemm_go<1, 1, 2, 2, 4, 2>(p, s); break;
+    case k64One: gemm_go<1, 1, 2, 2, 4, 4>(p, s); break;
+    }
+    if (p.splits > 1) {
+        const long threads = (long)p.M * ((p.N + 7) / 8);
+        hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+    }
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Workspace: A, et, en, then the chunk's weights.
+// Workspace: A, et, en, the chunk's weights, then the splits' sums.
 struct Plan {
     int kd, planes, chunk, total;          // chunk: weight rows (forward) or 128-runs (gradient) per GEMM
-    size_t et, en, wh, bytes;
+    size_t et, en, wh, part, bytes;
 };
 
 Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
@@ -574,7 +670,10 @@ Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
     p.et = align256((size_t)T * p.kd * 2);
     p.en = p.et + align256((size_t)T * 4);
     p.wh = p.en + align256((size_t)w.N * 2);
-    p.bytes = p.wh + align256(unit * p.chunk);
+    p.part = p.wh + align256(unit * p.chunk);
+    // (for any number of splits, so that more tokens never need less)
+    const long results = (long)T * (grad ? 128 * p.chunk : p.chunk);
+    p.bytes = p.part + (p.kd * p.planes < 1024 ? 0 : align256(std::min(kMaxSplits * results, split_results()) * sizeof(float)));
     return p;
 }
 
@@ -603,6 +702,7 @@ int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
         if (a.w.bits == 4) hipLaunchKernelGGL(linear_prep_kernel<4>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(linear_prep_kernel<2>, grid, dim3(256), 0, s, p);
         GemmArgs g{};
+        g.part = reinterpret_cast<float*>(ws + pl.part);
         g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = p.cn; g.kd = pl.kd; g.planes = pl.planes; g.et = p.et; g.en = p.en + c0;
         g.row_bias = a.row_bias ? a.row_bias + c0 : nullptr;
         g.residual = a.residual ? a.residual + c0 : nullptr;
@@ -635,6 +735,7 @@ int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
         if (a.w.bits == 4) hipLaunchKernelGGL(linear_grad_prep_kernel<4>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(linear_grad_prep_kernel<2>, grid, dim3(256), 0, s, p);
         GemmArgs g{};
+        g.part = reinterpret_cast<float*>(ws + pl.part);
         g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = 128 * p.cn; g.kd = pl.kd; g.planes = 1; g.et = p.et;
         g.ldy = a.lddx; g.y_type = MOE_BF16; g.y = a.dx + 128 * (size_t)c0;
         gemm(g, s);

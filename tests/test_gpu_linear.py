@@ -439,3 +439,13 @@ def test_a_matrix_in_chunks():
     LargeMatrix(1, 5000, 32768, 4, 128).linear(1500, f32=True, row_bias=True, residual=True, pad=0)
     LargeMatrix(2, 40000, 8192, 2, 64).linear(600, f32=False, row_bias=True, residual=False, pad=1)
     LargeMatrix(3, 300001, 1024, 4, 128).grad(1000, f32=False, pad=1)
+
+
+@pytest.mark.parametrize("T,N,K,bits,group", [(700, 60, 8192, 4, 64), (500, 20001, 384, 2, 128), (260, 24471, 1152, 4, 128),
+                                              (1100, 70, 4224, 4, 32), (1000, 900, 6400, 2, 128), (2100, 333, 9088, 4, 128)])
+def test_long_sums_over_few_tiles(T, N, K, bits, group):
+    """Sums split over workgroups, forward (two planes of the weights among them) and gradient."""
+    m = LargeMatrix(T + K, N, K, bits, group)
+    m.linear(T, f32=True, row_bias=True, residual=True, pad=1)
+    m.linear(T, f32=False, row_bias=False, residual=bits == 4, pad=0)
+    m.grad(T, f32=bits == 2, pad=N % 3)
