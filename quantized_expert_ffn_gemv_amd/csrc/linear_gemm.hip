@@ -39,6 +39,7 @@ constexpr int kMid = 16;                               // en of weights below 1/
 constexpr int kNone = 400;                             // exponent of zero rows: 2^-400 leaves no finite dy above 0
 constexpr int kStep = 32;                              // summed elements per block
 constexpr int kBlocks = 4;                             // rows are whole runs of this many blocks (zeros behind)
+constexpr int kKeep = 4;                               // pieces of a row of A a thread keeps
 constexpr int kPrepGroups = 8;                         // 128-runs of K a workgroup lays out
 // Laid-out weights per chunk: past the 256 MB cache, for enough tiles in a chunk's GEMM
 // (1024 tokens, 28672 x 8192: 128 MB 680 us, 256 MB 626, 512 MB 601, 1 GB 610; gradient,
@@ -98,36 +99,38 @@ struct PrepArgs {
     int c0, cn;               // this chunk's weight rows (forward) or 128-runs of K (gradient)
     int planes;
     int a_blocks;             // workgroups that lay out A (the first ones); 0 in later chunks
+    int a_rows;               // rows each: 1, or 4 (rows of at most 64 kKeep pieces: 3769 x 2240
+                              // x 256 24.6 us against 28.1, 4096 x 2048 x 2048 53.8 and 56.1)
 };
 
-// One row of A by a workgroup of 256, in pieces of eight values: the first 256 KEEP
-// pieces stay in registers between the maximum and the rounding, the rest is read
-// twice.  dy's values take 2^(kMid - en) of their weight row.  Every thread's KEEP
+// One row of A by LANES threads, a workgroup of 256 or a wave, in pieces of eight values:
+// the first LANES kKeep pieces stay in registers between the maximum and the rounding, the rest is read
+// twice.  dy's values take 2^(kMid - en) of their weight row.  Every thread's kKeep
 // loads are made whatever the row's length (past its whole pieces the last one again):
 // behind a branch each waited for the one before (4096 x 8192 of dy with its weights: 54 us against 46).
-template <bool GRAD, bool F32>
+template <bool GRAD, bool F32, int LANES>
 __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
-    constexpr int KEEP = 4, GROUP = 256 * KEEP, SIZE = F32 ? 4 : 2;
+    constexpr int KEEP = kKeep, GROUP = LANES * KEEP, SIZE = F32 ? 4 : 2;
     __shared__ float tops[4];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % LANES;
     const uint8_t* src = static_cast<const uint8_t*>(p.a) + (size_t)t * p.lda * SIZE;
     const int whole = p.len / 8, rest = p.len % 8, pieces = p.kd / 8, groups = (pieces + GROUP - 1) / GROUP;
     float v[KEEP][8], tail[8], top = 0.f;
     bool bad = false;
-    auto get = [&](int first) {                                    // pieces first + tid + 256 c (zeros past the whole ones)
+    auto get = [&](int first) {                                    // pieces first + tid + LANES c (zeros past the whole ones)
         uint32_t x[KEEP][F32 ? 8 : 4];
         uint4 e[KEEP];
         if (whole > 0) {
 #pragma unroll
             for (int c = 0; c < KEEP; ++c) {
-                const int i = min(first + tid + 256 * c, whole - 1);
+                const int i = min(first + tid + LANES * c, whole - 1);
                 __builtin_memcpy(x[c], src + (size_t)i * (8 * SIZE), 8 * SIZE);   // (rows of dy have any alignment)
                 if constexpr (GRAD) e[c] = *reinterpret_cast<const uint4*>(p.en + 8 * i);
             }
         }
 #pragma unroll
         for (int c = 0; c < KEEP; ++c) {
-            const bool in = first + tid + 256 * c < whole;
+            const bool in = first + tid + LANES * c < whole;
             const uint32_t ew[4] = {e[c].x, e[c].y, e[c].z, e[c].w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -165,9 +168,11 @@ __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
         for (int c = 0; c < KEEP; ++c) look(v[c]);
     }
     top = row_max<kWave>(bad ? INFINITY : top);
-    if ((tid & 63) == 0) tops[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    if constexpr (LANES > kWave) {
+        if ((tid & 63) == 0) tops[tid >> 6] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    }
     const int e = scale_exponent(top);
     if (tid == 0) p.et[t] = GRAD ? e + kMid : e;
     auto put = [&](const float (&x)[8], int i) {
@@ -182,9 +187,20 @@ __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
         if (g > 0) get(g * GROUP);
 #pragma unroll
         for (int c = 0; c < KEEP; ++c) {
-            const int i = g * GROUP + tid + 256 * c;
+            const int i = g * GROUP + tid + LANES * c;
             if (i < pieces && !(rest != 0 && i == whole)) put(v[c], i);
         }
+    }
+}
+
+// Rows of A of workgroup `blk`: one, or one a wave.
+template <bool GRAD, bool F32>
+__device__ __forceinline__ void prep_a(const PrepArgs& p, int blk) {
+    if (p.a_rows == 1) {
+        prep_a_row<GRAD, F32, 256>(p, blk);
+    } else {
+        const int t = __builtin_amdgcn_readfirstlane(blk * 4 + (int)(threadIdx.x >> 6));
+        if (t < p.T) prep_a_row<GRAD, F32, kWave>(p, t);
     }
 }
 
@@ -195,7 +211,7 @@ __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
 template <int BITS>
 __global__ __launch_bounds__(256) void linear_prep_kernel(PrepArgs p) {
     if ((int)blockIdx.x < p.a_blocks) {
-        prep_a_row<false, false>(p, blockIdx.x);
+        prep_a<false, false>(p, blockIdx.x);
         return;
     }
     __shared__ int ens[16];
@@ -257,8 +273,8 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(PrepArgs p) {
 template <int BITS>
 __global__ __launch_bounds__(256) void linear_grad_prep_kernel(PrepArgs p) {
     if ((int)blockIdx.x < p.a_blocks) {
-        if (p.a_type == MOE_F32) prep_a_row<true, true>(p, blockIdx.x);
-        else prep_a_row<true, false>(p, blockIdx.x);
+        if (p.a_type == MOE_F32) prep_a<true, true>(p, blockIdx.x);
+        else prep_a<true, false>(p, blockIdx.x);
         return;
     }
     const int tid = threadIdx.x, blk = (int)blockIdx.x - p.a_blocks;
@@ -696,7 +712,8 @@ int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
     for (int c0 = 0; c0 < pl.total; c0 += pl.chunk) {
         p.c0 = c0;
         p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
-        p.a_blocks = c0 == 0 ? a.T : 0;
+        p.a_rows = pl.kd <= 8 * kWave * kKeep ? 4 : 1;
+        p.a_blocks = c0 == 0 ? (a.T + p.a_rows - 1) / p.a_rows : 0;
         const int parts = (a.w.K / 128 + kPrepGroups - 1) / kPrepGroups;
         const dim3 grid((unsigned)(p.a_blocks + (p.cn + 15) / 16 * parts));
         if (a.w.bits == 4) hipLaunchKernelGGL(linear_prep_kernel<4>, grid, dim3(256), 0, s, p);
@@ -730,7 +747,8 @@ int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
     for (int c0 = 0; c0 < pl.total; c0 += pl.chunk) {
         p.c0 = c0;
         p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
-        p.a_blocks = c0 == 0 ? a.T : 0;
+        p.a_rows = pl.kd <= 8 * kWave * kKeep ? 4 : 1;
+        p.a_blocks = c0 == 0 ? (a.T + p.a_rows - 1) / p.a_rows : 0;
         const dim3 grid((unsigned)(p.a_blocks + p.cn * ((pl.kd + 127) / 128)));
         if (a.w.bits == 4) hipLaunchKernelGGL(linear_grad_prep_kernel<4>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(linear_grad_prep_kernel<2>, grid, dim3(256), 0, s, p);
