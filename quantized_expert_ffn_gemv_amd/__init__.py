@@ -426,6 +426,8 @@ def _want_rows(name: str, t, device, dtypes, rows: int, cols: int) -> int:
         raise ValueError(f"{name} holds {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {(rows, cols)} needed")
+    if t.is_contiguous():                    # (the common case, without its strides)
+        return cols
     to_row, to_col = t.stride()
     if to_col != 1 and cols > 1:
         raise ValueError(f"{name}'s rows are not contiguous")
@@ -440,7 +442,7 @@ def _enqueue(fn, device, stream, *args) -> None:
         stream = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without its object
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():                     # current_device() without its checks
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
