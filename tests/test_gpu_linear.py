@@ -449,3 +449,103 @@ def test_long_sums_over_few_tiles(T, N, K, bits, group):
     m.linear(T, f32=True, row_bias=True, residual=True, pad=1)
     m.linear(T, f32=False, row_bias=False, residual=bits == 4, pad=0)
     m.grad(T, f32=bits == 2, pad=N % 3)
+
+
+@pytest.mark.parametrize("T,N,K", [(2000, 1500, 768), (260, 24471, 1152), (300, 4100, 9088)])
+def test_graph_replay_and_streams_of_many_tokens(T, N, K):
+    """The laid-out products, and split ones, captured; replays and another stream's calls against eager."""
+    m = LargeMatrix(T, N, K, 4, 64)
+    x, dy = m.rows(T, K), m.rows(T, N, 1e-3)
+    y, dx = torch.empty(T, N, dtype=torch.bfloat16, device=DEV), torch.empty(T, K, dtype=torch.bfloat16, device=DEV)
+    fb, gb = moe.LinearBuffers.allocate(m.q, T, y.dtype), moe.LinearBuffers.allocate(m.q, T, dy.dtype, grad=True)
+    side = torch.cuda.Stream()
+
+    def step(stream=None):
+        moe.linear(m.q, x, y, fb, stream=stream)
+        moe.linear_grad(m.q, dy, dx, gb, stream=stream)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        x.copy_(m.rows(T, K))
+        dy.copy_(m.rows(T, N, 1e-3))
+        step()
+        torch.cuda.synchronize()
+        want = (y.clone(), dx.clone())
+        for again in (graph.replay, lambda: step(side)):
+            y.fill_(NAN)
+            dx.fill_(NAN)
+            fb.workspace.fill_(0xFF)
+            gb.workspace.fill_(0xFF)
+            torch.cuda.synchronize()
+            again()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[0]) and torch.equal(dx, want[1]), f"time {i}"
+
+
+def laid_out(seed=1, parts=None):
+    """A matrix and a token count whose products go through the laid-out copies."""
+    T, N, K = 1000, 2500, 640
+    m = Matrix(seed, N, K, 4, 64, parts=parts)
+    assert moe.linear_workspace_bytes(m.q, T, torch.bfloat16) >= T * K * 2
+    assert moe.linear_workspace_bytes(m.q, T, torch.bfloat16, grad=True) >= T * N * 2
+    return m, T
+
+
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_a_bad_row_of_many(bad):
+    m, T = laid_out()
+    x, dy = m.rows(T, m.K), m.rows(T, m.N)
+    y0, dx0 = run_linear(m, T, x=x), run_grad(m, T, dy=dy)
+    x[1, 70], dy[T - 1, 7] = bad, bad
+    y, dx = torch.empty_like(y0), torch.empty_like(dx0)
+    moe.linear(m.q, dev(x), y, moe.LinearBuffers.allocate(m.q, T, y.dtype))
+    moe.linear_grad(m.q, dev(dy), dx, moe.LinearBuffers.allocate(m.q, T, dx.dtype, grad=True))
+    assert not bool(torch.isfinite(y[1]).any()) and not bool(torch.isfinite(dx[T - 1]).any())
+    keep = torch.arange(T, device=DEV)
+    assert torch.equal(y[keep != 1], y0[keep != 1]) and torch.equal(dx[keep != T - 1], dx0[keep != T - 1])
+
+
+@pytest.mark.parametrize("kind", ["zero", "large", "tiny", "mixed", "rows"])
+def test_extremes_of_many_tokens(kind):
+    rng = np.random.default_rng(7)
+    q, s, b = ref.make_matrix(rng, 2500, 640, 4, 64)
+    if kind == "zero":
+        s[rng.random(s.shape) < 0.3] = 0
+        b[rng.random(b.shape) < 0.3] = 0
+        s[::3], b[::3] = 0, 0
+    elif kind == "large":
+        s[:] = np.float16(60000)
+        b[:] = np.float16(-65504)
+    elif kind == "tiny":
+        s[:] = np.float16(6e-8)
+        b[:] = np.float16(-6e-8)
+    elif kind == "mixed":
+        s[:] = np.exp(rng.uniform(np.log(1e-4), np.log(1.0), s.shape)).astype(np.float16)
+        b[:] = -s
+    m, T = laid_out(parts=(q, s, b))
+    x, dy = m.rows(T, m.K), m.rows(T, m.N)
+    if kind == "zero":
+        dy[:, ::3] *= np.float32(2.0) ** 40
+    if kind == "rows":
+        x, dy = (ref.bf16_round(a * np.float32(2.0) ** rng.integers(-90, 90, (T, 1)).astype(np.float32)) for a in (x, dy))
+        dy[5], x[6] = 0.0, 0.0
+    run_linear(m, T, x=x)
+    run_linear(m, T, f32=True, x=x)
+    run_grad(m, T, dy=dy)
+    run_grad(m, T, f32=True, pad=1, dy=dy)
+
+
+@pytest.mark.parametrize("T,N,K", [(1000, 2500, 640), (260, 24471, 1152), (700, 60, 8192), (300, 4100, 9088)])
+def test_residual_in_place_of_many_tokens(T, N, K):
+    m = LargeMatrix(N, N, K, 4, 128)
+    x, res = m.rows(T, K), m.rows(T, N)
+    rb = torch.randn(N, device=DEV, generator=m.gen)
+    buf = moe.LinearBuffers.allocate(m.q, T, torch.bfloat16)
+    apart, y = torch.empty_like(res), res.clone()
+    moe.linear(m.q, x, apart, buf, row_bias=rb, residual=res)
+    moe.linear(m.q, x, y, buf, row_bias=rb, residual=y)
+    assert torch.equal(y, apart) and not torch.equal(y, res)
