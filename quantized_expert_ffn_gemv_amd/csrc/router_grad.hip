@@ -305,7 +305,8 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteGradArgs 
             }
             pf = row_sum<LPT>(pf);
             const float zl = cz * lse, all = a.renorm ? 0.f : inner;
-            if (some) {
+            // (a token without either part stays 0 whatever its logits hold: a padded one's p may be NaN)
+            if (some && (losses || (a.dgates && !a.renorm))) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const float loss = losses ? fmaf(ca, f[i] - pf, zl) : 0.f;
