@@ -7,7 +7,7 @@
 // m and S by reductions over the lanes.  A row without a logit above -inf has
 // p = 0 everywhere.
 //
-// The gradient is bound by memory: 16384 x 512, 15.3 us (4.4 TB/s); 64 x 64, 2.4 us.  The
+// The gradient is bound by memory: 16384 x 512, 16.3 us (4.2 TB/s); 64 x 64, 2.4 us.  The
 // losses by their joins: 32 x 256, 5.1 us; 8191 x 128, 8.6 us; 16384 x 512, 16.9 us.
 #include <cmath>
 
@@ -53,29 +53,35 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     }
 }
 
-// v (logits) -> p in place; returns whether the row has a logit, and lse.  The
-// exponential is the hardware's of (L - m) log2 e: rounding the product leaves a
-// relative |L - m| 2^-24 in p, no more than rounding the logits themselves did,
-// and below 2^-126 of the row's largest p is 0.
+// e^d, d <= 0, to 2 ulp: the hardware's power of two of t = d log2 e rounded, times the
+// factor 1 + r ln 2 for what the rounding left out, r = d log2 e - t (log2 e in two
+// parts).  Without the factor a small p was off by |d| 2^-24.  Below 2^-126 the
+// hardware gives 0, and d is cut off there (an infinite one would make r NaN; a NaN stays).
+__device__ __forceinline__ float exp_down(float d) {
+    constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;   // log2 e - (float) 1.44269504
+    d = d < -128.f ? -128.f : d;
+    const float t = d * kLog2e;
+    const float r = fmaf(d, kLog2eRest, fmaf(d, kLog2e, -t));
+    return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.f);
+}
+
+// v (logits) -> p in place; returns whether the row has a logit, and lse.  A row without
+// one has a sum of 0; NaNs, which fmaxf skips, come back by the sum.
 template <int LPT, int PER>
 __device__ __forceinline__ bool softmax_row(float (&v)[PER], float& lse) {
     float m = v[0];
-    bool nan = v[0] != v[0];
 #pragma unroll
-    for (int i = 1; i < PER; ++i) {
-        m = fmaxf(m, v[i]);
-        nan |= v[i] != v[i];
-    }
-    m = row_max<LPT>(m);                                  // fmaxf skips NaNs: the sum below brings them back
-    const bool some = m > -INFINITY || row_max<LPT>(nan ? 1.f : 0.f) > 0.f;
+    for (int i = 1; i < PER; ++i) m = fmaxf(m, v[i]);
+    m = row_max<LPT>(m);
     const float base = m > -INFINITY ? m : 0.f;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        v[i] = __builtin_amdgcn_exp2f((v[i] - base) * 1.44269504f);
+        v[i] = exp_down(v[i] - base);
         s += v[i];
     }
     s = row_sum<LPT>(s);
+    const bool some = s != 0.f;
     const float r = some ? 1.f / s : 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] *= r;

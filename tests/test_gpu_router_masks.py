@@ -1,5 +1,5 @@
-"""The router's backward pass where padded tokens hold anything, against the 64-bit
-forms of weights_ref.py."""
+"""The router's backward pass where padded tokens hold anything, and the bits of its
+softmax: against the 64-bit forms of weights_ref.py."""
 import numpy as np
 import pytest
 import torch
@@ -52,3 +52,26 @@ def test_padded_tokens_may_hold_anything(T, E, k, bad):
     # gates from the softmax over all experts, without their gradient: the losses' part alone
     got = route(L, ids, g, False, None, counts, n, valid)
     assert not got[::3].any() and np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("E", [3, 60, 128, 256, 512, 1000])
+def test_softmax_keeps_small_probabilities(E):
+    """Logits whose differences are exact: a probability is off by a few roundings, however small it is.
+
+    p = exp(d) / S: the exponential's 2 U (hardware's 1 ulp) and its argument's correction, the
+    product with 1 / S (2 U) and S's own relative error (at most 16 values a lane, then 6
+    levels: 22 U, of sums whose small terms count nothing): 32 U in all."""
+    rng = np.random.default_rng(E)
+    T, k = 8, 2
+    L = (-rng.integers(0, 80 * 1024, (T, E)) / 1024.0).astype(np.float32)
+    L[:, 0] = 0.0
+    ids = np.argsort(-L, axis=1, kind="stable")[:, :k].astype(np.int32)
+    d = moe.dims(1, 128, 128, E, k)
+    buf = moe.BalanceBuffers.allocate(d)
+    for t in range(T):
+        c, P = torch.empty(E, dtype=torch.int32, device=DEV), torch.empty(E, device=DEV)
+        n, loss = torch.empty(1, dtype=torch.int32, device=DEV), torch.empty(2, device=DEV)
+        moe.balance_loss(d, dev(L[t:t + 1]), dev(ids[t:t + 1]), c, P, n, loss, buf)
+        want = ref.softmax(L[t:t + 1])[0][0]
+        off = np.abs(P.double().cpu().numpy() - want) / (32 * U * want)
+        assert off.max() <= 1.0, f"{off.max():.3g} times the bound"
