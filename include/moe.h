@@ -562,8 +562,8 @@ int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, 
  *   sync       int32 [MOE_LINEAR_SYNC_INTS] device memory, 256-byte aligned,
  *              holding zeros before the first call; each call leaves it zero.
  *              Calls that share a workspace or sync must be ordered (one stream).
- * Few tokens: dy times the scales enters as two bf16 parts (2^-16); many: as
- * moe_linear's operands (a float32 dy with 2^-11 too).
+ * Few tokens: dy times the scales enters as three bf16 parts (a float32's bits);
+ * many: as moe_linear's operands (a float32 dy with 2^-11 too).
  * Rows of dy with infinities or NaNs as for moe_linear's x. */
 #define MOE_LINEAR_SYNC_INTS 4096
 int moe_linear_grad(const moe_qmatrix* w, int32_t T, const void* dy, int64_t lddy, int dy_type, uint16_t* dx,

@@ -3,9 +3,10 @@
 // scale group,
 //   dx[t][k] = sum_n d[t][n] q[n][k] + sum_n dy[t][n] b[n]
 //            = (1/L) sum_n (128 + L q) d  +  sum_n dy (b - (128/L) s),
-// L the codes' lever.  d is carried as two bf16 parts (together 2^-16 of it left
-// out; dx is rounded to bf16's 2^-8), the codes are exact, the second sum and all
-// accumulation are float32.
+// L the codes' lever.  d is carried as three bf16 parts, which hold a float32's 24
+// bits (with two, 2^-16 of d was left out, and of 16 + q of it at a weight of zero: outputs
+// changed where terms cancel), the codes are exact, the second sum and all accumulation are
+// float32.
 //
 // The sum runs over weight rows, which the codes are not packed along.  A lane
 // takes one word (eight columns k) of eight rows; v_perm_b32 pairs the words of
@@ -20,8 +21,8 @@
 // rows at a time in turn; their sums meet in LDS, those of several workgroups in
 // the workspace, where the last to arrive adds them in order.
 //
-// Bound by latency where a wave has few rounds (1 token, 4096 x 4096 at 4 bits: 6.8 us;
-// 37 tokens, 5111 x 2048 at 2 bits, groups of 64: 10.8), by the code stream past that
+// Bound by latency where a wave has few rounds (1 token, 4096 x 4096 at 4 bits: 7.2 us;
+// 37 tokens, 5111 x 2048 at 2 bits, groups of 64: 11.5), by the code stream past that
 // (8 tokens, 49999 x 4096: 36 us, 3.0 TB/s of the bytes that have to move).
 #include <type_traits>
 
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
                     be[i + e] = fmaf(-kOffset<BITS>, vs[e], vb[e]);
                 }
             }
-            uint32_t hi[4], lo[4];
+            uint32_t parts[3][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float d[2];
@@ -166,13 +167,17 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
                     d[x] = g * s[r];
                     z[u] = fmaf(g, be[r], z[u]);
                 }
-                hi[i] = pack_bf16(d[0], d[1]);
-                lo[i] = pack_bf16(d[0] - __uint_as_float(hi[i] << 16), d[1] - __uint_as_float(hi[i] & 0xFFFF0000u));
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    parts[x][i] = pack_bf16(d[0], d[1]);
+                    d[0] -= __uint_as_float(parts[x][i] << 16);
+                    d[1] -= __uint_as_float(parts[x][i] & 0xFFFF0000u);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[u][j] = mfma16(hi, B[j], acc[u][j]);
+            for (int x = 0; x < 3; ++x)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[u][j] = mfma16(lo, B[j], acc[u][j]);
+                for (int j = 0; j < 8; ++j) acc[u][j] = mfma16(parts[x], B[j], acc[u][j]);
             // one scale group's products after another: together their operands would not fit the registers
             if (SPG > 1) __builtin_amdgcn_sched_barrier(0);
         }
