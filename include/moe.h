@@ -542,9 +542,13 @@ int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int gr
  *   y          bf16 or float32 (y_type) [T] rows of N elements, ldy >= N apart
  *   workspace  moe_linear_workspace_bytes(w, T, y_type, 0), 256-byte aligned
  *              (NULL where that is 0)
- * Many tokens: x and w enter the product as half-precision values scaled by a
- * power of two per row, which carry 2^-11 of a w (2^-22 where y is float32) and
- * values down to 2^-28 of their row's largest; few tokens: without rounding.
+ * Which kernels a call takes goes by its sizes; the products are a float32 sum's
+ * in all of them: x enters as it is, a w with 2^-22 of it left out at most (with
+ * none where the codes are streamed).  Where both are laid out as scaled halves,
+ * values of x less than 2^-28 of their row's largest, and weights less than 2^-17
+ * of theirs, may lose bits: 2^-39 of the largest at most.  Sums are taken in an
+ * order that goes by the sizes, T among them.  Finite x (and dy times w) past 2^100
+ * may overflow within a sum.
  * A row of x with an infinity or NaN gives a row of y of NaNs and infinities,
  * and changes no other row. */
 int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, const float* row_bias,
@@ -562,8 +566,8 @@ int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, 
  *   sync       int32 [MOE_LINEAR_SYNC_INTS] device memory, 256-byte aligned,
  *              holding zeros before the first call; each call leaves it zero.
  *              Calls that share a workspace or sync must be ordered (one stream).
- * Few tokens: dy times the scales enters as three bf16 parts (a float32's bits);
- * many: as moe_linear's operands (a float32 dy with 2^-11 too).
+ * Roundings as in moe_linear: dy (a float32 one too) and w with 2^-22 at most left
+ * out; dy counts with its weight row's largest |w| in what a row's largest is.
  * Rows of dy with infinities or NaNs as for moe_linear's x. */
 #define MOE_LINEAR_SYNC_INTS 4096
 int moe_linear_grad(const moe_qmatrix* w, int32_t T, const void* dy, int64_t lddy, int dy_type, uint16_t* dx,

@@ -36,15 +36,28 @@ size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
 size_t linear_workspace_bytes_up_to(const moe_qmatrix& w, int T, int type, bool grad);
 int launch_linear(const LinearArgs& a, hipStream_t s);
 int launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
-// Few tokens (linear_dec.hip): any T, the matrix read once per 16 or 32 tokens.
+// The codes streamed (linear_dec.hip): any T, the matrix read once per 16 or 32 tokens.
+struct StreamForm {
+    int nt, rt;               // tiles of 16 tokens and of 16 weight rows a workgroup multiplies at once
+    int gpw, waves;           // 128-runs of K a wave, waves a workgroup
+    int rbu;                  // tiles requested ahead
+    int resident;             // workgroups per token block, at most
+};
+StreamForm stream_form(const moe_qmatrix& w, int T, int runs);
 size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_dec(const LinearArgs& a, hipStream_t s);
-// Input gradient of few tokens (linear_grad_dec.hip).
+// Input gradient, the codes streamed (linear_grad_dec.hip).
+int grad_splits(const moe_qmatrix& w, int T);
 size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_grad_dec(const LinearGradArgs& a, hipStream_t s);
-// Many tokens (linear_gemm.hip).
+// Both operands laid out for a dense product (linear_gemm.hip).
 size_t linear_gemm_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
 int launch_linear_gemm(const LinearArgs& a, hipStream_t s);
 int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s);
+
+// Estimated times of a call (us); linear_gemm_us stops at the first part past `limit`.
+double linear_dec_us(const moe_qmatrix& w, int T);
+double linear_grad_dec_us(const moe_qmatrix& w, int T);
+double linear_gemm_us(const moe_qmatrix& w, int T, int type, bool grad, double limit);
 
 }  // namespace moe

@@ -11,6 +11,8 @@
 // Bound by the weight stream: 8 tokens x 49999 x 4096 at 4 bits, float32 out, take 26 us
 // (4.2 TB/s of the bytes that have to move), 28672 x 8192 32 us (3.9 TB/s); 4096 x 4096,
 // one or two tiles a CU, 7.5 us, most of it launch, start and the last tile.
+#include <algorithm>
+
 #include "launch_util.h"
 #include "linear.h"
 #include "mfma_ops.h"
@@ -47,8 +49,7 @@ __host__ __device__ inline int scale_pitch(int n) { return 8 * ((n + 7) / 8) + 8
 
 // Kernels of which two workgroups fit a CU's registers (128 a lane; with twice the
 // operands the bound made them spill: 8 tokens, 28672 x 4096, groups of 32 27 us against 23).
-template <int NT, int GPW>
-constexpr bool kTwoFit = NT * GPW <= 2;
+constexpr bool two_fit(int nt, int gpw) { return nt * gpw <= 2; }
 
 struct StreamArgs {
     LinearArgs l;
@@ -89,7 +90,7 @@ __device__ __forceinline__ uint4 load16_any(const uint16_t* p) {
 // times the codes' cache cycles: 16 rows' cache lines for two bytes each; 49999 x
 // 4096 38 us against 28).  The waves' sums meet in LDS, one barrier a tile.
 template <int BITS, int SPG, int NT, int RT, int GPW, int RBU>
-__global__ __launch_bounds__(64 * kStreamMaxWaves, (kTwoFit<NT, GPW> ? 4 : 2)) void linear_stream_kernel(StreamArgs sa) {
+__global__ __launch_bounds__(64 * kStreamMaxWaves, (two_fit(NT, GPW) ? 4 : 2)) void linear_stream_kernel(StreamArgs sa) {
     const LinearArgs& a = sa.l;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int RB = 16 * RT, STEPS = 4 / SPG, SW = (SPG + 1) / 2;
@@ -319,78 +320,101 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves, (kTwoFit<NT, GPW> ? 4 : 2)) v
     }
 }
 
-namespace {
-
-template <int BITS, int SPG, int NT, int RT, int GPW, int RBU>
-void stream_go(const StreamArgs& sa, int waves, int resident, int blocks, hipStream_t s) {
-    const LinearArgs& a = sa.l;
-    const int tiles = (a.w.N + 16 * RT - 1) / (16 * RT);
-    const int tokens = a.T < 16 * NT ? a.T : 16 * NT;
-    const dim3 grid((unsigned)(tiles < resident ? tiles : resident), (unsigned)blocks);
-    const size_t lds = (size_t)8 * 16 * RT * scale_pitch(sa.ng * SPG) +
-                       (size_t)(waves * GPW * NT * SPG * 16 + 2 * ((waves + 3) & ~3) * tokens * 16 * RT) * sizeof(float);
-    hipLaunchKernelGGL((linear_stream_kernel<BITS, SPG, NT, RT, GPW, RBU>), grid, dim3(64 * waves), lds, s, sa);
-}
-
-template <int BITS, int SPG, int NT, int RT, int GPW, int RBU>
-void stream_launch(const StreamArgs& sa, hipStream_t s) {
-    constexpr int PP = (RT * GPW * SPG + 15) / 16;
-    const LinearArgs& a = sa.l;
-    // waves for the groups, and threads for the pieces of a tile's scales (PP each)
-    const int pieces = 2 * 16 * RT * ((sa.ng * SPG + 7) / 8);
-    const int for_groups = (sa.ng + GPW - 1) / GPW, for_pieces = (pieces + 64 * PP - 1) / (64 * PP);
-    const int waves = for_groups > for_pieces ? for_groups : for_pieces;
-    const int blocks = (a.T + 16 * NT - 1) / (16 * NT);        // of tokens
-    const int tiles = (a.w.N + 16 * RT - 1) / (16 * RT);
-    // two workgroups a CU, one multiplying while the other's waves meet, where each still has
-    // four tiles of 16 rows (8 tokens, 4 bits: 49999 x 1024 12.7 us against 16.6, 49999 x 2048
-    // 17.7 and 20.8; with fewer tiles 8192 x 2048 7.7 and 6.6, 16384 x 512 6.9 and 6.6)
-    const bool two = kTwoFit<NT, GPW> && (long)tiles * RT * blocks >= 8L * device_cus();
-    const int all = device_cus() * ((two ? 2 : 1) * kStreamMaxWaves / waves), resident = all > blocks ? all / blocks : 1;
-    // one tile per workgroup: nothing to request ahead (1 token, 2048 x 1024: 3.4 us against 3.9)
-    if (RBU > 1 && tiles <= resident) stream_go<BITS, SPG, NT, RT, GPW, 1>(sa, waves, resident, blocks, s);
-    else stream_go<BITS, SPG, NT, RT, GPW, RBU>(sa, waves, resident, blocks, s);
-}
-
 // Two token tiles where their operands fit the registers (K <= 4096) and every CU has
 // more than two weight tiles to share its start among: 32 tokens, 4096 outputs, K =
 // 4096: 12.7 us against 10.2 with one, 8192: 16.5 and 14.5, 16384: 21.6 and 21.2,
 // 49999: 41 and 48; K = 2048: 8.2 and 7.4, 10.3 and 10.1, 14.1 and 15.4; 64 tokens,
 // 28672 outputs: 43 and 51.  A second ring entry per slot pays only where a slot is
 // one group (8 tokens, 49999 outputs, K = 1024: 16.6 us against 18.1; K = 2048: 21.3 and
-// 21.0; K = 4096: 30.0 and 29.2).
-template <int BITS, int SPG, int RT>
-void stream_groups(const StreamArgs& sa, hipStream_t s) {
-    const int ng = sa.ng;
-    const long work = (long)((sa.l.w.N + 16 * RT - 1) / (16 * RT)) * ((sa.l.T + 31) / 32);
-    if (sa.l.T > 16 && ng <= 32 && work > 2 * device_cus()) {
-        if (ng <= 8) stream_launch<BITS, SPG, 2, RT, 1, 2>(sa, s);
-        else if (ng <= 16) stream_launch<BITS, SPG, 2, RT, 2, 1>(sa, s);
-        else stream_launch<BITS, SPG, 2, RT, 4, 1>(sa, s);
-    } else if (ng <= 8) {
-        stream_launch<BITS, SPG, 1, RT, 1, 2>(sa, s);
-    } else if (ng <= 16) {
-        stream_launch<BITS, SPG, 1, RT, 2, 1>(sa, s);
-    } else if (ng <= 32) {
-        stream_launch<BITS, SPG, 1, RT, 4, 1>(sa, s);
-    } else if (ng <= 48) {
-        stream_launch<BITS, SPG, 1, RT, 6, 1>(sa, s);
-    } else {
-        stream_launch<BITS, SPG, 1, RT, 8, 1>(sa, s);
-    }
-}
-
+// 21.0; K = 4096: 30.0 and 29.2), and where a workgroup has a second tile to request ahead (1
+// token, 2048 x 1024: 3.4 us against 3.9).
 // Tiles of 32 weight rows (units of 1 KB) for 2-bit codes of groups of 128 where they
 // still give every CU one (8 tokens, K = 4096: 4096 outputs 7.7 us against 6.9 with 16
 // rows, 8192 8.2 and 8.6, 49999 24.8 and 27.1; K = 1024: 8192 outputs 4.5 and 5.4, 28672
 // 8.5 and 9.8); 4-bit codes gain nothing (49999 outputs: 30.0 and 29.4), nor do 2-bit
 // ones of finer groups (28672 outputs: 21.3 and 20.7).
-template <int BITS, int SPG>
-void stream_rows(const StreamArgs& sa, hipStream_t s) {
-    if constexpr (BITS == 2 && SPG == 1) {
-        if ((sa.l.w.N + 31) / 32 >= device_cus()) return stream_groups<BITS, SPG, 2>(sa, s);
+// Two workgroups a CU, one multiplying while the other's waves meet, where each still has
+// four tiles of 16 rows (8 tokens, 4 bits: 49999 x 1024 12.7 us against 16.6, 49999 x 2048
+// 17.7 and 20.8; with fewer tiles 8192 x 2048 7.7 and 6.6, 16384 x 512 6.9 and 6.6).
+StreamForm stream_form(const moe_qmatrix& w, int T, int runs) {
+    const int cus = device_cus(), spg = 128 / w.group_size;
+    StreamForm f{};
+    f.rt = w.bits == 2 && spg == 1 && (w.N + 31) / 32 >= cus ? 2 : 1;
+    const int tiles = (w.N + 16 * f.rt - 1) / (16 * f.rt);
+    f.nt = T > 16 && runs <= 32 && (long)tiles * ((T + 31) / 32) > 2 * cus ? 2 : 1;
+    f.gpw = runs <= 8 ? 1 : runs <= 16 ? 2 : runs <= 32 ? 4 : runs <= 48 ? 6 : 8;
+    // waves for the groups, and threads for the pieces of a tile's scales (pp each)
+    const int pp = (f.rt * f.gpw * spg + 15) / 16, pieces = 2 * 16 * f.rt * ((runs * spg + 7) / 8);
+    f.waves = std::max((runs + f.gpw - 1) / f.gpw, (pieces + 64 * pp - 1) / (64 * pp));
+    const int blocks = (T + 16 * f.nt - 1) / (16 * f.nt);      // of tokens
+    const bool two = two_fit(f.nt, f.gpw) && (long)tiles * f.rt * blocks >= 8L * cus;
+    const int all = cus * ((two ? 2 : 1) * kStreamMaxWaves / f.waves);
+    f.resident = all > blocks ? all / blocks : 1;
+    f.rbu = f.gpw == 1 && tiles > f.resident ? 2 : 1;
+    return f;
+}
+
+// A CU's units (16 weight rows, a token tile) by the form that takes them, and the starts.
+double linear_dec_us(const moe_qmatrix& w, int T) {
+    static const double start[3] = {6.2, 6.2, 5.9}, run[3] = {0.112, 0.147, 0.148};          // groups of 128, 64, 32
+    static const double wave[3] = {0.096, 0.105, 0.115};                                     // one run a wave, one token tile
+    static const double two[2][3] = {{0.48, 0.48, 0.58}, {0.82, 0.98, 1.12}};                // two, up to four waves and more
+    static const double unit[2][4][3] = {{{0.89, 1.03, 0.95}, {1.55, 2.3, 2.3}, {2.19, 2.64, 3.0}, {2.78, 3.4, 3.7}},
+                                         {{1.55, 1.75, 2.1}, {2.36, 2.7, 3.4}, {}, {}}};     // 2, 4, 6, 8 runs a wave
+    const int fine = w.group_size == 128 ? 0 : w.group_size == 64 ? 1 : 2;
+    double us = 0.;
+    for (int g0 = 0, all = w.K / 128; g0 < all; g0 += kStreamGroups) {
+        const int runs = std::min(all - g0, kStreamGroups);
+        const StreamForm f = stream_form(w, T, runs);
+        const double units = (double)((w.N + 15) / 16) * ((T + 16 * f.nt - 1) / (16 * f.nt)) / device_cus();
+        us += start[fine] + (f.nt == 2 && f.gpw == 1 ? 1.8 : 0.) + run[fine] * runs;
+        if (f.gpw == 1) us += units * (f.nt == 1 ? wave[fine] * runs : two[runs > 4][fine]);
+        else us += units * unit[f.nt - 1][f.gpw / 2 - 1][fine];
     }
-    stream_groups<BITS, SPG, 1>(sa, s);
+    return us;
+}
+
+namespace {
+
+template <int BITS, int SPG, int NT, int RT, int GPW, int RBU>
+void stream_go(const StreamArgs& sa, const StreamForm& f, hipStream_t s) {
+    const LinearArgs& a = sa.l;
+    const int tiles = (a.w.N + 16 * RT - 1) / (16 * RT), blocks = (a.T + 16 * NT - 1) / (16 * NT);
+    const int tokens = a.T < 16 * NT ? a.T : 16 * NT;
+    const dim3 grid((unsigned)(tiles < f.resident ? tiles : f.resident), (unsigned)blocks);
+    const size_t lds = (size_t)8 * 16 * RT * scale_pitch(sa.ng * SPG) +
+                       (size_t)(f.waves * GPW * NT * SPG * 16 + 2 * ((f.waves + 3) & ~3) * tokens * 16 * RT) * sizeof(float);
+    hipLaunchKernelGGL((linear_stream_kernel<BITS, SPG, NT, RT, GPW, RBU>), grid, dim3(64 * f.waves), lds, s, sa);
+}
+
+template <int BITS, int SPG, int RT>
+void stream_rows(const StreamArgs& sa, const StreamForm& f, hipStream_t s) {
+    if (f.nt == 2) {
+        if (f.gpw == 1 && f.rbu == 2) stream_go<BITS, SPG, 2, RT, 1, 2>(sa, f, s);
+        else if (f.gpw == 1) stream_go<BITS, SPG, 2, RT, 1, 1>(sa, f, s);
+        else if (f.gpw == 2) stream_go<BITS, SPG, 2, RT, 2, 1>(sa, f, s);
+        else stream_go<BITS, SPG, 2, RT, 4, 1>(sa, f, s);
+    } else if (f.gpw == 1) {
+        if (f.rbu == 2) stream_go<BITS, SPG, 1, RT, 1, 2>(sa, f, s);
+        else stream_go<BITS, SPG, 1, RT, 1, 1>(sa, f, s);
+    } else if (f.gpw == 2) {
+        stream_go<BITS, SPG, 1, RT, 2, 1>(sa, f, s);
+    } else if (f.gpw == 4) {
+        stream_go<BITS, SPG, 1, RT, 4, 1>(sa, f, s);
+    } else if (f.gpw == 6) {
+        stream_go<BITS, SPG, 1, RT, 6, 1>(sa, f, s);
+    } else {
+        stream_go<BITS, SPG, 1, RT, 8, 1>(sa, f, s);
+    }
+}
+
+template <int BITS, int SPG>
+void stream_launch(const StreamArgs& sa, hipStream_t s) {
+    const StreamForm f = stream_form(sa.l.w, sa.l.T, sa.ng);
+    if constexpr (BITS == 2 && SPG == 1) {
+        if (f.rt == 2) return stream_rows<BITS, SPG, 2>(sa, f, s);
+    }
+    stream_rows<BITS, SPG, 1>(sa, f, s);
 }
 
 }  // namespace
@@ -414,13 +438,13 @@ int launch_linear_dec(const LinearArgs& a, hipStream_t s) {
             sa.l.residual = nullptr;
         }
         if (a.w.bits == 4) {
-            if (spg == 1) stream_rows<4, 1>(sa, s);
-            else if (spg == 2) stream_rows<4, 2>(sa, s);
-            else stream_rows<4, 4>(sa, s);
+            if (spg == 1) stream_launch<4, 1>(sa, s);
+            else if (spg == 2) stream_launch<4, 2>(sa, s);
+            else stream_launch<4, 4>(sa, s);
         } else {
-            if (spg == 1) stream_rows<2, 1>(sa, s);
-            else if (spg == 2) stream_rows<2, 2>(sa, s);
-            else stream_rows<2, 4>(sa, s);
+            if (spg == 1) stream_launch<2, 1>(sa, s);
+            else if (spg == 2) stream_launch<2, 2>(sa, s);
+            else stream_launch<2, 4>(sa, s);
         }
     }
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;

@@ -3,23 +3,25 @@
 //   forward    y[t][n]  = sum_k x[t][k]  w[n][k]
 //   gradient   dx[t][k] = sum_n dy[t][n] w[n][k]
 // Both operands are laid out once per call in blocks of 32 along the summed index,
-// [block][row][32], so that a stage of a tile is one contiguous run (rows a power
-// of two apart met in one L2 channel: 4096 x 8192 x 2048 took 1.08 times as long with
+// [block][part][row][32], so that a stage of a tile is one contiguous run a part (rows a
+// power of two apart met in one L2 channel: 4096 x 8192 x 2048 took 1.08 times as long with
 // 256-wide tiles, 1.27 times with 128-wide ones):
-//   B  the weights as fp16, rows n forward and, transposed, rows k for the gradient,
-//      each weight row n scaled by a power of two 2^en so that its largest possible
-//      |w| lies in [2^14, 2^15): no overflow, and 29 binades of full fp16 precision
-//      below a row's largest weight;
+//   B  the weights as two fp16 parts, the second what the first leaves out (2^-22 of a
+//      weight and less), rows n forward and, transposed, rows k for the gradient, each weight
+//      row n scaled by a power of two 2^en so that its largest possible |w| lies in
+//      [2^14, 2^15): no overflow, and 39 binades down to the parts' last bit;
 //   A  the activations (or dy, which also takes the weight rows' 2^-en) as fp16,
 //      each token's row scaled by 2^et into the same range.  bf16 values keep all
-//      their bits there.
-// Powers of two leave the significands alone, so the roundings are fp16's of the
-// weights (2^-11 of each, an eighth of the bf16 result's own step; fp32 results
-// take the weights as two fp16 parts, 2^-22), float32's in the sums, and the
-// result's; a float32 dy takes fp16's too (2^-11).  Laying the weights out costs one
-// pass over the codes and 2 bytes a weight written and read; a matrix is taken in
-// chunks of output columns, which bound the workspace.
+//      their bits there; a float32 dy takes two parts like the weights, laid out one
+//      behind the other, and its second is multiplied with the weights' first only.
+// Powers of two leave the significands alone, so what is rounded is 2^-22 of an operand,
+// the sums in float32, and the result.  (One part of the weights, 2^-11, took 123 us where two
+// take 199, but terms that cancel showed it, and bf16 results differed by 8e-4 from those of
+// float32 operands, now 6e-5.)
+// Laying the weights out costs one pass over the codes and 4 bytes a weight written and
+// read; a matrix is taken in chunks of output columns, which bound the workspace.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch_util.h"
 #include "linear.h"
@@ -39,12 +41,12 @@ constexpr int kMid = 16;                               // en of weights below 1/
 constexpr int kNone = 400;                             // exponent of zero rows: 2^-400 leaves no finite dy above 0
 constexpr int kStep = 32;                              // summed elements per block
 constexpr int kBlocks = 4;                             // rows are whole runs of this many blocks (zeros behind)
+constexpr int kParts = 2;                              // fp16 parts of a weight
 constexpr int kKeep = 4;                               // pieces of a row of A a thread keeps
 constexpr int kPrepGroups = 8;                         // 128-runs of K a workgroup lays out
-// Laid-out weights per chunk: past the 256 MB cache, for enough tiles in a chunk's GEMM
-// (1024 tokens, 28672 x 8192: 128 MB 680 us, 256 MB 626, 512 MB 601, 1 GB 610; gradient,
-// 49999 x 4096: 1257, 1299, 777, 782; 4096 tokens, 49999 x 4096 forward: 1847, 1872, 1875, 1874).
-constexpr size_t kChunkBytes = (size_t)512 << 20;
+// Laid-out weights per chunk, at most: past the 256 MB cache, for enough tiles in a chunk's
+// GEMM.  The chunks of a matrix are of like size.
+constexpr size_t kChunkBytes = (size_t)1 << 30;
 
 __host__ __device__ inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
@@ -61,6 +63,13 @@ __device__ __forceinline__ int scale_exponent(float top) {
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const half2_t v = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, v);
+}
+
+// a and b as fp16 in hi, and what that leaves out in lo.
+__device__ __forceinline__ void split_half(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_half(a, b);
+    const half2_t h = __builtin_bit_cast(half2_t, hi);
+    lo = pack_half(a - (float)h[0], b - (float)h[1]);
 }
 
 // |w|'s bound over a row's groups, taken by `lanes` threads that start at `first`.
@@ -92,22 +101,22 @@ struct PrepArgs {
     int64_t lda;
     int a_type;
     int T, len, kd;           // rows; elements of a row; kd: len rounded up (zeros behind)
-    uint16_t* ah;             // fp16 [kd / 32][T][32]
+    uint16_t* ah;             // fp16 [a_parts][kd / 32][T][32]
     int32_t* et;              // [T]
     int16_t* en;              // [N]
-    uint16_t* wh;             // fp16: forward [planes][K / 32][rows][32], gradient [kd / 32][columns][32]
+    uint16_t* wh;             // fp16 [K / 32][kParts][rows][32], gradient [kd / 32][kParts][columns][32]
     int c0, cn;               // this chunk's weight rows (forward) or 128-runs of K (gradient)
-    int planes;
     int a_blocks;             // workgroups that lay out A (the first ones); 0 in later chunks
     int a_rows;               // rows each: 1, or 4 (rows of at most 64 kKeep pieces: 3769 x 2240
-                              // x 256 24.6 us against 28.1, 4096 x 2048 x 2048 53.8 and 56.1)
+                              // x 256, one part, 24.6 us against 28.1, 4096 x 2048 x 2048 53.8 and 56.1)
 };
 
 // One row of A by LANES threads, a workgroup of 256 or a wave, in pieces of eight values:
 // the first LANES kKeep pieces stay in registers between the maximum and the rounding, the rest is read
 // twice.  dy's values take 2^(kMid - en) of their weight row.  Every thread's kKeep
 // loads are made whatever the row's length (past its whole pieces the last one again):
-// behind a branch each waited for the one before (4096 x 8192 of dy with its weights: 54 us against 46).
+// behind a branch each waited for the one before (4096 x 8192 of dy with its weights in one part: 54
+// us against 46).
 template <bool GRAD, bool F32, int LANES>
 __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
     constexpr int KEEP = kKeep, GROUP = LANES * KEEP, SIZE = F32 ? 4 : 2;
@@ -176,11 +185,12 @@ __device__ __forceinline__ void prep_a_row(const PrepArgs& p, int t) {
     const int e = scale_exponent(top);
     if (tid == 0) p.et[t] = GRAD ? e + kMid : e;
     auto put = [&](const float (&x)[8], int i) {
-        uint32_t o[4];
+        uint32_t o[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = pack_half(ldexpf(x[2 * j], e), ldexpf(x[2 * j + 1], e));
-        *reinterpret_cast<uint4*>(p.ah + ((size_t)(8 * i / kStep) * p.T + t) * kStep + (8 * i & (kStep - 1))) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; ++j) split_half(ldexpf(x[2 * j], e), ldexpf(x[2 * j + 1], e), o[j], lo[j]);
+        uint16_t* dst = p.ah + ((size_t)(8 * i / kStep) * p.T + t) * kStep + (8 * i & (kStep - 1));
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (F32) *reinterpret_cast<uint4*>(dst + (size_t)p.T * p.kd) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
     if (rest != 0 && tid == 0) put(tail, whole);
     for (int g = 0; g < groups; ++g) {
@@ -235,7 +245,6 @@ __global__ __launch_bounds__(256) void linear_prep_kernel(PrepArgs p) {
     if (r >= p.cn) return;
     const size_t n = (size_t)(p.c0 + r);
     const int e = ens[rr];
-    const size_t plane = (size_t)p.cn * p.w.K;
     const uint8_t* src = p.w.q + n * (16 * BITS);
     const size_t step = (size_t)p.w.N * (16 * BITS);
 #pragma unroll 4
@@ -244,17 +253,13 @@ __global__ __launch_bounds__(256) void linear_prep_kernel(PrepArgs p) {
         const int k0 = 128 * g + 8 * wi;
         const size_t at = n * ngs + (k0 >> gshift);
         const float s = ldexpf(f16_bits_to_f32(p.w.scale[at]), e), b = ldexpf(f16_bits_to_f32(p.w.bias[at]), e);
-        uint16_t* dst = p.wh + ((size_t)(k0 / kStep) * p.cn + r) * kStep + (k0 & (kStep - 1));
+        uint16_t* dst = p.wh + ((size_t)(k0 / kStep) * (kParts * p.cn) + r) * kStep + (k0 & (kStep - 1));
         uint32_t o[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float w0 = fmaf(word_code<BITS>(c, 2 * j), s, b), w1 = fmaf(word_code<BITS>(c, 2 * j + 1), s, b);
-            o[j] = pack_half(w0, w1);
-            const half2_t h = __builtin_bit_cast(half2_t, o[j]);
-            lo[j] = pack_half(w0 - (float)h[0], w1 - (float)h[1]);
-        }
+        for (int j = 0; j < 4; ++j)
+            split_half(fmaf(word_code<BITS>(c, 2 * j), s, b), fmaf(word_code<BITS>(c, 2 * j + 1), s, b), o[j], lo[j]);
         *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-        if (p.planes == 2) *reinterpret_cast<uint4*>(dst + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(dst + (size_t)p.cn * kStep) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -295,24 +300,25 @@ __global__ __launch_bounds__(256) void linear_grad_prep_kernel(PrepArgs p) {
         s[i] = in ? ldexpf(f16_bits_to_f32(p.w.scale[at]), e) : 0.f;
         b[i] = in ? ldexpf(f16_bits_to_f32(p.w.bias[at]), e) : 0.f;
     }
-    uint16_t* dst = p.wh + ((size_t)(n0 / kStep) * (128 * p.cn) + 128 * gl + 8 * wi) * kStep + (n0 & (kStep - 1));
+    uint16_t* dst = p.wh + ((size_t)(n0 / kStep) * (kParts * 128 * p.cn) + 128 * gl + 8 * wi) * kStep + (n0 & (kStep - 1));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        uint32_t o[4];
+        uint32_t o[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            o[i] = pack_half(fmaf(word_code<BITS>(c[2 * i], j), s[2 * i], b[2 * i]),
-                             fmaf(word_code<BITS>(c[2 * i + 1], j), s[2 * i + 1], b[2 * i + 1]));
+            split_half(fmaf(word_code<BITS>(c[2 * i], j), s[2 * i], b[2 * i]),
+                       fmaf(word_code<BITS>(c[2 * i + 1], j), s[2 * i + 1], b[2 * i + 1]), o[i], lo[i]);
         *reinterpret_cast<uint4*>(dst + j * kStep) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + (j + 128 * (size_t)p.cn) * kStep) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
 namespace {
 
 struct GemmArgs {
-    const uint16_t* A;        // fp16 [kd / 32][M][32]
-    const uint16_t* B;        // fp16 [planes][kd / 32][N][32]
-    int M, N, kd, planes;
+    const uint16_t* A;        // fp16 [a_parts][kd / 32][M][32]
+    const uint16_t* B;        // fp16 [kd / 32][kParts][N][32]
+    int M, N, kd, a_parts;
     const int32_t* et;        // [M]
     const int16_t* en;        // [N], or NULL (folded into A)
     const float* row_bias;    // [N] or NULL
@@ -357,23 +363,24 @@ __device__ __forceinline__ void put_results(const GemmArgs& p, int t, int n, flo
 
 }  // namespace
 
-// C = A B^T in tiles of 32 WM WR x 32 WN WC by WR x WC waves (each 32 WM x 32 WN on
+// C = A (B1 + B2)^T in tiles of 32 WM WR x 32 WN WC by WR x WC waves (each 32 WM x 32 WN on
 // v_mfma_f32_32x32x16_f16: A lane l holds row l % 32 and k = 8 (l / 32) + i, B the
 // same of a column; accumulator 4 j + i is row 8 j + 4 (l / 32) + i of column
-// l % 32).  Stages of KB blocks of 32 summed elements pass through a ring of STAGES
-// LDS slots by direct-to-LDS loads waited for by count; one barrier a stage.
+// l % 32).  Stages of KB blocks of 32 summed elements, A's rows and both parts of B's, pass
+// through a ring of STAGES LDS slots by direct-to-LDS loads waited for by count; one barrier
+// a stage.  A's operands are read once for both parts.
 // A row's 64 bytes of a block are four 16-byte pieces, piece c of row r at place
 // c ^ ((r >> 2) & 3): 16 rows read at one piece hit all banks once.  Workgroups
 // on one XCD take neighbouring tiles (8 rows of tiles at a time), which share
-// their operands in its L2.  4096 x 8192 x 2048 takes 123 us (1.12 PF; a library half
-// product 105), of which a tile's first loads and its stores, with nothing to multiply,
-// are 8.5 us a round: tiles taken in turn by one workgroup, the loads running on into the
-// next, took 131.
+// their operands in its L2.  4096 x 8192 x 2048 takes 199 us for both parts (1.38 PF, what a
+// large library product of halves reaches here).  Tiles taken in turn by one workgroup, the
+// loads running on into the next, were slower (131 us against 123 with one part).
 template <int WM, int WN, int WR, int WC, int STAGES, int KB>
 __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_gemm_kernel(GemmArgs p) {
     constexpr int BM = 32 * WM * WR, BN = 32 * WN * WC, WAVES = WR * WC;
-    constexpr int BLOCK = (BM + BN) * 2 * kStep, SLOT = KB * BLOCK;   // bytes
+    constexpr int BLOCK = (BM + kParts * BN) * 2 * kStep, SLOT = KB * BLOCK;   // bytes
     constexpr int LOADS = BLOCK / kDma / WAVES;                         // a wave's loads per block
+    static_assert(LOADS * kDma * WAVES == BLOCK, "whole loads");
     extern __shared__ __attribute__((aligned(16))) uint8_t slots[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN, tiles = tm * tn;
@@ -392,35 +399,38 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const int chunk = LOADS * wid + i, row = 16 * chunk + (lane >> 2);
-        const int r = 16 * chunk < BM ? min(m0 + row, p.M - 1) - m0 : min(n0 + row - BM, p.N - 1) - n0;
+        const int part = row < BM + BN ? 0 : 1;
+        const int r = 16 * chunk < BM ? min(m0 + row, p.M - 1) - m0
+                                      : min(n0 + row - BM - part * BN, p.N - 1) - n0 + part * p.N;
         off[i] = (uint32_t)r * (2 * kStep) + 16u * ((lane & 3) ^ ((row >> 2) & 3));
     }
-    // blocks [first, last) of the sum, of blocks1 a plane, in whole stages (kd is whole stages)
-    const int blocks1 = p.kd / kStep, stages = blocks1 * p.planes / KB, each = (stages + p.splits - 1) / p.splits;
+    // blocks [first, last) of the sum, of blocks1 a part of A, in whole stages (kd is whole stages)
+    const int blocks1 = p.kd / kStep, stages = blocks1 * p.a_parts / KB, each = (stages + p.splits - 1) / p.splits;
     const int steps = min(each, stages - (int)blockIdx.y * each), first = (int)blockIdx.y * each * KB, last = first + steps * KB;
-    const size_t strideA = (size_t)p.M * (2 * kStep), strideB = (size_t)p.N * (2 * kStep);   // bytes from block to block
-    const uint8_t* firstA = reinterpret_cast<const uint8_t*>(p.A + (size_t)m0 * kStep);
-    const uint8_t* srcA = firstA + (size_t)(first < blocks1 ? first : first - blocks1) * strideA;
-    const uint8_t* srcB = reinterpret_cast<const uint8_t*>(p.B + (size_t)n0 * kStep) + (size_t)first * strideB;
-    // The loads of a stage are made in its PARTS = 2 KB halves of a block, half of a block's
-    // LOADS each; the sources then move on to the next block (past the end: the last again).
-    constexpr int PARTS = 2 * KB, EACH = LOADS / 2;
-    static_assert(LOADS % 2 == 0, "halves");
+    const int both = max(0, min(steps, (blocks1 - first) / KB));   // stages of A's first part: with both of B's
+    const size_t strideA = (size_t)p.M * (2 * kStep), strideB = (size_t)p.N * (kParts * 2 * kStep);   // bytes from block to block
+    const uint8_t* firstB = reinterpret_cast<const uint8_t*>(p.B + (size_t)n0 * kStep);
+    const uint8_t* srcA = reinterpret_cast<const uint8_t*>(p.A + (size_t)m0 * kStep) + (size_t)first * strideA;
+    const uint8_t* srcB = firstB + (size_t)(first < blocks1 ? first : first - blocks1) * strideB;
+    // The loads of a stage are made in its HALVES = 2 KB halves of a block, half of a block's
+    // LOADS each (the first the odd one too); the sources then move on to the next block (past
+    // the end: the last again).
+    constexpr int HALVES = 2 * KB, ODD = LOADS / 2, EVEN = LOADS - ODD;
     int staged = first, slot_in = 0;                               // next block, slot it goes to
-    auto put = [&](int part, int i) {                              // load i of a half
-        uint8_t* slot = slots + slot_in * SLOT + (part >> 1) * BLOCK + LOADS * wid * kDma;
-        const int c = EACH * (part & 1) + i;
+    auto put = [&](int half, int i) {                              // load i of a half
+        uint8_t* slot = slots + slot_in * SLOT + (half >> 1) * BLOCK + LOADS * wid * kDma;
+        const int c = EVEN * (half & 1) + i;
         dma16_sv(16 * (LOADS * wid + c) < BM ? srcA : srcB, off[c], slot + c * kDma);
     };
-    auto put_done = [&](int part) {
-        if (part & 1) {
+    auto put_done = [&](int half) {
+        if (half & 1) {
             ++staged;
             if (staged < last) {
-                srcA = staged == blocks1 ? firstA : srcA + strideA;
-                srcB += strideB;
+                srcA += strideA;
+                srcB = staged == blocks1 ? firstB : srcB + strideB;
             }
         }
-        if (part == PARTS - 1) slot_in = slot_in + 1 < STAGES ? slot_in + 1 : 0;
+        if (half == HALVES - 1) slot_in = slot_in + 1 < STAGES ? slot_in + 1 : 0;
     };
     floatx16_t acc[WM][WN];
 #pragma unroll
@@ -431,7 +441,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
     const int wm = wid / WC, wn = wid % WC, m = lane & 31, h = lane >> 5;
     const int arow = 32 * WM * wm + m, brow = BM + 32 * WN * wn + m;
-    half8_t a[2][WM], b[2][WN];
+    half8_t a[2][WM], b[2][kParts][WN];
     auto read = [&](int half, int at) {                            // half a block of the stage in slot `at`
         const uint8_t* slot = slots + at * SLOT + (half >> 1) * BLOCK;
         const int kk = half & 1;
@@ -440,30 +450,34 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
         for (int i = 0; i < WM; ++i) a[kk][i] = *reinterpret_cast<const half8_t*>(slot + (arow + 32 * i) * 64 + place);
 #pragma unroll
-        for (int j = 0; j < WN; ++j) b[kk][j] = *reinterpret_cast<const half8_t*>(slot + (brow + 32 * j) * 64 + place);
+        for (int x = 0; x < kParts; ++x)
+#pragma unroll
+            for (int j = 0; j < WN; ++j) b[kk][x][j] = *reinterpret_cast<const half8_t*>(slot + (brow + BN * x + 32 * j) * 64 + place);
         asm volatile("" ::: "memory");                             // the reads stay here, ahead of the products
         __builtin_amdgcn_sched_barrier(0);
     };
     // Half a block's products, a load of a later stage after every few of them: the loads issue
     // while the matrix cores work (made together behind the barrier, they left them idle).
-    auto multiply = [&](int part) {
-        constexpr int N = WM * WN;
-        const int kk = part & 1;
+    auto multiply = [&](int half, auto parts) {
+        constexpr int P = decltype(parts)::value, N = WM * WN * P;
+        const int kk = half & 1, each = kk ? ODD : EVEN;
 #pragma unroll
-        for (int i = 0; i < WM; ++i)
+        for (int x = 0; x < P; ++x)
 #pragma unroll
-            for (int j = 0; j < WN; ++j) {
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[kk][i], b[kk][j], acc[i][j], 0, 0, 0);
-                const int n = i * WN + j;
+            for (int i = 0; i < WM; ++i)
 #pragma unroll
-                for (int c = 0; c < EACH; ++c)
-                    if (n == (N * c + N / 2) / EACH) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        put(part, c);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-            }
-        put_done(part);
+                for (int j = 0; j < WN; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[kk][i], b[kk][x][j], acc[i][j], 0, 0, 0);
+                    const int n = (x * WM + i) * WN + j;
+#pragma unroll
+                    for (int c = 0; c < each; ++c)
+                        if (n == (N * c + N / 2) / each) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            put(half, c);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                }
+        put_done(half);
     };
     // During stage s the loads of stage s + STAGES - 1 are made, into the slot that stage
     // s - 1 left at the barrier; one half of a block is read from LDS while the other is
@@ -471,28 +485,30 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     static_assert(STAGES >= 3, "a stage in flight behind the next one");
     for (int s = 0; s + 1 < STAGES; ++s)
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
+        for (int half = 0; half < HALVES; ++half) {
 #pragma unroll
-            for (int c = 0; c < EACH; ++c) put(part, c);
-            put_done(part);
+            for (int c = 0; c < ((half & 1) ? ODD : EVEN); ++c) put(half, c);
+            put_done(half);
         }
-    wait_vmem<(STAGES - 2) * PARTS * EACH>();
+    wait_vmem<(STAGES - 2) * KB * LOADS>();
     lds_barrier();
     int at = 0;
     read(0, 0);
-    for (int s = 0; s < steps; ++s) {
+    auto stage = [&](auto parts) {
 #pragma unroll
-        for (int part = 0; part + 1 < PARTS; ++part) {
-            read(part + 1, at);
-            multiply(part);
+        for (int half = 0; half + 1 < HALVES; ++half) {
+            read(half + 1, at);
+            multiply(half, parts);
         }
-        // this wave's part of stage s + 1 has arrived; then every wave's, and stage s is read
-        wait_vmem<((STAGES - 3) * PARTS + PARTS - 1) * EACH>();
+        // this wave's part of the next stage has arrived; then every wave's, and this one is read
+        wait_vmem<(STAGES - 2) * KB * LOADS - ODD>();
         lds_barrier();
         at = at + 1 < STAGES ? at + 1 : 0;
         read(0, at);                                               // (past the end: a stage never used)
-        multiply(PARTS - 1);
-    }
+        multiply(HALVES - 1, parts);
+    };
+    for (int s = 0; s < both; ++s) stage(std::integral_constant<int, kParts>{});
+    for (int s = both; s < steps; ++s) stage(std::integral_constant<int, 1>{});
     wait_vmem<0>();                                                // loads past the last stage, before their LDS is used again
     lds_barrier();
     // each wave turns its sums around in LDS, 32 rows at a time: rows of 32 WN results
@@ -589,7 +605,7 @@ void gemm_go(const GemmArgs& p, hipStream_t s) {
     static_assert(kBlocks % KB == 0, "stages are whole");
     const int tm = (p.M + BM - 1) / BM, tn = (p.N + BN - 1) / BN;
     const int blocks = ((tm * tn + 7) / 8) * 8;
-    const size_t lds = (size_t)STAGES * KB * (BM + BN) * 2 * kStep;
+    const size_t lds = (size_t)STAGES * KB * (BM + kParts * BN) * 2 * kStep;
     hipLaunchKernelGGL((linear_gemm_kernel<WM, WN, WR, WC, STAGES, KB>), dim3((unsigned)blocks, (unsigned)p.splits),
                        dim3(64 * WR * WC), lds, s, p);
 }
@@ -604,60 +620,65 @@ long split_results() { return 65536L * device_cus(); }
 struct Choice {
     Tile tile;
     int splits;               // of the sum
+    double us;                // estimated
 };
 
-// Tiles by the time their rounds over the CUs take, in hundredths of one round of 256 x
-// 256 tiles (about 115 us for a sum of 4096):
-//   256 x 256  100, one a CU;              256 x 128  56, one a CU;
-//   128 x 128  60, two a CU, 42 with one;  64 x 64  28, two a CU, 19 with one, whose ring
-//   takes all of the LDS (330 x 2048 x 4096: 28.0 us against 30.1 with half of it).
-// Whole calls with each of the four, us:
-//   4096 x 8192 x 2048  141 165 167 236    3000 x 4096 x 4096  121 134 124 178
-//   4096 x 5120 x 2048  121 116 106 154    4096 x 2048 x 8192  193 158 167 234
-//   1500 x 4096 x 4096  101  73  75  92     700 x 4096 x 4096   98  65  52  55
-//   1024 x 2048 x 2048   58  42  34  32     512 x 4096 x 4096    -   -  50  42
+// Tiles and splits by estimated time, fitted to 391 products (T 64 .. 8192, N 16 .. 60000, K 128
+// .. 12800, both directions) with every tile and up to eight numbers of splits each; taking
+// the least estimate costs 1.6 % over taking the fastest, 44 % at most.  A round of tiles
+// over the CUs takes, for a sum of 4096,
+//   256 x 256  168 us, one a CU;                   256 x 128  90, one a CU;
+//   128 x 128  107, two a CU, 55 with one;         64 x 64    41, two a CU, 17 with one,
+//   whose ring takes all of the LDS (200 x 2048 x 4096: 33 us against 37 with half of it);
+// a last round with few tiles up to a quarter less.  Whole calls with each of the four, us:
+//   4096 x 8192 x 2048  218 265 242 338    3000 x 4096 x 4096  184 217 186 245
+//   4096 x 5120 x 2048  183 176 153 209    4096 x 2048 x 8192  327 254 256 333
+//   1500 x 4096 x 4096  156 114 113 130     700 x 4096 x 4096  151 108  80  81
+//   1024 x 2048 x 2048   84  61  46  38     512 x 4096 x 4096  151 106  79  57
+//   6000 x 6000 x 1024  163 173 144 209     300 x 30000 x 1024  78  89  74  81
 // Long sums over few tiles are split, where the shorter sums gain more than the join takes
-// (a launch, and the partial sums written and read); without and with: gradient, 253 x
-// 24471 x 4736 286 187, 1024 x 49999 x 4096 764 655, 64 x 30000 x 256 100 30; forward
-// 64 x 128 x 8192 33 17, 4000 x 512 x 8192 80 82.
-Choice gemm_choice(int M, int N, int kd, int planes) {
+// (a launch, and the partial sums written and read).  Without and with two, three and six: 489 x
+// 18984 x 8960 627 586 529 542, gradient 649 x 27100 x 2944 (256 x 256) 1848 1113 843 521.
+Choice gemm_choice(int M, int N, int kd, int a_parts) {
     const long cus = device_cus();
-    const int sum = kd * planes;
+    const int sum = kd * a_parts;
     auto tiles = [&](int rows, int cols) { return (long)((M + rows - 1) / rows) * ((N + cols - 1) / cols); };
-    auto two_a_cu = [&](long t, int one, int two) {
+    auto one_a_cu = [&](long t, double start, double round, double less) {
+        const long rest = t % cus;
+        return t / cus * (start + round) + (rest ? start + round * (1 - less * (1 - (double)rest / cus)) : 0.);
+    };
+    auto two_a_cu = [&](long t, double one, double two) {
         const long rest = t % (2 * cus);
-        return t / (2 * cus) * two + (rest == 0 ? 0 : rest <= cus ? one : two);
+        return t / (2 * cus) * two + (rest == 0 ? 0. : rest <= cus ? one : one + (two - one) * (double)(rest - cus) / cus);
     };
     const long t[4] = {tiles(256, 256), tiles(256, 128), tiles(128, 128), tiles(64, 64)};
     const int stage[4] = {1, 1, 1, 2};                             // blocks
-    Choice best{k256x256, 1};
-    double least = 0.;
+    Choice best{k256x256, 1, 0.};
     for (int s = 1; s == 1 || (s <= kMaxSplits && s * 512 <= sum && t[2] < 2 * cus && (long)s * M * N <= split_results()); ++s) {
-        const double join = s == 1 ? 0. : 3.5 + 2.3e-6 * s * M * N;
-        const long cost[4] = {(t[0] * s + cus - 1) / cus * 100, (t[1] * s + cus - 1) / cus * 56, two_a_cu(t[2] * s, 42, 60),
-                              two_a_cu(t[3] * s, 19, 28)};
+        // (A's second part meets one of B's two)
+        const double join = s == 1 ? 0. : 5 + 1.2e-6 * s * M * N, k = kd / 4096. * (a_parts == 2 ? 1.5 : 1.) / s;
+        const double cost[4] = {one_a_cu(t[0] * s, 3.4, 168 * k, 0.26), one_a_cu(t[1] * s, 4.3, 90 * k, 0.19),
+                                two_a_cu(t[2] * s, 1.3 + 55 * k, 107 * k), two_a_cu(t[3] * s, 17 * k, 41 * k)};
         for (int i = 0; i < 4; ++i) {
-            // (fewer tiles than CUs run faster than their rounds say: a split has to promise a fifth)
-            const double us = (1.15 / 4096 * sum / s * (double)cost[i] + join) * (s == 1 ? 1. : 1.25);
-            if ((s > 1 || i > 0) && us >= least) continue;
-            least = us;
+            const double us = cost[i] + join;
+            if ((s > 1 || i > 0) && us >= best.us) continue;
             const bool one = i == 3 && t[3] * s <= cus;
             const int stages = sum / kStep / (one ? 4 : stage[i]), each = (stages + s - 1) / s;
-            best = Choice{one ? k64One : (Tile)i, (stages + each - 1) / each};   // (no split without a stage)
+            best = Choice{one ? k64One : (Tile)i, (stages + each - 1) / each, us};   // (no split without a stage)
         }
     }
     return best;
 }
 
 void gemm(GemmArgs p, hipStream_t s) {
-    const Choice c = gemm_choice(p.M, p.N, p.kd, p.planes);
+    const Choice c = gemm_choice(p.M, p.N, p.kd, p.a_parts);
     p.splits = c.splits;
     switch (c.tile) {
     case k256x256: gemm_go<4, 2, 2, 4, 3, 1>(p, s); break;
-    case k256x128: gemm_go<4, 2, 2, 2, 6, 1>(p, s); break;
-    case k128: gemm_go<2, 2, 2, 2, 4, 1>(p, s); break;
-    case k64: gemm_go<1, 1, 2, 2, 4, 2>(p, s); break;
-    case k64One: gemm_go<1, 1, 2, 2, 4, 4>(p, s); break;
+    case k256x128: gemm_go<4, 2, 2, 2, 4, 1>(p, s); break;
+    case k128: gemm_go<2, 2, 2, 2, 3, 1>(p, s); break;
+    case k64: gemm_go<1, 1, 2, 2, 3, 2>(p, s); break;
+    case k64One: gemm_go<1, 1, 2, 2, 3, 4>(p, s); break;
     }
     if (p.splits > 1) {
         const long threads = (long)p.M * ((p.N + 7) / 8);
@@ -669,27 +690,28 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Workspace: A, et, en, the chunk's weights, then the splits' sums.
 struct Plan {
-    int kd, planes, chunk, total;          // chunk: weight rows (forward) or 128-runs (gradient) per GEMM
+    int kd, a_parts, chunk, total;         // chunk: weight rows (forward) or 128-runs (gradient) per GEMM
     size_t et, en, wh, part, bytes;
 };
 
 Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
     Plan p{};
     p.kd = grad ? round_up(w.N, kStep * kBlocks) : w.K;
-    p.planes = !grad && type == MOE_F32 ? 2 : 1;
+    p.a_parts = grad && type == MOE_F32 ? 2 : 1;
     p.total = grad ? w.K / 128 : w.N;
-    const size_t unit = grad ? (size_t)256 * p.kd : (size_t)2 * p.kd * p.planes;       // bytes
+    const size_t unit = (size_t)2 * kParts * p.kd * (grad ? 128 : 1);                  // bytes
     size_t c = kChunkBytes / unit;
-    const size_t least = grad ? 2 : 256;                                             // a tile's worth
-    c = c < least ? least : c;
-    p.chunk = (size_t)p.total < c ? p.total : (int)c;
-    p.et = align256((size_t)T * p.kd * 2);
+    const int tile = grad ? 2 : 256;                                                 // a tile's worth
+    const int most = c < (size_t)tile ? tile : c > (size_t)p.total ? p.total : (int)c / tile * tile;
+    const int chunks = (p.total + most - 1) / most;
+    p.chunk = std::min(round_up((p.total + chunks - 1) / chunks, tile), p.total);
+    p.et = align256((size_t)T * p.kd * 2 * p.a_parts);
     p.en = p.et + align256((size_t)T * 4);
     p.wh = p.en + align256((size_t)w.N * 2);
     p.part = p.wh + align256(unit * p.chunk);
     // (for any number of splits, so that more tokens never need less)
     const long results = (long)T * (grad ? 128 * p.chunk : p.chunk);
-    p.bytes = p.part + (p.kd * p.planes < 1024 ? 0 : align256(std::min(kMaxSplits * results, split_results()) * sizeof(float)));
+    p.bytes = p.part + (p.kd * p.a_parts < 1024 ? 0 : align256(std::min(kMaxSplits * results, split_results()) * sizeof(float)));
     return p;
 }
 
@@ -697,6 +719,18 @@ Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
 
 size_t linear_gemm_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad) {
     return plan_of(w, T, type, grad).bytes;
+}
+
+// The layouts' bytes, then the products.
+double linear_gemm_us(const moe_qmatrix& w, int T, int type, bool grad, double limit) {
+    const double N = w.N, K = w.K, wide = type == MOE_F32 ? 4 : 2, matrix = N * K * (2 * kParts + w.bits / 8.);   // bytes
+    double us = grad ? 11.9 + 0.351e-6 * matrix + 0.363e-6 * T * N * (wide + wide) + 0.414e-6 * T * K * 2
+                     : 8.8 + 0.4e-3 * K + 0.305e-6 * matrix + 0.278e-6 * T * K * 4 + 0.289e-6 * T * N * wide;
+    if (us >= limit) return us;
+    const Plan p = plan_of(w, T, type, grad);
+    for (int c0 = 0; c0 < p.total && us < limit; c0 += p.chunk)
+        us += gemm_choice(T, std::min(p.chunk, p.total - c0) * (grad ? 128 : 1), p.kd, p.a_parts).us;
+    return us;
 }
 
 int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
@@ -708,7 +742,6 @@ int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
     p.et = reinterpret_cast<int32_t*>(ws + pl.et);
     p.en = reinterpret_cast<int16_t*>(ws + pl.en);
     p.wh = reinterpret_cast<uint16_t*>(ws + pl.wh);
-    p.planes = pl.planes;
     for (int c0 = 0; c0 < pl.total; c0 += pl.chunk) {
         p.c0 = c0;
         p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
@@ -720,7 +753,7 @@ int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
         else hipLaunchKernelGGL(linear_prep_kernel<2>, grid, dim3(256), 0, s, p);
         GemmArgs g{};
         g.part = reinterpret_cast<float*>(ws + pl.part);
-        g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = p.cn; g.kd = pl.kd; g.planes = pl.planes; g.et = p.et; g.en = p.en + c0;
+        g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = p.cn; g.kd = pl.kd; g.a_parts = 1; g.et = p.et; g.en = p.en + c0;
         g.row_bias = a.row_bias ? a.row_bias + c0 : nullptr;
         g.residual = a.residual ? a.residual + c0 : nullptr;
         g.ldr = a.ldr; g.ldy = a.ldy; g.y_type = a.y_type;
@@ -740,7 +773,6 @@ int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
     p.et = reinterpret_cast<int32_t*>(ws + pl.et);
     p.en = reinterpret_cast<int16_t*>(ws + pl.en);
     p.wh = reinterpret_cast<uint16_t*>(ws + pl.wh);
-    p.planes = 1;
     const dim3 rows((unsigned)((a.w.N + 15) / 16));
     if (a.w.bits == 4) hipLaunchKernelGGL(linear_rows_kernel<4>, rows, dim3(256), 0, s, p);
     else hipLaunchKernelGGL(linear_rows_kernel<2>, rows, dim3(256), 0, s, p);
@@ -754,7 +786,7 @@ int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
         else hipLaunchKernelGGL(linear_grad_prep_kernel<2>, grid, dim3(256), 0, s, p);
         GemmArgs g{};
         g.part = reinterpret_cast<float*>(ws + pl.part);
-        g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = 128 * p.cn; g.kd = pl.kd; g.planes = 1; g.et = p.et;
+        g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = 128 * p.cn; g.kd = pl.kd; g.a_parts = pl.a_parts; g.et = p.et;
         g.ldy = a.lddx; g.y_type = MOE_BF16; g.y = a.dx + 128 * (size_t)c0;
         gemm(g, s);
     }

@@ -24,6 +24,7 @@
 // Bound by latency where a wave has few rounds (1 token, 4096 x 4096 at 4 bits: 7.2 us;
 // 37 tokens, 5111 x 2048 at 2 bits, groups of 64: 11.5), by the code stream past that
 // (8 tokens, 49999 x 4096: 36 us, 3.0 TB/s of the bytes that have to move).
+#include <algorithm>
 #include <type_traits>
 
 #include "launch_util.h"
@@ -272,8 +273,6 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
     }
 }
 
-namespace {
-
 // Splits of the weight rows, whole rounds of rows each: one workgroup a CU (4096 x
 // 4096, 1 token: 7.6 us; half as many 7.9, twice 9.2; 49999 x 4096, 8 tokens: 36, 58,
 // 39), rounded up where a CU holds two (SPG = 1), else down (3 x 96 workgroups took
@@ -292,7 +291,13 @@ int grad_splits(const moe_qmatrix& w, int T) {
     return (rounds + per - 1) / per;
 }
 
-}  // namespace
+// A CU's rounds of weight rows, and its workgroups' starts and ends.
+double linear_grad_dec_us(const moe_qmatrix& w, int T) {
+    static const double c[3][3] = {{4.7, 1.3, 0.4}, {4.5, 1.95, 0.9}, {4.4, 3.3, 0.45}};   // groups of 128, 64, 32
+    const double* f = c[w.group_size == 128 ? 0 : w.group_size == 64 ? 1 : 2];
+    const double per_cu = (double)(w.K / 128) * ((T + kTok - 1) / kTok) / device_cus(), rounds = (w.N + kRound - 1) / kRound;
+    return f[0] + f[1] * std::max(1.0, per_cu * rounds) + f[2] * per_cu;
+}
 
 size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T) {
     const int s = grad_splits(w, T);

@@ -1,9 +1,10 @@
-"""Gradients past a quantised matrix whose terms cancel: what is left shows the bits that the
+"""Dense quantised products whose terms cancel: what is left shows the bits that the
 operands were carried with, whichever kernels the sizes take.
 
 Only m terms of each sum differ from 0 (adding zeros rounds nothing), so the bound is
 that of weights_ref.py for a sum of m terms without any rounding of the operands:
-(m + 16) U32 of the terms' magnitudes, then half a step of the result's type.
+(m + 16) U32 of the terms' magnitudes, then half a step of the result's type.  The 16
+hold what a weight or a float32 dy may leave out, 2^-22 or 4 U32 of a term each.
 """
 import numpy as np
 import pytest
@@ -15,7 +16,8 @@ import weights_ref as ref
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
-SIZES = [(3, 90, 256), (40, 90, 256), (1, 24, 16384)]
+# few tokens, many, and one token with a long K and few rows (which the estimates give to the laid-out product)
+SIZES = [(3, 90, 256), (40, 90, 256), (1, 24, 32768), (1000, 2500, 640), (3000, 700, 1152)]
 
 
 def pack(codes, bits):
@@ -50,6 +52,34 @@ def check(got, want, terms, m, f32, what):
         bound = bound + ref.HALF_BF16 * (np.abs(want) + bound)
     worst = float(np.max(np.abs(got.double().cpu().numpy() - want) / (bound + 1e-37)))
     assert worst <= 1.0, f"{what}: {worst:.3g} times the bound"
+
+
+@pytest.mark.parametrize("bits,group", [(4, 128), (4, 32), (2, 64)])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,N,K", SIZES)
+def test_forward(T, N, K, f32, bits, group):
+    """a (w1 + w2 - w3 - w4), the four weights of one group with equal sums of codes: exactly 0."""
+    rng = np.random.default_rng(T + bits)
+    codes = rng.integers(0, 1 << bits, (N, K))
+    x = np.zeros((T, K), np.float32)
+    for g in range(K // group):                          # columns g G .. g G + 3 of every group
+        at = g * group
+        codes[:, at + 2] = rng.integers(0, 1 << bits, N)
+        total = codes[:, at] + codes[:, at + 1]
+        top = (1 << bits) - 1
+        codes[:, at + 2] = np.clip(codes[:, at + 2], np.maximum(total - top, 0), np.minimum(total, top))
+        codes[:, at + 3] = total - codes[:, at + 2]
+    s = scales(rng, N, K // group)
+    b = (-rng.uniform(0, 9, s.shape) * s.astype(np.float32)).astype(np.float16)
+    m = Matrix(codes, s, b, bits, group)
+    a = ref.bf16_round(rng.standard_normal(T).astype(np.float32))
+    at = group * rng.integers(0, K // group, T)
+    for i, sign in enumerate((1, 1, -1, -1)):
+        x[np.arange(T), at + i] = sign * a
+    y = torch.empty(T, N, dtype=torch.float32 if f32 else torch.bfloat16, device=DEV)
+    moe.linear(m.q, dev(x, torch.bfloat16), y, moe.LinearBuffers.allocate(m.q, T, y.dtype))
+    want = x.astype(np.float64) @ m.W.T
+    check(y, want, np.abs(x).astype(np.float64) @ m.mag.T, 4, f32, "forward")
 
 
 @pytest.mark.parametrize("bits,group", [(4, 128), (4, 32), (2, 64)])
