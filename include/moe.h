@@ -532,6 +532,22 @@ typedef struct moe_qmatrix {
  * between calls is scratch. */
 int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int grad, size_t* bytes);
 
+/* Which kernels a call of exactly T tokens takes, for tests and measurements
+ * (host-only; the matrix' pointers are not used).  kernels int32 [8] (host), zeros
+ * where not said:
+ *   [0]  MOE_LINEAR_STREAMED, MOE_LINEAR_LAID_OUT, or 0 (T = 0: none)
+ *   streamed, moe_linear:       [1] tokens / 16 and [2] weight rows / 16 of a tile,
+ *                               [3] 128-runs of K a wave, [4] tiles requested
+ *                               ahead, [5] launches ([1] .. [4]: the first one's)
+ *   streamed, moe_linear_grad:  [1] workgroups that share a run's weight rows
+ *   laid out:                   [1] rows and [2] columns of a tile, [3] splits of
+ *                               the sum, [4] 32-element blocks a stage, [5] chunks
+ *                               of the matrix ([1] .. [4]: the first one's), [6]
+ *                               fp16 parts of x or dy */
+#define MOE_LINEAR_STREAMED 1
+#define MOE_LINEAR_LAID_OUT 2
+int moe_linear_kernels(const moe_qmatrix* w, int32_t T, int type, int grad, int32_t* kernels);
+
 /* y[t][n] = sum_k x[t][k] w[n][k] (+ row_bias[n]) (+ residual[t][n]), sums in
  * float32, rounded once to y's type (nearest, ties to even).
  *   x          bf16 [T] rows of K elements, ldx elements apart; 16-byte aligned,

@@ -33,7 +33,7 @@ EXPORTS = (
     "moe_combine", "moe_combine_shared",
     "moe_zero_point_bias", "moe_stream_read",
     "moe_route_counts", "moe_hot_set", "moe_residency_plan", "moe_expert_copy",
-    "moe_linear_workspace_bytes", "moe_linear", "moe_linear_grad",
+    "moe_linear_workspace_bytes", "moe_linear_kernels", "moe_linear", "moe_linear_grad",
     "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward", "moe_combine_backward",
 )
 
@@ -118,6 +118,7 @@ def lib() -> ctypes.CDLL:
     L.moe_expert_copy.argtypes = [Dp, ctypes.c_int, Wp, Wp, i32, P, P, i32, P]
     Mp, i64 = ctypes.POINTER(QMatrixC), ctypes.c_int64
     L.moe_linear_workspace_bytes.argtypes = [Mp, i32, ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)]
+    L.moe_linear_kernels.argtypes = [Mp, i32, ctypes.c_int, ctypes.c_int, ctypes.POINTER(i32)]
     L.moe_linear.argtypes = [Mp, i32, P, i64, P, P, i64, P, i64, ctypes.c_int, P, sz, P]
     L.moe_linear_grad.argtypes = [Mp, i32, P, i64, ctypes.c_int, P, i64, P, sz, P, P]
     L.moe_balance_workspace_bytes.argtypes = [Dp, ctypes.POINTER(sz)]
@@ -483,6 +484,17 @@ def linear_workspace_bytes(w: QMatrix, T: int, dtype, grad: bool = False) -> int
     return int(out.value)
 
 
+LINEAR_STREAMED, LINEAR_LAID_OUT = 1, 2      # MOE_LINEAR_STREAMED, MOE_LINEAR_LAID_OUT
+
+
+def linear_kernels(w: QMatrix, T: int, dtype, grad: bool = False) -> tuple:
+    """moe_linear_kernels: which kernels a call of exactly T tokens takes (8 numbers); dtype
+    as for linear_workspace_bytes."""
+    out = (ctypes.c_int32 * 8)()
+    _check(lib().moe_linear_kernels(w._ref, int(T), _element_type(dtype), int(bool(grad)), out))
+    return tuple(out)
+
+
 @dataclass
 class LinearBuffers:
     """What linear() or linear_grad() need beside their operands, for calls with
@@ -627,7 +639,7 @@ __all__ = [
     "topk_from_logits", "slot_lookup", "permute", "expert_ffn_q4",
     "expert_ffn_q2", "expert_gateup", "expert_down", "expert_ffn_fused", "expert_ffn_fused_shared", "expert_ffn_fused_noalloc", "NOALLOC_WORKSPACE_BYTES", "combine", "combine_shared", "zero_point_bias", "stream_read", "STREAM_SINK_INTS", "route_counts", "hot_set", "residency_plan",
     "expert_copy", "RESIDENCY_LISTS", "ResidencyC", "LayerBuffers", "ResidentExperts", "resident_layer_forward", "SharedBuffers", "SharedExpert", "layer_forward", "StackLayer", "stack_forward", "EXPORTS",
-    "QMatrix", "LinearBuffers", "linear", "linear_grad", "linear_workspace_bytes", "LINEAR_SYNC_INTS", "BF16", "F32",
+    "QMatrix", "LinearBuffers", "linear", "linear_grad", "linear_workspace_bytes", "linear_kernels", "LINEAR_STREAMED", "LINEAR_LAID_OUT", "LINEAR_SYNC_INTS", "BF16", "F32",
     "BalanceBuffers", "balance_loss", "balance_workspace_bytes", "BALANCE_SYNC_INTS", "route_backward", "combine_backward",
     "RouterGradBuffers", "router_losses", "router_backward",
     "group_major", "ALGO_AUTO", "ALGO_GEMV", "ALGO_MFMA", "ALGO_GEMM", "OP_ROUTE", "OP_LOOKUP", "OP_PERMUTE", "OP_FFN", "OP_COMBINE",

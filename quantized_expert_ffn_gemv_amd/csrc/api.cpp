@@ -653,6 +653,16 @@ int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int gr
     return ok();
 }
 
+int moe_linear_kernels(const moe_qmatrix* w, int32_t T, int type, int grad, int32_t* kernels) {
+    const char* fn = "moe_linear_kernels";
+    if (kernels == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: kernels is NULL", fn);
+    const int st = check_qmatrix(fn, w, T, type, false);
+    if (st) return st;
+    std::memset(kernels, 0, 8 * sizeof(int32_t));
+    if (T > 0) moe::linear_kernels(*w, T, type, grad != 0, kernels);
+    return ok();
+}
+
 int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, const float* row_bias,
                const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int y_type, void* ws, size_t ws_bytes,
                void* stream) {

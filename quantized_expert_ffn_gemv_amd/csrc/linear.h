@@ -34,6 +34,8 @@ struct LinearGradArgs {
 // Workspace of a call of T tokens, and of all calls of 1 .. T tokens.
 size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
 size_t linear_workspace_bytes_up_to(const moe_qmatrix& w, int T, int type, bool grad);
+// moe_linear_kernels' answer, for T > 0.
+void linear_kernels(const moe_qmatrix& w, int T, int type, bool grad, int32_t* kernels);
 int launch_linear(const LinearArgs& a, hipStream_t s);
 int launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
 // The codes streamed (linear_dec.hip): any T, the matrix read once per 16 or 32 tokens.
@@ -45,6 +47,7 @@ struct StreamForm {
 };
 StreamForm stream_form(const moe_qmatrix& w, int T, int runs);
 size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T);
+void linear_dec_kernels(const moe_qmatrix& w, int T, int32_t* kernels);
 int launch_linear_dec(const LinearArgs& a, hipStream_t s);
 // Input gradient, the codes streamed (linear_grad_dec.hip).
 int grad_splits(const moe_qmatrix& w, int T);
@@ -52,6 +55,7 @@ size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T);
 int launch_linear_grad_dec(const LinearGradArgs& a, hipStream_t s);
 // Both operands laid out for a dense product (linear_gemm.hip).
 size_t linear_gemm_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);
+void linear_gemm_kernels(const moe_qmatrix& w, int T, int type, bool grad, int32_t* kernels);
 int launch_linear_gemm(const LinearArgs& a, hipStream_t s);
 int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s);
 

@@ -41,6 +41,17 @@ size_t linear_workspace_bytes_up_to(const moe_qmatrix& w, int T, int type, bool 
     return most;
 }
 
+void linear_kernels(const moe_qmatrix& w, int T, int type, bool grad, int32_t* kernels) {
+    if (!streams(w, T, type, grad)) {
+        kernels[0] = MOE_LINEAR_LAID_OUT;
+        linear_gemm_kernels(w, T, type, grad, kernels);
+        return;
+    }
+    kernels[0] = MOE_LINEAR_STREAMED;
+    if (grad) kernels[1] = grad_splits(w, T);
+    else linear_dec_kernels(w, T, kernels);
+}
+
 int launch_linear(const LinearArgs& a, hipStream_t s) {
     return streams(a.w, a.T, a.y_type, false) ? launch_linear_dec(a, s) : launch_linear_gemm(a, s);
 }

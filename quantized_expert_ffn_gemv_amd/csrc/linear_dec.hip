@@ -423,6 +423,16 @@ size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T) {
     return w.K / 128 > kStreamGroups ? (size_t)T * w.N * sizeof(float) : 0;
 }
 
+void linear_dec_kernels(const moe_qmatrix& w, int T, int32_t* kernels) {
+    const int runs = w.K / 128;
+    const StreamForm f = stream_form(w, T, std::min(runs, kStreamGroups));
+    kernels[1] = f.nt;
+    kernels[2] = f.rt;
+    kernels[3] = f.gpw;
+    kernels[4] = f.rbu;
+    kernels[5] = (runs + kStreamGroups - 1) / kStreamGroups;
+}
+
 // K beyond what a workgroup's registers hold is taken in several launches, each
 // adding to the sums that the last one left in the workspace.
 int launch_linear_dec(const LinearArgs& a, hipStream_t s) {

@@ -733,6 +733,18 @@ double linear_gemm_us(const moe_qmatrix& w, int T, int type, bool grad, double l
     return us;
 }
 
+void linear_gemm_kernels(const moe_qmatrix& w, int T, int type, bool grad, int32_t* kernels) {
+    static const int32_t shape[][3] = {{256, 256, 1}, {256, 128, 1}, {128, 128, 1}, {64, 64, 2}, {64, 64, 4}};   // by Tile
+    const Plan p = plan_of(w, T, type, grad);
+    const Choice c = gemm_choice(T, p.chunk * (grad ? 128 : 1), p.kd, p.a_parts);
+    kernels[1] = shape[c.tile][0];
+    kernels[2] = shape[c.tile][1];
+    kernels[3] = c.splits;
+    kernels[4] = shape[c.tile][2];
+    kernels[5] = (p.total + p.chunk - 1) / p.chunk;
+    kernels[6] = p.a_parts;
+}
+
 int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
     const Plan pl = plan_of(a.w, a.T, a.y_type, false);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
