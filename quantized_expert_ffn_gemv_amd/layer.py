@@ -73,6 +73,7 @@ class LayerBuffers:
     sync: torch.Tensor            # int32 [DISPATCH_SYNC_INTS], zeros (route_dispatch's counters)
     ffn_sync: torch.Tensor        # int32 [FFN_SYNC_INTS], zeros (expert_ffn_fused's counters)
     shared_rows: bool = False     # y_rows and workspace also hold a shared expert's T rows
+    renormalize: Optional[bool] = None   # how the last layer step on these buffers made topk_w (None: no step yet)
 
     def ffn_timed_out(self) -> bool:
         """True if an expert_ffn_fused call on these buffers had a down item give
@@ -172,6 +173,7 @@ def layer_forward(buf: LayerBuffers, x: torch.Tensor, w_router: torch.Tensor,
             raise ValueError("shared expert needs SharedBuffers allocated for this T, H and its I")
         expert_ffn_fused(sb.d, shared.weights.bits, x, sb.buf.work_list, sb.buf.n_work, shared.weights,
                          sb.buf.workspace, sb.buf.y_rows, sb.buf.ffn_sync, algo, stream)
+    buf.renormalize = bool(renormalize)
     if fused:
         route_dispatch(d, x, w_router, router_bias, renormalize, buf.logits, buf.topk_ids, buf.topk_w,
                        slot_of_expert, n_slots, buf.pair_slot, buf.miss, buf.n_miss, buf.counts, buf.offsets,
@@ -215,6 +217,7 @@ class RouterGradBuffers:
     topk_w_grad: torch.Tensor     # float32 [T, k]
     logits_grad: torch.Tensor     # float32 [T, E]
     scratch: BalanceBuffers
+    counted: bool = False         # counts and n_valid are set (by router_losses())
 
     @staticmethod
     def allocate(d: Dims, device="cuda") -> "RouterGradBuffers":
@@ -233,19 +236,30 @@ def router_losses(buf: LayerBuffers, grads: RouterGradBuffers, valid: Optional[t
     padded tokens.  Returns grads.losses (on the GPU)."""
     balance_loss(buf.d, buf.logits, buf.topk_ids, grads.counts, grads.prob_mean, grads.n_valid, grads.losses,
                  grads.scratch, valid, stream)
+    grads.counted = True
     return grads.losses
 
 
 def router_backward(buf: LayerBuffers, grads: RouterGradBuffers, out_grad: torch.Tensor,
                     losses_grad: Optional[torch.Tensor] = None, valid: Optional[torch.Tensor] = None,
-                    y_rows_grad: Optional[torch.Tensor] = None, renormalize: bool = True, stream=None) -> torch.Tensor:
+                    y_rows_grad: Optional[torch.Tensor] = None, renormalize: Optional[bool] = None,
+                    stream=None) -> torch.Tensor:
     """The way back through a layer step on `buf` to its logits, from out_grad
     (bf16 [T, H]; also the residual's gradient) and losses_grad (float32 [2] on
-    the GPU, the gradients of router_losses()'s two losses, with the same valid).
+    the GPU, the gradients of router_losses()'s two losses, with the same valid;
+    refused before router_losses() has set the counts).  renormalize: None for the
+    step's own (True where no layer step has run on `buf`, as after the routing
+    calls alone); another value than the step's is refused.
     The gates of a shared expert's step are unchanged by it, so this holds for
     such a step too.  y_rows_grad: None, or bf16 [T*k, H] for the gradient of the
     expert rows.  Returns grads.logits_grad; the router weight's gradient is
     logits_grad^T x and its bias' the sum of logits_grad over the tokens."""
+    if losses_grad is not None and not grads.counted:
+        raise ValueError("the losses' gradient needs the counts of router_losses()")
+    if renormalize is None:
+        renormalize = buf.renormalize is not False
+    elif buf.renormalize is not None and bool(renormalize) != buf.renormalize:
+        raise ValueError(f"the step's gates were made with renormalize={buf.renormalize}")
     combine_backward(buf.d, out_grad, buf.y_rows, buf.pair_to_row, buf.topk_w, grads.topk_w_grad, y_rows_grad, stream)
     route_backward(buf.d, buf.logits, buf.topk_ids, buf.topk_w, renormalize, grads.logits_grad, grads.topk_w_grad,
                    losses_grad, grads.counts, grads.n_valid, valid, stream)
@@ -355,6 +369,7 @@ def resident_layer_forward(buf: LayerBuffers, res: ResidentExperts, x: torch.Ten
     import torch as _t
     d = buf.d
     main = _t.cuda.current_stream() if copy_stream is not None else None
+    buf.renormalize = True
     route_dispatch(d, x, w_router, router_bias, True, buf.logits, buf.topk_ids, buf.topk_w, res.slot_of_expert,
                    res.n_slots, buf.pair_slot, buf.miss, buf.n_miss, buf.counts, buf.offsets, buf.sorted_pairs,
                    buf.pair_to_row, buf.active, buf.n_active, buf.work_list, buf.n_work, host_doorbell,
