@@ -555,6 +555,7 @@ int moe_linear_kernels(const moe_qmatrix* w, int32_t T, int type, int grad, int3
  *   row_bias   float32 [N] or NULL
  *   residual   bf16 [T] rows of N elements, ldr >= N apart, or NULL; may be y
  *              itself (bf16, ldr == ldy), else y overlaps no input
+ *              (refused; column slices of one buffer do not overlap)
  *   y          bf16 or float32 (y_type) [T] rows of N elements, ldy >= N apart
  *   workspace  moe_linear_workspace_bytes(w, T, y_type, 0), 256-byte aligned
  *              (NULL where that is 0)
@@ -577,7 +578,7 @@ int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, 
  *   dy         bf16 or float32 (dy_type) [T] rows of N elements, lddy >= N
  *              elements apart, aligned to its element
  *   dx         bf16 [T] rows of K elements, lddx apart; 16-byte aligned, lddx >=
- *              K a multiple of 8; overlaps no input
+ *              K a multiple of 8; overlaps no input (refused for dy)
  *   workspace  moe_linear_workspace_bytes(w, T, dy_type, 1), 256-byte aligned
  *   sync       int32 [MOE_LINEAR_SYNC_INTS] device memory, 256-byte aligned,
  *              holding zeros before the first call; each call leaves it zero.

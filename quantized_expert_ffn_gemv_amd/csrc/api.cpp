@@ -168,6 +168,17 @@ int check_qmatrix(const char* fn, const moe_qmatrix* w, int32_t T, int type, boo
     return MOE_OK;
 }
 
+// Whether T rows of wa and wb bytes, la and lb bytes apart, share a byte.  Rows of one
+// stride are compared exactly (column slices of one buffer share none), others by their
+// whole extents.
+bool rows_meet(const void* a, int64_t la, int64_t wa, const void* b, int64_t lb, int64_t wb, int32_t T) {
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));   // where b starts in a
+    if (d >= (T - 1) * la + wa || -d >= (T - 1) * lb + wb) return false;
+    if (la != lb || T == 1) return true;
+    const int64_t off = (d % la + la) % la;                       // b's columns within a's rows
+    return off < wa || off + wb > la;
+}
+
 int check_linear_workspace(const char* fn, const moe_qmatrix* w, int32_t T, int type, bool grad, const void* ws,
                            size_t ws_bytes) {
     const size_t need = moe::linear_workspace_bytes(*w, T, type, grad);
@@ -683,6 +694,11 @@ int moe_linear(const moe_qmatrix* w, int32_t T, const uint16_t* x, int64_t ldx, 
         return fail(MOE_ERR_INVALID_ARG, "%s: y is the residual but differs from it in type or row stride", fn);
     st = check_linear_workspace(fn, w, T, y_type, false, ws, ws_bytes);
     if (st) return st;
+    const int64_t e = y_type == MOE_F32 ? 4 : 2, wy = e * w->N;
+    if (rows_meet(y, e * ldy, wy, x, 2 * ldx, 2 * (int64_t)w->K, T) ||
+        (residual && residual != y && rows_meet(y, e * ldy, wy, residual, 2 * ldr, 2 * (int64_t)w->N, T)) ||
+        (row_bias && rows_meet(y, (T - 1) * e * ldy + wy, (T - 1) * e * ldy + wy, row_bias, 4 * (int64_t)w->N, 4 * (int64_t)w->N, 1)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
     moe::LinearArgs a{};
     a.w = *w; a.T = T; a.x = x; a.ldx = ldx; a.row_bias = row_bias; a.residual = residual; a.ldr = ldr;
     a.y = y; a.ldy = ldy; a.y_type = y_type; a.ws = ws;
@@ -705,6 +721,9 @@ int moe_linear_grad(const moe_qmatrix* w, int32_t T, const void* dy, int64_t ldd
     REQUIRE_PTR(sync, 256);
     st = check_linear_workspace(fn, w, T, dy_type, true, ws, ws_bytes);
     if (st) return st;
+    const int64_t e = dy_type == MOE_F32 ? 4 : 2;
+    if (rows_meet(dx, 2 * lddx, 2 * (int64_t)w->K, dy, e * lddy, e * w->N, T))
+        return fail(MOE_ERR_INVALID_ARG, "%s: dx overlaps dy", fn);
     moe::LinearGradArgs a{};
     a.w = *w; a.T = T; a.dy = dy; a.lddy = lddy; a.dy_type = dy_type; a.dx = dx; a.lddx = lddx; a.ws = ws; a.sync = sync;
     st = moe::launch_linear_grad(a, as_stream(stream));
