@@ -527,8 +527,8 @@ typedef struct moe_qmatrix {
 
 /* Device workspace of moe_linear (grad = 0) or moe_linear_grad (grad = 1) for any
  * call of up to T tokens with this element type of y or dy (host-only; the
- * matrix' pointers are not used).  It is 0 for moe_linear of few tokens with K up
- * to 8192.  A workspace serves calls of one stream at a time; what it holds
+ * matrix' pointers are not used).  It is 0 for moe_linear of up to 16 tokens with K
+ * up to 8192, and 2.3 GB at most: laid-out weights and tokens are taken in turns.  A workspace serves calls of one stream at a time; what it holds
  * between calls is scratch. */
 int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int grad, size_t* bytes);
 
@@ -543,7 +543,7 @@ int moe_linear_workspace_bytes(const moe_qmatrix* w, int32_t T, int type, int gr
  *   laid out:                   [1] rows and [2] columns of a tile, [3] splits of
  *                               the sum, [4] 32-element blocks a stage, [5] chunks
  *                               of the matrix ([1] .. [4]: the first one's), [6]
- *                               fp16 parts of x or dy */
+ *                               fp16 parts of x or dy, [7] turns of the tokens */
 #define MOE_LINEAR_STREAMED 1
 #define MOE_LINEAR_LAID_OUT 2
 int moe_linear_kernels(const moe_qmatrix* w, int32_t T, int type, int grad, int32_t* kernels);

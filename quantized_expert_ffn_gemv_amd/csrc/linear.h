@@ -52,6 +52,7 @@ int launch_linear_dec(const LinearArgs& a, hipStream_t s);
 // Input gradient, the codes streamed (linear_grad_dec.hip).
 int grad_splits(const moe_qmatrix& w, int T);
 size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T);
+size_t linear_grad_dec_most_bytes(const moe_qmatrix& w, int T);
 int launch_linear_grad_dec(const LinearGradArgs& a, hipStream_t s);
 // Both operands laid out for a dense product (linear_gemm.hip).
 size_t linear_gemm_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad);

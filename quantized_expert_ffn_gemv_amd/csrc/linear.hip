@@ -33,11 +33,13 @@ size_t linear_workspace_bytes(const moe_qmatrix& w, int T, int type, bool grad) 
     return grad ? linear_grad_dec_workspace_bytes(w, T) : linear_dec_workspace_bytes(w, T);
 }
 
-// The needs do not grow with T alone: the gradient's splits fall as tokens rise, and more
-// tokens may take kernels that need less.
+// Laid-out products never need less for more tokens, so the first number of tokens from above
+// that takes them says whether their need counts; the streamed ones' does not grow with T alone
+// (the gradient's splits fall).
 size_t linear_workspace_bytes_up_to(const moe_qmatrix& w, int T, int type, bool grad) {
-    size_t most = 0;
-    for (int t = 1; t <= T; ++t) most = std::max(most, linear_workspace_bytes(w, t, type, grad));
+    size_t most = grad ? linear_grad_dec_most_bytes(w, T) : linear_dec_workspace_bytes(w, T);
+    for (int t = T; t >= 1; --t)
+        if (!streams(w, t, type, grad)) return std::max(most, linear_gemm_workspace_bytes(w, T, type, grad));
     return most;
 }
 

@@ -419,13 +419,21 @@ void stream_launch(const StreamArgs& sa, hipStream_t s) {
 
 }  // namespace
 
+// Tokens at once: all, or where K takes several launches as many as have 1 GB of sums (a tile
+// of tokens reads the whole matrix either way).
+static int tokens_at_once(const moe_qmatrix& w, int T) {
+    if (w.K / 128 <= kStreamGroups) return T;
+    const long most = ((1L << 30) / (4L * w.N)) / 32 * 32;         // (N is at most 2^20)
+    return T < most ? T : (int)most;
+}
+
 size_t linear_dec_workspace_bytes(const moe_qmatrix& w, int T) {
-    return w.K / 128 > kStreamGroups ? (size_t)T * w.N * sizeof(float) : 0;
+    return w.K / 128 > kStreamGroups ? (size_t)tokens_at_once(w, T) * w.N * sizeof(float) : 0;
 }
 
 void linear_dec_kernels(const moe_qmatrix& w, int T, int32_t* kernels) {
     const int runs = w.K / 128;
-    const StreamForm f = stream_form(w, T, std::min(runs, kStreamGroups));
+    const StreamForm f = stream_form(w, tokens_at_once(w, T), std::min(runs, kStreamGroups));
     kernels[1] = f.nt;
     kernels[2] = f.rt;
     kernels[3] = f.gpw;
@@ -435,7 +443,7 @@ void linear_dec_kernels(const moe_qmatrix& w, int T, int32_t* kernels) {
 
 // K beyond what a workgroup's registers hold is taken in several launches, each
 // adding to the sums that the last one left in the workspace.
-int launch_linear_dec(const LinearArgs& a, hipStream_t s) {
+static void launch_turn(const LinearArgs& a, hipStream_t s) {
     const int NG = a.w.K / 128, spg = 128 / a.w.group_size;
     for (int g0 = 0; g0 < NG; g0 += kStreamGroups) {
         StreamArgs sa{a, g0, NG - g0 < kStreamGroups ? NG - g0 : kStreamGroups, nullptr};
@@ -456,6 +464,19 @@ int launch_linear_dec(const LinearArgs& a, hipStream_t s) {
             else if (spg == 2) stream_launch<2, 2>(sa, s);
             else stream_launch<2, 4>(sa, s);
         }
+    }
+}
+
+int launch_linear_dec(const LinearArgs& a, hipStream_t s) {
+    const int at_once = tokens_at_once(a.w, a.T);
+    const size_t e = a.y_type == MOE_F32 ? 4 : 2;
+    for (int t0 = 0; t0 < a.T; t0 += at_once) {
+        LinearArgs b = a;
+        b.T = std::min(at_once, a.T - t0);
+        b.x = a.x + (int64_t)t0 * a.ldx;
+        b.residual = a.residual ? a.residual + (int64_t)t0 * a.ldr : nullptr;
+        b.y = static_cast<uint8_t*>(a.y) + (int64_t)t0 * a.ldy * e;
+        launch_turn(b, s);
     }
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

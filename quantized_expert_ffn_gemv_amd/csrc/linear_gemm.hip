@@ -45,8 +45,10 @@ constexpr int kParts = 2;                              // fp16 parts of a weight
 constexpr int kKeep = 4;                               // pieces of a row of A a thread keeps
 constexpr int kPrepGroups = 8;                         // 128-runs of K a workgroup lays out
 // Laid-out weights per chunk, at most: past the 256 MB cache, for enough tiles in a chunk's
-// GEMM.  The chunks of a matrix are of like size.
+// GEMM.  The chunks of a matrix are of like size.  Laid-out rows of x or dy, the same: calls of
+// more tokens take them in turns, the weights of a chunk laid out once.
 constexpr size_t kChunkBytes = (size_t)1 << 30;
+constexpr int kLeastTokens = 256;
 
 __host__ __device__ inline int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
@@ -690,6 +692,7 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Workspace: A, et, en, the chunk's weights, then the splits' sums.
 struct Plan {
+    int tokens;                            // per GEMM
     int kd, a_parts, chunk, total;         // chunk: weight rows (forward) or 128-runs (gradient) per GEMM
     size_t et, en, wh, part, bytes;
 };
@@ -699,18 +702,23 @@ Plan plan_of(const moe_qmatrix& w, int T, int type, bool grad) {
     p.kd = grad ? round_up(w.N, kStep * kBlocks) : w.K;
     p.a_parts = grad && type == MOE_F32 ? 2 : 1;
     p.total = grad ? w.K / 128 : w.N;
+    const size_t row = (size_t)2 * p.kd * p.a_parts;                                   // bytes of a row of A
+    const int at_once = std::max(kLeastTokens, (int)(kChunkBytes / row) / kLeastTokens * kLeastTokens);
+    const int turns = (T + at_once - 1) / at_once;
+    p.tokens = std::min(round_up((T + turns - 1) / turns, kLeastTokens), T);
     const size_t unit = (size_t)2 * kParts * p.kd * (grad ? 128 : 1);                  // bytes
     size_t c = kChunkBytes / unit;
     const int tile = grad ? 2 : 256;                                                 // a tile's worth
     const int most = c < (size_t)tile ? tile : c > (size_t)p.total ? p.total : (int)c / tile * tile;
     const int chunks = (p.total + most - 1) / most;
     p.chunk = std::min(round_up((p.total + chunks - 1) / chunks, tile), p.total);
-    p.et = align256((size_t)T * p.kd * 2 * p.a_parts);
-    p.en = p.et + align256((size_t)T * 4);
+    const int most_tokens = std::min(T, at_once);                  // (the turns' even share may fall as T grows)
+    p.et = align256(row * most_tokens);
+    p.en = p.et + align256((size_t)most_tokens * 4);
     p.wh = p.en + align256((size_t)w.N * 2);
     p.part = p.wh + align256(unit * p.chunk);
     // (for any number of splits, so that more tokens never need less)
-    const long results = (long)T * (grad ? 128 * p.chunk : p.chunk);
+    const long results = (long)most_tokens * (grad ? 128 * p.chunk : p.chunk);
     p.bytes = p.part + (p.kd * p.a_parts < 1024 ? 0 : align256(std::min(kMaxSplits * results, split_results()) * sizeof(float)));
     return p;
 }
@@ -728,80 +736,111 @@ double linear_gemm_us(const moe_qmatrix& w, int T, int type, bool grad, double l
                      : 8.8 + 0.4e-3 * K + 0.305e-6 * matrix + 0.278e-6 * T * K * 4 + 0.289e-6 * T * N * wide;
     if (us >= limit) return us;
     const Plan p = plan_of(w, T, type, grad);
-    for (int c0 = 0; c0 < p.total && us < limit; c0 += p.chunk)
-        us += gemm_choice(T, std::min(p.chunk, p.total - c0) * (grad ? 128 : 1), p.kd, p.a_parts).us;
+    // whole chunks and turns alike, then the last ones
+    const int wide_c = grad ? 128 : 1, last_c = p.total % p.chunk, last_t = T % p.tokens;
+    auto products = [&](int tokens, int chunk, double times) {
+        if (tokens > 0 && chunk > 0 && us < limit) us += times * gemm_choice(tokens, chunk * wide_c, p.kd, p.a_parts).us;
+    };
+    products(p.tokens, p.chunk, (double)(T / p.tokens) * (p.total / p.chunk));
+    products(last_t, p.chunk, p.total / p.chunk);
+    products(p.tokens, last_c, T / p.tokens);
+    products(last_t, last_c, 1);
     return us;
 }
 
 void linear_gemm_kernels(const moe_qmatrix& w, int T, int type, bool grad, int32_t* kernels) {
     static const int32_t shape[][3] = {{256, 256, 1}, {256, 128, 1}, {128, 128, 1}, {64, 64, 2}, {64, 64, 4}};   // by Tile
     const Plan p = plan_of(w, T, type, grad);
-    const Choice c = gemm_choice(T, p.chunk * (grad ? 128 : 1), p.kd, p.a_parts);
+    const Choice c = gemm_choice(p.tokens, p.chunk * (grad ? 128 : 1), p.kd, p.a_parts);
     kernels[1] = shape[c.tile][0];
     kernels[2] = shape[c.tile][1];
     kernels[3] = c.splits;
     kernels[4] = shape[c.tile][2];
     kernels[5] = (p.total + p.chunk - 1) / p.chunk;
     kernels[6] = p.a_parts;
+    kernels[7] = (T + p.tokens - 1) / p.tokens;
 }
 
-int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
-    const Plan pl = plan_of(a.w, a.T, a.y_type, false);
-    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+namespace {
+
+PrepArgs prep_of(const moe_qmatrix& w, const Plan& pl, uint8_t* ws) {
     PrepArgs p{};
-    p.w = a.w; p.a = a.x; p.lda = a.ldx; p.a_type = MOE_BF16; p.T = a.T; p.len = a.w.K; p.kd = pl.kd;
+    p.w = w;
+    p.kd = pl.kd;
     p.ah = reinterpret_cast<uint16_t*>(ws);
     p.et = reinterpret_cast<int32_t*>(ws + pl.et);
     p.en = reinterpret_cast<int16_t*>(ws + pl.en);
     p.wh = reinterpret_cast<uint16_t*>(ws + pl.wh);
-    for (int c0 = 0; c0 < pl.total; c0 += pl.chunk) {
-        p.c0 = c0;
-        p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
-        p.a_rows = pl.kd <= 8 * kWave * kKeep ? 4 : 1;
-        p.a_blocks = c0 == 0 ? (a.T + p.a_rows - 1) / p.a_rows : 0;
-        const int parts = (a.w.K / 128 + kPrepGroups - 1) / kPrepGroups;
-        const dim3 grid((unsigned)(p.a_blocks + (p.cn + 15) / 16 * parts));
-        if (a.w.bits == 4) hipLaunchKernelGGL(linear_prep_kernel<4>, grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL(linear_prep_kernel<2>, grid, dim3(256), 0, s, p);
-        GemmArgs g{};
-        g.part = reinterpret_cast<float*>(ws + pl.part);
-        g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = p.cn; g.kd = pl.kd; g.a_parts = 1; g.et = p.et; g.en = p.en + c0;
-        g.row_bias = a.row_bias ? a.row_bias + c0 : nullptr;
-        g.residual = a.residual ? a.residual + c0 : nullptr;
-        g.ldr = a.ldr; g.ldy = a.ldy; g.y_type = a.y_type;
-        g.y = a.y_type == MOE_F32 ? static_cast<void*>(static_cast<float*>(a.y) + c0)
-                                  : static_cast<void*>(static_cast<uint16_t*>(a.y) + c0);
-        gemm(g, s);
+    p.a_rows = pl.kd <= 8 * kWave * kKeep ? 4 : 1;
+    return p;
+}
+
+// Every chunk of the matrix with every turn of tokens: the chunk is laid out in the first
+// turn's launch, the tokens in the first chunk's, or in each one's where there are several
+// turns (they share their place).  prep(p, w) lays out p's tokens and, with w, the chunk;
+// product(t0, c0, p) multiplies.
+template <typename PREP, typename PRODUCT>
+void by_chunks(const Plan& pl, PrepArgs p, int T, const uint8_t* a, int64_t row, PREP prep, PRODUCT product) {
+    for (p.c0 = 0; p.c0 < pl.total; p.c0 += pl.chunk) {
+        p.cn = std::min(pl.chunk, pl.total - p.c0);
+        for (int t0 = 0; t0 < T; t0 += pl.tokens) {
+            p.T = std::min(pl.tokens, T - t0);
+            p.a = a + (int64_t)t0 * row;
+            p.a_blocks = p.c0 == 0 || pl.tokens < T ? (p.T + p.a_rows - 1) / p.a_rows : 0;
+            prep(p, t0 == 0);
+            product(t0, p);
+        }
     }
+}
+
+}  // namespace
+
+int launch_linear_gemm(const LinearArgs& a, hipStream_t s) {
+    const Plan pl = plan_of(a.w, a.T, a.y_type, false);
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    PrepArgs p = prep_of(a.w, pl, ws);
+    p.lda = a.ldx; p.a_type = MOE_BF16; p.len = a.w.K;
+    const int parts = (a.w.K / 128 + kPrepGroups - 1) / kPrepGroups, e = a.y_type == MOE_F32 ? 4 : 2;
+    by_chunks(pl, p, a.T, reinterpret_cast<const uint8_t*>(a.x), 2 * a.ldx,
+        [&](const PrepArgs& q, bool w) {
+            const dim3 grid((unsigned)(q.a_blocks + (w ? (q.cn + 15) / 16 * parts : 0)));
+            if (a.w.bits == 4) hipLaunchKernelGGL(linear_prep_kernel<4>, grid, dim3(256), 0, s, q);
+            else hipLaunchKernelGGL(linear_prep_kernel<2>, grid, dim3(256), 0, s, q);
+        },
+        [&](int t0, const PrepArgs& q) {
+            GemmArgs g{};
+            g.part = reinterpret_cast<float*>(ws + pl.part);
+            g.A = q.ah; g.B = q.wh; g.M = q.T; g.N = q.cn; g.kd = pl.kd; g.a_parts = 1; g.et = q.et; g.en = q.en + q.c0;
+            g.row_bias = a.row_bias ? a.row_bias + q.c0 : nullptr;
+            g.residual = a.residual ? a.residual + (int64_t)t0 * a.ldr + q.c0 : nullptr;
+            g.ldr = a.ldr; g.ldy = a.ldy; g.y_type = a.y_type;
+            g.y = static_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + q.c0) * e;
+            gemm(g, s);
+        });
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int launch_linear_grad_gemm(const LinearGradArgs& a, hipStream_t s) {
     const Plan pl = plan_of(a.w, a.T, a.dy_type, true);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    PrepArgs p{};
-    p.w = a.w; p.a = a.dy; p.lda = a.lddy; p.a_type = a.dy_type; p.T = a.T; p.len = a.w.N; p.kd = pl.kd;
-    p.ah = reinterpret_cast<uint16_t*>(ws);
-    p.et = reinterpret_cast<int32_t*>(ws + pl.et);
-    p.en = reinterpret_cast<int16_t*>(ws + pl.en);
-    p.wh = reinterpret_cast<uint16_t*>(ws + pl.wh);
+    PrepArgs p = prep_of(a.w, pl, ws);
+    p.lda = a.lddy; p.a_type = a.dy_type; p.len = a.w.N;
     const dim3 rows((unsigned)((a.w.N + 15) / 16));
     if (a.w.bits == 4) hipLaunchKernelGGL(linear_rows_kernel<4>, rows, dim3(256), 0, s, p);
     else hipLaunchKernelGGL(linear_rows_kernel<2>, rows, dim3(256), 0, s, p);
-    for (int c0 = 0; c0 < pl.total; c0 += pl.chunk) {
-        p.c0 = c0;
-        p.cn = pl.total - c0 < pl.chunk ? pl.total - c0 : pl.chunk;
-        p.a_rows = pl.kd <= 8 * kWave * kKeep ? 4 : 1;
-        p.a_blocks = c0 == 0 ? (a.T + p.a_rows - 1) / p.a_rows : 0;
-        const dim3 grid((unsigned)(p.a_blocks + p.cn * ((pl.kd + 127) / 128)));
-        if (a.w.bits == 4) hipLaunchKernelGGL(linear_grad_prep_kernel<4>, grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL(linear_grad_prep_kernel<2>, grid, dim3(256), 0, s, p);
-        GemmArgs g{};
-        g.part = reinterpret_cast<float*>(ws + pl.part);
-        g.A = p.ah; g.B = p.wh; g.M = a.T; g.N = 128 * p.cn; g.kd = pl.kd; g.a_parts = pl.a_parts; g.et = p.et;
-        g.ldy = a.lddx; g.y_type = MOE_BF16; g.y = a.dx + 128 * (size_t)c0;
-        gemm(g, s);
-    }
+    by_chunks(pl, p, a.T, static_cast<const uint8_t*>(a.dy), (a.dy_type == MOE_F32 ? 4 : 2) * a.lddy,
+        [&](const PrepArgs& q, bool w) {
+            const dim3 grid((unsigned)(q.a_blocks + (w ? q.cn * ((pl.kd + 127) / 128) : 0)));
+            if (a.w.bits == 4) hipLaunchKernelGGL(linear_grad_prep_kernel<4>, grid, dim3(256), 0, s, q);
+            else hipLaunchKernelGGL(linear_grad_prep_kernel<2>, grid, dim3(256), 0, s, q);
+        },
+        [&](int t0, const PrepArgs& q) {
+            GemmArgs g{};
+            g.part = reinterpret_cast<float*>(ws + pl.part);
+            g.A = q.ah; g.B = q.wh; g.M = q.T; g.N = 128 * q.cn; g.kd = pl.kd; g.a_parts = pl.a_parts; g.et = q.et;
+            g.ldy = a.lddx; g.y_type = MOE_BF16; g.y = a.dx + (int64_t)t0 * a.lddx + 128 * (size_t)q.c0;
+            gemm(g, s);
+        });
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

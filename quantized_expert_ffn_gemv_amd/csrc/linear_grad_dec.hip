@@ -304,6 +304,14 @@ size_t linear_grad_dec_workspace_bytes(const moe_qmatrix& w, int T) {
     return s == 1 ? 0 : (size_t)((T + kTok - 1) / kTok) * (w.K / 128) * s * kTok * 128 * sizeof(float);
 }
 
+// The most of any call of up to T tokens: splits go by the tokens of one block, then by the
+// blocks, and past a block for every CU there is one.
+size_t linear_grad_dec_most_bytes(const moe_qmatrix& w, int T) {
+    size_t most = 0;
+    for (int t = 1; t <= T && t <= kTok * (kCounters + 1); t += t < kTok ? 1 : kTok) most = std::max(most, linear_grad_dec_workspace_bytes(w, t));
+    return std::max(most, linear_grad_dec_workspace_bytes(w, T));
+}
+
 namespace {
 
 template <int BITS, int SPG>

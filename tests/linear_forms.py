@@ -31,6 +31,8 @@ GRAD_F32 = [(520, 16, 2944, 4, 32), (440, 4100, 640, 4, 32), (1500, 333, 640, 4,
             (520, 16, 8192, 4, 32), (520, 1500, 4096, 4, 32), (440, 700, 16384, 4, 32), (130, 9000, 4096, 4, 32),
             (2500, 130, 6400, 2, 128), (130, 4100, 16384, 4, 32)]
 LAID_OUT = (2500, 2500, 640, 4, 64)          # in both directions and types
+# More laid-out tokens than are taken at once: forward, gradient with bf16 and with float32 dy.
+TURNS = [(20000, 1200, 32768, 4, 128), (5600, 100001, 256, 4, 128), (2900, 100001, 384, 2, 32)]
 
 
 def kernels(T, N, K, bits, group, f32=False, grad=False):

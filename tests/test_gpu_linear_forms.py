@@ -103,6 +103,31 @@ def test_laid_out_gradient_tiles(size, f32):
     Matrix(T + N, N, K, bits, group).grad(T, f32, pad=N % 3)
 
 
+def test_tokens_in_turns():
+    """More tokens than are laid out at once, the last turn a short one."""
+    T, N, K, bits, group = forms.TURNS[0]
+    Matrix(1, N, K, bits, group).linear(T, f32=False, row_bias=True, residual=True, pad=1)
+    for (T, N, K, bits, group), f32 in ((forms.TURNS[1], False), (forms.TURNS[2], True)):
+        Matrix(2, N, K, bits, group).grad(T, f32, pad=1)
+
+
+def test_streamed_tokens_in_turns():
+    """A long K's float32 sums of more than 1 GB: 256 tokens and 44, as two calls."""
+    T, N, K = 300, 1048576, 8320
+    assert forms.kernels(T, N, K, 2, 128)[0] == moe.LINEAR_STREAMED
+    g = torch.Generator(DEV).manual_seed(3)
+    q = torch.randint(0, 256, (K // 128, N, 32), dtype=torch.uint8, device=DEV, generator=g)
+    s, b = (0.01 * torch.rand(N, K // 128, device=DEV, generator=g).half() for _ in range(2))
+    w = moe.QMatrix(2, 128, q, s, b)
+    x, res = torch.randn(T, K, device=DEV, generator=g).bfloat16(), torch.randn(T, N, device=DEV, generator=g).bfloat16()
+    y, apart = torch.empty_like(res), torch.empty_like(res)
+    buf = moe.LinearBuffers.allocate(w, T, y.dtype)
+    moe.linear(w, x, y, buf, residual=res)
+    for rows in (slice(0, 256), slice(256, T)):
+        moe.linear(w, x[rows], apart[rows], buf, residual=res[rows])
+    assert torch.equal(y, apart) and not torch.equal(y, res)
+
+
 @pytest.mark.parametrize("T,N,K,bits,group", [(1, 31, 128, 4, 128), (3, 5000, 384, 4, 64), (16, 257, 1152, 2, 32),
                                               (17, 9001, 256, 4, 32), (40, 700, 2048, 2, 64), (100, 300, 128, 4, 128)])
 def test_streamed_gradients(T, N, K, bits, group):

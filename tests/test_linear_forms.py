@@ -62,3 +62,24 @@ def test_the_size_that_is_laid_out_whatever_its_types():
     for f32 in (False, True):
         for grad in (False, True):
             assert forms.kernels(*forms.LAID_OUT, f32, grad)[0] == moe.LINEAR_LAID_OUT
+
+
+def test_workspaces_are_bounded_and_quickly_told():
+    """2.3 GB for any sizes, never less for more tokens, and no call's own need is more."""
+    for N in (1, 1000, 49999, 1 << 20):
+        for K in (128, 4096, 8320, 32768):
+            for f32 in (False, True):
+                for grad in (False, True):
+                    w, sizes = moe.QMatrixC(None, None, None, N, K, 32, 4), []
+                    for T in (1, 16, 17, 255, 300, 5000, 20000, 65536):
+                        out = ctypes.c_size_t(0)
+                        L = moe.lib()
+                        assert L.moe_linear_workspace_bytes(ctypes.byref(w), T, int(f32), int(grad), ctypes.byref(out)) == moe.OK
+                        sizes.append(out.value)
+                    assert sizes == sorted(sizes) and sizes[-1] <= 2.3e9
+
+
+def test_tokens_in_turns():
+    for size, grad, turns in ((forms.LAID_OUT, False, 1), (forms.LAID_OUT, True, 1), (forms.TURNS[0], False, 2),
+                              (forms.TURNS[1], True, 2), (forms.TURNS[2], True, 2)):
+        assert forms.kernels(*size, size == forms.TURNS[2], grad)[7] == turns
