@@ -19,8 +19,10 @@ namespace {
 //   forward  512 x 4096 x 4096 45, 58    700 x 4096 x 4096 59, 80   1500 x 4096 x 4096 111, 113
 //            1024 x 2048 x 2048 34, 38   4096 x 4096 x 1024 101, 71   100 x 325 x 9216  20, 31
 //            1000 x 2500 x 640 (groups of 64) 32, 28; float32 result 32, 29
+//            float32 results: 1024 x 8192 x 2048 93, 78   4096 x 8192 x 2048 396, 236   1024 x 49999 x 4096 755, 1011
 //   gradient 1749 x 388 x 640 (groups of 32) 27, 18   304 x 6 x 16768 18, 24
 //            1000 x 2500 x 640 (groups of 64) 36, 34   148 x 25955 x 10880 (groups of 32) 991, 1146
+//            253 x 24471 x 4736 270, 372; float32 dy: 1024 x 49999 x 4096 1656, 1493   4096 x 8192 x 2048 528, 410
 bool streams(const moe_qmatrix& w, int T, int type, bool grad) {
     const double us = grad ? linear_grad_dec_us(w, T) : linear_dec_us(w, T);
     return us <= linear_gemm_us(w, T, type, grad, us);

@@ -10,7 +10,7 @@
 //
 // Bound by the weight stream: 8 tokens x 49999 x 4096 at 4 bits, float32 out, take 26 us
 // (4.2 TB/s of the bytes that have to move), 28672 x 8192 32 us (3.9 TB/s); 4096 x 4096,
-// one or two tiles a CU, 7.5 us, most of it launch, start and the last tile.
+// one or two tiles a CU, 6.8 us, most of it launch, start and the last tile.
 #include <algorithm>
 
 #include "launch_util.h"
@@ -321,21 +321,19 @@ __global__ __launch_bounds__(64 * kStreamMaxWaves, (two_fit(NT, GPW) ? 4 : 2)) v
 }
 
 // Two token tiles where their operands fit the registers (K <= 4096) and every CU has
-// more than two weight tiles to share its start among: 32 tokens, 4096 outputs, K =
-// 4096: 12.7 us against 10.2 with one, 8192: 16.5 and 14.5, 16384: 21.6 and 21.2,
-// 49999: 41 and 48; K = 2048: 8.2 and 7.4, 10.3 and 10.1, 14.1 and 15.4; 64 tokens,
-// 28672 outputs: 43 and 51.  A second ring entry per slot pays only where a slot is
-// one group (8 tokens, 49999 outputs, K = 1024: 16.6 us against 18.1; K = 2048: 21.3 and
-// 21.0; K = 4096: 30.0 and 29.2), and where a workgroup has a second tile to request ahead (1
-// token, 2048 x 1024: 3.4 us against 3.9).
+// more than two weight tiles to share its start among; with one and with two, us: 32 tokens, K =
+// 4096: 4096 outputs 9.8, 12.2; 8192 13.0, 15.4; 16384 18.8, 19.4; 49999 45.3, 38.6; K = 2048: 6.3,
+// 7.4; 8.9, 9.1; 13.4, 12.9; 26.7, 25.3; 64 tokens, 28672 x 4096 46.5, 37.2.
+// A second ring entry per slot where a slot is one group and a workgroup has a second tile to
+// request ahead: without and with, 8 tokens, 400000 x 1024 69.0, 64.0; 49999 x 1024 11.9, 12.0; 28672 x
+// 1024 9.5, 9.2; 2 bits 8.1, 8.5.
 // Tiles of 32 weight rows (units of 1 KB) for 2-bit codes of groups of 128 where they
-// still give every CU one (8 tokens, K = 4096: 4096 outputs 7.7 us against 6.9 with 16
-// rows, 8192 8.2 and 8.6, 49999 24.8 and 27.1; K = 1024: 8192 outputs 4.5 and 5.4, 28672
-// 8.5 and 9.8); 4-bit codes gain nothing (49999 outputs: 30.0 and 29.4), nor do 2-bit
-// ones of finer groups (28672 outputs: 21.3 and 20.7).
+// still give every CU one; with 16 rows and with 32, 8 tokens, K = 4096: 4096 outputs 6.1, 7.0; 8192
+// 7.6, 7.4; 49999 22.8, 20.9; K = 1024: 4096 3.8, 4.0; 8192 4.7, 4.1; 28672 9.3, 7.3.  (4-bit codes
+// and finer groups gained nothing when they were built, and are not.)
 // Two workgroups a CU, one multiplying while the other's waves meet, where each still has
-// four tiles of 16 rows (8 tokens, 4 bits: 49999 x 1024 12.7 us against 16.6, 49999 x 2048
-// 17.7 and 20.8; with fewer tiles 8192 x 2048 7.7 and 6.6, 16384 x 512 6.9 and 6.6).
+// four tiles of 16 rows; with one and with two, 8 tokens, 4 bits: 49999 x 1024 15.4, 11.8; 49999 x
+// 2048 17.7, 15.5; 16384 x 1024 6.6, 6.3; with fewer tiles 8192 x 2048 5.6, 6.4; 16384 x 512 5.7, 6.4.
 StreamForm stream_form(const moe_qmatrix& w, int T, int runs) {
     const int cus = device_cus(), spg = 128 / w.group_size;
     StreamForm f{};

@@ -21,9 +21,10 @@
 // rows at a time in turn; their sums meet in LDS, those of several workgroups in
 // the workspace, where the last to arrive adds them in order.
 //
-// Bound by latency where a wave has few rounds (1 token, 4096 x 4096 at 4 bits: 7.2 us;
-// 37 tokens, 5111 x 2048 at 2 bits, groups of 64: 11.5), by the code stream past that
-// (8 tokens, 49999 x 4096: 36 us, 3.0 TB/s of the bytes that have to move).
+// Bound by latency where a wave has few rounds (1 token, 4096 x 4096 at 4 bits: 7.1 us;
+// 37 tokens, 5111 x 2048 at 2 bits, groups of 64: 12), by the code stream past that
+// (8 tokens, 49999 x 4096: 37 us, 3.0 TB/s of the bytes that have to move; float32 dy 36;
+// groups of 32 73, by their matrix instructions).
 #include <algorithm>
 #include <type_traits>
 
@@ -274,9 +275,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void linear_grad_dec_kernel(GradAr
 }
 
 // Splits of the weight rows, whole rounds of rows each: one workgroup a CU (4096 x
-// 4096, 1 token: 7.6 us; half as many 7.9, twice 9.2; 49999 x 4096, 8 tokens: 36, 58,
-// 39), rounded up where a CU holds two (SPG = 1), else down (3 x 96 workgroups took
-// a second turn: 21 us against 11); and partial sums, written and read, of at most
+// 4096, 1 token: 7.1 us; half as many 8.1, twice 7.8; 49999 x 4096, 8 tokens: 37, 60,
+// 39), rounded up where a CU holds two (SPG = 1), else down (twice as many, 37 x 5111 x 2048 at
+// groups of 64: 16.7 us against 12.3); and partial sums, written and read, of at most
 // twice the codes' bytes.
 int grad_splits(const moe_qmatrix& w, int T) {
     // (more than one split only where runs times token blocks are fewer than the counters)

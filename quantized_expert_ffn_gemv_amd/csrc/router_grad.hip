@@ -8,7 +8,7 @@
 // p = 0 everywhere.
 //
 // The gradient is bound by memory: 16384 x 512, 16.3 us (4.2 TB/s); 64 x 64, 2.4 us.  The
-// losses by their joins: 32 x 256, 5.1 us; 8191 x 128, 8.6 us; 16384 x 512, 16.9 us.
+// losses by their joins: 32 x 256, 5.4 us; 8191 x 128, 8.5 us; 16384 x 512, 17.1 us.
 #include <cmath>
 
 #include "common.h"
@@ -19,7 +19,7 @@ namespace moe {
 namespace {
 
 // Workgroups of the losses: 512 threads (1024: 16384 x 512 15.3 us against 16.8, but 32 x
-// 256 and 1024 x 128 slower), at most 256 (half as many: 16384 x 512 23.4 us against 16.9,
+// 256 and 1024 x 128 slower; both, by the batch, is not built), at most 256 (half as many: 16384 x 512 23.4 us against 16.9,
 // 8191 x 128 10.1 and 8.8), 16 joined by one ticket (32: slower at every size).
 constexpr int kThreads = 256, kBalThreads = 512;
 constexpr int kBalTree = 16;
@@ -416,7 +416,7 @@ int launch_route_backward(const moe_dims& d, const float* logits, const int32_t*
         constexpr int L = lpt.value, P = per.value;
         const long tpb = 4 * (kWave / L);
         long blocks = ((long)d.T + tpb - 1) / tpb;
-        blocks = blocks > 2048 ? 2048 : blocks;           // (16384 x 512: 16.8 us; 1024 18.3, 8192 18.6)
+        blocks = blocks > 2048 ? 2048 : blocks;           // (16384 x 512: 17.8 us; 1024 19.4, 4096 18.6, 8192 18.3)
         if (vec) hipLaunchKernelGGL((route_backward_kernel<L, P, true>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
         else hipLaunchKernelGGL((route_backward_kernel<L, P, false>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
     });
