@@ -778,7 +778,7 @@ PrepArgs prep_of(const moe_qmatrix& w, const Plan& pl, uint8_t* ws) {
 // Every chunk of the matrix with every turn of tokens: the chunk is laid out in the first
 // turn's launch, the tokens in the first chunk's, or in each one's where there are several
 // turns (they share their place).  prep(p, w) lays out p's tokens and, with w, the chunk;
-// product(t0, c0, p) multiplies.
+// product(t0, p) multiplies.
 template <typename PREP, typename PRODUCT>
 void by_chunks(const Plan& pl, PrepArgs p, int T, const uint8_t* a, int64_t row, PREP prep, PRODUCT product) {
     for (p.c0 = 0; p.c0 < pl.total; p.c0 += pl.chunk) {
