@@ -424,7 +424,7 @@ def _own_logprobs(s):
     import quantized_expert_ffn_gemv_amd as moe
     c = s["case"]
     if "buf" not in s:
-        s["buf"] = moe.LogprobBuffers.allocate(c["T"], c["V"], s["logits"].dtype, c["top"])
+        s["buf"] = moe.LogprobBuffers.allocate(c["T"], c["V"], c["top"])
     moe.logprobs(s["logits"], s["tokens"], s["logp"], s["stats"], s["buf"], entropy=s["entropy"], top_ids=s["top_ids"],
                  top_logp=s["top_logp"])
     out = {"logp": s["logp"]}
