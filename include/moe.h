@@ -656,6 +656,153 @@ int moe_combine_backward(const moe_dims* dims, const uint16_t* out_grad, const u
                          const int32_t* pair_to_row, const float* topk_w, float* topk_w_grad, uint16_t* y_rows_grad,
                          void* stream);
 
+/* ------------------------------------------------------- low-rank adapters
+ * Adapters of many requests beside a shared projection (moe_linear's, or any
+ * other), the projection frozen: token t uses adapter i = ids[t], or none where
+ * that is outside [0, n).  Both factors are stored by rank:
+ *   a      bf16 [n][R][K]
+ *   b      bf16 [n][R] rows of ldb elements, of which the first N are used; ldb a
+ *          multiple of 8
+ *   scale  float32 [n]
+ *   rank   int32 [n] or NULL (R for all): ranks rank[i] and up of adapter i are
+ *          left out and not read (values outside [0, R] count as the nearer end)
+ * a and b are 16-byte aligned.  Limits: 1 <= n <= 1024; 1 <= R <= 128; K a
+ * multiple of 128, 128 <= K <= 32768; 8 <= N <= 1048576; 0 <= T <= 65536.  The
+ * struct is a host object, read during the call only. */
+typedef struct moe_adapters {
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t ldb;
+    const float* scale;
+    const int32_t* rank;
+    int32_t n;
+    int32_t R;
+    int32_t K;
+    int32_t N;
+} moe_adapters;
+
+/* Activations kept in 8 bits: row t's columns 128 g .. 128 g + 127 are
+ * q[t][k] * scale[t][g], with
+ *   scale = max |x| / 127 over the 128 columns (float32, one division),
+ *   q     = 127 x / max |x| rounded to the nearest whole number, ties to even
+ * (0 and 0 where all are 0).  128 columns with an infinity or NaN get the scale
+ * NaN and codes 0: all of them read as NaN.
+ *   q      int8 [rows][K], 16-byte aligned
+ *   scale  float32 [rows][K/128], 4-byte aligned
+ * Limits: 0 <= rows <= 4194304; K a multiple of 128, 128 <= K <= 32768.  The
+ * struct is a host object, read during the call only. */
+typedef struct moe_checkpoint {
+    int8_t* q;
+    float* scale;
+    int32_t rows;
+    int32_t K;
+} moe_checkpoint;
+
+/* Device workspace of moe_adapter (grad = 0) or moe_adapter_grad (grad = 1) for any
+ * call of up to T tokens (host-only; the struct's pointers are not used).  A
+ * workspace serves calls of one stream at a time; it is scratch between calls. */
+int moe_adapter_workspace_bytes(const moe_adapters* adapters, int32_t T, int grad, size_t* bytes);
+
+/* y[t][n] = base[t][n] + scale[i] sum_r h[t][r] b[i][r][n],
+ * h[t][r] = sum_k x[t][k] a[i][r][k]   (r < rank[i]; 0 past it and without an adapter),
+ * all sums in float32, h not rounded further, y rounded once to its type.
+ *   ids        int32 [T]
+ *   x          bf16 [T] rows of K elements, ldx >= K apart
+ *   base       rows of N elements of y's type, ldbase >= N apart, e.g. what moe_linear
+ *              wrote; may be y itself (ldbase == ldy), or NULL (0)
+ *   y          bf16 or float32 (y_type) [T] rows of N elements, ldy >= N apart;
+ *              overlaps no other input (refused for x and base)
+ *   h          float32 [T][R] or NULL: receives h, for moe_adapter_grad
+ *   workspace  moe_adapter_workspace_bytes(adapters, T, 0), 256-byte aligned
+ * Rows are aligned to their elements.  A row of x with an infinity or NaN changes no
+ * other row.  Sums are taken in a fixed order: equal calls give equal bits. */
+int moe_adapter(const moe_adapters* adapters, int32_t T, const int32_t* ids, const uint16_t* x, int64_t ldx,
+                const void* base, int64_t ldbase, void* y, int64_t ldy, int y_type, float* h, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* The gradients of moe_adapter from dy, with g[t][r] = scale[i] sum_n dy[t][n] b[i][r][n]:
+ *   dx[t][k]    = dx_base[t][k] + sum_r g[t][r] a[i][r][k]              (bf16)
+ *   da[i][r][k] = sum over adapter i's tokens of g[t][r] x[t][k]        (float32)
+ *   db[i][r][n] = scale[i] sum over its tokens of h[t][r] dy[t][n]      (float32)
+ * Every element of da and db is written: 0 for adapters without a token and past
+ * the rank.  (base's gradient is dy; scale is a constant.)
+ *   dy       bf16 or float32 (dy_type) rows of N elements, lddy >= N apart
+ *   x        bf16 rows of K elements, ldx >= K apart, or NULL with x_saved: a
+ *            checkpoint of T rows of K.  Neither is used without da.
+ *   h        float32 [T][R] of moe_adapter; not used without db
+ *   dx       rows of K elements, lddx >= K apart, or NULL.  dx_base: what else
+ *            flows into dx (moe_linear_grad's result), may be dx itself, or NULL (0).
+ *   da       float32 [n][R][K] or NULL;  db  float32 [n][R][N] or NULL
+ *   workspace  moe_adapter_workspace_bytes(adapters, T, 1), 256-byte aligned
+ * dx, da and db overlap no input (refused for dx with dy, x and dx_base).  Sums in
+ * float32 in a fixed order; with float32 dy, 2^-24 of a product of db is left out. */
+int moe_adapter_grad(const moe_adapters* adapters, int32_t T, const int32_t* ids, const void* dy, int64_t lddy,
+                     int dy_type, const uint16_t* x, int64_t ldx, const moe_checkpoint* x_saved, const float* h,
+                     const uint16_t* dx_base, int64_t lddx_base, uint16_t* dx, int64_t lddx, float* da, float* db,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------- token probabilities
+ * From logits [T] rows of V elements (bf16 or float32, `type`), ld >= V apart, with
+ * m = max_v L[t][v], d_v = L[t][v] - m, S = sum_v exp d_v:
+ *   stats    float32 [T][2]  m and log S (both -inf for a row without a logit above
+ *                            -inf); what moe_logprobs_grad reads
+ *   logp     float32 [T]     d_v - log S at v = tokens[t]; 0 where tokens[t] is outside
+ *                            [0, V) (a token that is not scored); -inf for a masked one
+ *   entropy  float32 [T] or NULL   log S - sum_v exp(d_v) d_v / S; 0 for a row without a logit
+ *   top_ids  int32 [T][n_top], top_logp float32 [T][n_top]: the n_top largest logits, best
+ *            first, equal ones (also -0 and +0) by the lower index, and their d_v - log S.
+ *            NaNs and logits of -inf are not taken: -1 and -inf where there are no more.
+ *            n_top 0 .. 64; not used where it is 0.
+ * A NaN or +inf in a row makes its stats[1], logp, entropy and top_logp NaN; no other row changes.
+ *   tokens     int32 [T]
+ *   workspace  moe_logprobs_workspace_bytes(T, V, n_top), 256-byte aligned (NULL where 0)
+ *   sync       int32 [MOE_LOGPROBS_SYNC_INTS] device memory, 256-byte aligned, zeros before the
+ *              first call; each call leaves it zero.  Calls that share a workspace or sync
+ *              must be ordered (one stream).
+ * Limits: 0 <= T <= 65536, 1 <= V <= 1048576.  Sums in float32 in a fixed order. */
+#define MOE_LOGPROBS_SYNC_INTS 8192
+int moe_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top, size_t* bytes);
+int moe_logprobs(int32_t T, int32_t V, const void* logits, int64_t ld, int type, const int32_t* tokens, float* logp,
+                 float* stats, float* entropy, int32_t n_top, int32_t* top_ids, float* top_logp, void* workspace,
+                 size_t workspace_bytes, int32_t* sync, void* stream);
+
+/* d logits [T] rows of V, every element written: with p_v = exp(d_v - log S) and the gradients
+ * w of logp (0 where tokens[t] is outside [0, V)) and u of entropy,
+ *   w ([v = tokens[t]] - p_v) - u p_v (d_v - log S + entropy[t]).
+ * The alternatives are constants.  A row with w = u = 0, or without a logit, gets zeros and is
+ * not read.
+ *   logp_grad      float32 [T] or NULL (0);  entropy_grad float32 [T] or NULL (0; entropy is
+ *                  then not used)
+ *   logits_grad    bf16 or float32 (grad_type) rows, ldg >= V apart; may be the logits
+ *                  themselves (same type and row stride), else overlaps no input (refused for
+ *                  logits). */
+int moe_logprobs_grad(int32_t T, int32_t V, const void* logits, int64_t ld, int type, const int32_t* tokens,
+                      const float* stats, const float* logp_grad, const float* entropy, const float* entropy_grad,
+                      void* logits_grad, int64_t ldg, int grad_type, void* stream);
+
+/* ------------------------------------------------- activations kept in 8 bits
+ * moe_checkpoint_save writes a checkpoint of bf16 rows (ldx >= K elements apart, 2-byte
+ * aligned); moe_checkpoint_restore writes bf16(q scale) to such rows. */
+int moe_checkpoint_save(const moe_checkpoint* checkpoint, const uint16_t* x, int64_t ldx, void* stream);
+int moe_checkpoint_restore(const moe_checkpoint* checkpoint, uint16_t* x, int64_t ldx, void* stream);
+
+/* moe_combine_backward with the expert rows kept in a checkpoint of T*k rows or more
+ * (a shared expert's follow) of H columns: the dot products are taken with q scale. */
+int moe_combine_backward_saved(const moe_dims* dims, const uint16_t* out_grad, const moe_checkpoint* y_rows,
+                               const int32_t* pair_to_row, const float* topk_w, float* topk_w_grad,
+                               uint16_t* y_rows_grad, void* stream);
+
+/* The gradient of steps 1's router weight and bias from d logits [T][E] (moe_route_backward's):
+ *   w_router_grad[e][h]  = sum_t logits_grad[t][e] x[t][h]   (float32 [E][H])
+ *   router_bias_grad[e]  = sum_t logits_grad[t][e]           (float32 [E], or NULL)
+ * x: bf16 [T] rows of H elements, ldx >= H apart, or NULL with x_saved, a checkpoint of T rows
+ * of H.  With T = 0 all are 0.  workspace: moe_router_weight_workspace_bytes(dims), 256-byte
+ * aligned (NULL where 0).  Only T, E and H of dims are used (k and group_size are checked). */
+int moe_router_weight_workspace_bytes(const moe_dims* dims, size_t* bytes);
+int moe_router_weight_grad(const moe_dims* dims, const float* logits_grad, const uint16_t* x, int64_t ldx,
+                           const moe_checkpoint* x_saved, float* w_router_grad, float* router_bias_grad,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* Measurement aid, not a step of the layer: reads `bytes` of device memory at
  * `src` once, with 16-byte loads spread over every compute unit, and writes
  * the XOR of what each workgroup read into sink[0 .. MOE_STREAM_SINK_INTS),

@@ -35,6 +35,10 @@ EXPORTS = (
     "moe_route_counts", "moe_hot_set", "moe_residency_plan", "moe_expert_copy",
     "moe_linear_workspace_bytes", "moe_linear_kernels", "moe_linear", "moe_linear_grad",
     "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward", "moe_combine_backward",
+    "moe_adapter_workspace_bytes", "moe_adapter", "moe_adapter_grad",
+    "moe_logprobs_workspace_bytes", "moe_logprobs", "moe_logprobs_grad",
+    "moe_checkpoint_save", "moe_checkpoint_restore", "moe_combine_backward_saved",
+    "moe_router_weight_workspace_bytes", "moe_router_weight_grad",
 )
 
 
@@ -75,6 +79,18 @@ class QMatrixC(ctypes.Structure):
     """struct moe_qmatrix (include/moe.h)."""
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group_size", ctypes.c_int32), ("bits", ctypes.c_int32)]
+
+
+class AdaptersC(ctypes.Structure):
+    """struct moe_adapters (include/moe.h)."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("rank", ctypes.c_void_p), ("n", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("N", ctypes.c_int32)]
+
+
+class CheckpointC(ctypes.Structure):
+    """struct moe_checkpoint (include/moe.h)."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int32), ("K", ctypes.c_int32)]
 
 
 _lib = None
@@ -125,6 +141,18 @@ def lib() -> ctypes.CDLL:
     L.moe_balance_loss.argtypes = [Dp, P, P, P, P, P, P, P, P, sz, P, P]
     L.moe_route_backward.argtypes = [Dp, P, P, P, ctypes.c_int, P, P, P, P, P, P, P]
     L.moe_combine_backward.argtypes = [Dp, P, P, P, P, P, P, P]
+    Ap, Cp, szp, i = ctypes.POINTER(AdaptersC), ctypes.POINTER(CheckpointC), ctypes.POINTER(sz), ctypes.c_int
+    L.moe_adapter_workspace_bytes.argtypes = [Ap, i32, i, szp]
+    L.moe_adapter.argtypes = [Ap, i32, P, P, i64, P, i64, P, i64, i, P, P, sz, P]
+    L.moe_adapter_grad.argtypes = [Ap, i32, P, P, i64, i, P, i64, Cp, P, P, i64, P, i64, P, P, P, sz, P]
+    L.moe_logprobs_workspace_bytes.argtypes = [i32, i32, i32, szp]
+    L.moe_logprobs.argtypes = [i32, i32, P, i64, i, P, P, P, P, i32, P, P, P, sz, P, P]
+    L.moe_logprobs_grad.argtypes = [i32, i32, P, i64, i, P, P, P, P, P, P, i64, i, P]
+    L.moe_checkpoint_save.argtypes = [Cp, P, i64, P]
+    L.moe_checkpoint_restore.argtypes = [Cp, P, i64, P]
+    L.moe_combine_backward_saved.argtypes = [Dp, P, Cp, P, P, P, P, P]
+    L.moe_router_weight_workspace_bytes.argtypes = [Dp, szp]
+    L.moe_router_weight_grad.argtypes = [Dp, P, P, i64, Cp, P, P, P, sz, P]
     for name in EXPORTS[3:]:
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -619,15 +647,270 @@ def combine_backward(d: Dims, out_grad, y_rows, pair_to_row, topk_w, topk_w_grad
     """moe_combine_backward: the gates' gradient topk_w_grad float32 [T, k] and, if
     given, the expert rows' gradient y_rows_grad bfloat16 [T*k, H] from out_grad
     bfloat16 [T, H] (the residual's gradient is out_grad itself).  y_rows may hold
-    more rows than T*k (a shared expert's); y_rows_grad's first T*k are written."""
+    more rows than T*k (a shared expert's); y_rows_grad's first T*k are written.
+    y_rows may also be a Checkpoint of them (moe_combine_backward_saved)."""
     dev, T, H, k = out_grad.device, d.T, d.H, d.k
     P = T * k
     if pair_to_row.numel() < P:
         raise ValueError(f"pair_to_row has {pair_to_row.numel()} entries, {P} needed")
-    _enqueue(lib().moe_combine_backward, dev, stream, ctypes.byref(d), _want("out_grad", out_grad, dev, _BITS16, (T, H)),
-             _want_pair_rows("y_rows", y_rows, dev, P, H), _want("pair_to_row", pair_to_row, dev, _I32S),
+    if isinstance(y_rows, Checkpoint):
+        y_rows.check("y_rows", dev, P, H, more=True)
+        fn, y = lib().moe_combine_backward_saved, y_rows._ref
+    else:
+        fn, y = lib().moe_combine_backward, _want_pair_rows("y_rows", y_rows, dev, P, H)
+    _enqueue(fn, dev, stream, ctypes.byref(d), _want("out_grad", out_grad, dev, _BITS16, (T, H)),
+             y, _want("pair_to_row", pair_to_row, dev, _I32S),
              _want("topk_w", topk_w, dev, _F32S, (T, k)), _want("topk_w_grad", topk_w_grad, dev, _F32S, (T, k)),
              None if y_rows_grad is None else _want_pair_rows("y_rows_grad", y_rows_grad, dev, P, H))
+
+
+# ------------------------------------------------ activations kept in 8 bits
+
+@dataclass(frozen=True, eq=False)
+class Checkpoint:
+    """bfloat16 rows kept in 8 bits (struct moe_checkpoint): codes int8 [rows, K] and
+    scales float32 [rows, K/128], K a multiple of 128."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+    def __post_init__(self):
+        if self.q.dim() != 2 or self.q.shape[1] % 128:
+            raise ValueError(f"q has shape {tuple(self.q.shape)}, rows of a multiple of 128 needed")
+        rows, K = self.q.shape
+        dev = self.q.device
+        c = CheckpointC(_want("q", self.q, dev, (torch.int8,)), _want("scale", self.scale, dev, _F32S, (rows, K // 128)),
+                        rows, K)
+        for name, v in (("rows", rows), ("K", K), ("_c", c), ("_ref", ctypes.byref(c))):
+            object.__setattr__(self, name, v)
+
+    @staticmethod
+    def allocate(rows: int, K: int, device="cuda") -> "Checkpoint":
+        return Checkpoint(torch.empty((rows, K), dtype=torch.int8, device=device),
+                          torch.empty((rows, K // 128), dtype=torch.float32, device=device))
+
+    def check(self, name: str, device, rows: int, K: int, more: bool = False) -> None:
+        if self.q.device != device:
+            raise ValueError(f"{name} is on {self.q.device}, not on {device}")
+        if self.K != K or (self.rows < rows if more else self.rows != rows):
+            raise ValueError(f"{name} keeps {(self.rows, self.K)}, {'at least ' if more else ''}{(rows, K)} needed")
+
+
+def checkpoint_save(x, checkpoint: Checkpoint, stream=None):
+    """moe_checkpoint_save: x bfloat16 [rows, K], rows contiguous (any row stride)."""
+    dev = checkpoint.q.device
+    ldx = _want_rows("x", x, dev, _BITS16, checkpoint.rows, checkpoint.K)
+    _enqueue(lib().moe_checkpoint_save, dev, stream, checkpoint._ref, x.data_ptr(), ldx)
+
+
+def checkpoint_restore(checkpoint: Checkpoint, x, stream=None):
+    """moe_checkpoint_restore: into x bfloat16 [rows, K], rows contiguous (any row stride)."""
+    dev = checkpoint.q.device
+    ldx = _want_rows("x", x, dev, _BITS16, checkpoint.rows, checkpoint.K)
+    _enqueue(lib().moe_checkpoint_restore, dev, stream, checkpoint._ref, x.data_ptr(), ldx)
+
+
+def _kept_rows(name: str, x, device, rows: int, K: int):
+    """(address, row stride, checkpoint) of bfloat16 rows or of a Checkpoint of them."""
+    if isinstance(x, Checkpoint):
+        x.check(name, device, rows, K)
+        return None, 0, x._ref
+    ldx = _want_rows(name, x, device, _BITS16, rows, K)
+    return x.data_ptr(), ldx, None
+
+
+def router_weight_workspace_bytes(d: Dims) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().moe_router_weight_workspace_bytes(ctypes.byref(d), ctypes.byref(out)))
+    return int(out.value)
+
+
+@dataclass
+class RouterWeightBuffers:
+    """router_weight_grad()'s scratch, for calls of up to these dims' T, one at a time on one stream."""
+    workspace: torch.Tensor       # uint8
+
+    @staticmethod
+    def allocate(d: Dims, device="cuda") -> "RouterWeightBuffers":
+        return RouterWeightBuffers(torch.empty(max(router_weight_workspace_bytes(d), 256), dtype=torch.uint8, device=device))
+
+
+def router_weight_grad(d: Dims, logits_grad, x, w_router_grad, buffers: RouterWeightBuffers, bias_grad=None, stream=None):
+    """moe_router_weight_grad: w_router_grad float32 [E, H] (and bias_grad float32 [E])
+    from logits_grad float32 [T, E] and x bfloat16 [T, H], rows contiguous, or a
+    Checkpoint of it."""
+    dev, T, E, H = logits_grad.device, d.T, d.E, d.H
+    at, ldx, saved = _kept_rows("x", x, dev, T, H)
+    ws, nbytes = _scratch(buffers, dev)
+    _enqueue(lib().moe_router_weight_grad, dev, stream, ctypes.byref(d), _want("logits_grad", logits_grad, dev, _F32S, (T, E)),
+             at, ldx, saved, _want("w_router_grad", w_router_grad, dev, _F32S, (E, H)),
+             None if bias_grad is None else _want("bias_grad", bias_grad, dev, _F32S, (E,)), ws, nbytes)
+
+
+# --------------------------------------------------------- low-rank adapters
+
+@dataclass(frozen=True, eq=False)
+class Adapters:
+    """Low-rank adapters of many requests (struct moe_adapters): a bfloat16 [n, R, K],
+    b bfloat16 [n, R, N] whose rows may be the first N columns of a wider buffer
+    [n, R, ldb] (ldb a multiple of 8; pack() makes one), scale float32 [n], rank int32
+    [n] or None (R for all)."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: torch.Tensor
+    rank: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        if self.a.dim() != 3 or self.b.dim() != 3:
+            raise ValueError("a and b need shapes [n, R, K] and [n, R, N]")
+        n, R, K = self.a.shape
+        N, dev, b = self.b.shape[2], self.a.device, self.b
+        at = _want("a", self.a, dev, _BITS16)
+        if b.device != dev or b.dtype not in _BITS16 or b.shape[:2] != (n, R):
+            raise ValueError(f"b is {b.dtype} {tuple(b.shape)} on {b.device}, bfloat16 {(n, R, 'N')} on {dev} needed")
+        ldb = b.stride(1) if R > 1 else b.stride(0) if n > 1 else (N + 7) // 8 * 8
+        if (N > 1 and b.stride(2) != 1) or ldb < N or ldb % 8 or (n > 1 and b.stride(0) != R * ldb):
+            raise ValueError("b's rows need one stride, a multiple of 8 elements (Adapters.pack() lays them out)")
+        if b.storage_offset() + n * R * ldb > b.untyped_storage().nbytes() // b.element_size():
+            raise ValueError("b's last row ends before its stride (Adapters.pack() lays them out)")
+        c = AdaptersC(at, b.data_ptr(), ldb, _want("scale", self.scale, dev, _F32S, (n,)),
+                      None if self.rank is None else _want("rank", self.rank, dev, _I32S, (n,)), n, R, K, N)
+        for name, v in (("n", n), ("R", R), ("K", K), ("N", N), ("_c", c), ("_ref", ctypes.byref(c))):
+            object.__setattr__(self, name, v)
+
+    @staticmethod
+    def pack(downs, ups, scales, device="cuda") -> "Adapters":
+        """From each adapter's down matrix [r_i, K] and up matrix [N, r_i] (the product's
+        order) and scale: one set with R the largest r_i."""
+        ranks = [d.shape[0] for d in downs]
+        n, R, K, N = len(downs), max(ranks), downs[0].shape[1], ups[0].shape[0]
+        a = torch.zeros((n, R, K), dtype=torch.bfloat16, device=device)
+        b = torch.zeros((n, R, (N + 7) // 8 * 8), dtype=torch.bfloat16, device=device)
+        for i, (down, up) in enumerate(zip(downs, ups)):
+            a[i, :ranks[i]] = down
+            b[i, :ranks[i], :N] = up.t()
+        return Adapters(a, b[:, :, :N], torch.tensor([float(s) for s in scales], dtype=torch.float32, device=device),
+                        None if min(ranks) == R else torch.tensor(ranks, dtype=torch.int32, device=device))
+
+
+def adapter_workspace_bytes(adapters: Adapters, T: int, grad: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().moe_adapter_workspace_bytes(adapters._ref, int(T), int(bool(grad)), ctypes.byref(out)))
+    return int(out.value)
+
+
+@dataclass
+class AdapterBuffers:
+    """adapter()'s scratch (adapter_grad()'s with grad), for calls with these adapters (or a
+    set of their sizes) of up to T tokens, one at a time on one stream."""
+    workspace: torch.Tensor       # uint8
+
+    @staticmethod
+    def allocate(adapters: Adapters, T: int, grad: bool = False) -> "AdapterBuffers":
+        return AdapterBuffers(torch.empty(max(adapter_workspace_bytes(adapters, T, grad), 256), dtype=torch.uint8,
+                                          device=adapters.a.device))
+
+
+def adapter(adapters: Adapters, ids, x, y, buffers: AdapterBuffers, base=None, h=None, stream=None):
+    """moe_adapter: y = base + scale h b, h = a x of each token's adapter.  ids int32 [T]
+    (outside [0, n): none); x bfloat16 [T, K]; y bfloat16 or float32 [T, N]; base like y
+    (may be y itself) or None (0); rows contiguous, any row strides; h float32 [T, R] or
+    None: receives h for adapter_grad()."""
+    dev, T = adapters.a.device, x.shape[0]
+    ldx = _want_rows("x", x, dev, _BITS16, T, adapters.K)
+    ldy = _want_rows("y", y, dev, _VALUES, T, adapters.N)
+    ldb = 0 if base is None else _want_rows("base", base, dev, _VALUES, T, adapters.N)
+    kind = _element_type(y.dtype)
+    if base is not None and _element_type(base.dtype) != kind:
+        raise ValueError(f"base holds {base.dtype}, y {y.dtype}")
+    ws, nbytes = _scratch(buffers, dev)
+    _enqueue(lib().moe_adapter, dev, stream, adapters._ref, T, _want("ids", ids, dev, _I32S, (T,)), x.data_ptr(), ldx,
+             None if base is None else base.data_ptr(), ldb, y.data_ptr(), ldy, kind,
+             None if h is None else _want("h", h, dev, _F32S, (T, adapters.R)), ws, nbytes)
+
+
+def adapter_grad(adapters: Adapters, ids, dy, x, h, buffers: AdapterBuffers, dx=None, dx_base=None, da=None, db=None,
+                 stream=None):
+    """moe_adapter_grad: from dy bfloat16 or float32 [T, N], each written if given: dx
+    bfloat16 [T, K] (+ dx_base, which may be dx itself), da float32 [n, R, K] (needs x:
+    bfloat16 [T, K] or a Checkpoint of it, else None), db float32 [n, R, N] (needs h, else
+    None).  buffers: AdapterBuffers.allocate(adapters, T, grad=True)."""
+    dev, T, n, R, K, N = adapters.a.device, dy.shape[0], adapters.n, adapters.R, adapters.K, adapters.N
+    lddy = _want_rows("dy", dy, dev, _VALUES, T, N)
+    if (da is not None and x is None) or (db is not None and h is None):
+        raise ValueError("da needs x, and db h")
+    at, ldx, saved = (None, 0, None) if da is None else _kept_rows("x", x, dev, T, K)
+    lddx = 0 if dx is None else _want_rows("dx", dx, dev, _BITS16, T, K)
+    if dx_base is not None and dx is None:
+        raise ValueError("dx_base without dx")
+    ldbase = 0 if dx_base is None else _want_rows("dx_base", dx_base, dev, _BITS16, T, K)
+    ws, nbytes = _scratch(buffers, dev)
+    _enqueue(lib().moe_adapter_grad, dev, stream, adapters._ref, T, _want("ids", ids, dev, _I32S, (T,)), dy.data_ptr(), lddy,
+             _element_type(dy.dtype), at, ldx, saved, None if db is None else _want("h", h, dev, _F32S, (T, R)),
+             None if dx_base is None else dx_base.data_ptr(), ldbase, None if dx is None else dx.data_ptr(), lddx,
+             None if da is None else _want("da", da, dev, _F32S, (n, R, K)),
+             None if db is None else _want("db", db, dev, _F32S, (n, R, N)), ws, nbytes)
+
+
+# ------------------------------------------------------- token probabilities
+
+LOGPROBS_SYNC_INTS = 8192                    # MOE_LOGPROBS_SYNC_INTS
+
+
+def logprobs_workspace_bytes(T: int, V: int, n_top: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().moe_logprobs_workspace_bytes(int(T), int(V), int(n_top), ctypes.byref(out)))
+    return int(out.value)
+
+
+@dataclass
+class LogprobBuffers:
+    """logprobs()'s scratch, for calls of up to T rows of V logits with up to n_top
+    alternatives, one at a time on one stream."""
+    workspace: torch.Tensor       # uint8
+    sync: torch.Tensor            # int32 [LOGPROBS_SYNC_INTS], zeros (every call leaves them zero)
+
+    @staticmethod
+    def allocate(T: int, V: int, n_top: int = 0, device="cuda") -> "LogprobBuffers":
+        nbytes = max([256] + [logprobs_workspace_bytes(T, V, n) for n in range(n_top + 1)])
+        return LogprobBuffers(torch.empty(nbytes, dtype=torch.uint8, device=device),
+                              torch.zeros(LOGPROBS_SYNC_INTS, dtype=torch.int32, device=device))
+
+
+def logprobs(logits, tokens, logp, stats, buffers: LogprobBuffers, entropy=None, top_ids=None, top_logp=None, stream=None):
+    """moe_logprobs: logits bfloat16 or float32 [T, V], rows contiguous (any row stride);
+    tokens int32 [T] (outside [0, V): not scored) -> logp float32 [T], stats float32 [T, 2]
+    (maximum, logarithm of the sum relative to it; logprobs_grad()'s), entropy float32 [T]
+    or None, top_ids int32 and top_logp float32 [T, n_top] (n_top up to 64) or both None."""
+    dev, (T, V) = logits.device, logits.shape
+    ld = _want_rows("logits", logits, dev, _VALUES, T, V)
+    if (top_ids is None) != (top_logp is None):
+        raise ValueError("top_ids and top_logp go together")
+    n = 0 if top_ids is None else top_ids.shape[-1]
+    ws, nbytes = _scratch(buffers, dev)
+    _enqueue(lib().moe_logprobs, dev, stream, T, V, logits.data_ptr(), ld, _element_type(logits.dtype),
+             _want("tokens", tokens, dev, _I32S, (T,)), _want("logp", logp, dev, _F32S, (T,)),
+             _want("stats", stats, dev, _F32S, (T, 2)), None if entropy is None else _want("entropy", entropy, dev, _F32S, (T,)),
+             n, None if top_ids is None else _want("top_ids", top_ids, dev, _I32S, (T, n)),
+             None if top_logp is None else _want("top_logp", top_logp, dev, _F32S, (T, n)), ws, nbytes,
+             _want("buffers.sync", buffers.sync, dev, _I32S, (LOGPROBS_SYNC_INTS,)))
+
+
+def logprobs_grad(logits, tokens, stats, logits_grad, logp_grad=None, entropy=None, entropy_grad=None, stream=None):
+    """moe_logprobs_grad: logits_grad bfloat16 or float32 [T, V] (rows contiguous; may be the
+    logits themselves) from the gradients of logp and entropy (float32 [T], None: none) and
+    what logprobs() wrote (entropy with entropy_grad only)."""
+    dev, (T, V) = logits.device, logits.shape
+    ld = _want_rows("logits", logits, dev, _VALUES, T, V)
+    ldg = _want_rows("logits_grad", logits_grad, dev, _VALUES, T, V)
+    if entropy_grad is not None and entropy is None:
+        raise ValueError("entropy_grad needs entropy")
+    rows = (T,)
+    _enqueue(lib().moe_logprobs_grad, dev, stream, T, V, logits.data_ptr(), ld, _element_type(logits.dtype),
+             _want("tokens", tokens, dev, _I32S, rows), _want("stats", stats, dev, _F32S, (T, 2)),
+             None if logp_grad is None else _want("logp_grad", logp_grad, dev, _F32S, rows),
+             None if entropy_grad is None else _want("entropy", entropy, dev, _F32S, rows),
+             None if entropy_grad is None else _want("entropy_grad", entropy_grad, dev, _F32S, rows),
+             logits_grad.data_ptr(), ldg, _element_type(logits_grad.dtype))
 
 
 from .layer import (LayerBuffers, ResidentExperts, RouterGradBuffers, SharedBuffers, SharedExpert, StackLayer,  # noqa: E402
@@ -642,5 +925,8 @@ __all__ = [
     "QMatrix", "LinearBuffers", "linear", "linear_grad", "linear_workspace_bytes", "linear_kernels", "LINEAR_STREAMED", "LINEAR_LAID_OUT", "LINEAR_SYNC_INTS", "BF16", "F32",
     "BalanceBuffers", "balance_loss", "balance_workspace_bytes", "BALANCE_SYNC_INTS", "route_backward", "combine_backward",
     "RouterGradBuffers", "router_losses", "router_backward",
+    "Checkpoint", "checkpoint_save", "checkpoint_restore", "RouterWeightBuffers", "router_weight_grad", "router_weight_workspace_bytes",
+    "Adapters", "AdapterBuffers", "adapter", "adapter_grad", "adapter_workspace_bytes",
+    "LogprobBuffers", "logprobs", "logprobs_grad", "logprobs_workspace_bytes", "LOGPROBS_SYNC_INTS",
     "group_major", "ALGO_AUTO", "ALGO_GEMV", "ALGO_MFMA", "ALGO_GEMM", "OP_ROUTE", "OP_LOOKUP", "OP_PERMUTE", "OP_FFN", "OP_COMBINE",
 ]

@@ -1,0 +1,538 @@
+// Low-rank adapters of many requests beside a shared projection.  With i = ids[t], both
+// factors stored by rank (A [R][K], B [R][N]),
+//   h[t][r] = sum_k x[t][k] A_i[r][k],     y[t][n] = base[t][n] + s_i sum_r h[t][r] B_i[r][n];
+// backwards with dy for x and the factors changed over:
+//   g[t][r] = sum_n dy[t][n] B_i[r][n],    dx[t][k] = base[t][k] + s_i sum_r g[t][r] A_i[r][k],
+// so two kernels serve both directions: `shrink` (sums along the rows) and `expand` (sums over
+// the ranks).  The factors' gradients are weight_grad.hip's.
+//
+// A workgroup has up to 16 or 64 tokens of one adapter, so that an adapter's rows are read once
+// for them.  Few tokens (decode): a workgroup finds its tile by looking through the ids; more: a
+// first kernel puts the tokens in order.  Sums along the rows are split over workgroups where tiles
+// are few; expand adds the parts.
+//
+// Operands of v_mfma_f32_16x16x32_bf16 straight from memory.  shrink: both run along the sum,
+// 16 bytes a lane.  expand: the factor's rows run across the sum; a lane takes 8 columns of 8
+// ranks (4 where R <= 16) and turns the block by v_perm_b32; column j of every lane's 8 is
+// one product, so that a lane ends with 8 neighbouring columns of y for 4 tokens: 16-byte
+// loads and stores.  x and the factors are exact operands, h and a float32 dy go as three bf16
+// parts (all 24 bits); sums are float32, y is rounded once.
+#include <algorithm>
+#include <type_traits>
+
+#include "adapters.h"
+#include "launch_util.h"
+#include "token_tiles.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kUnitCols = 128;            // columns of a wave's step in shrink, of a wave in expand
+
+struct ShrinkArgs {
+    TokenSets who;
+    TokenPlan plan;
+    const uint16_t* w;        // [n][R][ldw]
+    int64_t ldw;
+    const void* x;
+    int64_t ldx;
+    int C, splits, units;     // units of 128 columns a split (a multiple of kWaves, but for the last)
+    float* part;              // [splits][T][16 RT]
+};
+
+struct ExpandArgs {
+    TokenSets who;
+    TokenPlan plan;
+    const uint16_t* w;
+    int64_t ldw;
+    const float* scale;
+    const float* part;
+    int splits, C;
+    const void* base;
+    int64_t ldbase;
+    void* y;
+    int64_t ldy;
+    float* h;                 // [T][R] or NULL
+};
+
+// This workgroup's tokens, into `list` (padded with the last one): their number and adapter (-1: none).
+template <bool PLAN>
+__device__ __forceinline__ int my_tile(const TokenSets& who, const TokenPlan& plan, int idx, int& set, int* list) {
+    constexpr int TOK = PLAN ? kPlanTile : kScanTile;
+    const int tid = threadIdx.x;
+    if constexpr (PLAN) {
+        if (idx >= ld_scalar(plan.counts, 0)) return 0;
+        const int4 e = plan.tiles[idx];
+        set = __builtin_amdgcn_readfirstlane(e.x);
+        const int rows = __builtin_amdgcn_readfirstlane(e.z);
+        if (tid < TOK) list[tid] = plan.order[e.y + min(tid, rows - 1)];
+        __syncthreads();
+        return rows;
+    } else {
+        __shared__ int own[kWaves][TOK];
+        const int wid = tid >> 6;
+        const int rows = scan_tile(who, idx, set, own[wid]);
+        if (rows == 0) return 0;
+        if (tid < TOK) list[tid] = own[0][min(tid, rows - 1)];
+        __syncthreads();
+        return rows;
+    }
+}
+
+}  // namespace
+
+template <int RT, bool F32, bool PLAN>
+__global__ __launch_bounds__(64 * kWaves) void adapter_shrink_kernel(ShrinkArgs a) {
+    constexpr int NT = PLAN ? kPlanTile / 16 : 1, PARTS = F32 ? 3 : 1;
+    __shared__ int list[16 * NT];
+    __shared__ __attribute__((aligned(16))) float sums[kWaves][16][16 * RT + 4];
+    int set;
+    const int rows = my_tile<PLAN>(a.who, a.plan, (int)blockIdx.y, set, list);
+    if (rows == 0 || set < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int rank = a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), a.who.R) : a.who.R;
+    const int all = (a.C + kUnitCols - 1) / kUnitCols;
+    const int u0 = (int)blockIdx.x * a.units, u1 = min(u0 + a.units, all);
+    const uint16_t* w[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+        w[rt] = a.w + ((int64_t)set * a.who.R + min(16 * rt + c, max(rank - 1, 0))) * a.ldw;
+    int64_t xrow[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xrow[nt] = (int64_t)list[16 * nt + c] * a.ldx;
+    floatx4_t acc[NT][RT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[nt][rt] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    // 32 columns; with TAIL some of them do not exist (both operands read as 0 there)
+    auto step = [&](int col, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        uint32_t wf[RT][4], xf[NT][PARTS][4], m[4];
+        const int at = TAIL ? first_of_8(col, a.C) : col;
+        if constexpr (TAIL) mask_first(col - at, m);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const uint4 v = load_bf16x8(w[rt] + at);
+            wf[rt][0] = v.x; wf[rt][1] = v.y; wf[rt][2] = v.z; wf[rt][3] = v.w;
+            if constexpr (TAIL)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) wf[rt][d] &= m[d];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (F32) {
+                float v[8];
+                __builtin_memcpy(v, static_cast<const float*>(a.x) + xrow[nt] + at, 32);
+                if constexpr (TAIL)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = j >= col - at ? v[j] : 0.f;
+                bf16_parts<PARTS>(v, xf[nt]);
+            } else {
+                const uint4 v = load_bf16x8(static_cast<const uint16_t*>(a.x) + xrow[nt] + at);
+                xf[nt][0][0] = v.x; xf[nt][0][1] = v.y; xf[nt][0][2] = v.z; xf[nt][0][3] = v.w;
+                if constexpr (TAIL)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) xf[nt][0][d] &= m[d];
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) acc[nt][rt] = mfma16(wf[rt], xf[nt][p], acc[nt][rt]);
+    };
+    for (int u = u0 + wid; u < u1; u += kWaves) {
+        const int c0 = u * kUnitCols + 8 * q;
+        if ((u + 1) * kUnitCols <= a.C) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) step(c0 + 32 * p, std::false_type{});
+        } else {
+            for (int p = 0; p < 4; ++p) step(c0 + 32 * p, std::true_type{});
+        }
+    }
+    // the waves' sums, 16 tokens at a time; ranks past the adapter's are 0
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (16 * nt >= rows) break;
+        if (nt) __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) *reinterpret_cast<floatx4_t*>(&sums[wid][c][16 * rt + 4 * q]) = acc[nt][rt];
+        __syncthreads();
+        for (int e = tid; e < 16 * 4 * RT; e += 64 * kWaves) {
+            const int row = e / (4 * RT), r = 4 * (e % (4 * RT));
+            if (16 * nt + row >= rows) break;
+            floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[0][row][r]);
+#pragma unroll
+            for (int k = 1; k < kWaves; ++k) v += *reinterpret_cast<const floatx4_t*>(&sums[k][row][r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.f;
+            *reinterpret_cast<floatx4_t*>(a.part + ((int64_t)blockIdx.x * a.who.T + list[16 * nt + row]) * (16 * RT) + r) = v;
+        }
+    }
+}
+
+// RT = 1: products over 16 ranks (v_mfma_f32_16x16x16_bf16); else over 32 at a time.
+template <int RT, bool F32, bool PLAN>
+__global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs a) {
+    constexpr int NT = PLAN ? kPlanTile / 16 : 1, TOK = 16 * NT, RP = 16 * RT, KS = RT == 1 ? 1 : RT / 2;
+    constexpr int HS = RP + 4, PARTS = 3, PER = RT == 1 ? 4 : 8;      // ranks a lane holds of a step
+    __shared__ int list[TOK];
+    __shared__ __attribute__((aligned(16))) float hs[TOK][HS];
+    int set;
+    const int rows = my_tile<PLAN>(a.who, a.plan, (int)blockIdx.y, set, list);
+    if (rows == 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int R = a.who.R;
+    const int rank = set < 0 ? 0 : a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), R) : R;
+    const int own = ((int)blockIdx.x * kWaves + wid) * kUnitCols + 8 * c;
+    const int col = first_of_8(own, a.C), shift = own - col;           // 8 or more: no column is this lane's
+
+    // the sums of the tile's tokens: the splits' parts
+    const float s = set < 0 ? 0.f : ld_scalar(a.scale, set);
+    for (int e = tid; e < TOK * (RP / 4); e += 64 * kWaves) {
+        const int row = e / (RP / 4), r = 4 * (e % (RP / 4));
+        floatx4_t v{0.f, 0.f, 0.f, 0.f};
+        if (row < rows && set >= 0)
+            for (int k = 0; k < a.splits; ++k)
+                v += *reinterpret_cast<const floatx4_t*>(a.part + ((int64_t)k * a.who.T + list[row]) * RP + r);
+        if (a.h && blockIdx.x == 0 && row < rows)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r + i < R) a.h[(int64_t)list[row] * R + r + i] = v[i];
+        *reinterpret_cast<floatx4_t*>(&hs[row][r]) = v * s;
+    }
+    __syncthreads();
+    if (a.y == nullptr || (int)(blockIdx.x * kWaves + wid) * kUnitCols >= a.C) return;
+    if (set < 0 && a.y == a.base) return;
+
+    // the factor's block, turned: column j of the lane's 8, its ranks in order
+    uint32_t wf[KS][8][PER / 2];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        uint4 rowv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= PER) { rowv[i] = make_uint4(0, 0, 0, 0); continue; }
+            rowv[i] = load_bf16x8(a.w + ((int64_t)max(set, 0) * R + min(32 * ks + PER * q + i, max(rank - 1, 0))) * a.ldw + col);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)                                  // (what lies past the rank may be no number)
+            if (32 * ks + PER * q + i >= rank) rowv[i] = make_uint4(0, 0, 0, 0);
+        uint32_t t[8][4];
+        turn8(rowv, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int d = 0; d < PER / 2; ++d) wf[ks][j][d] = t[j][d];
+    }
+    const bool some = rank > 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (16 * nt >= rows) break;
+        floatx4_t acc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        // the base's rows 4 q + i (the list is padded with its last token)
+        uint4 bb[4][F32 ? 2 : 1];
+        if (a.base) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldbase + col;
+                if constexpr (F32) __builtin_memcpy(bb[i], static_cast<const float*>(a.base) + at, 32);
+                else bb[i][0] = load_bf16x8(static_cast<const uint16_t*>(a.base) + at);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < (F32 ? 2 : 1); ++d) bb[i][d] = make_uint4(0, 0, 0, 0);
+        }
+        if (some) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                float v[8];
+                uint32_t hp[PARTS][4];
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    const floatx4_t f = i < PER ? *reinterpret_cast<const floatx4_t*>(&hs[16 * nt + c][32 * ks + PER * q + i])
+                                                : floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i + e] = f[e];
+                }
+                bf16_parts<PARTS>(v, hp);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if constexpr (RT == 1) {
+                            typedef short s16x4_t __attribute__((ext_vector_type(4)));
+                            const uint2 A = make_uint2(hp[p][0], hp[p][1]), B = make_uint2(wf[0][j][0], wf[0][j][1]);
+                            acc[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4_t, A),
+                                                                              __builtin_bit_cast(s16x4_t, B), acc[j], 0, 0, 0);
+                        } else {
+                            acc[j] = mfma16(hp[p], wf[ks][j], acc[j]);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (shift >= 8 || 16 * nt + 4 * q + i >= rows) continue;
+            const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldy + col;
+            float v[8];
+            if constexpr (F32) {
+                __builtin_memcpy(v, bb[i], 32);
+            } else {
+                const uint32_t b[4] = {bb[i][0].x, bb[i][0].y, bb[i][0].z, bb[i][0].w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((j & 1) ? b[j >> 1] & 0xFFFF0000u : b[j >> 1] << 16);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
+            if constexpr (F32) {
+                float* out = static_cast<float*>(a.y) + at;
+                if (shift == 0) {
+                    __builtin_memcpy(out, v, 32);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= shift) out[j] = v[j];
+                }
+            } else {
+                uint16_t* out = static_cast<uint16_t*>(a.y) + at;
+                uint32_t o[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) o[d] = pack_bf16(v[2 * d], v[2 * d + 1]);
+                if (shift == 0) {
+                    __builtin_memcpy(out, o, 16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= shift) out[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+                }
+            }
+        }
+    }
+}
+
+// Tokens in order of their adapters (equal ones in token order), and the tiles and chunks made of
+// them.  One workgroup: wave w has a run of the tokens; its counts per adapter, scanned over waves
+// and adapters, are where its tokens of each go.
+constexpr int kPlanWaves = 16;
+__global__ __launch_bounds__(64 * kPlanWaves) void adapter_plan_kernel(TokenSets who, TokenPlan plan) {
+    extern __shared__ int counts[];                   // [kPlanWaves][n + 1]; set n: tokens without an adapter
+    __shared__ int4 wave_total[kPlanWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sets = who.n + 1;
+    const int run = ((who.T + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64;
+    const int t0 = wid * run, t1 = min(t0 + run, who.T);
+    for (int i = tid; i < kPlanWaves * sets; i += 64 * kPlanWaves) counts[i] = 0;
+    __syncthreads();
+    auto set_at = [&](int t) { const int i = set_of(who.ids, t, who.n); return i < 0 ? who.n : i; };
+    for (int t = t0 + lane; t < t1; t += 64) atomicAdd(&counts[wid * sets + set_at(t)], 1);
+    __syncthreads();
+    // thread i: set i (at most 1025 sets, so the first threads may have a second one)
+    int first = 0, tile = 0, chunk = 0, slot = 0;     // running totals of the sets before this round's
+    for (int base = 0; base < sets; base += 64 * kPlanWaves) {
+        const int i = base + tid;
+        int mine = 0;
+        if (i < sets)
+            for (int w = 0; w < kPlanWaves; ++w) mine += counts[w * sets + i];
+        const int chunks = i < who.n ? max(1, (mine + plan.chunk - 1) / plan.chunk) : 0;
+        int4 v = make_int4(mine, (mine + kPlanTile - 1) / kPlanTile, chunks, chunks > 1 ? chunks : 0);
+        const int4 own = v;
+        for (int off = 1; off < 64; off <<= 1) {
+            const int4 o = make_int4(__shfl_up(v.x, off), __shfl_up(v.y, off), __shfl_up(v.z, off), __shfl_up(v.w, off));
+            if (lane >= off) { v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w; }
+        }
+        if (lane == 63) wave_total[wid] = v;
+        __syncthreads();
+        int4 before = make_int4(first, tile, chunk, slot);
+        for (int w = 0; w < kPlanWaves; ++w) {
+            const int4 o = wave_total[w];
+            if (w < wid) { before.x += o.x; before.y += o.y; before.z += o.z; before.w += o.w; }
+            first += o.x; tile += o.y; chunk += o.z; slot += o.w;
+        }
+        before.x += v.x - own.x; before.y += v.y - own.y; before.z += v.z - own.z; before.w += v.w - own.w;
+        if (i < sets) {
+            for (int k = 0; k < own.y; ++k)
+                plan.tiles[before.y + k] = make_int4(i < who.n ? i : -1, before.x + k * kPlanTile, min(kPlanTile, own.x - k * kPlanTile), 0);
+            for (int k = 0; k < own.z; ++k)
+                plan.chunks[before.z + k] = make_int4(i, before.x + k * plan.chunk, min(plan.chunk, own.x - k * plan.chunk),
+                                                      own.z > 1 ? before.w + k : -1);
+            if (i < who.n) plan.joins[i] = make_int2(before.w, own.w);
+            int at = before.x;
+            for (int w = 0; w < kPlanWaves; ++w) {
+                const int cnt = counts[w * sets + i];
+                counts[w * sets + i] = at;
+                at += cnt;
+            }
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        plan.counts[0] = tile;
+        plan.counts[1] = chunk;
+    }
+    // 64 tokens at a time: a token's place is its set's next one plus those of the set in lower lanes
+    for (int t = t0 + lane; t - lane < t1; t += 64) {
+        const int set = t < t1 ? set_at(t) : -1;
+        uint64_t left = __ballot(set >= 0);
+        while (left) {
+            const int lead = __ffsll((unsigned long long)left) - 1;
+            const int which = __shfl(set, lead, kWave);
+            const uint64_t same = __ballot(set == which);
+            const int at = counts[wid * sets + which];
+            if (set == which)
+                plan.order[at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] = t;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            if (lane == 0) counts[wid * sets + which] = at + __popcll(same);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            left &= ~same;
+        }
+    }
+}
+
+namespace {
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+bool planned(int T) { return T > kScanTokens; }
+
+// Workgroups' worth of tiles, and how the columns of a shrink are split: workgroups twice the
+// CUs where there are columns for it, four waves each with a unit at least.
+constexpr int kMostSplits = 16, kShrinkBlocks = 512;
+int shrink_splits(int T, int n, int C) {
+    const int sets = std::max(1, std::min(n, T));
+    const int tiles = planned(T) ? (T + kPlanTile - 1) / kPlanTile + sets / 2 : sets;
+    const int units = (C + kUnitCols - 1) / kUnitCols, most = (units + kWaves - 1) / kWaves;
+    return std::min({(kShrinkBlocks + tiles - 1) / tiles, most, kMostSplits});
+}
+
+// Rows of partial sums that calls of up to T tokens need at most: no more splits than kMostSplits,
+// and past kScanTokens no more than (kShrinkBlocks + tiles) / tiles with T / kPlanTile tiles or more.
+int64_t part_rows(int T) { return std::min((int64_t)kMostSplits * T, (int64_t)kShrinkBlocks * kPlanTile + T); }
+
+struct Space {
+    float* part;
+    float* g;
+    TokenPlan plan;
+    float* grad_part;
+    size_t bytes;
+};
+
+Space space(const moe_adapters& m, int T, bool grad, const WeightGradPlan& p, void* ws) {
+    char* at = static_cast<char*>(ws);
+    auto take = [&](size_t n) { char* r = at; at += up256(n); return r; };
+    Space sp{};
+    sp.part = reinterpret_cast<float*>(take((size_t)part_rows(T) * 16 * rank_tiles(m.R) * 4));
+    if (grad) {
+        sp.g = reinterpret_cast<float*>(take((size_t)T * m.R * 4));
+        sp.grad_part = reinterpret_cast<float*>(take(p.most_floats * 4));
+    }
+    if (planned(T)) {
+        const int tiles = T / kPlanTile + m.n + 1, chunk = grad ? p.chunk : T;
+        sp.plan.order = reinterpret_cast<int32_t*>(take((size_t)T * 4));
+        sp.plan.tiles = reinterpret_cast<int4*>(take((size_t)tiles * 16));
+        sp.plan.chunks = reinterpret_cast<int4*>(take((size_t)(T / kLeastChunk + m.n) * 16));
+        sp.plan.joins = reinterpret_cast<int2*>(take((size_t)m.n * 8));
+        sp.plan.counts = reinterpret_cast<int32_t*>(take(8));
+        sp.plan.chunk = chunk;
+    }
+    sp.bytes = (size_t)(at - static_cast<char*>(ws));
+    return sp;
+}
+
+template <bool F32, bool PLAN>
+void shrink_go(const ShrinkArgs& a, dim3 grid, hipStream_t s) {
+    switch (rank_tiles(a.who.R)) {
+        case 1: hipLaunchKernelGGL((adapter_shrink_kernel<1, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
+        case 2: hipLaunchKernelGGL((adapter_shrink_kernel<2, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
+        case 4: hipLaunchKernelGGL((adapter_shrink_kernel<4, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
+        default: hipLaunchKernelGGL((adapter_shrink_kernel<8, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a);
+    }
+}
+
+template <bool F32, bool PLAN>
+void expand_go(const ExpandArgs& a, dim3 grid, hipStream_t s) {
+    switch (rank_tiles(a.who.R)) {
+        case 1: hipLaunchKernelGGL((adapter_expand_kernel<1, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
+        case 2: hipLaunchKernelGGL((adapter_expand_kernel<2, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
+        case 4: hipLaunchKernelGGL((adapter_expand_kernel<4, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
+        default: hipLaunchKernelGGL((adapter_expand_kernel<8, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a);
+    }
+}
+
+unsigned tile_blocks(const TokenSets& who) {
+    return planned(who.T) ? (unsigned)(who.T / kPlanTile + (who.n < who.T ? who.n : who.T) + 1) : (unsigned)who.T;
+}
+
+void shrink(const TokenSets& who, const Space& sp, const uint16_t* w, int64_t ldw, int C, const void* x, int64_t ldx, bool f32,
+            hipStream_t s) {
+    ShrinkArgs a{};
+    a.who = who; a.plan = sp.plan; a.w = w; a.ldw = ldw; a.C = C; a.x = x; a.ldx = ldx; a.part = sp.part;
+    a.splits = shrink_splits(who.T, who.n, C);
+    const int units = (C + kUnitCols - 1) / kUnitCols;
+    a.units = ((units + a.splits - 1) / a.splits + kWaves - 1) / kWaves * kWaves;
+    const dim3 grid((unsigned)a.splits, tile_blocks(who));
+    if (planned(who.T)) f32 ? shrink_go<true, true>(a, grid, s) : shrink_go<false, true>(a, grid, s);
+    else f32 ? shrink_go<true, false>(a, grid, s) : shrink_go<false, false>(a, grid, s);
+}
+
+void expand(const TokenSets& who, const Space& sp, int splits, const float* scale, const uint16_t* w, int64_t ldw, int C,
+            const void* base, int64_t ldbase, void* y, int64_t ldy, bool f32, float* h, hipStream_t s) {
+    ExpandArgs a{};
+    a.who = who; a.plan = sp.plan; a.w = w; a.ldw = ldw; a.scale = scale; a.part = sp.part; a.splits = splits; a.C = C;
+    a.base = base; a.ldbase = ldbase; a.y = y; a.ldy = ldy; a.h = h;
+    const unsigned blocks = y ? (unsigned)((C + kWaves * kUnitCols - 1) / (kWaves * kUnitCols)) : 1u;
+    const dim3 grid(blocks, tile_blocks(who));
+    if (planned(who.T)) f32 ? expand_go<true, true>(a, grid, s) : expand_go<false, true>(a, grid, s);
+    else f32 ? expand_go<true, false>(a, grid, s) : expand_go<false, false>(a, grid, s);
+}
+
+void make_plan(const TokenSets& who, const TokenPlan& plan, hipStream_t s) {
+    hipLaunchKernelGGL(adapter_plan_kernel, dim3(1), dim3(64 * kPlanWaves), kPlanWaves * (who.n + 1) * 4, s, who, plan);
+}
+
+}  // namespace
+
+size_t adapter_workspace_bytes(const moe_adapters& m, int T, bool grad) {
+    const WeightGradPlan p = grad ? weight_grad_plan(T, m.n, m.R, m.K, m.N) : WeightGradPlan{};
+    return space(m, T, grad, p, nullptr).bytes;
+}
+
+int launch_adapter(const moe_adapters& m, int T, const int32_t* ids, const uint16_t* x, int64_t ldx, const void* base,
+                   int64_t ldbase, void* y, int64_t ldy, int y_type, float* h, void* ws, hipStream_t s) {
+    const TokenSets who{ids, m.rank, T, m.n, m.R};
+    const Space sp = space(m, T, false, WeightGradPlan{}, ws);
+    if (planned(T)) make_plan(who, sp.plan, s);
+    shrink(who, sp, m.a, m.K, m.K, x, ldx, false, s);
+    expand(who, sp, shrink_splits(T, m.n, m.K), m.scale, m.b, m.ldb, m.N, base, ldbase, y, ldy, y_type == MOE_F32, h, s);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int launch_adapter_grad(const AdapterGradArgs& a, hipStream_t s) {
+    const moe_adapters& m = a.m;
+    const TokenSets who{a.ids, m.rank, a.T, m.n, m.R};
+    const WeightGradPlan p = weight_grad_plan(a.T, m.n, m.R, m.K, m.N);
+    const Space sp = space(m, a.T, true, p, a.ws);
+    const bool f32 = a.dy_type == MOE_F32;
+    if (planned(a.T)) make_plan(who, sp.plan, s);
+    if (a.T > 0 && (a.dx || a.da)) {
+        shrink(who, sp, m.b, m.ldb, m.N, a.dy, a.lddy, f32, s);
+        expand(who, sp, shrink_splits(a.T, m.n, m.N), m.scale, m.a, m.K, m.K, a.dx_base, a.lddx_base, a.dx, a.lddx, false, sp.g, s);
+    }
+    WeightGradCall calls[2];
+    int n = 0;
+    if (a.da) calls[n++] = WeightGradCall{sp.g, m.R, a.x, a.ldx, a.xscale, a.xscale ? kCodes : MOE_BF16, m.K, a.da, nullptr};
+    if (a.db) calls[n++] = WeightGradCall{a.h, m.R, a.dy, a.lddy, nullptr, a.dy_type, m.N, a.db, nullptr};
+    if (n) return launch_weight_grad(who, planned(a.T) ? &sp.plan : nullptr, m.scale, p, calls, n, sp.grad_part, s);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // namespace moe

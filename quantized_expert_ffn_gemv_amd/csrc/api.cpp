@@ -7,8 +7,10 @@
 #include <cstdio>
 #include <cstring>
 
+#include "adapters.h"
 #include "common.h"
 #include "linear.h"
+#include "logprobs.h"
 #include "moe.h"
 
 namespace {
@@ -179,15 +181,82 @@ bool rows_meet(const void* a, int64_t la, int64_t wa, const void* b, int64_t lb,
     return off < wa || off + wb > la;
 }
 
-int check_linear_workspace(const char* fn, const moe_qmatrix* w, int32_t T, int type, bool grad, const void* ws,
-                           size_t ws_bytes) {
-    const size_t need = moe::linear_workspace_bytes(*w, T, type, grad);
+// A workspace of `need` bytes (NULL where that is 0).
+int check_scratch(const char* fn, size_t need, const void* ws, size_t ws_bytes) {
     if (need == 0) return MOE_OK;
     if (ws == nullptr || ws_bytes < need)
         return fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", fn, need,
                     ws == nullptr ? (size_t)0 : ws_bytes);
     if (!aligned(ws, 256)) return fail(MOE_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
     return MOE_OK;
+}
+
+int check_tokens(const char* fn, int32_t T) {
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T = %d is negative", fn, T);
+    if (T > 65536) return fail(MOE_ERR_UNSUPPORTED, "%s: T = %d exceeds 65536", fn, T);
+    return MOE_OK;
+}
+
+int check_type(const char* fn, const char* what, int type) {
+    if (type != MOE_BF16 && type != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %s %d (MOE_BF16 or MOE_F32)", fn, what, type);
+    return MOE_OK;
+}
+
+int check_rows_of_logits(const char* fn, int32_t T, int32_t V, int32_t n_top) {
+    const int st = check_tokens(fn, T);
+    if (st) return st;
+    if (V < 1 || V > 1048576) return fail(MOE_ERR_UNSUPPORTED, "%s: V = %d outside [1, 1048576]", fn, V);
+    if (n_top < 0 || n_top > 64) return fail(MOE_ERR_UNSUPPORTED, "%s: n_top = %d outside [0, 64]", fn, n_top);
+    return MOE_OK;
+}
+
+// A set of adapters; the pointers too if `pointers`.
+int check_adapters(const char* fn, const moe_adapters* m, int32_t T, bool pointers) {
+    if (m == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: adapters is NULL", fn);
+    int st = check_tokens(fn, T);
+    if (st) return st;
+    if (m->n < 1 || m->n > 1024) return fail(MOE_ERR_UNSUPPORTED, "%s: n = %d outside [1, 1024]", fn, m->n);
+    if (m->R < 1 || m->R > 128) return fail(MOE_ERR_UNSUPPORTED, "%s: R = %d outside [1, 128]", fn, m->R);
+    if (m->K < 128 || m->K > 32768 || m->K % 128 != 0)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 128 in [128, 32768]", fn, m->K);
+    if (m->N < 8 || m->N > 1048576) return fail(MOE_ERR_UNSUPPORTED, "%s: N = %d outside [8, 1048576]", fn, m->N);
+    if (m->ldb < m->N || m->ldb % 8 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: ldb = %lld must be a multiple of 8, at least N = %d", fn, (long long)m->ldb, m->N);
+    if (!pointers) return MOE_OK;
+    REQUIRE_PTR(m->a, 16);
+    REQUIRE_PTR(m->b, 16);
+    REQUIRE_PTR(m->scale, 4);
+    if (m->rank && !aligned(m->rank, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: rank is not 4-byte aligned", fn);
+    return MOE_OK;
+}
+
+// Rows of `cols` elements of `wide` bytes, ld apart.
+int check_rows(const char* fn, const char* name, const void* p, int64_t ld, int32_t cols, int wide) {
+    if (p == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (!aligned(p, wide)) return fail(MOE_ERR_INVALID_ARG, "%s: %s is not %d-byte aligned", fn, name, wide);
+    if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "%s: the rows of %s are %lld apart, less than %d", fn, name, (long long)ld, cols);
+    return MOE_OK;
+}
+
+// A checkpoint of at least `rows` rows of K.
+int check_checkpoint(const char* fn, const char* name, const moe_checkpoint* c, int64_t rows, int32_t K) {
+    if (c == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (c->K < 128 || c->K > 32768 || c->K % 128 != 0)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: K = %d of %s must be a multiple of 128 in [128, 32768]", fn, c->K, name);
+    if (c->rows < 0 || c->rows > 4194304) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %d of %s outside [0, 4194304]", fn, c->rows, name);
+    if (K > 0 && c->K != K) return fail(MOE_ERR_INVALID_ARG, "%s: %s has rows of %d, %d needed", fn, name, c->K, K);
+    if (c->rows < rows) return fail(MOE_ERR_INVALID_ARG, "%s: %s has %d rows, %lld needed", fn, name, c->rows, (long long)rows);
+    if (c->rows == 0) return MOE_OK;
+    if (!c->q || !c->scale) return fail(MOE_ERR_INVALID_ARG, "%s: %s has a NULL pointer", fn, name);
+    if (!aligned(c->q, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: the codes of %s are not 16-byte aligned", fn, name);
+    if (!aligned(c->scale, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: the scales of %s are not 4-byte aligned", fn, name);
+    return MOE_OK;
+}
+
+int check_linear_workspace(const char* fn, const moe_qmatrix* w, int32_t T, int type, bool grad, const void* ws,
+                           size_t ws_bytes) {
+    return check_scratch(fn, moe::linear_workspace_bytes(*w, T, type, grad), ws, ws_bytes);
 }
 
 }  // namespace
@@ -812,6 +881,234 @@ int moe_combine_backward(const moe_dims* d, const uint16_t* out_grad, const uint
     }
     st = moe::launch_combine_backward(*d, out_grad, y_rows, pair_to_row, topk_w, topk_w_grad, y_rows_grad,
                                       as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_adapter_workspace_bytes(const moe_adapters* m, int32_t T, int grad, size_t* bytes) {
+    const char* fn = "moe_adapter_workspace_bytes";
+    if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+    const int st = check_adapters(fn, m, T, false);
+    if (st) return st;
+    *bytes = moe::adapter_workspace_bytes(*m, T, grad != 0);
+    return ok();
+}
+
+int moe_adapter(const moe_adapters* m, int32_t T, const int32_t* ids, const uint16_t* x, int64_t ldx, const void* base,
+                int64_t ldbase, void* y, int64_t ldy, int y_type, float* h, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "moe_adapter";
+    int st = check_adapters(fn, m, T, T != 0);
+    if (!st) st = check_type(fn, "element type", y_type);
+    if (st) return st;
+    if (T == 0) return ok();
+    const int e = y_type == MOE_F32 ? 4 : 2;
+    REQUIRE_PTR(ids, 4);
+    st = check_rows(fn, "x", x, ldx, m->K, 2);
+    if (!st) st = check_rows(fn, "y", y, ldy, m->N, e);
+    if (!st && base) st = check_rows(fn, "base", base, ldbase, m->N, e);
+    if (st) return st;
+    if (h && !aligned(h, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: h is not 4-byte aligned", fn);
+    if (base == y && ldbase != ldy) return fail(MOE_ERR_INVALID_ARG, "%s: y is the base but differs from it in row stride", fn);
+    st = check_scratch(fn, moe::adapter_workspace_bytes(*m, T, false), ws, ws_bytes);
+    if (st) return st;
+    const int64_t wy = (int64_t)e * m->N;
+    if (rows_meet(y, e * ldy, wy, x, 2 * ldx, 2 * (int64_t)m->K, T) ||
+        (base && base != y && rows_meet(y, e * ldy, wy, base, e * ldbase, wy, T)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
+    st = moe::launch_adapter(*m, T, ids, x, ldx, base, ldbase, y, ldy, y_type, h, ws, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_adapter_grad(const moe_adapters* m, int32_t T, const int32_t* ids, const void* dy, int64_t lddy, int dy_type,
+                     const uint16_t* x, int64_t ldx, const moe_checkpoint* x_saved, const float* h,
+                     const uint16_t* dx_base, int64_t lddx_base, uint16_t* dx, int64_t lddx, float* da, float* db,
+                     void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "moe_adapter_grad";
+    int st = check_adapters(fn, m, T, T != 0);
+    if (!st) st = check_type(fn, "element type", dy_type);
+    if (st) return st;
+    if (da && !aligned(da, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: da is not 4-byte aligned", fn);
+    if (db && !aligned(db, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: db is not 4-byte aligned", fn);
+    const int e = dy_type == MOE_F32 ? 4 : 2;
+    moe::AdapterGradArgs a{};
+    a.m = *m; a.T = T; a.ids = ids; a.dy = dy; a.lddy = lddy; a.dy_type = dy_type; a.h = h;
+    a.dx_base = dx ? dx_base : nullptr; a.lddx_base = lddx_base; a.dx = dx; a.lddx = lddx; a.da = da; a.db = db; a.ws = ws;
+    if (T > 0) {
+        REQUIRE_PTR(ids, 4);
+        st = check_rows(fn, "dy", dy, lddy, m->N, e);
+        if (!st && da && x) st = check_rows(fn, "x", x, ldx, m->K, 2);
+        if (!st && dx) st = check_rows(fn, "dx", dx, lddx, m->K, 2);
+        if (!st && a.dx_base) st = check_rows(fn, "dx_base", dx_base, lddx_base, m->K, 2);
+        if (st) return st;
+        if (da && (x != nullptr) == (x_saved != nullptr))
+            return fail(MOE_ERR_INVALID_ARG, "%s: da needs either x or x_saved", fn);
+        if (da && x_saved) {
+            st = check_checkpoint(fn, "x_saved", x_saved, T, m->K);
+            if (st) return st;
+        }
+        if (db) REQUIRE_PTR(h, 4);
+        if (a.dx_base == dx && dx && lddx_base != lddx)
+            return fail(MOE_ERR_INVALID_ARG, "%s: dx is dx_base but differs from it in row stride", fn);
+        const int64_t wx = 2 * (int64_t)m->K;
+        if (dx && (rows_meet(dx, 2 * lddx, wx, dy, e * lddy, (int64_t)e * m->N, T) ||
+                   (da && x && rows_meet(dx, 2 * lddx, wx, x, 2 * ldx, wx, T)) ||
+                   (a.dx_base && a.dx_base != dx && rows_meet(dx, 2 * lddx, wx, dx_base, 2 * lddx_base, wx, T))))
+            return fail(MOE_ERR_INVALID_ARG, "%s: dx overlaps an input", fn);
+    }
+    st = check_scratch(fn, moe::adapter_workspace_bytes(*m, T, true), ws, ws_bytes);
+    if (st) return st;
+    if (x_saved && da && T > 0) {
+        a.x = x_saved->q; a.ldx = m->K; a.xscale = x_saved->scale;
+    } else {
+        a.x = x; a.ldx = ldx;
+    }
+    if (T == 0) a.dx = nullptr;
+    st = moe::launch_adapter_grad(a, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top, size_t* bytes) {
+    const char* fn = "moe_logprobs_workspace_bytes";
+    if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+    const int st = check_rows_of_logits(fn, T, V, n_top);
+    if (st) return st;
+    *bytes = moe::logprobs_workspace_bytes(T, V, n_top);
+    return ok();
+}
+
+int moe_logprobs(int32_t T, int32_t V, const void* logits, int64_t ld, int type, const int32_t* tokens, float* logp,
+                 float* stats, float* entropy, int32_t n_top, int32_t* top_ids, float* top_logp, void* ws,
+                 size_t ws_bytes, int32_t* sync, void* stream) {
+    const char* fn = "moe_logprobs";
+    int st = check_rows_of_logits(fn, T, V, n_top);
+    if (!st) st = check_type(fn, "element type", type);
+    if (st) return st;
+    if (T == 0) return ok();
+    st = check_rows(fn, "logits", logits, ld, V, type == MOE_F32 ? 4 : 2);
+    if (st) return st;
+    REQUIRE_PTR(tokens, 4);
+    REQUIRE_PTR(logp, 4);
+    REQUIRE_PTR(stats, 4);
+    if (entropy && !aligned(entropy, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: entropy is not 4-byte aligned", fn);
+    if (n_top) {
+        REQUIRE_PTR(top_ids, 4);
+        REQUIRE_PTR(top_logp, 4);
+    }
+    REQUIRE_PTR(sync, 256);
+    st = check_scratch(fn, moe::logprobs_workspace_of(T, V, n_top), ws, ws_bytes);
+    if (st) return st;
+    moe::LogprobArgs a{};
+    a.T = T; a.V = V; a.logits = logits; a.ld = ld; a.type = type; a.tokens = tokens; a.logp = logp; a.stats = stats;
+    a.entropy = entropy; a.n_top = n_top; a.top_ids = top_ids; a.top_logp = top_logp; a.part = static_cast<float*>(ws); a.sync = sync;
+    st = moe::launch_logprobs(a, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_logprobs_grad(int32_t T, int32_t V, const void* logits, int64_t ld, int type, const int32_t* tokens,
+                      const float* stats, const float* logp_grad, const float* entropy, const float* entropy_grad,
+                      void* logits_grad, int64_t ldg, int grad_type, void* stream) {
+    const char* fn = "moe_logprobs_grad";
+    int st = check_rows_of_logits(fn, T, V, 0);
+    if (!st) st = check_type(fn, "element type", type);
+    if (!st) st = check_type(fn, "gradient's element type", grad_type);
+    if (st) return st;
+    if (T == 0) return ok();
+    const int64_t e = type == MOE_F32 ? 4 : 2, eg = grad_type == MOE_F32 ? 4 : 2;
+    st = check_rows(fn, "logits", logits, ld, V, (int)e);
+    if (!st) st = check_rows(fn, "logits_grad", logits_grad, ldg, V, (int)eg);
+    if (st) return st;
+    REQUIRE_PTR(tokens, 4);
+    REQUIRE_PTR(stats, 4);
+    if (logp_grad && !aligned(logp_grad, 4)) return fail(MOE_ERR_INVALID_ARG, "%s: logp_grad is not 4-byte aligned", fn);
+    if (entropy_grad) {
+        REQUIRE_PTR(entropy_grad, 4);
+        REQUIRE_PTR(entropy, 4);
+    }
+    if (logits_grad == logits ? (type != grad_type || ld != ldg) : rows_meet(logits_grad, eg * ldg, eg * V, logits, e * ld, e * V, T))
+        return fail(MOE_ERR_INVALID_ARG, "%s: logits_grad overlaps the logits in another type or stride", fn);
+    const moe::LogprobGradArgs a{T, V, logits, ld, type, tokens, stats, logp_grad, entropy, entropy_grad, logits_grad, ldg, grad_type};
+    st = moe::launch_logprobs_grad(a, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_checkpoint_save(const moe_checkpoint* c, const uint16_t* x, int64_t ldx, void* stream) {
+    const char* fn = "moe_checkpoint_save";
+    int st = check_checkpoint(fn, "checkpoint", c, 0, 0);
+    if (st) return st;
+    if (c->rows == 0) return ok();
+    st = check_rows(fn, "x", x, ldx, c->K, 2);
+    if (st) return st;
+    st = moe::launch_checkpoint_save(*c, x, ldx, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_checkpoint_restore(const moe_checkpoint* c, uint16_t* x, int64_t ldx, void* stream) {
+    const char* fn = "moe_checkpoint_restore";
+    int st = check_checkpoint(fn, "checkpoint", c, 0, 0);
+    if (st) return st;
+    if (c->rows == 0) return ok();
+    st = check_rows(fn, "x", x, ldx, c->K, 2);
+    if (st) return st;
+    st = moe::launch_checkpoint_restore(*c, x, ldx, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_combine_backward_saved(const moe_dims* d, const uint16_t* out_grad, const moe_checkpoint* y_rows,
+                               const int32_t* pair_to_row, const float* topk_w, float* topk_w_grad,
+                               uint16_t* y_rows_grad, void* stream) {
+    const char* fn = "moe_combine_backward_saved";
+    int st = check_dims(fn, d, true, false);
+    if (!st) st = check_checkpoint(fn, "y_rows", y_rows, (int64_t)d->T * d->k, d->H);
+    if (st) return st;
+    if (d->T == 0) return ok();
+    REQUIRE_PTR(out_grad, 16);
+    REQUIRE_PTR(pair_to_row, 4);
+    REQUIRE_PTR(topk_w_grad, 4);
+    if (y_rows_grad) {
+        REQUIRE_PTR(y_rows_grad, 16);
+        REQUIRE_PTR(topk_w, 4);
+        if (y_rows_grad == out_grad) return fail(MOE_ERR_INVALID_ARG, "%s: y_rows_grad is one of the inputs", fn);
+    }
+    st = moe::launch_combine_backward_saved(*d, out_grad, *y_rows, pair_to_row, topk_w, topk_w_grad, y_rows_grad, as_stream(stream));
+    if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
+    return ok();
+}
+
+int moe_router_weight_workspace_bytes(const moe_dims* d, size_t* bytes) {
+    const char* fn = "moe_router_weight_workspace_bytes";
+    if (bytes == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+    const int st = check_dims(fn, d, true, false);
+    if (st) return st;
+    *bytes = moe::router_weight_workspace_bytes(d->T, d->E, d->H);
+    return ok();
+}
+
+int moe_router_weight_grad(const moe_dims* d, const float* logits_grad, const uint16_t* x, int64_t ldx,
+                           const moe_checkpoint* x_saved, float* w_router_grad, float* router_bias_grad, void* ws,
+                           size_t ws_bytes, void* stream) {
+    const char* fn = "moe_router_weight_grad";
+    int st = check_dims(fn, d, true, false);
+    if (st) return st;
+    REQUIRE_PTR(w_router_grad, 4);
+    if (router_bias_grad && !aligned(router_bias_grad, 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: router_bias_grad is not 4-byte aligned", fn);
+    if (d->T > 0) {
+        REQUIRE_PTR(logits_grad, 4);
+        if ((x != nullptr) == (x_saved != nullptr)) return fail(MOE_ERR_INVALID_ARG, "%s: either x or x_saved is needed", fn);
+        st = x ? check_rows(fn, "x", x, ldx, d->H, 2) : check_checkpoint(fn, "x_saved", x_saved, d->T, d->H);
+        if (st) return st;
+    }
+    st = check_scratch(fn, moe::router_weight_workspace_bytes(d->T, d->E, d->H), ws, ws_bytes);
+    if (st) return st;
+    const bool saved = d->T > 0 && x_saved;
+    st = moe::launch_router_weight_grad(d->T, d->E, d->H, logits_grad, saved ? (const void*)x_saved->q : x, saved ? d->H : ldx,
+                                        saved ? x_saved->scale : nullptr, w_router_grad, router_bias_grad, ws, as_stream(stream));
     if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
     return ok();
 }

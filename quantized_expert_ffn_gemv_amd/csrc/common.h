@@ -235,6 +235,11 @@ int launch_combine_shared(const moe_dims& d, const uint16_t* y, const int32_t* p
 // The combine in reverse (combine_backward.hip); dy may be NULL.
 int launch_combine_backward(const moe_dims& d, const uint16_t* dout, const uint16_t* y, const int32_t* p2r,
                             const float* gates, float* dgates, uint16_t* dy, hipStream_t s);
+// Rows kept in 8 bits, and the combine in reverse from them (checkpoint.hip).
+int launch_checkpoint_save(const moe_checkpoint& c, const uint16_t* x, int64_t ldx, hipStream_t s);
+int launch_checkpoint_restore(const moe_checkpoint& c, uint16_t* x, int64_t ldx, hipStream_t s);
+int launch_combine_backward_saved(const moe_dims& d, const uint16_t* dout, const moe_checkpoint& y, const int32_t* p2r,
+                                  const float* gates, float* dgates, uint16_t* dy, hipStream_t s);
 // The router's losses and backward pass (router_grad.hip).
 size_t balance_workspace_bytes(const moe_dims& d);
 int launch_balance_loss(const moe_dims& d, const float* logits, const int32_t* ids, const uint8_t* valid,

@@ -53,18 +53,6 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     }
 }
 
-// e^d, d <= 0, to 2 ulp: the hardware's power of two of t = d log2 e rounded, times the
-// factor 1 + r ln 2 for what the rounding left out, r = d log2 e - t (log2 e in two
-// parts).  Without the factor a small p was off by |d| 2^-24.  Below 2^-126 the
-// hardware gives 0, and d is cut off there (an infinite one would make r NaN; a NaN stays).
-__device__ __forceinline__ float exp_down(float d) {
-    constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;   // log2 e - (float) 1.44269504
-    d = d < -128.f ? -128.f : d;
-    const float t = d * kLog2e;
-    const float r = fmaf(d, kLog2eRest, fmaf(d, kLog2e, -t));
-    return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.f);
-}
-
 // v (logits) -> p in place; returns whether the row has a logit, and lse.  A row without
 // one has a sum of 0; NaNs, which fmaxf skips, come back by the sum.
 template <int LPT, int PER>

@@ -1,5 +1,5 @@
 // Row-wise helpers of the gradient and loss kernels: packed bf16 rounding,
-// reductions over the lanes that share a row, and the arrival ticket by which
+// the exponential of softmax rows, reductions over the lanes that share a row, and the arrival ticket by which
 // the last workgroup of a group joins the others' partial sums.
 #pragma once
 
@@ -43,6 +43,18 @@ __device__ __forceinline__ float row_max(float v) {
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
     return row_reduce<LANES>(v, [](float a, float b) { return a + b; });
+}
+
+// e^d, d <= 0, to 2 ulp: the hardware's power of two of t = d log2 e rounded, times the
+// factor 1 + r ln 2 for what the rounding left out, r = d log2 e - t (log2 e in two
+// parts).  Without the factor a small p was off by |d| 2^-24.  Below 2^-126 the
+// hardware gives 0, and d is cut off there (an infinite one would make r NaN; a NaN stays).
+__device__ __forceinline__ float exp_down(float d) {
+    constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;   // log2 e - (float) 1.44269504
+    d = d < -128.f ? -128.f : d;
+    const float t = d * kLog2e;
+    const float r = fmaf(d, kLog2eRest, fmaf(d, kLog2e, -t));
+    return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.f);
 }
 
 // Device-scope accesses for data handed between workgroups of one launch: they

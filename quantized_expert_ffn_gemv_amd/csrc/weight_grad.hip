@@ -1,0 +1,412 @@
+// Gradients of a matrix that tokens share: for set i of tokens (an adapter's, or all of them)
+//   d[i][r][c] = s_i sum_{t in i} g[t][r] x[t][c]      (float32)
+// with g float32 and x bf16, float32, or a checkpoint's int8 codes with one scale for 128 columns.
+// The adapters' factors (r a rank, x the layer's input or dy) and the router's weight (r an
+// expert, x the router's input) are of this form.
+//
+// The sum runs over tokens, across the rows of both operands.  A wave has 128 columns: a lane
+// takes 8 columns of 8 tokens and turns the block by v_perm_b32; column j of every lane's 8 is
+// one v_mfma_f32_16x16x32_bf16 over 32 tokens and 16 r, so that a lane ends with 8 neighbouring
+// columns of 4 r.  g goes as three bf16 parts (all 24 bits); bf16 x and codes are exact, a
+// code's scale goes into g (128 columns have one); a float32 x goes as three parts too, of whose
+// nine products the six largest are taken (2^-24 of the product left out).
+//
+// A workgroup's waves share its tokens and meet in LDS (many tokens), or have 128 columns each
+// (few).  Where columns and r give too few workgroups, tokens are split in chunks, whose sums a
+// second kernel adds in order.  No atomics: equal calls give equal bits.
+#include <algorithm>
+
+#include "adapters.h"
+#include "token_tiles.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kGradWaves = 8;
+constexpr int kStep = 32;                 // tokens a product
+enum ListKind { kAll = 0, kScan = 1, kPlan = 2 };
+
+struct GradArgs {
+    TokenSets who;
+    TokenPlan plan;
+    const float* scale;       // [n] or NULL
+    WeightGradCall w;
+    int chunk;                // kAll: tokens an entry
+    float* part;              // [slots][R C (+ R)]
+    int64_t slot_floats;
+};
+
+template <int XT>
+struct XFrag {
+    uint4 v[XT == MOE_F32 ? 16 : XT == kCodes ? 4 : 8];
+    float s[XT == kCodes ? 8 : 1];
+};
+
+}  // namespace
+
+template <int XT, int RTW, int LIST, int WT>
+__global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a) {
+    constexpr int LISTED = LIST == kAll ? 1 : LIST == kScan ? kScanTokens : kMostChunk;
+    __shared__ int list[LISTED];
+    __shared__ int found;
+    __shared__ __attribute__((aligned(16))) float sums[WT == 1 ? 1 : kGradWaves][16][132];
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int R = a.who.R, C = a.w.C;
+    int set = 0, first = 0, cnt, slot = -1;
+    if constexpr (LIST == kAll) {
+        first = (int)blockIdx.z * a.chunk;
+        cnt = min(a.chunk, a.who.T - first);
+        slot = gridDim.z > 1 ? (int)blockIdx.z : -1;
+    } else if constexpr (LIST == kScan) {
+        set = blockIdx.z;
+        if (wid == 0) {
+            int id[kScanTokens / 64], n = 0;
+#pragma unroll
+            for (int k = 0; k < kScanTokens / 64; ++k) id[k] = k * 64 < a.who.T ? a.who.ids[min(k * 64 + lane, a.who.T - 1)] : -1;
+#pragma unroll
+            for (int k = 0; k < kScanTokens / 64; ++k) {
+                const int t = k * 64 + lane;
+                const bool mine = t < a.who.T && id[k] == set;
+                const uint64_t mask = __ballot(mine);
+                if (mine) list[n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = t;
+                n += __popcll(mask);
+            }
+            if (lane == 0) found = n;
+        }
+        __syncthreads();
+        cnt = __builtin_amdgcn_readfirstlane(found);
+    } else {
+        if ((int)blockIdx.z >= ld_scalar(a.plan.counts, 1)) return;
+        const int4 e = a.plan.chunks[blockIdx.z];
+        set = __builtin_amdgcn_readfirstlane(e.x);
+        cnt = __builtin_amdgcn_readfirstlane(e.z);
+        slot = __builtin_amdgcn_readfirstlane(e.w);
+        for (int k = tid; k < cnt; k += 64 * kGradWaves) list[k] = a.plan.order[e.y + k];
+        __syncthreads();
+    }
+    const int rank = a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), R) : R;
+    const int r0 = 16 * RTW * (int)blockIdx.y;
+    const int block = WT == 1 ? (int)blockIdx.x * kGradWaves + wid : (int)blockIdx.x;    // of 128 columns
+    const int own = 128 * block + 8 * c, col = first_of_8(own, C), shift = own - col;    // 8 or more: none are this lane's
+    if (WT == 1 && 128 * block >= C) return;
+
+    floatx4_t acc[RTW][8];
+    float bsum[RTW];
+#pragma unroll
+    for (int rt = 0; rt < RTW; ++rt) {
+        bsum[rt] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[rt][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    const bool biased = LIST == kAll && a.w.bias != nullptr && block == 0;
+    const int gcol[2] = {min(r0 + c, max(rank - 1, 0)), min(r0 + 16 + c, max(rank - 1, 0))};
+    auto load = [&](XFrag<XT>& f, float (&g)[RTW][8], int step) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = kStep * step + 8 * q + i, kc = min(k, cnt - 1);
+            const int64_t t = LIST == kAll ? first + kc : list[kc];
+            if constexpr (XT == MOE_BF16) {
+                f.v[i] = load_bf16x8(static_cast<const uint16_t*>(a.w.x) + t * a.w.ldx + col);
+            } else if constexpr (XT == MOE_F32) {
+                __builtin_memcpy(&f.v[2 * i], static_cast<const float*>(a.w.x) + t * a.w.ldx + col, 32);
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.w.x) + t * a.w.ldx + col);
+                (i & 1) ? (f.v[i >> 1].z = v.x, f.v[i >> 1].w = v.y) : (f.v[i >> 1].x = v.x, f.v[i >> 1].y = v.y);
+                f.s[i] = a.w.xscale[t * (C / 128) + block];
+            }
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) {
+                const float v = a.w.g[t * a.w.ldg + gcol[rt]];
+                g[rt][i] = k < cnt ? v : 0.f;
+            }
+        }
+    };
+    auto compute = [&](const XFrag<XT>& f, float (&g)[RTW][8]) {
+        uint32_t gp[RTW][3][4];
+#pragma unroll
+        for (int rt = 0; rt < RTW; ++rt) {
+            if (biased)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bsum[rt] += g[rt][i];
+            if constexpr (XT == kCodes)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[rt][i] *= f.s[i];
+            bf16_parts<3>(g[rt], gp[rt]);
+        }
+        if constexpr (XT == MOE_F32) {
+            float v[8][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) __builtin_memcpy(v[i], &f.v[2 * i], 32);
+#pragma unroll
+            for (int px = 0; px < 3; ++px) {
+                uint4 rowv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t o[1][4];
+                    float rest[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) rest[j] = v[i][j];
+                    bf16_parts<1>(rest, o);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float d = v[i][j] - __uint_as_float((j & 1) ? o[0][j >> 1] & 0xFFFF0000u : o[0][j >> 1] << 16);
+                        v[i][j] = fabsf(v[i][j]) < INFINITY ? d : 0.f;
+                    }
+                    rowv[i] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+                }
+                uint32_t b[8][4];
+                turn8(rowv, b);
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt)
+#pragma unroll
+                    for (int p = 0; p < 3 - px; ++p)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[rt][j] = mfma16(gp[rt][p], b[j], acc[rt][j]);
+            }
+        } else {
+            uint32_t b[8][4];
+            if constexpr (XT == kCodes) {
+                // byte j of tokens 2 p and 2 p + 1: small integers, whose float32 has its bits in the upper half
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const uint32_t w[2][2] = {{f.v[p].x, f.v[p].y}, {f.v[p].z, f.v[p].w}};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float lo = (float)(int8_t)(w[0][j >> 2] >> (8 * (j & 3)));
+                        const float hi = (float)(int8_t)(w[1][j >> 2] >> (8 * (j & 3)));
+                        b[j][p] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+                    }
+                }
+            } else {
+                turn8(f.v, b);
+            }
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt)
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[rt][j] = mfma16(gp[rt][p], b[j], acc[rt][j]);
+        }
+    };
+    if (r0 < rank) {
+        const int steps = (cnt + kStep - 1) / kStep, w0 = WT == 1 ? 0 : wid;
+        if constexpr (XT == MOE_F32) {
+            for (int k = w0; k < steps; k += WT) {
+                XFrag<XT> f;
+                float g[RTW][8];
+                load(f, g, k);
+                compute(f, g);
+            }
+        } else if (w0 < steps) {
+            // the next step's loads are always made (the last again at the end), so that no branch waits for them
+            XFrag<XT> f0, f1;
+            float g0[RTW][8], g1[RTW][8];
+            load(f0, g0, w0);
+            for (int k = w0; k < steps; k += 2 * WT) {
+                load(f1, g1, min(k + WT, steps - 1));
+                compute(f0, g0);
+                if (k + WT >= steps) break;
+                load(f0, g0, min(k + 2 * WT, steps - 1));
+                compute(f1, g1);
+            }
+        }
+    }
+    const float s = slot < 0 && a.scale ? ld_scalar(a.scale, set) : 1.f;
+    float* out = slot < 0 ? a.w.out + (int64_t)set * R * C : a.part + (int64_t)slot * a.slot_floats;
+    float* bias = slot < 0 ? a.w.bias : a.part + (int64_t)slot * a.slot_floats + (int64_t)R * C;
+    if constexpr (WT == 1) {
+        if (shift >= 8) return;
+#pragma unroll
+        for (int rt = 0; rt < RTW; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + 16 * rt + 4 * q + i;
+                if (r >= R) continue;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = r < rank ? acc[rt][j][i] * s : 0.f;
+                float* to = out + (int64_t)r * C + col;
+                if (shift == 0) {
+                    __builtin_memcpy(to, v, 32);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= shift) to[j] = v[j];
+                }
+            }
+    } else {
+        const int row = tid >> 5, c4 = 4 * (tid & 31), wide = min(C - 128 * block - c4, 4);
+#pragma unroll
+        for (int rt = 0; rt < RTW; ++rt) {
+            if (rt) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float* to = &sums[wid][4 * q + i][8 * c];
+                if (shift == 0) {
+                    *reinterpret_cast<floatx4_t*>(to) = floatx4_t{acc[rt][0][i], acc[rt][1][i], acc[rt][2][i], acc[rt][3][i]};
+                    *reinterpret_cast<floatx4_t*>(to + 4) = floatx4_t{acc[rt][4][i], acc[rt][5][i], acc[rt][6][i], acc[rt][7][i]};
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= shift) to[j - shift] = acc[rt][j][i];
+                }
+            }
+            __syncthreads();
+            const int r = r0 + 16 * rt + row;
+            if (r < R && wide > 0) {
+                floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[0][row][c4]);
+#pragma unroll
+                for (int w = 1; w < kGradWaves; ++w) v += *reinterpret_cast<const floatx4_t*>(&sums[w][row][c4]);
+                v = r < rank ? v * s : floatx4_t{0.f, 0.f, 0.f, 0.f};
+                float* to = out + (int64_t)r * C + 128 * block + c4;
+                if (wide >= 4) __builtin_memcpy(to, &v, 16);
+                else
+                    for (int j = 0; j < wide; ++j) to[j] = v[j];
+            }
+        }
+        if constexpr (LIST == kAll) {
+            if (!biased) return;
+            __syncthreads();
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) {
+                float v = bsum[rt];
+                v += __shfl_xor(v, 16, kWave);
+                v += __shfl_xor(v, 32, kWave);
+                if (q == 0) sums[wid][rt][c] = v;
+            }
+            __syncthreads();
+            if (tid < 16 * RTW && r0 + tid < R) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kGradWaves; ++w) v += sums[w][tid >> 4][tid & 15];
+                bias[r0 + tid] = v;
+            }
+        }
+    }
+}
+
+// The chunks' sums of a set that has several, in order.  joins NULL: one set of `number` chunks.
+__global__ __launch_bounds__(256) void weight_grad_join_kernel(GradArgs a, int number) {
+    const int set = blockIdx.y;
+    int2 j = make_int2(0, number);
+    if (a.plan.joins) j = a.plan.joins[set];
+    if (j.y == 0) return;
+    const int64_t size = (int64_t)a.who.R * a.w.C, all = size + (a.w.bias ? a.who.R : 0);
+    const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (e >= all) return;
+    const float* p = a.part + (int64_t)j.x * a.slot_floats + e;
+    const float s = a.scale ? a.scale[set] : 1.f;
+    float* out = a.w.out + (int64_t)set * size + e;
+    if (e + 4 <= size) {
+        floatx4_t v{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < j.y; ++k) {
+            floatx4_t o;
+            __builtin_memcpy(&o, p + k * a.slot_floats, 16);
+            v += o;
+        }
+        v *= s;
+        __builtin_memcpy(out, &v, 16);
+        return;
+    }
+    for (int i = 0; i < 4 && e + i < all; ++i) {
+        float v = 0.f;
+        for (int k = 0; k < j.y; ++k) v += p[k * a.slot_floats + i];
+        if (e + i < size) out[i] = v * s;
+        else a.w.bias[e + i - size] = v;
+    }
+}
+
+namespace {
+
+int groups_of(int R) { return R <= 16 ? 1 : (R + 31) / 32; }
+
+template <int XT, int RTW, int LIST>
+void grad_go(const GradArgs& a, int blocks, unsigned entries, bool few, hipStream_t s) {
+    const unsigned gy = (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW));
+    if (few && LIST != kAll) {
+        const dim3 grid((unsigned)((blocks + kGradWaves - 1) / kGradWaves), gy, entries);
+        hipLaunchKernelGGL((weight_grad_kernel<XT, RTW, LIST == kAll ? kScan : LIST, 1>), grid, dim3(64 * kGradWaves), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((weight_grad_kernel<XT, RTW, LIST, kGradWaves>), dim3((unsigned)blocks, gy, entries),
+                           dim3(64 * kGradWaves), 0, s, a);
+    }
+}
+
+template <int XT>
+void grad_list(const GradArgs& a, int kind, int blocks, unsigned entries, bool few, hipStream_t s) {
+    const bool one = a.who.R <= 16;
+    if (kind == kAll) {
+        if constexpr (XT != MOE_F32) one ? grad_go<XT, 1, kAll>(a, blocks, entries, few, s) : grad_go<XT, 2, kAll>(a, blocks, entries, few, s);
+    } else if (kind == kScan) {
+        one ? grad_go<XT, 1, kScan>(a, blocks, entries, few, s) : grad_go<XT, 2, kScan>(a, blocks, entries, few, s);
+    } else {
+        one ? grad_go<XT, 1, kPlan>(a, blocks, entries, few, s) : grad_go<XT, 2, kPlan>(a, blocks, entries, few, s);
+    }
+}
+
+}  // namespace
+
+// ids: tokens up to kScanTokens are one chunk (every workgroup finds its own).
+static WeightGradPlan plan_of(int T, int n, int R, int C0, int C1, bool ids) {
+    WeightGradPlan p{};
+    if (ids && T <= kScanTokens) {
+        p.chunk = T > 0 ? T : 1;
+        return p;
+    }
+    const int wgs = groups_of(R) * ((C0 + 127) / 128 + (C1 + 127) / 128);
+    const int want = (512 + wgs - 1) / wgs;
+    const int even = ((T + want - 1) / want + kLeastChunk - 1) / kLeastChunk * kLeastChunk;
+    p.chunk = std::max(kLeastChunk, std::min(even, kMostChunk));
+    // a set in several chunks has more than `chunk` tokens, and one chunk at most is not full
+    if (T > p.chunk) p.slots = n == 1 ? (T + p.chunk - 1) / p.chunk : 2 * (T / p.chunk);
+    const size_t most = T <= kLeastChunk ? 0 : 2 * std::max<size_t>(want, (T + kMostChunk - 1) / kMostChunk);
+    p.most_floats = most * (size_t)R * ((size_t)C0 + C1 + 1);
+    return p;
+}
+
+WeightGradPlan weight_grad_plan(int T, int n, int R, int C0, int C1) { return plan_of(T, n, R, C0, C1, true); }
+
+static int weight_grad(const TokenSets& who, int kind, const TokenPlan* plan, const float* scale, const WeightGradPlan& p,
+                       const WeightGradCall* calls, int n_calls, float* part, hipStream_t s) {
+    const unsigned chunks = who.T > p.chunk ? (unsigned)((who.T + p.chunk - 1) / p.chunk) : 1u;
+    // few tokens a set: a wave's 128 columns each
+    const bool few = kind != kAll && who.T <= 64 * who.n;
+    for (int i = 0; i < n_calls; ++i) {
+        const WeightGradCall& w = calls[i];
+        GradArgs a{};
+        a.who = who;
+        if (plan) a.plan = *plan;
+        a.scale = scale; a.w = w; a.chunk = p.chunk; a.part = part;
+        a.slot_floats = (int64_t)who.R * w.C + (w.bias ? who.R : 0);
+        part += p.slots * a.slot_floats;
+        const int blocks = (w.C + 127) / 128;
+        const unsigned entries = kind == kAll ? chunks : kind == kScan ? (unsigned)who.n : (unsigned)(who.T / p.chunk + who.n);
+        if (w.x_type == kCodes) grad_list<kCodes>(a, kind, blocks, entries, few, s);
+        else if (w.x_type == MOE_F32) grad_list<MOE_F32>(a, kind, blocks, entries, few, s);
+        else grad_list<MOE_BF16>(a, kind, blocks, entries, few, s);
+        if (p.slots) {
+            const int64_t all = (int64_t)who.R * w.C + (w.bias ? who.R : 0);
+            hipLaunchKernelGGL(weight_grad_join_kernel, dim3((unsigned)((all + 1023) / 1024), (unsigned)who.n), dim3(256), 0, s, a,
+                               (int)chunks);
+        }
+    }
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int launch_weight_grad(const TokenSets& who, const TokenPlan* plan, const float* scale, const WeightGradPlan& p,
+                       const WeightGradCall* calls, int n_calls, float* part, hipStream_t s) {
+    return weight_grad(who, plan ? kPlan : kScan, plan, scale, p, calls, n_calls, part, s);
+}
+
+size_t router_weight_workspace_bytes(int T, int E, int H) { return plan_of(T, 1, E, H, 0, false).most_floats * 4; }
+
+int launch_router_weight_grad(int T, int E, int H, const float* dlogits, const void* x, int64_t ldx, const float* xscale,
+                              float* dw, float* dbias, void* ws, hipStream_t s) {
+    const TokenSets who{nullptr, nullptr, T, 1, E};
+    const WeightGradCall call{dlogits, E, x, ldx, xscale, xscale ? kCodes : MOE_BF16, H, dw, dbias};
+    return weight_grad(who, kAll, nullptr, nullptr, plan_of(T, 1, E, H, 0, false), &call, 1, static_cast<float*>(ws), s);
+}
+
+}  // namespace moe
