@@ -913,8 +913,8 @@ def logprobs_grad(logits, tokens, stats, logits_grad, logp_grad=None, entropy=No
              logits_grad.data_ptr(), ldg, _element_type(logits_grad.dtype))
 
 
-from .layer import (LayerBuffers, ResidentExperts, RouterGradBuffers, SharedBuffers, SharedExpert, StackLayer,  # noqa: E402
-                    layer_forward, resident_layer_forward, router_backward, router_losses, stack_forward)  # (orchestration of the calls above)
+from .layer import (AdaptedBuffers, LayerBuffers, ResidentExperts, RouterGradBuffers, SharedBuffers, SharedExpert,  # noqa: E402
+                    StackLayer, adapted_linear, adapted_linear_backward, layer_forward, resident_layer_forward, router_backward, router_losses, stack_forward)  # (orchestration of the calls above)
 
 __all__ = [
     "lib", "abi_version", "status_string", "last_error", "MoeError", "Dims", "dims", "QWeights",
@@ -927,6 +927,7 @@ __all__ = [
     "RouterGradBuffers", "router_losses", "router_backward",
     "Checkpoint", "checkpoint_save", "checkpoint_restore", "RouterWeightBuffers", "router_weight_grad", "router_weight_workspace_bytes",
     "Adapters", "AdapterBuffers", "adapter", "adapter_grad", "adapter_workspace_bytes",
+    "AdaptedBuffers", "adapted_linear", "adapted_linear_backward",
     "LogprobBuffers", "logprobs", "logprobs_grad", "logprobs_workspace_bytes", "LOGPROBS_SYNC_INTS",
     "group_major", "ALGO_AUTO", "ALGO_GEMV", "ALGO_MFMA", "ALGO_GEMM", "OP_ROUTE", "OP_LOOKUP", "OP_PERMUTE", "OP_FFN", "OP_COMBINE",
 ]

@@ -34,6 +34,10 @@ that is captured once in a HIP graph and replayed per token.
 side of a step with the quantised experts frozen: the router's losses after the
 routing, and the way back from the layer's output to the logits.
 
+``AdaptedBuffers``, ``adapted_linear`` and ``adapted_linear_backward`` run a dense quantised
+projection with each token's low-rank adapter beside it, and the way back to the
+adapters' factors and the input, the projection frozen.
+
 This module only orders the calls; the arithmetic is in the HIP kernels.
 """
 from __future__ import annotations
@@ -44,10 +48,11 @@ from typing import Optional, Sequence
 import torch
 
 from . import (ALGO_AUTO, DISPATCH_SYNC_INTS, FFN_SYNC_INTS, OP_FFN, RESIDENCY_LISTS, WORK_ENTRY_INTS, Dims,
-               BalanceBuffers, QWeights, balance_loss, combine, combine_backward, combine_shared, dims, expert_copy,
-               expert_ffn_fused, expert_ffn_fused_shared, expert_ffn_q2, expert_ffn_q4, permute, residency_plan,
-               route_backward, route_counts, route_dispatch, route_topk, slot_lookup, work_list_capacity,
-               workspace_bytes)
+               AdapterBuffers, Adapters, BalanceBuffers, Checkpoint, LinearBuffers, QMatrix, QWeights, RouterWeightBuffers,
+               adapter, adapter_grad, balance_loss, combine, combine_backward, combine_shared, dims, expert_copy,
+               expert_ffn_fused, expert_ffn_fused_shared, expert_ffn_q2, expert_ffn_q4, linear, linear_grad, permute,
+               residency_plan, route_backward, route_counts, route_dispatch, route_topk, router_weight_grad, slot_lookup,
+               work_list_capacity, workspace_bytes)
 
 
 @dataclass
@@ -243,7 +248,9 @@ def router_losses(buf: LayerBuffers, grads: RouterGradBuffers, valid: Optional[t
 def router_backward(buf: LayerBuffers, grads: RouterGradBuffers, out_grad: torch.Tensor,
                     losses_grad: Optional[torch.Tensor] = None, valid: Optional[torch.Tensor] = None,
                     y_rows_grad: Optional[torch.Tensor] = None, renormalize: Optional[bool] = None,
-                    stream=None) -> torch.Tensor:
+                    stream=None, y_saved: Optional[Checkpoint] = None, x=None,
+                    w_router_grad: Optional[torch.Tensor] = None, router_bias_grad: Optional[torch.Tensor] = None,
+                    weight_buffers: Optional[RouterWeightBuffers] = None) -> torch.Tensor:
     """The way back through a layer step on `buf` to its logits, from out_grad
     (bf16 [T, H]; also the residual's gradient) and losses_grad (float32 [2] on
     the GPU, the gradients of router_losses()'s two losses, with the same valid;
@@ -252,18 +259,75 @@ def router_backward(buf: LayerBuffers, grads: RouterGradBuffers, out_grad: torch
     calls alone); another value than the step's is refused.
     The gates of a shared expert's step are unchanged by it, so this holds for
     such a step too.  y_rows_grad: None, or bf16 [T*k, H] for the gradient of the
-    expert rows.  Returns grads.logits_grad; the router weight's gradient is
-    logits_grad^T x and its bias' the sum of logits_grad over the tokens."""
+    expert rows.  y_saved: a Checkpoint of the step's expert rows (checkpoint_save() of
+    buf.y_rows after it), read in their place, so that later steps may use buf.y_rows.
+    Returns grads.logits_grad; with w_router_grad (float32 [E, H]) also the router
+    weight's gradient logits_grad^T x is written, from the step's input x (bf16 [T, H] or a
+    Checkpoint of it), and router_bias_grad (float32 [E]), the sum of logits_grad over the
+    tokens; weight_buffers: RouterWeightBuffers.allocate(buf.d)."""
     if losses_grad is not None and not grads.counted:
         raise ValueError("the losses' gradient needs the counts of router_losses()")
     if renormalize is None:
         renormalize = buf.renormalize is not False
     elif buf.renormalize is not None and bool(renormalize) != buf.renormalize:
         raise ValueError(f"the step's gates were made with renormalize={buf.renormalize}")
-    combine_backward(buf.d, out_grad, buf.y_rows, buf.pair_to_row, buf.topk_w, grads.topk_w_grad, y_rows_grad, stream)
+    if w_router_grad is None and router_bias_grad is not None:
+        raise ValueError("router_bias_grad goes with w_router_grad")
+    if w_router_grad is not None and (x is None or weight_buffers is None):
+        raise ValueError("w_router_grad needs the step's x and weight_buffers")
+    combine_backward(buf.d, out_grad, buf.y_rows if y_saved is None else y_saved, buf.pair_to_row, buf.topk_w,
+                     grads.topk_w_grad, y_rows_grad, stream)
     route_backward(buf.d, buf.logits, buf.topk_ids, buf.topk_w, renormalize, grads.logits_grad, grads.topk_w_grad,
                    losses_grad, grads.counts, grads.n_valid, valid, stream)
+    if w_router_grad is not None:
+        router_weight_grad(buf.d, grads.logits_grad, x, w_router_grad, weight_buffers, router_bias_grad, stream)
     return grads.logits_grad
+
+
+@dataclass
+class AdaptedBuffers:
+    """What adapted_linear() needs, and with grad adapted_linear_backward(), for up to T
+    tokens, one call at a time on one stream."""
+    linear: LinearBuffers
+    adapter: AdapterBuffers
+    linear_back: Optional[LinearBuffers] = None
+    adapter_back: Optional[AdapterBuffers] = None
+
+    @staticmethod
+    def allocate(w: QMatrix, adapters: Adapters, T: int, dtype, grad: bool = False) -> "AdaptedBuffers":
+        return AdaptedBuffers(
+            linear=LinearBuffers.allocate(w, T, dtype), adapter=AdapterBuffers.allocate(adapters, T),
+            linear_back=LinearBuffers.allocate(w, T, dtype, grad=True) if grad else None,
+            adapter_back=AdapterBuffers.allocate(adapters, T, grad=True) if grad else None)
+
+
+def _beside(w: QMatrix, adapters: Adapters) -> None:
+    if (adapters.K, adapters.N) != (w.K, w.N):
+        raise ValueError(f"adapters of {(adapters.N, adapters.K)} beside a projection of {(w.N, w.K)}")
+
+
+def adapted_linear(w: QMatrix, adapters: Adapters, ids, x, y, buffers: AdaptedBuffers, row_bias=None, residual=None,
+                   h=None, stream=None) -> None:
+    """y = x W^T (+ row_bias) (+ residual) + each token's adapter: linear(), then adapter()
+    on y in place (a bfloat16 y is rounded by both).  ids int32 [T]; h: float32 [T, R] or
+    None, for adapted_linear_backward()."""
+    _beside(w, adapters)
+    linear(w, x, y, buffers.linear, row_bias, residual, stream)
+    adapter(adapters, ids, x, y, buffers.adapter, base=y, h=h, stream=stream)
+
+
+def adapted_linear_backward(w: QMatrix, adapters: Adapters, ids, dy, x, h, buffers: AdaptedBuffers, dx=None, da=None,
+                            db=None, stream=None) -> None:
+    """The way back through adapted_linear(): dx = dy W + the adapters' part (linear_grad(),
+    then adapter_grad() on it in place), da and db the factors' gradients, each if given.  x:
+    the input or a Checkpoint of it (for da), h adapted_linear()'s (for db).  (The residual's
+    gradient is dy.)"""
+    _beside(w, adapters)
+    if buffers.adapter_back is None:
+        raise ValueError("buffers allocated without grad")
+    if dx is not None:
+        linear_grad(w, dy, dx, buffers.linear_back, stream)
+    adapter_grad(adapters, ids, dy, x, h, buffers.adapter_back, dx=dx, dx_base=dx, da=da, db=db, stream=stream)
 
 
 @dataclass
