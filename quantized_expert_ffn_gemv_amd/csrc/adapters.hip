@@ -194,14 +194,48 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs 
     const int own = ((int)blockIdx.x * kWaves + wid) * kUnitCols + 8 * c;
     const int col = first_of_8(own, a.C), shift = own - col;           // 8 or more: no column is this lane's
 
-    // the sums of the tile's tokens: the splits' parts
+    // every load that needs only the list goes out first: the factor's rows, the base's of the first 16
+    // tokens (rows 4 q + i; the list is padded with its last token)
+    uint4 rowv[KS][8], bb[2][4][F32 ? 2 : 1];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            rowv[ks][i] = i >= PER ? make_uint4(0, 0, 0, 0)
+                                   : load_bf16x8(a.w + ((int64_t)max(set, 0) * R + min(32 * ks + PER * q + i, max(rank - 1, 0))) * a.ldw + col);
+    auto load_base = [&](int nt) {
+        if (a.base) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldbase + col;
+                if constexpr (F32) __builtin_memcpy(bb[nt & 1][i], static_cast<const float*>(a.base) + at, 32);
+                else bb[nt & 1][i][0] = load_bf16x8(static_cast<const uint16_t*>(a.base) + at);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < (F32 ? 2 : 1); ++d) bb[nt & 1][i][d] = make_uint4(0, 0, 0, 0);
+        }
+    };
+    if (a.y) load_base(0);
+
+    // the sums of the tile's tokens: the splits' parts, four at a time
     const float s = set < 0 ? 0.f : ld_scalar(a.scale, set);
     for (int e = tid; e < TOK * (RP / 4); e += 64 * kWaves) {
         const int row = e / (RP / 4), r = 4 * (e % (RP / 4));
         floatx4_t v{0.f, 0.f, 0.f, 0.f};
-        if (row < rows && set >= 0)
-            for (int k = 0; k < a.splits; ++k)
-                v += *reinterpret_cast<const floatx4_t*>(a.part + ((int64_t)k * a.who.T + list[row]) * RP + r);
+        if (row < rows && set >= 0) {
+            const float* p = a.part + (int64_t)list[row] * RP + r;
+            for (int k = 0; k < a.splits; k += 4) {
+                floatx4_t o[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    o[u] = *reinterpret_cast<const floatx4_t*>(p + (int64_t)min(k + u, a.splits - 1) * a.who.T * RP);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v += k + u < a.splits ? o[u] : floatx4_t{0.f, 0.f, 0.f, 0.f};
+            }
+        }
         if (a.h && blockIdx.x == 0 && row < rows)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -216,17 +250,11 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs 
     uint32_t wf[KS][8][PER / 2];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-        uint4 rowv[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= PER) { rowv[i] = make_uint4(0, 0, 0, 0); continue; }
-            rowv[i] = load_bf16x8(a.w + ((int64_t)max(set, 0) * R + min(32 * ks + PER * q + i, max(rank - 1, 0))) * a.ldw + col);
-        }
 #pragma unroll
         for (int i = 0; i < PER; ++i)                                  // (what lies past the rank may be no number)
-            if (32 * ks + PER * q + i >= rank) rowv[i] = make_uint4(0, 0, 0, 0);
+            if (32 * ks + PER * q + i >= rank) rowv[ks][i] = make_uint4(0, 0, 0, 0);
         uint32_t t[8][4];
-        turn8(rowv, t);
+        turn8(rowv[ks], t);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -239,21 +267,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs 
         floatx4_t acc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-        // the base's rows 4 q + i (the list is padded with its last token)
-        uint4 bb[4][F32 ? 2 : 1];
-        if (a.base) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldbase + col;
-                if constexpr (F32) __builtin_memcpy(bb[i], static_cast<const float*>(a.base) + at, 32);
-                else bb[i][0] = load_bf16x8(static_cast<const uint16_t*>(a.base) + at);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int d = 0; d < (F32 ? 2 : 1); ++d) bb[i][d] = make_uint4(0, 0, 0, 0);
-        }
+        if (16 * (nt + 1) < rows) load_base(nt + 1);
         if (some) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -288,9 +302,10 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs 
             const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldy + col;
             float v[8];
             if constexpr (F32) {
-                __builtin_memcpy(v, bb[i], 32);
+                __builtin_memcpy(v, bb[nt & 1][i], 32);
             } else {
-                const uint32_t b[4] = {bb[i][0].x, bb[i][0].y, bb[i][0].z, bb[i][0].w};
+                const uint4 own16 = bb[nt & 1][i][0];
+                const uint32_t b[4] = {own16.x, own16.y, own16.z, own16.w};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((j & 1) ? b[j >> 1] & 0xFFFF0000u : b[j >> 1] << 16);
             }
@@ -332,10 +347,30 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapter_plan_kernel(TokenSets
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, sets = who.n + 1;
     const int run = ((who.T + kPlanWaves - 1) / kPlanWaves + 63) / 64 * 64;
     const int t0 = wid * run, t1 = min(t0 + run, who.T);
+    // the wave's next 8 x 64 tokens' sets (n: none; -1: past the run), their loads together
+    auto sets_at = [&](int t, int (&v)[8]) {
+        int id[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) id[j] = who.ids[min(t + 64 * j + lane, who.T - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = t + 64 * j + lane >= t1 ? -1 : (unsigned)id[j] < (unsigned)who.n ? id[j] : who.n;
+    };
+    int held[8];
+    sets_at(t0, held);
     for (int i = tid; i < kPlanWaves * sets; i += 64 * kPlanWaves) counts[i] = 0;
     __syncthreads();
-    auto set_at = [&](int t) { const int i = set_of(who.ids, t, who.n); return i < 0 ? who.n : i; };
-    for (int t = t0 + lane; t < t1; t += 64) atomicAdd(&counts[wid * sets + set_at(t)], 1);
+    for (int t = t0; t < t1; t += 512) {
+        int v[8];
+        if (t == t0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = held[j];
+        } else {
+            sets_at(t, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (v[j] >= 0) atomicAdd(&counts[wid * sets + v[j]], 1);
+    }
     __syncthreads();
     // thread i: set i (at most 1025 sets, so the first threads may have a second one)
     int first = 0, tile = 0, chunk = 0, slot = 0;     // running totals of the sets before this round's
@@ -381,20 +416,36 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapter_plan_kernel(TokenSets
         plan.counts[1] = chunk;
     }
     // 64 tokens at a time: a token's place is its set's next one plus those of the set in lower lanes
-    for (int t = t0 + lane; t - lane < t1; t += 64) {
-        const int set = t < t1 ? set_at(t) : -1;
-        uint64_t left = __ballot(set >= 0);
-        while (left) {
-            const int lead = __ffsll((unsigned long long)left) - 1;
-            const int which = __shfl(set, lead, kWave);
-            const uint64_t same = __ballot(set == which);
-            const int at = counts[wid * sets + which];
-            if (set == which)
-                plan.order[at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] = t;
+    for (int t = t0; t < t1; t += 512) {
+        int v[8];
+        if (t == t0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = held[j];
+        } else {
+            sets_at(t, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint64_t left = __ballot(v[j] >= 0);
+            int place = 0;                                 // of this lane among its set's here, and the set's next place
+            int size = 0;
+            while (left) {
+                const int which = __builtin_amdgcn_readlane(v[j], __ffsll((unsigned long long)left) - 1);
+                const uint64_t same = __ballot(v[j] == which);
+                if (v[j] == which) {
+                    place = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+                    size = __popcll(same);
+                }
+                left &= ~same;
+            }
+            if (v[j] >= 0) {
+                int* next = &counts[wid * sets + v[j]];
+                const int at = *next;
+                plan.order[at + place] = t + 64 * j + lane;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+                if (place == 0) *next = at + size;
+            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-            if (lane == 0) counts[wid * sets + which] = at + __popcll(same);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-            left &= ~same;
         }
     }
 }

@@ -31,10 +31,11 @@ struct GradArgs {
     TokenSets who;
     TokenPlan plan;
     const float* scale;       // [n] or NULL
-    WeightGradCall w;
+    WeightGradCall w[2];      // a launch has one or two matrices
+    int blocks0;              // workgroups (first grid axis) of the first
     int chunk;                // kAll: tokens an entry
-    float* part;              // [slots][R C (+ R)]
-    int64_t slot_floats;
+    float* part[2];           // [slots][R C (+ R)]
+    int64_t slot_floats[2];
 };
 
 template <int XT>
@@ -43,54 +44,17 @@ struct XFrag {
     float s[XT == kCodes ? 8 : 1];
 };
 
-}  // namespace
-
+// One workgroup's block of 128 columns, XT the kind of x.
 template <int XT, int RTW, int LIST, int WT>
-__global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a) {
-    constexpr int LISTED = LIST == kAll ? 1 : LIST == kScan ? kScanTokens : kMostChunk;
-    __shared__ int list[LISTED];
-    __shared__ int found;
-    __shared__ __attribute__((aligned(16))) float sums[WT == 1 ? 1 : kGradWaves][16][132];
+__device__ __forceinline__ void weight_grad_block(const GradArgs& a, const WeightGradCall& w, int xblock, float* part, int64_t slot_floats,
+                                                  int set, int first, int cnt, int slot, const int* list, float (*sums)[16][132]) {
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int R = a.who.R, C = a.w.C;
-    int set = 0, first = 0, cnt, slot = -1;
-    if constexpr (LIST == kAll) {
-        first = (int)blockIdx.z * a.chunk;
-        cnt = min(a.chunk, a.who.T - first);
-        slot = gridDim.z > 1 ? (int)blockIdx.z : -1;
-    } else if constexpr (LIST == kScan) {
-        set = blockIdx.z;
-        if (wid == 0) {
-            int id[kScanTokens / 64], n = 0;
-#pragma unroll
-            for (int k = 0; k < kScanTokens / 64; ++k) id[k] = k * 64 < a.who.T ? a.who.ids[min(k * 64 + lane, a.who.T - 1)] : -1;
-#pragma unroll
-            for (int k = 0; k < kScanTokens / 64; ++k) {
-                const int t = k * 64 + lane;
-                const bool mine = t < a.who.T && id[k] == set;
-                const uint64_t mask = __ballot(mine);
-                if (mine) list[n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = t;
-                n += __popcll(mask);
-            }
-            if (lane == 0) found = n;
-        }
-        __syncthreads();
-        cnt = __builtin_amdgcn_readfirstlane(found);
-    } else {
-        if ((int)blockIdx.z >= ld_scalar(a.plan.counts, 1)) return;
-        const int4 e = a.plan.chunks[blockIdx.z];
-        set = __builtin_amdgcn_readfirstlane(e.x);
-        cnt = __builtin_amdgcn_readfirstlane(e.z);
-        slot = __builtin_amdgcn_readfirstlane(e.w);
-        for (int k = tid; k < cnt; k += 64 * kGradWaves) list[k] = a.plan.order[e.y + k];
-        __syncthreads();
-    }
+    const int R = a.who.R, C = w.C;
     const int rank = a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), R) : R;
     const int r0 = 16 * RTW * (int)blockIdx.y;
-    const int block = WT == 1 ? (int)blockIdx.x * kGradWaves + wid : (int)blockIdx.x;    // of 128 columns
+    const int block = xblock;               // of 128 columns
     const int own = 128 * block + 8 * c, col = first_of_8(own, C), shift = own - col;    // 8 or more: none are this lane's
-    if (WT == 1 && 128 * block >= C) return;
 
     floatx4_t acc[RTW][8];
     float bsum[RTW];
@@ -100,7 +64,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[rt][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
     }
-    const bool biased = LIST == kAll && a.w.bias != nullptr && block == 0;
+    const bool biased = LIST == kAll && w.bias != nullptr && block == 0;
     const int gcol[2] = {min(r0 + c, max(rank - 1, 0)), min(r0 + 16 + c, max(rank - 1, 0))};
     auto load = [&](XFrag<XT>& f, float (&g)[RTW][8], int step) {
 #pragma unroll
@@ -108,17 +72,17 @@ __global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a
             const int k = kStep * step + 8 * q + i, kc = min(k, cnt - 1);
             const int64_t t = LIST == kAll ? first + kc : list[kc];
             if constexpr (XT == MOE_BF16) {
-                f.v[i] = load_bf16x8(static_cast<const uint16_t*>(a.w.x) + t * a.w.ldx + col);
+                f.v[i] = load_bf16x8(static_cast<const uint16_t*>(w.x) + t * w.ldx + col);
             } else if constexpr (XT == MOE_F32) {
-                __builtin_memcpy(&f.v[2 * i], static_cast<const float*>(a.w.x) + t * a.w.ldx + col, 32);
+                __builtin_memcpy(&f.v[2 * i], static_cast<const float*>(w.x) + t * w.ldx + col, 32);
             } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.w.x) + t * a.w.ldx + col);
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(w.x) + t * w.ldx + col);
                 (i & 1) ? (f.v[i >> 1].z = v.x, f.v[i >> 1].w = v.y) : (f.v[i >> 1].x = v.x, f.v[i >> 1].y = v.y);
-                f.s[i] = a.w.xscale[t * (C / 128) + block];
+                f.s[i] = w.xscale[t * (C / 128) + block];
             }
 #pragma unroll
             for (int rt = 0; rt < RTW; ++rt) {
-                const float v = a.w.g[t * a.w.ldg + gcol[rt]];
+                const float v = w.g[t * w.ldg + gcol[rt]];
                 g[rt][i] = k < cnt ? v : 0.f;
             }
         }
@@ -214,8 +178,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a
         }
     }
     const float s = slot < 0 && a.scale ? ld_scalar(a.scale, set) : 1.f;
-    float* out = slot < 0 ? a.w.out + (int64_t)set * R * C : a.part + (int64_t)slot * a.slot_floats;
-    float* bias = slot < 0 ? a.w.bias : a.part + (int64_t)slot * a.slot_floats + (int64_t)R * C;
+    float* out = slot < 0 ? w.out + (int64_t)set * R * C : part + (int64_t)slot * slot_floats;
+    float* bias = slot < 0 ? w.bias : part + (int64_t)slot * slot_floats + (int64_t)R * C;
     if constexpr (WT == 1) {
         if (shift >= 8) return;
 #pragma unroll
@@ -258,7 +222,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a
             if (r < R && wide > 0) {
                 floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[0][row][c4]);
 #pragma unroll
-                for (int w = 1; w < kGradWaves; ++w) v += *reinterpret_cast<const floatx4_t*>(&sums[w][row][c4]);
+                for (int k = 1; k < WT; ++k) v += *reinterpret_cast<const floatx4_t*>(&sums[k][row][c4]);
                 v = r < rank ? v * s : floatx4_t{0.f, 0.f, 0.f, 0.f};
                 float* to = out + (int64_t)r * C + 128 * block + c4;
                 if (wide >= 4) __builtin_memcpy(to, &v, 16);
@@ -280,11 +244,62 @@ __global__ __launch_bounds__(64 * kGradWaves) void weight_grad_kernel(GradArgs a
             if (tid < 16 * RTW && r0 + tid < R) {
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < kGradWaves; ++w) v += sums[w][tid >> 4][tid & 15];
+                for (int k = 0; k < WT; ++k) v += sums[k][tid >> 4][tid & 15];
                 bias[r0 + tid] = v;
             }
         }
     }
+}
+
+}  // namespace
+
+template <int RTW, int LIST, int WT>
+__global__ __launch_bounds__(64 * WT, 2) void weight_grad_kernel(GradArgs a) {
+    constexpr int LISTED = LIST == kAll ? 1 : LIST == kScan ? kScanTokens : kMostChunk;
+    __shared__ int list[LISTED];
+    __shared__ int found;
+    __shared__ __attribute__((aligned(16))) float sums[WT][16][132];
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int set = 0, first = 0, cnt, slot = -1;
+    if constexpr (LIST == kAll) {
+        first = (int)blockIdx.z * a.chunk;
+        cnt = min(a.chunk, a.who.T - first);
+        slot = gridDim.z > 1 ? (int)blockIdx.z : -1;
+    } else if constexpr (LIST == kScan) {
+        set = blockIdx.z;
+        if (wid == 0) {
+            int id[kScanTokens / 64], n = 0;
+#pragma unroll
+            for (int k = 0; k < kScanTokens / 64; ++k) id[k] = k * 64 < a.who.T ? a.who.ids[min(k * 64 + lane, a.who.T - 1)] : -1;
+#pragma unroll
+            for (int k = 0; k < kScanTokens / 64; ++k) {
+                const int t = k * 64 + lane;
+                const bool mine = t < a.who.T && id[k] == set;
+                const uint64_t mask = __ballot(mine);
+                if (mine) list[n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = t;
+                n += __popcll(mask);
+            }
+            if (lane == 0) found = n;
+        }
+        __syncthreads();
+        cnt = __builtin_amdgcn_readfirstlane(found);
+    } else {
+        if ((int)blockIdx.z >= ld_scalar(a.plan.counts, 1)) return;
+        const int4 e = a.plan.chunks[blockIdx.z];
+        set = __builtin_amdgcn_readfirstlane(e.x);
+        cnt = __builtin_amdgcn_readfirstlane(e.z);
+        slot = __builtin_amdgcn_readfirstlane(e.w);
+        for (int k = tid; k < cnt; k += 64 * WT) list[k] = a.plan.order[e.y + k];
+        __syncthreads();
+    }
+    const bool second = (int)blockIdx.x >= a.blocks0;
+    const WeightGradCall& w = a.w[second];
+    const int block = (int)blockIdx.x - (second ? a.blocks0 : 0);
+    float* part = a.part[second];
+    const int64_t floats = a.slot_floats[second];
+    if (w.x_type == MOE_BF16) weight_grad_block<MOE_BF16, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
+    else if (w.x_type == kCodes) weight_grad_block<kCodes, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
+    else if constexpr (LIST != kAll) weight_grad_block<MOE_F32, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
 }
 
 // The chunks' sums of a set that has several, in order.  joins NULL: one set of `number` chunks.
@@ -293,18 +308,22 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(GradArgs a, int n
     int2 j = make_int2(0, number);
     if (a.plan.joins) j = a.plan.joins[set];
     if (j.y == 0) return;
-    const int64_t size = (int64_t)a.who.R * a.w.C, all = size + (a.w.bias ? a.who.R : 0);
-    const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    const bool second = (int)blockIdx.x >= a.blocks0;
+    const WeightGradCall& w = a.w[second];
+    const int64_t size = (int64_t)a.who.R * w.C, all = a.slot_floats[second];
+    const int64_t e = 4 * ((int64_t)(blockIdx.x - (second ? a.blocks0 : 0)) * 256 + threadIdx.x);
     if (e >= all) return;
-    const float* p = a.part + (int64_t)j.x * a.slot_floats + e;
+    const float* p = a.part[second] + (int64_t)j.x * all + e;
     const float s = a.scale ? a.scale[set] : 1.f;
-    float* out = a.w.out + (int64_t)set * size + e;
+    float* out = w.out + (int64_t)set * size + e;
     if (e + 4 <= size) {
         floatx4_t v{0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < j.y; ++k) {
-            floatx4_t o;
-            __builtin_memcpy(&o, p + k * a.slot_floats, 16);
-            v += o;
+        for (int k = 0; k < j.y; k += 4) {
+            floatx4_t o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) __builtin_memcpy(&o[u], p + min(k + u, j.y - 1) * all, 16);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v += k + u < j.y ? o[u] : floatx4_t{0.f, 0.f, 0.f, 0.f};
         }
         v *= s;
         __builtin_memcpy(out, &v, 16);
@@ -312,9 +331,9 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(GradArgs a, int n
     }
     for (int i = 0; i < 4 && e + i < all; ++i) {
         float v = 0.f;
-        for (int k = 0; k < j.y; ++k) v += p[k * a.slot_floats + i];
+        for (int k = 0; k < j.y; ++k) v += p[k * all + i];
         if (e + i < size) out[i] = v * s;
-        else a.w.bias[e + i - size] = v;
+        else w.bias[e + i - size] = v;
     }
 }
 
@@ -322,28 +341,14 @@ namespace {
 
 int groups_of(int R) { return R <= 16 ? 1 : (R + 31) / 32; }
 
-template <int XT, int RTW, int LIST>
-void grad_go(const GradArgs& a, int blocks, unsigned entries, bool few, hipStream_t s) {
-    const unsigned gy = (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW));
-    if (few && LIST != kAll) {
-        const dim3 grid((unsigned)((blocks + kGradWaves - 1) / kGradWaves), gy, entries);
-        hipLaunchKernelGGL((weight_grad_kernel<XT, RTW, LIST == kAll ? kScan : LIST, 1>), grid, dim3(64 * kGradWaves), 0, s, a);
-    } else {
-        hipLaunchKernelGGL((weight_grad_kernel<XT, RTW, LIST, kGradWaves>), dim3((unsigned)blocks, gy, entries),
-                           dim3(64 * kGradWaves), 0, s, a);
-    }
-}
-
-template <int XT>
-void grad_list(const GradArgs& a, int kind, int blocks, unsigned entries, bool few, hipStream_t s) {
-    const bool one = a.who.R <= 16;
-    if (kind == kAll) {
-        if constexpr (XT != MOE_F32) one ? grad_go<XT, 1, kAll>(a, blocks, entries, few, s) : grad_go<XT, 2, kAll>(a, blocks, entries, few, s);
-    } else if (kind == kScan) {
-        one ? grad_go<XT, 1, kScan>(a, blocks, entries, few, s) : grad_go<XT, 2, kScan>(a, blocks, entries, few, s);
-    } else {
-        one ? grad_go<XT, 1, kPlan>(a, blocks, entries, few, s) : grad_go<XT, 2, kPlan>(a, blocks, entries, few, s);
-    }
+template <int RTW>
+void grad_go(const GradArgs& a, int kind, int blocks, unsigned entries, bool few, hipStream_t s) {
+    const dim3 grid((unsigned)blocks, (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW)), entries), many(64 * kGradWaves), one(64);
+    if (kind == kAll) hipLaunchKernelGGL((weight_grad_kernel<RTW, kAll, kGradWaves>), grid, many, 0, s, a);
+    else if (kind == kScan && few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, 1>), grid, one, 0, s, a);
+    else if (kind == kScan) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, kGradWaves>), grid, many, 0, s, a);
+    else if (few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kPlan, 1>), grid, one, 0, s, a);
+    else hipLaunchKernelGGL((weight_grad_kernel<RTW, kPlan, kGradWaves>), grid, many, 0, s, a);
 }
 
 }  // namespace
@@ -356,7 +361,7 @@ static WeightGradPlan plan_of(int T, int n, int R, int C0, int C1, bool ids) {
         return p;
     }
     const int wgs = groups_of(R) * ((C0 + 127) / 128 + (C1 + 127) / 128);
-    const int want = (512 + wgs - 1) / wgs;
+    const int want = (256 + wgs - 1) / wgs;
     const int even = ((T + want - 1) / want + kLeastChunk - 1) / kLeastChunk * kLeastChunk;
     p.chunk = std::max(kLeastChunk, std::min(even, kMostChunk));
     // a set in several chunks has more than `chunk` tokens, and one chunk at most is not full
@@ -371,26 +376,29 @@ WeightGradPlan weight_grad_plan(int T, int n, int R, int C0, int C1) { return pl
 static int weight_grad(const TokenSets& who, int kind, const TokenPlan* plan, const float* scale, const WeightGradPlan& p,
                        const WeightGradCall* calls, int n_calls, float* part, hipStream_t s) {
     const unsigned chunks = who.T > p.chunk ? (unsigned)((who.T + p.chunk - 1) / p.chunk) : 1u;
-    // few tokens a set: a wave's 128 columns each
+    // few tokens a set: a wave has them all
     const bool few = kind != kAll && who.T <= 64 * who.n;
+    GradArgs a{};
+    a.who = who;
+    if (plan) a.plan = *plan;
+    a.scale = scale; a.chunk = p.chunk;
+    int blocks = 0, joins = 0, joins0 = 0;
     for (int i = 0; i < n_calls; ++i) {
-        const WeightGradCall& w = calls[i];
-        GradArgs a{};
-        a.who = who;
-        if (plan) a.plan = *plan;
-        a.scale = scale; a.w = w; a.chunk = p.chunk; a.part = part;
-        a.slot_floats = (int64_t)who.R * w.C + (w.bias ? who.R : 0);
-        part += p.slots * a.slot_floats;
-        const int blocks = (w.C + 127) / 128;
-        const unsigned entries = kind == kAll ? chunks : kind == kScan ? (unsigned)who.n : (unsigned)(who.T / p.chunk + who.n);
-        if (w.x_type == kCodes) grad_list<kCodes>(a, kind, blocks, entries, few, s);
-        else if (w.x_type == MOE_F32) grad_list<MOE_F32>(a, kind, blocks, entries, few, s);
-        else grad_list<MOE_BF16>(a, kind, blocks, entries, few, s);
-        if (p.slots) {
-            const int64_t all = (int64_t)who.R * w.C + (w.bias ? who.R : 0);
-            hipLaunchKernelGGL(weight_grad_join_kernel, dim3((unsigned)((all + 1023) / 1024), (unsigned)who.n), dim3(256), 0, s, a,
-                               (int)chunks);
-        }
+        a.w[i] = calls[i];
+        a.slot_floats[i] = (int64_t)who.R * calls[i].C + (calls[i].bias ? who.R : 0);
+        a.part[i] = part;
+        part += p.slots * a.slot_floats[i];
+        if (i == 0) a.blocks0 = (calls[0].C + 127) / 128;
+        blocks += (calls[i].C + 127) / 128;
+        joins += (int)((a.slot_floats[i] + 1023) / 1024);
+        if (i == 0) joins0 = joins;
+    }
+    const unsigned entries = kind == kAll ? chunks : kind == kScan ? (unsigned)who.n : (unsigned)(who.T / p.chunk + who.n);
+    if (who.R <= 16) grad_go<1>(a, kind, blocks, entries, few, s);
+    else grad_go<2>(a, kind, blocks, entries, few, s);
+    if (p.slots) {
+        a.blocks0 = joins0;
+        hipLaunchKernelGGL(weight_grad_join_kernel, dim3((unsigned)joins, (unsigned)who.n), dim3(256), 0, s, a, (int)chunks);
     }
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
