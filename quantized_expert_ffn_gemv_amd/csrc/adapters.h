@@ -14,15 +14,14 @@ struct TokenSets {
 };
 
 // The tokens in order of their adapters, made once a call where there are too many for every
-// workgroup to look through the ids itself.  Entries are (adapter, first place in order, tokens,
-// slot), n_* of them; tokens without an adapter come last, as adapter -1.
+// workgroup to look through the ids itself; tokens without an adapter come last, as set -1.
 struct TokenPlan {
     int32_t* order;           // [T]
-    int4* tiles;              // up to kPlanTile tokens
-    int4* chunks;             // up to `chunk` tokens of one adapter, at least one entry for every adapter; slot: where
-                              // an adapter with several has its partial sums, else -1
-    int32_t* counts;          // [0] tiles, [1] chunks
-    int2* joins;              // [n]: an adapter's first slot and its number (0: it has none)
+    int4* tiles;              // [T / kPlanTile + n + 1]: (set, first place in order, tokens up to kPlanTile or 0)
+    int4* chunks;             // [T / chunk + n]: (set or -1 for an empty entry, first place, tokens, slot), each adapter's
+                              // tokens by up to `chunk`, one entry where it has none; slot: where an adapter with
+                              // several has its partial sums, else -1
+    int2* joins;              // [n]: an adapter's first slot and their number (0: it has none)
     int chunk;
 };
 constexpr int kPlanTile = 64;
@@ -97,7 +96,7 @@ struct WeightGradPlan {
     int slots;                // partial sums at most (0: none are split)
     size_t most_floats;       // of the partial sums of any call of up to T tokens
 };
-constexpr int kLeastChunk = 256, kMostChunk = 2048;
+constexpr int kLeastChunk = 256, kMostChunk = 1024;
 WeightGradPlan weight_grad_plan(int T, int n, int R, int C0, int C1);
 int launch_weight_grad(const TokenSets& who, const TokenPlan* plan, const float* scale, const WeightGradPlan& p,
                        const WeightGradCall* calls, int n_calls, float* part, hipStream_t s);

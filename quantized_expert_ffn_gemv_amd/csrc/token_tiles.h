@@ -41,35 +41,40 @@ __device__ __forceinline__ int scan_tile(const TokenSets& who, int leader, int& 
     return min(count - first, kScanTile);
 }
 
-// Rounded to bf16, and what that leaves out, PARTS times: 8 floats to PARTS operands of 4 words.
-template <int PARTS>
-__device__ __forceinline__ void bf16_parts(float (&v)[8], uint32_t (&out)[PARTS][4]) {
+// 8 floats as three bf16 operands of 4 words that add up to them: the upper 8 bits of each, the next 8
+// of what is left, and the rest, cut and not rounded, which leaves nothing of a float32's 24 bits.  (An
+// infinity's rest is a NaN.)
+__device__ __forceinline__ void bf16_parts(const float (&v)[8], uint32_t (&out)[3][4]) {
+    constexpr uint32_t HI = 0x07060302u;
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p)
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+        out[0][i] = __builtin_amdgcn_perm(b, a, HI);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            out[p][i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-            if (p + 1 < PARTS) {
-                // an infinity leaves no rest (inf - inf would make the sum of its parts a NaN)
-                const float a = v[2 * i] - __uint_as_float(out[p][i] << 16);
-                const float b = v[2 * i + 1] - __uint_as_float(out[p][i] & 0xFFFF0000u);
-                v[2 * i] = fabsf(v[2 * i]) < INFINITY ? a : 0.f;
-                v[2 * i + 1] = fabsf(v[2 * i + 1]) < INFINITY ? b : 0.f;
-            }
+        for (int p = 1; p < 3; ++p) {
+            a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xFFFF0000u));
+            b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xFFFF0000u));
+            out[p][i] = __builtin_amdgcn_perm(b, a, HI);
         }
+    }
 }
 
-// rows[i]: 8 bf16 columns of row i -> out[j]: column j of the 8 rows, in row order.
-__device__ __forceinline__ void turn8(const uint4 (&rows)[8], uint32_t (&out)[8][4]) {
+// rows[i]: 8 bf16 columns of row i -> out[j]: column 4 half + j of the 8 rows, in row order.
+__device__ __forceinline__ void turn4(const uint4* rows, int half, uint32_t (&out)[4][4]) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+    for (int d = 0; d < 2; ++d)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const uint32_t a = reinterpret_cast<const uint32_t*>(&rows[2 * p])[d];
-            const uint32_t b = reinterpret_cast<const uint32_t*>(&rows[2 * p + 1])[d];
+            const uint32_t a = reinterpret_cast<const uint32_t*>(&rows[2 * p])[2 * half + d];
+            const uint32_t b = reinterpret_cast<const uint32_t*>(&rows[2 * p + 1])[2 * half + d];
             out[2 * d][p] = __builtin_amdgcn_perm(b, a, 0x05040100u);
             out[2 * d + 1][p] = __builtin_amdgcn_perm(b, a, 0x07060302u);
         }
+}
+
+__device__ __forceinline__ void turn8(const uint4 (&rows)[8], uint32_t (&out)[8][4]) {
+    turn4(rows, 0, reinterpret_cast<uint32_t (&)[4][4]>(out[0]));
+    turn4(rows, 1, reinterpret_cast<uint32_t (&)[4][4]>(out[4]));
 }
 
 // Columns come 8 to a lane.  Where fewer are left (C no multiple of 8; C is 8 or more) the

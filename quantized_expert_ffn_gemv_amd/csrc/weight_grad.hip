@@ -15,6 +15,7 @@
 // (few).  Where columns and r give too few workgroups, tokens are split in chunks, whose sums a
 // second kernel adds in order.  No atomics: equal calls give equal bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "adapters.h"
 #include "token_tiles.h"
@@ -26,6 +27,9 @@ namespace {
 constexpr int kGradWaves = 8;
 constexpr int kStep = 32;                 // tokens a product
 enum ListKind { kAll = 0, kScan = 1, kPlan = 2 };
+// Waves a SIMD that the registers are held to: with 16 r two workgroups a CU hide each other's
+// loads; with 32 one fits, whose waves have the next step's loads in flight instead.
+template <int RTW, int WT, bool F32> constexpr int kGradResident = F32 ? 2 : RTW > 1 ? 3 : WT > 1 ? 4 : 3;
 
 struct GradArgs {
     TokenSets who;
@@ -41,19 +45,29 @@ struct GradArgs {
 template <int XT>
 struct XFrag {
     uint4 v[XT == MOE_F32 ? 16 : XT == kCodes ? 4 : 8];
-    float s[XT == kCodes ? 8 : 1];
+    float s;                  // codes: the scale of token lane % 32
+};
+
+// A set's tokens in LDS, padded with the last to whole steps: numbers, and bytes to their rows of x.
+template <int LIST>
+struct Listed {
+    static constexpr int N = LIST == kAll ? 8 : LIST == kScan ? kScanTokens : kMostChunk;
+    __attribute__((aligned(16))) int token[N];
+    __attribute__((aligned(16))) int64_t row[N];
 };
 
 // One workgroup's block of 128 columns, XT the kind of x.
 template <int XT, int RTW, int LIST, int WT>
-__device__ __forceinline__ void weight_grad_block(const GradArgs& a, const WeightGradCall& w, int xblock, float* part, int64_t slot_floats,
-                                                  int set, int first, int cnt, int slot, const int* list, float (*sums)[16][132]) {
+__device__ __forceinline__ void weight_grad_block(const GradArgs& a, const WeightGradCall& w, int block, float* part, int64_t slot_floats,
+                                                  int set, int first, int cnt, int slot, const Listed<LIST>& list,
+                                                  float (*sums)[16][132]) {
+    constexpr int ES = XT == MOE_F32 ? 4 : XT == kCodes ? 1 : 2;
+    constexpr bool EARLY = RTW < 4 || XT == kCodes;     // (64 r and a bf16 x: no registers for the next step's x)
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int R = a.who.R, C = w.C;
     const int rank = a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), R) : R;
     const int r0 = 16 * RTW * (int)blockIdx.y;
-    const int block = xblock;               // of 128 columns
     const int own = 128 * block + 8 * c, col = first_of_8(own, C), shift = own - col;    // 8 or more: none are this lane's
 
     floatx4_t acc[RTW][8];
@@ -65,115 +79,177 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
         for (int j = 0; j < 8; ++j) acc[rt][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
     }
     const bool biased = LIST == kAll && w.bias != nullptr && block == 0;
-    const int gcol[2] = {min(r0 + c, max(rank - 1, 0)), min(r0 + 16 + c, max(rank - 1, 0))};
-    auto load = [&](XFrag<XT>& f, float (&g)[RTW][8], int step) {
+    // product rt has the r's r_at(row) + rt: a lane's g of all RTW products are neighbours
+    auto r_at = [&](int row) { return min(r0 + RTW * row, R - RTW); };
+    const uint32_t gcol = r_at(c);
+    const char* x = static_cast<const char*>(w.x);
+    const int64_t xlane = ((int64_t)(8 * q) * w.ldx + col) * ES;            // (kAll: rows are a constant stride apart)
+    const uint32_t ldg = (uint32_t)w.ldg, ngs = (uint32_t)C / 128;
+    // 32 tokens; with TAIL (kAll) some of them past the end: the last again, their g 0
+    auto load_x = [&](XFrag<XT>& f, int step, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const int k0 = kStep * step;
+        const char* row[8];
+        if constexpr (LIST == kAll) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (TAIL) row[i] = x + ((int64_t)(first + min(k0 + 8 * q + i, cnt - 1)) * w.ldx + col) * ES;
+                else row[i] = x + (int64_t)(first + k0 + i) * w.ldx * ES + xlane;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[i] = x + list.row[k0 + 8 * q + i] + (int64_t)col * ES;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int k = kStep * step + 8 * q + i, kc = min(k, cnt - 1);
-            const int64_t t = LIST == kAll ? first + kc : list[kc];
             if constexpr (XT == MOE_BF16) {
-                f.v[i] = load_bf16x8(static_cast<const uint16_t*>(w.x) + t * w.ldx + col);
+                __builtin_memcpy(&f.v[i], row[i], 16);
             } else if constexpr (XT == MOE_F32) {
-                __builtin_memcpy(&f.v[2 * i], static_cast<const float*>(w.x) + t * w.ldx + col, 32);
+                __builtin_memcpy(&f.v[2 * i], row[i], 32);
             } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(w.x) + t * w.ldx + col);
+                const uint2 v = *reinterpret_cast<const uint2*>(row[i]);
                 (i & 1) ? (f.v[i >> 1].z = v.x, f.v[i >> 1].w = v.y) : (f.v[i >> 1].x = v.x, f.v[i >> 1].y = v.y);
-                f.s[i] = w.xscale[t * (C / 128) + block];
-            }
-#pragma unroll
-            for (int rt = 0; rt < RTW; ++rt) {
-                const float v = w.g[t * w.ldg + gcol[rt]];
-                g[rt][i] = k < cnt ? v : 0.f;
             }
         }
+        if constexpr (XT == kCodes) {
+            uint32_t t;
+            if constexpr (LIST == kAll) t = first + (TAIL ? min(k0 + (lane & 31), cnt - 1) : k0 + (lane & 31));
+            else t = list.token[k0 + (lane & 31)];
+            f.s = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(w.xscale) + (uint64_t)(4 * (__umul24(t, ngs) + block)));
+        }
     };
-    auto compute = [&](const XFrag<XT>& f, float (&g)[RTW][8]) {
-        uint32_t gp[RTW][3][4];
+    auto load_g = [&](float (&g)[RTW][8], int step, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const int k0 = kStep * step;
+        uint32_t tok[8];
+        if constexpr (LIST == kAll) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tok[i] = first + (TAIL ? min(k0 + 8 * q + i, cnt - 1) : k0 + 8 * q + i);
+        } else {
+            *reinterpret_cast<uint4*>(tok) = *reinterpret_cast<const uint4*>(&list.token[k0 + 8 * q]);
+            *reinterpret_cast<uint4*>(tok + 4) = *reinterpret_cast<const uint4*>(&list.token[k0 + 8 * q + 4]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float gv[RTW];
+            __builtin_memcpy(gv, reinterpret_cast<const char*>(w.g) + (uint64_t)(4 * (__umul24(tok[i], ldg) + gcol)), 4 * RTW);
+#pragma unroll
+            for (int rt = 0; rt < RTW; ++rt) g[rt][i] = gv[rt];
+        }
+    };
+    // g's operands: times the codes' scales, 0 past the end, as three bf16 parts
+    auto prepare_g = [&](const XFrag<XT>& f, float (&g)[RTW][8], uint32_t (&gp)[RTW][3][4], int step, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        float xs[8];
+        if constexpr (XT == kCodes)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) xs[i] = __shfl(f.s, 8 * q + i, kWave);
 #pragma unroll
         for (int rt = 0; rt < RTW; ++rt) {
+            if constexpr (LIST != kAll || TAIL)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[rt][i] = kStep * step + 8 * q + i < cnt ? g[rt][i] : 0.f;
             if (biased)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) bsum[rt] += g[rt][i];
             if constexpr (XT == kCodes)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[rt][i] *= f.s[i];
-            bf16_parts<3>(g[rt], gp[rt]);
+                for (int i = 0; i < 8; ++i) g[rt][i] *= xs[i];
+            bf16_parts(g[rt], gp[rt]);
         }
-        if constexpr (XT == MOE_F32) {
-            float v[8][8];
+    };
+    // columns 4 half .. 4 half + 3 of the block, turned
+    auto prepare_x = [&](const XFrag<XT>& f, int half, uint32_t (&b)[4][4]) {
+        if constexpr (XT == kCodes) {
+            // byte j of tokens 2 p and 2 p + 1: small integers, whose float32 has its bits in the upper half
 #pragma unroll
-            for (int i = 0; i < 8; ++i) __builtin_memcpy(v[i], &f.v[2 * i], 32);
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t lo4 = half ? f.v[p].y : f.v[p].x, hi4 = half ? f.v[p].w : f.v[p].z;
 #pragma unroll
-            for (int px = 0; px < 3; ++px) {
-                uint4 rowv[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t o[1][4];
-                    float rest[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) rest[j] = v[i][j];
-                    bf16_parts<1>(rest, o);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float d = v[i][j] - __uint_as_float((j & 1) ? o[0][j >> 1] & 0xFFFF0000u : o[0][j >> 1] << 16);
-                        v[i][j] = fabsf(v[i][j]) < INFINITY ? d : 0.f;
-                    }
-                    rowv[i] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = (float)(int8_t)(lo4 >> (8 * j)), hi = (float)(int8_t)(hi4 >> (8 * j));
+                    b[j][p] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
                 }
-                uint32_t b[8][4];
-                turn8(rowv, b);
-#pragma unroll
-                for (int rt = 0; rt < RTW; ++rt)
-#pragma unroll
-                    for (int p = 0; p < 3 - px; ++p)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[rt][j] = mfma16(gp[rt][p], b[j], acc[rt][j]);
             }
-        } else {
-            uint32_t b[8][4];
-            if constexpr (XT == kCodes) {
-                // byte j of tokens 2 p and 2 p + 1: small integers, whose float32 has its bits in the upper half
+        } else if constexpr (XT == MOE_BF16) {
+            turn4(f.v, half, b);
+        }
+    };
+    auto multiply = [&](const uint32_t (&gp)[RTW][3][4], int half, const uint32_t (&b)[4][4], int parts) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const uint32_t w[2][2] = {{f.v[p].x, f.v[p].y}, {f.v[p].z, f.v[p].w}};
+        for (int rt = 0; rt < RTW; ++rt)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float lo = (float)(int8_t)(w[0][j >> 2] >> (8 * (j & 3)));
-                        const float hi = (float)(int8_t)(w[1][j >> 2] >> (8 * (j & 3)));
-                        b[j][p] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-                    }
-                }
-            } else {
-                turn8(f.v, b);
+            for (int p = 0; p < 3; ++p)
+                if (p < parts)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[rt][4 * half + j] = mfma16(gp[rt][p], b[j], acc[rt][4 * half + j]);
+    };
+    // float32 x: its upper 8 bits with all of g's parts, the next 8 with two, the rest with one
+    auto multiply_f32 = [&](const XFrag<XT>& f, const uint32_t (&gp)[RTW][3][4]) {
+        float v[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) __builtin_memcpy(v[i], &f.v[(2 * i) % (sizeof(f.v) / 16)], 32);
+#pragma unroll
+        for (int px = 0; px < 3; ++px) {
+            uint4 rowv[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t o[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    o[d] = __builtin_amdgcn_perm(__float_as_uint(v[i][2 * d + 1]), __float_as_uint(v[i][2 * d]), 0x07060302u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] -= __uint_as_float(__float_as_uint(v[i][j]) & 0xFFFF0000u);
+                rowv[i] = make_uint4(o[0], o[1], o[2], o[3]);
             }
 #pragma unroll
-            for (int rt = 0; rt < RTW; ++rt)
-#pragma unroll
-                for (int p = 0; p < 3; ++p)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[rt][j] = mfma16(gp[rt][p], b[j], acc[rt][j]);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t b[4][4];
+                turn4(rowv, half, b);
+                multiply(gp, half, b, 3 - px);
+            }
         }
     };
     if (r0 < rank) {
-        const int steps = (cnt + kStep - 1) / kStep, w0 = WT == 1 ? 0 : wid;
-        if constexpr (XT == MOE_F32) {
-            for (int k = w0; k < steps; k += WT) {
-                XFrag<XT> f;
-                float g[RTW][8];
-                load(f, g, k);
-                compute(f, g);
+        const int steps = LIST == kAll ? cnt / kStep : (cnt + kStep - 1) / kStep, w0 = WT == 1 ? 0 : wid;
+        const std::false_type full{};
+        XFrag<XT> f;
+        float g[RTW][8];
+        uint32_t gp[RTW][3][4], b[4][4];
+        if (w0 < steps) {
+            load_g(g, w0, full);
+            load_x(f, w0, full);
+        }
+        for (int k = w0; k < steps; k += WT) {
+            // the next step's loads go out as their registers come free, before the products (always: the last
+            // step's again at the end)
+            const int next = min(k + WT, steps - 1);
+            prepare_g(f, g, gp, k, full);
+            load_g(g, next, full);
+            if constexpr (XT == MOE_F32) {
+                multiply_f32(f, gp);
+                load_x(f, next, full);
+            } else {
+                __builtin_amdgcn_sched_barrier(0);
+                prepare_x(f, 0, b);
+                multiply(gp, 0, b, 3);
+                __builtin_amdgcn_sched_barrier(0);
+                prepare_x(f, 1, b);
+                if constexpr (EARLY) load_x(f, next, full);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(gp, 1, b, 3);
+                if constexpr (!EARLY) load_x(f, next, full);
             }
-        } else if (w0 < steps) {
-            // the next step's loads are always made (the last again at the end), so that no branch waits for them
-            XFrag<XT> f0, f1;
-            float g0[RTW][8], g1[RTW][8];
-            load(f0, g0, w0);
-            for (int k = w0; k < steps; k += 2 * WT) {
-                load(f1, g1, min(k + WT, steps - 1));
-                compute(f0, g0);
-                if (k + WT >= steps) break;
-                load(f0, g0, min(k + 2 * WT, steps - 1));
-                compute(f1, g1);
+        }
+        if (LIST == kAll && cnt % kStep && wid == steps % WT) {
+            const std::true_type tail{};
+            load_g(g, steps, tail);
+            load_x(f, steps, tail);
+            prepare_g(f, g, gp, steps, tail);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                prepare_x(f, half, b);
+                if constexpr (XT != MOE_F32) multiply(gp, half, b, 3);
             }
         }
     }
@@ -186,8 +262,8 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
         for (int rt = 0; rt < RTW; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = r0 + 16 * rt + 4 * q + i;
-                if (r >= R) continue;
+                const int r = r_at(4 * q + i) + rt;
+                if (r < r0 + RTW * (4 * q + i)) continue;          // (another row's)
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = r < rank ? acc[rt][j][i] * s : 0.f;
@@ -201,7 +277,7 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
                 }
             }
     } else {
-        const int row = tid >> 5, c4 = 4 * (tid & 31), wide = min(C - 128 * block - c4, 4);
+        const int c4 = 4 * (tid & 31), wide = min(C - 128 * block - c4, 4);
 #pragma unroll
         for (int rt = 0; rt < RTW; ++rt) {
             if (rt) __syncthreads();
@@ -218,8 +294,10 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
                 }
             }
             __syncthreads();
-            const int r = r0 + 16 * rt + row;
-            if (r < R && wide > 0) {
+#pragma unroll
+            for (int row = tid >> 5; row < 16; row += 2 * WT) {
+                const int r = r_at(row) + rt;
+                if (r < r0 + RTW * row || wide <= 0) continue;             // (another row's)
                 floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[0][row][c4]);
 #pragma unroll
                 for (int k = 1; k < WT; ++k) v += *reinterpret_cast<const floatx4_t*>(&sums[k][row][c4]);
@@ -241,11 +319,12 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
                 if (q == 0) sums[wid][rt][c] = v;
             }
             __syncthreads();
-            if (tid < 16 * RTW && r0 + tid < R) {
+            if (tid < 16 * RTW) {
+                const int r = r_at(tid & 15) + (tid >> 4);
                 float v = 0.f;
 #pragma unroll
                 for (int k = 0; k < WT; ++k) v += sums[k][tid >> 4][tid & 15];
-                bias[r0 + tid] = v;
+                if (r >= r0 + RTW * (tid & 15)) bias[r] = v;
             }
         }
     }
@@ -253,53 +332,70 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
 
 }  // namespace
 
-template <int RTW, int LIST, int WT>
-__global__ __launch_bounds__(64 * WT, 2) void weight_grad_kernel(GradArgs a) {
-    constexpr int LISTED = LIST == kAll ? 1 : LIST == kScan ? kScanTokens : kMostChunk;
-    __shared__ int list[LISTED];
+// F32: the second matrix' x may be float32.
+template <int RTW, int LIST, int WT, bool F32>
+__global__ __launch_bounds__(64 * WT, (kGradResident<RTW, WT, F32>)) void weight_grad_kernel(GradArgs a) {
+    __shared__ Listed<LIST> list;
     __shared__ int found;
     __shared__ __attribute__((aligned(16))) float sums[WT][16][132];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool second = (int)blockIdx.x >= a.blocks0;
+    const WeightGradCall& w = a.w[second];
     int set = 0, first = 0, cnt, slot = -1;
     if constexpr (LIST == kAll) {
         first = (int)blockIdx.z * a.chunk;
         cnt = min(a.chunk, a.who.T - first);
         slot = gridDim.z > 1 ? (int)blockIdx.z : -1;
-    } else if constexpr (LIST == kScan) {
-        set = blockIdx.z;
-        if (wid == 0) {
-            int id[kScanTokens / 64], n = 0;
+    } else {
+        const int64_t bytes = w.ldx * (w.x_type == MOE_F32 ? 4 : w.x_type == kCodes ? 1 : 2);
+        if constexpr (LIST == kScan) {
+            set = blockIdx.z;
+            if (wid == 0) {
+                int id[kScanTokens / 64], n = 0;
 #pragma unroll
-            for (int k = 0; k < kScanTokens / 64; ++k) id[k] = k * 64 < a.who.T ? a.who.ids[min(k * 64 + lane, a.who.T - 1)] : -1;
+                for (int k = 0; k < kScanTokens / 64; ++k) id[k] = k * 64 < a.who.T ? a.who.ids[min(k * 64 + lane, a.who.T - 1)] : -1;
 #pragma unroll
-            for (int k = 0; k < kScanTokens / 64; ++k) {
-                const int t = k * 64 + lane;
-                const bool mine = t < a.who.T && id[k] == set;
-                const uint64_t mask = __ballot(mine);
-                if (mine) list[n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = t;
-                n += __popcll(mask);
+                for (int k = 0; k < kScanTokens / 64; ++k) {
+                    const int t = k * 64 + lane;
+                    const bool mine = t < a.who.T && id[k] == set;
+                    const uint64_t mask = __ballot(mine);
+                    if (mine) {
+                        const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+                        list.token[at] = t;
+                        list.row[at] = t * bytes;
+                    }
+                    n += __popcll(mask);
+                }
+                if (lane == 0) found = n;
             }
-            if (lane == 0) found = n;
+            __syncthreads();
+            cnt = __builtin_amdgcn_readfirstlane(found);
+        } else {
+            const int4 e = a.plan.chunks[blockIdx.z];
+            set = __builtin_amdgcn_readfirstlane(e.x);
+            if (set < 0) return;
+            cnt = __builtin_amdgcn_readfirstlane(e.z);
+            slot = __builtin_amdgcn_readfirstlane(e.w);
+            for (int k = tid; k < cnt; k += 64 * WT) {
+                const int t = a.plan.order[e.y + k];
+                list.token[k] = t;
+                list.row[k] = t * bytes;
+            }
+            __syncthreads();
+        }
+        // (cnt up to a multiple of 32: the lists hold whole steps)
+        if (tid < kStep && cnt > 0 && cnt % kStep && tid >= cnt % kStep) {
+            list.token[cnt - cnt % kStep + tid] = list.token[cnt - 1];
+            list.row[cnt - cnt % kStep + tid] = list.row[cnt - 1];
         }
         __syncthreads();
-        cnt = __builtin_amdgcn_readfirstlane(found);
-    } else {
-        if ((int)blockIdx.z >= ld_scalar(a.plan.counts, 1)) return;
-        const int4 e = a.plan.chunks[blockIdx.z];
-        set = __builtin_amdgcn_readfirstlane(e.x);
-        cnt = __builtin_amdgcn_readfirstlane(e.z);
-        slot = __builtin_amdgcn_readfirstlane(e.w);
-        for (int k = tid; k < cnt; k += 64 * WT) list[k] = a.plan.order[e.y + k];
-        __syncthreads();
     }
-    const bool second = (int)blockIdx.x >= a.blocks0;
-    const WeightGradCall& w = a.w[second];
     const int block = (int)blockIdx.x - (second ? a.blocks0 : 0);
     float* part = a.part[second];
     const int64_t floats = a.slot_floats[second];
-    if (w.x_type == MOE_BF16) weight_grad_block<MOE_BF16, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
-    else if (w.x_type == kCodes) weight_grad_block<kCodes, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
-    else if constexpr (LIST != kAll) weight_grad_block<MOE_F32, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
+    if (w.x_type == kCodes) weight_grad_block<kCodes, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
+    else if (!F32 || w.x_type == MOE_BF16) weight_grad_block<MOE_BF16, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
+    else weight_grad_block<F32 ? MOE_F32 : MOE_BF16, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
 }
 
 // The chunks' sums of a set that has several, in order.  joins NULL: one set of `number` chunks.
@@ -339,16 +435,19 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(GradArgs a, int n
 
 namespace {
 
-int groups_of(int R) { return R <= 16 ? 1 : (R + 31) / 32; }
+// r's of 16 a wave, the most that is not past R by more than a product
+int products_of(int R) { return R <= 16 ? 1 : 2; }
+int groups_of(int R) { return (R + 16 * products_of(R) - 1) / (16 * products_of(R)); }
 
-template <int RTW>
+template <int RTW, bool F32>
 void grad_go(const GradArgs& a, int kind, int blocks, unsigned entries, bool few, hipStream_t s) {
-    const dim3 grid((unsigned)blocks, (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW)), entries), many(64 * kGradWaves), one(64);
-    if (kind == kAll) hipLaunchKernelGGL((weight_grad_kernel<RTW, kAll, kGradWaves>), grid, many, 0, s, a);
-    else if (kind == kScan && few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, 1>), grid, one, 0, s, a);
-    else if (kind == kScan) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, kGradWaves>), grid, many, 0, s, a);
-    else if (few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kPlan, 1>), grid, one, 0, s, a);
-    else hipLaunchKernelGGL((weight_grad_kernel<RTW, kPlan, kGradWaves>), grid, many, 0, s, a);
+    constexpr int WT = RTW == 2 ? 4 : kGradWaves;
+    const dim3 grid((unsigned)blocks, (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW)), entries), many(64 * WT), one(64);
+    if (kind == kAll) hipLaunchKernelGGL((weight_grad_kernel<RTW, kAll, WT, false>), grid, many, 0, s, a);
+    else if (kind == kScan && few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, 1, F32>), grid, one, 0, s, a);
+    else if (kind == kScan) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, WT, F32>), grid, many, 0, s, a);
+    else if (few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kPlan, 1, F32>), grid, one, 0, s, a);
+    else hipLaunchKernelGGL((weight_grad_kernel<RTW, kPlan, WT, F32>), grid, many, 0, s, a);
 }
 
 }  // namespace
@@ -361,12 +460,12 @@ static WeightGradPlan plan_of(int T, int n, int R, int C0, int C1, bool ids) {
         return p;
     }
     const int wgs = groups_of(R) * ((C0 + 127) / 128 + (C1 + 127) / 128);
-    const int want = (256 + wgs - 1) / wgs;
+    const int want = ((R > 16 ? 512 : 256) + wgs - 1) / wgs;
     const int even = ((T + want - 1) / want + kLeastChunk - 1) / kLeastChunk * kLeastChunk;
-    p.chunk = std::max(kLeastChunk, std::min(even, kMostChunk));
+    p.chunk = std::max(kLeastChunk, ids ? std::min(even, kMostChunk) : even);
     // a set in several chunks has more than `chunk` tokens, and one chunk at most is not full
-    if (T > p.chunk) p.slots = n == 1 ? (T + p.chunk - 1) / p.chunk : 2 * (T / p.chunk);
-    const size_t most = T <= kLeastChunk ? 0 : 2 * std::max<size_t>(want, (T + kMostChunk - 1) / kMostChunk);
+    if (T > p.chunk) p.slots = n == 1 ? (T + p.chunk - 1) / p.chunk : 2 * T / p.chunk;
+    const size_t most = T <= kLeastChunk ? 0 : ids ? 2 * std::max<size_t>(want, (T + kMostChunk - 1) / kMostChunk) : want;
     p.most_floats = most * (size_t)R * ((size_t)C0 + C1 + 1);
     return p;
 }
@@ -394,8 +493,9 @@ static int weight_grad(const TokenSets& who, int kind, const TokenPlan* plan, co
         if (i == 0) joins0 = joins;
     }
     const unsigned entries = kind == kAll ? chunks : kind == kScan ? (unsigned)who.n : (unsigned)(who.T / p.chunk + who.n);
-    if (who.R <= 16) grad_go<1>(a, kind, blocks, entries, few, s);
-    else grad_go<2>(a, kind, blocks, entries, few, s);
+    const bool f32 = calls[n_calls - 1].x_type == MOE_F32;
+    if (products_of(who.R) == 1) f32 ? grad_go<1, true>(a, kind, blocks, entries, few, s) : grad_go<1, false>(a, kind, blocks, entries, few, s);
+    else f32 ? grad_go<2, true>(a, kind, blocks, entries, few, s) : grad_go<2, false>(a, kind, blocks, entries, few, s);
     if (p.slots) {
         a.blocks0 = joins0;
         hipLaunchKernelGGL(weight_grad_join_kernel, dim3((unsigned)joins, (unsigned)who.n), dim3(256), 0, s, a, (int)chunks);
