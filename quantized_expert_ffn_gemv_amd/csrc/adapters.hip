@@ -55,23 +55,29 @@ struct ExpandArgs {
     void* y;
     int64_t ldy;
     float* h;                 // [T][R] or NULL
+    // instead of parts: the sums are taken here, x (bf16) times w1
+    const uint16_t* w1;       // [n][R][K]
+    const uint16_t* x;
+    int64_t ldx;
+    int K, blocks;            // workgroups a tile
 };
 
 // This workgroup's tokens, into `list` (padded with the last one): their number and adapter (-1: none).
-template <bool PLAN>
+template <bool PLAN, int NW = kWaves, int SUBS = 1>
 __device__ __forceinline__ int my_tile(const TokenSets& who, const TokenPlan& plan, int idx, int& set, int* list) {
-    constexpr int TOK = PLAN ? kPlanTile : kScanTile;
+    constexpr int TOK = PLAN ? kPlanTile / SUBS : kScanTile;
     const int tid = threadIdx.x;
     if constexpr (PLAN) {
-        const int4 e = plan.tiles[idx];
+        const int4 e = plan.tiles[idx / SUBS];
+        const int sub = idx % SUBS * TOK;
         set = __builtin_amdgcn_readfirstlane(e.x);
-        const int rows = __builtin_amdgcn_readfirstlane(e.z);
-        if (rows == 0) return 0;
-        if (tid < TOK) list[tid] = plan.order[e.y + min(tid, rows - 1)];
+        const int rows = min(__builtin_amdgcn_readfirstlane(e.z) - sub, TOK);
+        if (rows <= 0) return 0;
+        if (tid < TOK) list[tid] = plan.order[e.y + sub + min(tid, rows - 1)];
         __syncthreads();
         return rows;
     } else {
-        __shared__ int own[kWaves][TOK];
+        __shared__ int own[NW][TOK];
         const int wid = tid >> 6;
         const int rows = scan_tile(who, idx, set, own[wid]);
         if (rows == 0) return 0;
@@ -178,20 +184,34 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_shrink_kernel(ShrinkArgs 
 }
 
 // RT = 1: products over 16 ranks (v_mfma_f32_16x16x16_bf16); else over 32 at a time.
-template <int RT, bool F32, bool PLAN>
-__global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs a) {
-    constexpr int NT = PLAN ? kPlanTile / 16 : 1, TOK = 16 * NT, RP = 16 * RT, KS = RT == 1 ? 1 : RT / 2;
+// SELF: the workgroup takes the tile's sums itself, all of K over its eight waves, instead of reading
+// shrink's: one launch, for few tokens with small factors; the workgroups of a tile sit on one XCD, so that
+// they share a's rows in its L2.
+constexpr int kSelfWaves = 8;
+// A planned tile is two workgroups here (4096 tokens, 2048 -> 8192, rank 32: 35.6 us by one of 64 tokens,
+// which filled the card one and a half times, 32.2 by two).
+constexpr int kExpandSubs = 2;
+template <int RT, bool F32, bool PLAN, bool SELF>
+__global__ __launch_bounds__(64 * (SELF ? kSelfWaves : kWaves)) void adapter_expand_kernel(ExpandArgs a) {
+    constexpr int NW = SELF ? kSelfWaves : kWaves;
+    constexpr int NT = PLAN ? kPlanTile / kExpandSubs / 16 : 1, TOK = 16 * NT, RP = 16 * RT, KS = RT == 1 ? 1 : RT / 2;
     constexpr int HS = RP + 4, PARTS = 3, PER = RT == 1 ? 4 : 8;      // ranks a lane holds of a step
     __shared__ int list[TOK];
     __shared__ __attribute__((aligned(16))) float hs[TOK][HS];
-    int set;
-    const int rows = my_tile<PLAN>(a.who, a.plan, (int)blockIdx.y, set, list);
+    __shared__ __attribute__((aligned(16))) float sums[SELF ? NW : 1][SELF ? 16 : 1][HS];
+    int set, xblock = blockIdx.x, tile = blockIdx.y;
+    if constexpr (SELF) {
+        tile = (int)(blockIdx.x & 7) + 8 * ((int)(blockIdx.x >> 3) / a.blocks);
+        xblock = (int)(blockIdx.x >> 3) % a.blocks;
+        if (tile >= a.who.T) return;
+    }
+    const int rows = my_tile<PLAN, NW, kExpandSubs>(a.who, a.plan, tile, set, list);
     if (rows == 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int R = a.who.R;
     const int rank = set < 0 ? 0 : a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), R) : R;
-    const int own = ((int)blockIdx.x * kWaves + wid) * kUnitCols + 8 * c;
+    const int own = (xblock * NW + wid) * kUnitCols + 8 * c;
     const int col = first_of_8(own, a.C), shift = own - col;           // 8 or more: no column is this lane's
 
     // every load that needs only the list goes out first: the factor's rows, the base's of the first 16
@@ -220,30 +240,62 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_expand_kernel(ExpandArgs 
     };
     if (a.y) load_base(0);
 
-    // the sums of the tile's tokens: the splits' parts, four at a time
     const float s = set < 0 ? 0.f : ld_scalar(a.scale, set);
-    for (int e = tid; e < TOK * (RP / 4); e += 64 * kWaves) {
+    if constexpr (SELF) {
+        const uint16_t* w[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) w[rt] = a.w1 + ((int64_t)max(set, 0) * R + min(16 * rt + c, max(rank - 1, 0))) * a.K;
+        const uint16_t* x = a.x + (int64_t)list[c] * a.ldx;
+        floatx4_t acc[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        for (int u = rank > 0 ? wid : a.K; u < a.K / kUnitCols; u += NW)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int at = u * kUnitCols + 32 * p + 8 * q;
+                const uint4 xv = load_bf16x8(x + at);
+                const uint32_t xf[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const uint4 v = load_bf16x8(w[rt] + at);
+                    const uint32_t wf[4] = {v.x, v.y, v.z, v.w};
+                    acc[rt] = mfma16(wf, xf, acc[rt]);
+                }
+            }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) *reinterpret_cast<floatx4_t*>(&sums[wid][c][16 * rt + 4 * q]) = acc[rt];
+        __syncthreads();
+    }
+    // the sums of the tile's tokens: the splits' parts, four at a time, or the waves'
+    for (int e = tid; e < TOK * (RP / 4); e += 64 * NW) {
         const int row = e / (RP / 4), r = 4 * (e % (RP / 4));
         floatx4_t v{0.f, 0.f, 0.f, 0.f};
         if (row < rows && set >= 0) {
-            const float* p = a.part + (int64_t)list[row] * RP + r;
-            for (int k = 0; k < a.splits; k += 4) {
-                floatx4_t o[4];
+            if constexpr (SELF) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    o[u] = *reinterpret_cast<const floatx4_t*>(p + (int64_t)min(k + u, a.splits - 1) * a.who.T * RP);
+                for (int k = 0; k < NW; ++k) v += *reinterpret_cast<const floatx4_t*>(&sums[k][row][r]);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) v += k + u < a.splits ? o[u] : floatx4_t{0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.f;
+            } else {
+                const float* p = a.part + (int64_t)list[row] * RP + r;
+                for (int k = 0; k < a.splits; k += 4) {
+                    floatx4_t o[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        o[u] = *reinterpret_cast<const floatx4_t*>(p + (int64_t)min(k + u, a.splits - 1) * a.who.T * RP);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v += k + u < a.splits ? o[u] : floatx4_t{0.f, 0.f, 0.f, 0.f};
+                }
             }
         }
-        if (a.h && blockIdx.x == 0 && row < rows)
+        if (a.h && xblock == 0 && row < rows)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (r + i < R) a.h[(int64_t)list[row] * R + r + i] = v[i];
         *reinterpret_cast<floatx4_t*>(&hs[row][r]) = v * s;
     }
     __syncthreads();
-    if (a.y == nullptr || (int)(blockIdx.x * kWaves + wid) * kUnitCols >= a.C) return;
+    if (a.y == nullptr || (xblock * NW + wid) * kUnitCols >= a.C) return;
     if (set < 0 && a.y == a.base) return;
 
     // the factor's block, turned: column j of the lane's 8, its ranks in order
@@ -486,13 +538,13 @@ void shrink_go(const ShrinkArgs& a, dim3 grid, hipStream_t s) {
     }
 }
 
-template <bool F32, bool PLAN>
+template <bool F32, bool PLAN, bool SELF>
 void expand_go(const ExpandArgs& a, dim3 grid, hipStream_t s) {
     switch (rank_tiles(a.who.R)) {
-        case 1: hipLaunchKernelGGL((adapter_expand_kernel<1, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
-        case 2: hipLaunchKernelGGL((adapter_expand_kernel<2, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
-        case 4: hipLaunchKernelGGL((adapter_expand_kernel<4, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a); break;
-        default: hipLaunchKernelGGL((adapter_expand_kernel<8, F32, PLAN>), grid, dim3(64 * kWaves), 0, s, a);
+        case 1: hipLaunchKernelGGL((adapter_expand_kernel<1, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a); break;
+        case 2: hipLaunchKernelGGL((adapter_expand_kernel<2, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a); break;
+        case 4: hipLaunchKernelGGL((adapter_expand_kernel<4, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a); break;
+        default: hipLaunchKernelGGL((adapter_expand_kernel<8, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a);
     }
 }
 
@@ -518,10 +570,14 @@ void expand(const TokenSets& who, const Space& sp, int splits, const float* scal
     a.who = who; a.plan = sp.plan; a.w = w; a.ldw = ldw; a.scale = scale; a.part = sp.part; a.splits = splits; a.C = C;
     a.base = base; a.ldbase = ldbase; a.y = y; a.ldy = ldy; a.h = h;
     const unsigned blocks = y ? (unsigned)((C + kWaves * kUnitCols - 1) / (kWaves * kUnitCols)) : 1u;
-    const dim3 grid(blocks, tile_blocks(who));
-    if (planned(who.T)) f32 ? expand_go<true, true>(a, grid, s) : expand_go<false, true>(a, grid, s);
-    else f32 ? expand_go<true, false>(a, grid, s) : expand_go<false, false>(a, grid, s);
+    const dim3 grid(blocks, tile_blocks(who) * (planned(who.T) ? kExpandSubs : 1));
+    if (planned(who.T)) f32 ? expand_go<true, true, false>(a, grid, s) : expand_go<false, true, false>(a, grid, s);
+    else f32 ? expand_go<true, false, false>(a, grid, s) : expand_go<false, false, false>(a, grid, s);
 }
+
+// Few tokens in one launch, every workgroup with all of its tile's sums.
+int self_blocks(const moe_adapters& m) { return (m.N + kSelfWaves * kUnitCols - 1) / (kSelfWaves * kUnitCols); }
+bool one_launch(const moe_adapters& m, int T) { return !planned(T) && m.R <= 32 && m.R * m.K <= 32768; }
 
 void make_plan(const TokenSets& who, const TokenPlan& plan, hipStream_t s) {
     hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)who.n + 1), dim3(64 * kPlanWaves), 0, s, who, plan);
@@ -538,6 +594,14 @@ int launch_adapter(const moe_adapters& m, int T, const int32_t* ids, const uint1
                    int64_t ldbase, void* y, int64_t ldy, int y_type, float* h, void* ws, hipStream_t s) {
     const TokenSets who{ids, m.rank, T, m.n, m.R};
     const Space sp = space(m, T, false, WeightGradPlan{}, ws);
+    if (one_launch(m, T)) {
+        ExpandArgs a{};
+        a.who = who; a.w = m.b; a.ldw = m.ldb; a.scale = m.scale; a.C = m.N; a.base = base; a.ldbase = ldbase; a.y = y; a.ldy = ldy;
+        a.h = h; a.w1 = m.a; a.x = x; a.ldx = ldx; a.K = m.K; a.blocks = self_blocks(m);
+        const dim3 grid(8u * (unsigned)((T + 7) / 8 * a.blocks));
+        y_type == MOE_F32 ? expand_go<true, false, true>(a, grid, s) : expand_go<false, false, true>(a, grid, s);
+        return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    }
     if (planned(T)) make_plan(who, sp.plan, s);
     shrink(who, sp, m.a, m.K, m.K, x, ldx, false, s);
     expand(who, sp, shrink_splits(T, m.n, m.K), m.scale, m.b, m.ldb, m.N, base, ldbase, y, ldy, y_type == MOE_F32, h, s);

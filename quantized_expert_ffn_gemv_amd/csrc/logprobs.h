@@ -17,7 +17,7 @@ struct LogprobArgs {
     int n_top;
     int32_t* top_ids;
     float* top_logp;
-    float* part;              // [T][splits][4 + 2 n_top]
+    float* part;              // [T][splits][part_words]
     int32_t* sync;
     int splits, pieces;       // workgroups a row; 16-byte pieces of a row each
 };

@@ -29,6 +29,8 @@ namespace {
 
 constexpr int kUnroll = 4;                 // 16-byte pieces a thread and step
 constexpr int kList = 1024;                // candidates kept
+constexpr int kRankStep = 8;               // candidates compared with at once
+constexpr int kKeep = 64;                  // candidates that a workgroup hands on where several share a row
 constexpr int kRowCounters = 512, kRowStride = MOE_LOGPROBS_SYNC_INTS / kRowCounters;
 constexpr float kLog2e = 1.44269504f;
 
@@ -76,6 +78,9 @@ __device__ __forceinline__ float lane_bound(float x, int want) {
     return t <= kOrderedLow ? -INFINITY : unordered(t);
 }
 
+// What a workgroup hands on: its sums, its candidates' number, values and indices.
+__host__ __device__ constexpr int part_words(int n_top) { return n_top ? 4 + 2 * kKeep : 4; }
+
 struct Sums {
     float m, s, w;
 };
@@ -99,8 +104,8 @@ __device__ __forceinline__ Sums wave_join(Sums a) {
 }
 
 struct List {
-    float v[kList];
-    int i[kList];
+    __attribute__((aligned(16))) float v[kList + kRankStep];
+    __attribute__((aligned(16))) int i[kList + kRankStep];
     int count;
     float bound[4];
 };
@@ -129,41 +134,74 @@ __device__ __forceinline__ float bound_of(List& L, float lane_max, int n) {
     return b;
 }
 
-// The best n of the list's entries, best first: out(place, value, index) for each, (-inf, -1)
-// where there are no more.
+// Each entry's place among the list's c (all threads call it, the list complete); out(place, value,
+// index) for the best n, (-inf, -1) where there are no more.
+template <int NW, typename OUT>
+__device__ __forceinline__ void rank_list(List& L, int c, int n, OUT out) {
+    constexpr int NT = 64 * NW;
+    if ((int)threadIdx.x < kRankStep) {
+        L.v[c + threadIdx.x] = -INFINITY;              // (before none)
+        L.i[c + threadIdx.x] = 0x7FFFFFFF;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < c; k += NT) {
+        const float x = L.v[k];
+        const int i = L.i[k];
+        int place = 0;
+        for (int o = 0; o < c; o += kRankStep) {
+            float v[kRankStep];
+            int at[kRankStep];
+#pragma unroll
+            for (int u = 0; u < kRankStep; u += 4) {
+                *reinterpret_cast<float4*>(v + u) = *reinterpret_cast<const float4*>(&L.v[o + u]);
+                *reinterpret_cast<int4*>(at + u) = *reinterpret_cast<const int4*>(&L.i[o + u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kRankStep; ++u) place += before(v[u], at[u], x, i);
+        }
+        if (place < n) out(place, x, i);
+    }
+    for (int k = c + (int)threadIdx.x; k < n; k += NT) out(k, -INFINITY, -1);
+}
+
+// The best n of the threads' EACH entries (index -1: none), best first, by way of the list: those that
+// reach the bound of all, ranked.
+template <int NW, int EACH, typename OUT>
+__device__ __forceinline__ void best_of_entries(List& L, const float (&v)[EACH], const int (&at)[EACH], int n, OUT out) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) top = fmaxf(top, at[e] >= 0 ? v[e] : -INFINITY);
+    const float b = bound_of<NW>(L, top, n);
+    __syncthreads();
+    if (threadIdx.x == 0) L.count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+        if (at[e] >= 0 && v[e] >= b) append(L, v[e], at[e]);
+    __syncthreads();
+    const int c = L.count;
+    rank_list<NW>(L, c, n, out);
+}
+
+// The best n of the list's entries.
 template <int NW, typename OUT>
 __device__ __forceinline__ void best_of(List& L, int n, OUT out) {
     constexpr int NT = 64 * NW, EACH = kList / NT;
     __syncthreads();
-    int c = min(L.count, kList);
-    float v[EACH], top = -INFINITY;
+    const int c = min(L.count, kList);
+    if (c <= kKeep) {
+        rank_list<NW>(L, c, n, out);
+        return;
+    }
+    float v[EACH];
     int at[EACH];
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
         const int k = e * NT + (int)threadIdx.x;
         v[e] = k < c ? L.v[k] : -INFINITY;
         at[e] = k < c ? L.i[k] : -1;
-        top = fmaxf(top, v[e]);
     }
-    if (c > 64) {
-        const float b = bound_of<NW>(L, top, n);
-        __syncthreads();
-        if (threadIdx.x == 0) L.count = 0;
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < EACH; ++e)
-            if (at[e] >= 0 && v[e] >= b) append(L, v[e], at[e]);
-        __syncthreads();
-        c = L.count;
-    }
-    for (int k = threadIdx.x; k < c; k += NT) {
-        const float x = L.v[k];
-        const int i = L.i[k];
-        int place = 0;
-        for (int o = 0; o < c; ++o) place += before(L.v[o], L.i[o], x, i);
-        if (place < n) out(place, x, i);
-    }
-    for (int k = c + (int)threadIdx.x; k < n; k += NT) out(k, -INFINITY, -1);
+    best_of_entries<NW, EACH>(L, v, at, n, out);
 }
 
 // The list overflowed: its entries again, exactly the best n (or all there are) of elements
@@ -308,30 +346,50 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobArgs a) {
             }
         }
     }
+    float kept[kList / NT];                            // the splits' candidates, where there are several
+    int kept_at[kList / NT];
     if (a.splits > 1) {
-        const int words = 4 + 2 * n;
+        const int words = part_words(n);
         float* mine = a.part + ((int64_t)t * a.splits + split) * words;
-        if (tid < 3) put_device(mine + tid, tid == 0 ? sum.m : tid == 1 ? sum.s : sum.w);
-        if constexpr (TOP)
-            best_of<NW>(L, n, [&](int place, float v, int i) {
-                put_device(mine + 4 + place, v);
-                put_device(mine + 4 + n + place, __int_as_float(i));
-            });
-        if (!arrive_last(a.sync + t * kRowStride, a.splits, &flag)) return;
-        const float* all = a.part + (int64_t)t * a.splits * words;
-        sum = Sums{-INFINITY, 0.f, 0.f};
-        if (lane < a.splits) sum = Sums{get_device(all + lane * words), get_device(all + lane * words + 1), get_device(all + lane * words + 2)};
-        sum = wave_join(sum);
+        int handed = 0;
         if constexpr (TOP) {
-            if (tid == 0) L.count = 0;
             __syncthreads();
-            for (int k = tid; k < a.splits * n; k += NT) {
-                const float* from = all + (k / n) * words + 4 + k % n;
-                const float v = get_device(from);
-                const int i = __float_as_int(get_device(from + n));
-                if (i >= 0) append(L, v, i);
+            const int c = min(L.count, kList);
+            handed = c <= kKeep ? c : n;
+            if (c <= kKeep) {
+                if (tid < c) {
+                    put_device(mine + 4 + tid, L.v[tid]);
+                    put_device(mine + 4 + kKeep + tid, __int_as_float(L.i[tid]));
+                }
+            } else {
+                best_of<NW>(L, n, [&](int place, float v, int i) {
+                    put_device(mine + 4 + place, v);
+                    put_device(mine + 4 + kKeep + place, __int_as_float(i));
+                });
             }
         }
+        if (tid < 4) put_device(mine + tid, tid == 0 ? sum.m : tid == 1 ? sum.s : tid == 2 ? sum.w : __int_as_float(handed));
+        if (!arrive_last(a.sync + t * kRowStride, a.splits, &flag)) return;
+        // every load before the first use: the sums by lanes, the candidates a wave a split at a time
+        const float* all = a.part + (int64_t)t * a.splits * words;
+        const float* from = all + min(lane, a.splits - 1) * words;
+        sum = Sums{get_device(from), get_device(from + 1), get_device(from + 2)};
+        if constexpr (TOP) {
+            const int counts = __float_as_int(get_device(from + 3));
+#pragma unroll
+            for (int e = 0; e < kList / NT; ++e) {
+                const float* entry = all + min(e * NW + wid, a.splits - 1) * words + 4 + lane;
+                kept[e] = get_device(entry);
+                kept_at[e] = __float_as_int(get_device(entry + kKeep));
+            }
+#pragma unroll
+            for (int e = 0; e < kList / NT; ++e) {
+                const int s = e * NW + wid;
+                if (s >= a.splits || lane >= __shfl(counts, min(s, a.splits - 1), kWave)) kept_at[e] = -1;
+            }
+        }
+        if (lane >= a.splits) sum = Sums{-INFINITY, 0.f, 0.f};
+        sum = wave_join(sum);
     }
     const bool some = sum.m > -INFINITY || sum.s != sum.s;
     const float base = sum.m > -INFINITY ? sum.m : 0.f;
@@ -342,11 +400,14 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobArgs a) {
         a.logp[t] = !scored ? 0.f : some ? picked - base - log_s : -INFINITY;
         if (a.entropy) a.entropy[t] = some ? log_s - sum.w / sum.s : 0.f;
     }
-    if constexpr (TOP)
-        best_of<NW>(L, n, [&](int place, float v, int i) {
+    if constexpr (TOP) {
+        auto out = [&](int place, float v, int i) {
             a.top_ids[(int64_t)t * n + place] = i;
             a.top_logp[(int64_t)t * n + place] = i < 0 ? -INFINITY : v - base - log_s;
-        });
+        };
+        if (a.splits > 1) best_of_entries<NW, kList / NT>(L, kept, kept_at, n, out);
+        else best_of<NW>(L, n, out);
+    }
 }
 
 namespace {
@@ -441,7 +502,7 @@ int row_splits(int T, int V, int n_top) {
     if (T > kRowCounters || V <= kShortRow) return 1;
     const int steps = (V / 4 + 256 * kUnroll - 1) / (256 * kUnroll);
     int splits = std::min({(512 + T - 1) / T, steps, 64});
-    if (n_top) splits = std::min(splits, kList / n_top);
+    if (n_top) splits = std::min(splits, kList / kKeep);
     return splits;
 }
 
@@ -462,7 +523,7 @@ void logprobs_type(const LogprobArgs& a, hipStream_t s) {
 
 size_t logprobs_workspace_of(int T, int V, int n_top) {
     const int splits = row_splits(T, V, n_top);
-    return splits > 1 ? (size_t)T * splits * (4 + 2 * n_top) * 4 : 0;
+    return splits > 1 ? (size_t)T * splits * part_words(n_top) * 4 : 0;
 }
 
 // Calls of fewer tokens may have more workgroups a row: the most that any has.
