@@ -211,8 +211,16 @@ __global__ __launch_bounds__(64 * (SELF ? kSelfWaves : kWaves)) void adapter_exp
     const int c = lane & 15, q = lane >> 4;
     const int R = a.who.R;
     const int rank = set < 0 ? 0 : a.who.rank ? min(max(ld_scalar(a.who.rank, set), 0), R) : R;
-    const int own = (xblock * NW + wid) * kUnitCols + 8 * c;
-    const int col = first_of_8(own, a.C), shift = own - col;           // 8 or more: no column is this lane's
+    // the lane's columns: 8 neighbours, or of a float32 y twice 4, 64 apart, so that a store of 16 bytes a lane
+    // is whole lines (8 neighbours, every other 16 bytes: 4096 tokens, 2048 -> 8192 75.7 us, so 69.9)
+    constexpr int G = F32 ? 2 : 1, GW = 8 / G;
+    int col[G], shift[G];                                              // shift GW or more: no column is this lane's
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int own = (xblock * NW + wid) * kUnitCols + 64 * g + GW * c;
+        col[g] = min(own, a.C - GW);
+        shift[g] = own - col[g];
+    }
 
     // every load that needs only the list goes out first: the factor's rows, the base's of the first 16
     // tokens (rows 4 q + i; the list is padded with its last token)
@@ -221,15 +229,20 @@ __global__ __launch_bounds__(64 * (SELF ? kSelfWaves : kWaves)) void adapter_exp
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            rowv[ks][i] = i >= PER ? make_uint4(0, 0, 0, 0)
-                                   : load_bf16x8(a.w + ((int64_t)max(set, 0) * R + min(32 * ks + PER * q + i, max(rank - 1, 0))) * a.ldw + col);
+        {
+            rowv[ks][i] = make_uint4(0, 0, 0, 0);
+            if (i >= PER) continue;
+            const uint16_t* row = a.w + ((int64_t)max(set, 0) * R + min(32 * ks + PER * q + i, max(rank - 1, 0))) * a.ldw;
+#pragma unroll
+            for (int g = 0; g < G; ++g) __builtin_memcpy(reinterpret_cast<char*>(&rowv[ks][i]) + 2 * GW * g, row + col[g], 2 * GW);
+        }
     auto load_base = [&](int nt) {
         if (a.base) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldbase + col;
-                if constexpr (F32) __builtin_memcpy(bb[nt & 1][i], static_cast<const float*>(a.base) + at, 32);
-                else bb[nt & 1][i][0] = load_bf16x8(static_cast<const uint16_t*>(a.base) + at);
+                const char* row = static_cast<const char*>(a.base) + (int64_t)list[16 * nt + 4 * q + i] * a.ldbase * (F32 ? 4 : 2);
+#pragma unroll
+                for (int g = 0; g < G; ++g) __builtin_memcpy(&bb[nt & 1][i][g], row + col[g] * (F32 ? 4 : 2), 16);
             }
         } else {
 #pragma unroll
@@ -350,39 +363,37 @@ __global__ __launch_bounds__(64 * (SELF ? kSelfWaves : kWaves)) void adapter_exp
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (shift >= 8 || 16 * nt + 4 * q + i >= rows) continue;
-            const int64_t at = (int64_t)list[16 * nt + 4 * q + i] * a.ldy + col;
-            float v[8];
-            if constexpr (F32) {
-                __builtin_memcpy(v, bb[nt & 1][i], 32);
-            } else {
-                const uint4 own16 = bb[nt & 1][i][0];
-                const uint32_t b[4] = {own16.x, own16.y, own16.z, own16.w};
+            if (16 * nt + 4 * q + i >= rows) continue;
+            const int64_t row = (int64_t)list[16 * nt + 4 * q + i] * a.ldy;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((j & 1) ? b[j >> 1] & 0xFFFF0000u : b[j >> 1] << 16);
-            }
+            for (int g = 0; g < G; ++g) {
+                if (shift[g] >= GW) continue;
+                const uint4 base = bb[nt & 1][i][g];
+                const uint32_t b[4] = {base.x, base.y, base.z, base.w};
+                if constexpr (F32) {
+                    float v[4], *out = static_cast<float*>(a.y) + row + col[g];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += acc[j][i];
-            if constexpr (F32) {
-                float* out = static_cast<float*>(a.y) + at;
-                if (shift == 0) {
-                    __builtin_memcpy(out, v, 32);
+                    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(b[j]) + acc[4 * g + j][i];
+                    if (shift[g] == 0) {
+                        __builtin_memcpy(out, v, 16);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j >= shift[g]) out[j] = v[j];
+                    }
                 } else {
+                    uint32_t o[4];
+                    uint16_t* out = static_cast<uint16_t*>(a.y) + row + col[g];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j >= shift) out[j] = v[j];
-                }
-            } else {
-                uint16_t* out = static_cast<uint16_t*>(a.y) + at;
-                uint32_t o[4];
+                    for (int d = 0; d < 4; ++d)
+                        o[d] = pack_bf16(__uint_as_float(b[d] << 16) + acc[2 * d][i], __uint_as_float(b[d] & 0xFFFF0000u) + acc[2 * d + 1][i]);
+                    if (shift[g] == 0) {
+                        __builtin_memcpy(out, o, 16);
+                    } else {
 #pragma unroll
-                for (int d = 0; d < 4; ++d) o[d] = pack_bf16(v[2 * d], v[2 * d + 1]);
-                if (shift == 0) {
-                    __builtin_memcpy(out, o, 16);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j >= shift) out[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+                        for (int j = 0; j < 8; ++j)
+                            if (j >= shift[g]) out[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+                    }
                 }
             }
         }
@@ -538,14 +549,20 @@ void shrink_go(const ShrinkArgs& a, dim3 grid, hipStream_t s) {
     }
 }
 
-template <bool F32, bool PLAN, bool SELF>
+template <bool F32, bool PLAN>
 void expand_go(const ExpandArgs& a, dim3 grid, hipStream_t s) {
     switch (rank_tiles(a.who.R)) {
-        case 1: hipLaunchKernelGGL((adapter_expand_kernel<1, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a); break;
-        case 2: hipLaunchKernelGGL((adapter_expand_kernel<2, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a); break;
-        case 4: hipLaunchKernelGGL((adapter_expand_kernel<4, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a); break;
-        default: hipLaunchKernelGGL((adapter_expand_kernel<8, F32, PLAN, SELF>), grid, dim3(64 * (SELF ? kSelfWaves : kWaves)), 0, s, a);
+        case 1: hipLaunchKernelGGL((adapter_expand_kernel<1, F32, PLAN, false>), grid, dim3(64 * kWaves), 0, s, a); break;
+        case 2: hipLaunchKernelGGL((adapter_expand_kernel<2, F32, PLAN, false>), grid, dim3(64 * kWaves), 0, s, a); break;
+        case 4: hipLaunchKernelGGL((adapter_expand_kernel<4, F32, PLAN, false>), grid, dim3(64 * kWaves), 0, s, a); break;
+        default: hipLaunchKernelGGL((adapter_expand_kernel<8, F32, PLAN, false>), grid, dim3(64 * kWaves), 0, s, a);
     }
+}
+
+template <bool F32>
+void self_go(const ExpandArgs& a, dim3 grid, hipStream_t s) {
+    if (a.who.R <= 16) hipLaunchKernelGGL((adapter_expand_kernel<1, F32, false, true>), grid, dim3(64 * kSelfWaves), 0, s, a);
+    else hipLaunchKernelGGL((adapter_expand_kernel<2, F32, false, true>), grid, dim3(64 * kSelfWaves), 0, s, a);
 }
 
 unsigned tile_blocks(const TokenSets& who) {
@@ -571,8 +588,8 @@ void expand(const TokenSets& who, const Space& sp, int splits, const float* scal
     a.base = base; a.ldbase = ldbase; a.y = y; a.ldy = ldy; a.h = h;
     const unsigned blocks = y ? (unsigned)((C + kWaves * kUnitCols - 1) / (kWaves * kUnitCols)) : 1u;
     const dim3 grid(blocks, tile_blocks(who) * (planned(who.T) ? kExpandSubs : 1));
-    if (planned(who.T)) f32 ? expand_go<true, true, false>(a, grid, s) : expand_go<false, true, false>(a, grid, s);
-    else f32 ? expand_go<true, false, false>(a, grid, s) : expand_go<false, false, false>(a, grid, s);
+    if (planned(who.T)) f32 ? expand_go<true, true>(a, grid, s) : expand_go<false, true>(a, grid, s);
+    else f32 ? expand_go<true, false>(a, grid, s) : expand_go<false, false>(a, grid, s);
 }
 
 // Few tokens in one launch, every workgroup with all of its tile's sums.
@@ -599,7 +616,7 @@ int launch_adapter(const moe_adapters& m, int T, const int32_t* ids, const uint1
         a.who = who; a.w = m.b; a.ldw = m.ldb; a.scale = m.scale; a.C = m.N; a.base = base; a.ldbase = ldbase; a.y = y; a.ldy = ldy;
         a.h = h; a.w1 = m.a; a.x = x; a.ldx = ldx; a.K = m.K; a.blocks = self_blocks(m);
         const dim3 grid(8u * (unsigned)((T + 7) / 8 * a.blocks));
-        y_type == MOE_F32 ? expand_go<true, false, true>(a, grid, s) : expand_go<false, false, true>(a, grid, s);
+        y_type == MOE_F32 ? self_go<true>(a, grid, s) : self_go<false>(a, grid, s);
         return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
     }
     if (planned(T)) make_plan(who, sp.plan, s);

@@ -412,13 +412,14 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobArgs a) {
 
 namespace {
 
-constexpr int kGradPieces = 4;             // of 8 elements a thread
+constexpr int kGradElements = 32;          // elements a thread
 
 }  // namespace
 
-template <int TYPE, int GTYPE>
-__global__ __launch_bounds__(256) void logprobs_grad_kernel(LogprobGradArgs a, unsigned blocks) {
-    constexpr int WIDE = GTYPE == MOE_F32 ? 4 : 2;
+template <int TYPE, int GTYPE, int NT>
+__global__ __launch_bounds__(NT) void logprobs_grad_kernel(LogprobGradArgs a, unsigned blocks) {
+    constexpr int WIDE = GTYPE == MOE_F32 ? 4 : 2, IN = TYPE == MOE_F32 ? 4 : 2;
+    constexpr int PE = 16 / WIDE, PIECES = kGradElements / PE;     // elements of a 16-byte piece of the gradient, pieces a thread
     const int t = blockIdx.x / blocks, block = blockIdx.x % blocks, tid = threadIdx.x;
     const int token = ld_scalar(a.tokens, t);
     const bool scored = (unsigned)token < (unsigned)a.V;
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(256) void logprobs_grad_kernel(LogprobGradArgs a, u
     const char* row = static_cast<const char*>(a.logits) + (int64_t)t * a.ld * (TYPE == MOE_F32 ? 4 : 2);
     char* out = static_cast<char*>(a.dlogits) + (int64_t)t * a.ldg * WIDE;
     const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / WIDE, a.V);
-    const int pieces = (a.V - head) / 8, tail = a.V - head - pieces * 8;
+    const int pieces = (a.V - head) / PE, tail = a.V - head - pieces * PE;
     auto grad = [&](float x, int v) {
         const float lp = x - base - log_s;
         const float p = exp_down(lp);
@@ -440,53 +441,56 @@ __global__ __launch_bounds__(256) void logprobs_grad_kernel(LogprobGradArgs a, u
     };
     // head and tail, one a lane of the first workgroup
     if (block == 0) {
-        const int v = tid < head ? tid : tid >= 32 && tid < 32 + tail ? head + pieces * 8 + tid - 32 : -1;
+        const int v = tid < head ? tid : tid >= 32 && tid < 32 + tail ? head + pieces * PE + tid - 32 : -1;
         if (v >= 0) {
             const float g = none ? 0.f : grad(element<TYPE>(row, v), v);
             if constexpr (GTYPE == MOE_F32) reinterpret_cast<float*>(out)[v] = g;
             else reinterpret_cast<uint16_t*>(out)[v] = (uint16_t)pack_bf16(g, 0.f);
         }
     }
-    const int p0 = block * 256 * kGradPieces + tid;
+    const int p0 = block * NT * PIECES + tid;
     if (none) {
 #pragma unroll
-        for (int k = 0; k < kGradPieces; ++k) {
-            const int p = p0 + 256 * k;
+        for (int k = 0; k < PIECES; ++k) {
+            const int p = p0 + NT * k;
             if (p >= pieces) break;
-            uint4* to = reinterpret_cast<uint4*>(out + ((int64_t)head + 8 * p) * WIDE);
-            to[0] = make_uint4(0, 0, 0, 0);
-            if constexpr (GTYPE == MOE_F32) to[1] = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(out + ((int64_t)head + PE * p) * WIDE) = make_uint4(0, 0, 0, 0);
         }
         return;
     }
-    uint4 q[kGradPieces][TYPE == MOE_F32 ? 2 : 1];
+    uint32_t q[PIECES][PE * IN / 4];
 #pragma unroll
-    for (int k = 0; k < kGradPieces; ++k) {
-        const int p = min(p0 + 256 * k, pieces - 1);
-        if (pieces > 0) __builtin_memcpy(q[k], row + ((int64_t)head + 8 * p) * (TYPE == MOE_F32 ? 4 : 2), TYPE == MOE_F32 ? 32 : 16);
+    for (int k = 0; k < PIECES; ++k) {
+        const int p = min(p0 + NT * k, pieces - 1);
+        if (pieces > 0) __builtin_memcpy(q[k], row + ((int64_t)head + PE * p) * IN, PE * IN);
     }
 #pragma unroll
-    for (int k = 0; k < kGradPieces; ++k) {
-        const int p = p0 + 256 * k;
+    for (int k = 0; k < PIECES; ++k) {
+        const int p = p0 + NT * k;
         if (p >= pieces) break;
-        float x[8], g[8];
-        if constexpr (TYPE == MOE_F32) __builtin_memcpy(x, q[k], 32);
-        else unpack<MOE_BF16>(q[k][0], x);
-        const int v = head + 8 * p;
+        float x[PE], g[PE];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < PE; ++j)
+            x[j] = TYPE == MOE_F32 ? __uint_as_float(q[k][j])
+                                   : __uint_as_float((j & 1) ? q[k][j >> 1] & 0xFFFF0000u : q[k][j >> 1] << 16);
+        const int v = head + PE * p;
+#pragma unroll
+        for (int j = 0; j < PE; ++j) {
             const float lp = x[j] - base - log_s;
             g[j] = exp_down(lp) * fmaf(-u, fmaxf(lp, -1e4f) + H, -w);
         }
-        if (scored && token >= v && token < v + 8)
+        if (scored && token >= v && token < v + PE)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < PE; ++j)
                 if (v + j == token) g[j] = grad(x[j], token);
         uint4* to = reinterpret_cast<uint4*>(out + (int64_t)v * WIDE);
         if constexpr (GTYPE == MOE_F32) {
-            __builtin_memcpy(to, g, 32);
+            __builtin_memcpy(to, g, 16);
         } else {
-            to[0] = make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+            uint32_t o[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) o[d] = pack_bf16(g[(2 * d) % PE], g[(2 * d + 1) % PE]);
+            *to = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -519,6 +523,15 @@ void logprobs_type(const LogprobArgs& a, hipStream_t s) {
     else a.entropy ? logprobs_go<TYPE, false, true>(a, s) : logprobs_go<TYPE, false, false>(a, s);
 }
 
+template <int TYPE, int GTYPE>
+void grad_threads(const LogprobGradArgs& a, hipStream_t s) {
+    const int threads = a.V <= kShortRow ? 64 : 256;
+    const unsigned blocks = (unsigned)std::max(1, (a.V + threads * kGradElements - 1) / (threads * kGradElements));
+    const dim3 grid(blocks * (unsigned)a.T);
+    if (threads == 64) hipLaunchKernelGGL((logprobs_grad_kernel<TYPE, GTYPE, 64>), grid, dim3(64), 0, s, a, blocks);
+    else hipLaunchKernelGGL((logprobs_grad_kernel<TYPE, GTYPE, 256>), grid, dim3(256), 0, s, a, blocks);
+}
+
 }  // namespace
 
 size_t logprobs_workspace_of(int T, int V, int n_top) {
@@ -544,15 +557,8 @@ int launch_logprobs(LogprobArgs a, hipStream_t s) {
 }
 
 int launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s) {
-    const unsigned blocks = (unsigned)std::max(1, (a.V / 8 + 256 * kGradPieces - 1) / (256 * kGradPieces));
-    const dim3 grid(blocks * (unsigned)a.T);
-    if (a.type == MOE_F32) {
-        if (a.grad_type == MOE_F32) hipLaunchKernelGGL((logprobs_grad_kernel<MOE_F32, MOE_F32>), grid, dim3(256), 0, s, a, blocks);
-        else hipLaunchKernelGGL((logprobs_grad_kernel<MOE_F32, MOE_BF16>), grid, dim3(256), 0, s, a, blocks);
-    } else {
-        if (a.grad_type == MOE_F32) hipLaunchKernelGGL((logprobs_grad_kernel<MOE_BF16, MOE_F32>), grid, dim3(256), 0, s, a, blocks);
-        else hipLaunchKernelGGL((logprobs_grad_kernel<MOE_BF16, MOE_BF16>), grid, dim3(256), 0, s, a, blocks);
-    }
+    if (a.type == MOE_F32) a.grad_type == MOE_F32 ? grad_threads<MOE_F32, MOE_F32>(a, s) : grad_threads<MOE_F32, MOE_BF16>(a, s);
+    else a.grad_type == MOE_F32 ? grad_threads<MOE_BF16, MOE_F32>(a, s) : grad_threads<MOE_BF16, MOE_BF16>(a, s);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -21,22 +21,27 @@ __device__ __forceinline__ int scan_tile(const TokenSets& who, int leader, int& 
     set = __builtin_amdgcn_readfirstlane(set_of(who.ids, leader, who.n));
     int id[kScanTokens / 64];
 #pragma unroll
-    for (int c = 0; c < kScanTokens / 64; ++c)
-        id[c] = c * 64 < who.T ? who.ids[min(c * 64 + lane, who.T - 1)] : 0;
+    for (int c = 0; c < kScanTokens / 64; ++c) {
+        if (c * 64 >= who.T) break;
+        id[c] = who.ids[min(c * 64 + lane, who.T - 1)];
+    }
     int count = 0, first = 0;
 #pragma unroll
     for (int c = 0; c < kScanTokens / 64; ++c) {
+        if (c * 64 >= who.T) break;
         const int t = c * 64 + lane;
         const int mine = (unsigned)id[c] < (unsigned)who.n ? id[c] : -1;
         const bool same = t < who.T && mine == set;
         const uint64_t mask = __ballot(same);
         const int place = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        if (c == leader >> 6) first = __shfl(place, leader & 63, kWave);
+        if (c == leader >> 6) {
+            first = __builtin_amdgcn_readlane(place, leader & 63);
+            if (first % kScanTile) return 0;
+        }
         const int at = place - first;
         if (same && t >= leader && at < kScanTile) list[at] = t;
         count += __popcll(mask);
     }
-    if (first % kScanTile) return 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     return min(count - first, kScanTile);
 }

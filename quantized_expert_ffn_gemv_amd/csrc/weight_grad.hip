@@ -36,7 +36,7 @@ struct GradArgs {
     TokenPlan plan;
     const float* scale;       // [n] or NULL
     WeightGradCall w[2];      // a launch has one or two matrices
-    int blocks0;              // workgroups (first grid axis) of the first
+    int groups0;              // workgroups (first grid axis) of the first
     int chunk;                // kAll: tokens an entry
     float* part[2];           // [slots][R C (+ R)]
     int64_t slot_floats[2];
@@ -256,31 +256,19 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
     const float s = slot < 0 && a.scale ? ld_scalar(a.scale, set) : 1.f;
     float* out = slot < 0 ? w.out + (int64_t)set * R * C : part + (int64_t)slot * slot_floats;
     float* bias = slot < 0 ? w.bias : part + (int64_t)slot * slot_floats + (int64_t)R * C;
-    if constexpr (WT == 1) {
-        if (shift >= 8) return;
-#pragma unroll
-        for (int rt = 0; rt < RTW; ++rt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = r_at(4 * q + i) + rt;
-                if (r < r0 + RTW * (4 * q + i)) continue;          // (another row's)
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = r < rank ? acc[rt][j][i] * s : 0.f;
-                float* to = out + (int64_t)r * C + col;
-                if (shift == 0) {
-                    __builtin_memcpy(to, v, 32);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j >= shift) to[j] = v[j];
-                }
-            }
-    } else {
-        const int c4 = 4 * (tid & 31), wide = min(C - 128 * block - c4, 4);
+    // By way of LDS, so that a store has whole rows of 512 bytes (from the products' layout, 8 columns a
+    // lane, every other 16 bytes: 256 adapters 4096 x 4096 50.8 us, most of them zeros); with one
+    // token wave each has a part of its own and no barrier.
+    {
+        constexpr bool ONE = WT == 1;
+        auto meet = [&] {
+            if constexpr (ONE) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            else __syncthreads();
+        };
+        const int at = ONE ? lane : tid, c4 = 4 * (at & 31), wide = min(C - 128 * block - c4, 4);
 #pragma unroll
         for (int rt = 0; rt < RTW; ++rt) {
-            if (rt) __syncthreads();
+            if (rt) meet();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float* to = &sums[wid][4 * q + i][8 * c];
@@ -293,12 +281,12 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
                         if (j >= shift) to[j - shift] = acc[rt][j][i];
                 }
             }
-            __syncthreads();
+            meet();
 #pragma unroll
-            for (int row = tid >> 5; row < 16; row += 2 * WT) {
+            for (int row = at >> 5; row < 16; row += 2 * WT) {
                 const int r = r_at(row) + rt;
                 if (r < r0 + RTW * row || wide <= 0) continue;             // (another row's)
-                floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[0][row][c4]);
+                floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[ONE ? wid : 0][row][c4]);
 #pragma unroll
                 for (int k = 1; k < WT; ++k) v += *reinterpret_cast<const floatx4_t*>(&sums[k][row][c4]);
                 v = r < rank ? v * s : floatx4_t{0.f, 0.f, 0.f, 0.f};
@@ -333,13 +321,16 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
 }  // namespace
 
 // F32: the second matrix' x may be float32.
+// WT == 1: kFewWaves waves, each with all of the set's tokens and 128 columns.
+constexpr int kFewWaves = 4;
 template <int RTW, int LIST, int WT, bool F32>
-__global__ __launch_bounds__(64 * WT, (kGradResident<RTW, WT, F32>)) void weight_grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(64 * (WT > 1 ? WT : kFewWaves), (kGradResident<RTW, WT, F32>)) void weight_grad_kernel(GradArgs a) {
+    constexpr int THREADS = 64 * (WT > 1 ? WT : kFewWaves);
     __shared__ Listed<LIST> list;
     __shared__ int found;
-    __shared__ __attribute__((aligned(16))) float sums[WT][16][132];
+    __shared__ __attribute__((aligned(16))) float sums[THREADS / 64][16][132];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool second = (int)blockIdx.x >= a.blocks0;
+    const bool second = (int)blockIdx.x >= a.groups0;
     const WeightGradCall& w = a.w[second];
     int set = 0, first = 0, cnt, slot = -1;
     if constexpr (LIST == kAll) {
@@ -353,9 +344,13 @@ __global__ __launch_bounds__(64 * WT, (kGradResident<RTW, WT, F32>)) void weight
             if (wid == 0) {
                 int id[kScanTokens / 64], n = 0;
 #pragma unroll
-                for (int k = 0; k < kScanTokens / 64; ++k) id[k] = k * 64 < a.who.T ? a.who.ids[min(k * 64 + lane, a.who.T - 1)] : -1;
+                for (int k = 0; k < kScanTokens / 64; ++k) {
+                    if (k * 64 >= a.who.T) break;
+                    id[k] = a.who.ids[min(k * 64 + lane, a.who.T - 1)];
+                }
 #pragma unroll
                 for (int k = 0; k < kScanTokens / 64; ++k) {
+                    if (k * 64 >= a.who.T) break;
                     const int t = k * 64 + lane;
                     const bool mine = t < a.who.T && id[k] == set;
                     const uint64_t mask = __ballot(mine);
@@ -376,7 +371,7 @@ __global__ __launch_bounds__(64 * WT, (kGradResident<RTW, WT, F32>)) void weight
             if (set < 0) return;
             cnt = __builtin_amdgcn_readfirstlane(e.z);
             slot = __builtin_amdgcn_readfirstlane(e.w);
-            for (int k = tid; k < cnt; k += 64 * WT) {
+            for (int k = tid; k < cnt; k += THREADS) {
                 const int t = a.plan.order[e.y + k];
                 list.token[k] = t;
                 list.row[k] = t * bytes;
@@ -390,7 +385,11 @@ __global__ __launch_bounds__(64 * WT, (kGradResident<RTW, WT, F32>)) void weight
         }
         __syncthreads();
     }
-    const int block = (int)blockIdx.x - (second ? a.blocks0 : 0);
+    int block = (int)blockIdx.x - (second ? a.groups0 : 0);
+    if constexpr (WT == 1) {
+        block = block * kFewWaves + wid;
+        if (128 * block >= w.C) return;
+    }
     float* part = a.part[second];
     const int64_t floats = a.slot_floats[second];
     if (w.x_type == kCodes) weight_grad_block<kCodes, RTW, LIST, WT>(a, w, block, part, floats, set, first, cnt, slot, list, sums);
@@ -404,10 +403,10 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(GradArgs a, int n
     int2 j = make_int2(0, number);
     if (a.plan.joins) j = a.plan.joins[set];
     if (j.y == 0) return;
-    const bool second = (int)blockIdx.x >= a.blocks0;
+    const bool second = (int)blockIdx.x >= a.groups0;
     const WeightGradCall& w = a.w[second];
     const int64_t size = (int64_t)a.who.R * w.C, all = a.slot_floats[second];
-    const int64_t e = 4 * ((int64_t)(blockIdx.x - (second ? a.blocks0 : 0)) * 256 + threadIdx.x);
+    const int64_t e = 4 * ((int64_t)(blockIdx.x - (second ? a.groups0 : 0)) * 256 + threadIdx.x);
     if (e >= all) return;
     const float* p = a.part[second] + (int64_t)j.x * all + e;
     const float s = a.scale ? a.scale[set] : 1.f;
@@ -442,7 +441,7 @@ int groups_of(int R) { return (R + 16 * products_of(R) - 1) / (16 * products_of(
 template <int RTW, bool F32>
 void grad_go(const GradArgs& a, int kind, int blocks, unsigned entries, bool few, hipStream_t s) {
     constexpr int WT = RTW == 2 ? 4 : kGradWaves;
-    const dim3 grid((unsigned)blocks, (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW)), entries), many(64 * WT), one(64);
+    const dim3 grid((unsigned)blocks, (unsigned)((a.who.R + 16 * RTW - 1) / (16 * RTW)), entries), many(64 * WT), one(64 * kFewWaves);
     if (kind == kAll) hipLaunchKernelGGL((weight_grad_kernel<RTW, kAll, WT, false>), grid, many, 0, s, a);
     else if (kind == kScan && few) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, 1, F32>), grid, one, 0, s, a);
     else if (kind == kScan) hipLaunchKernelGGL((weight_grad_kernel<RTW, kScan, WT, F32>), grid, many, 0, s, a);
@@ -487,8 +486,9 @@ static int weight_grad(const TokenSets& who, int kind, const TokenPlan* plan, co
         a.slot_floats[i] = (int64_t)who.R * calls[i].C + (calls[i].bias ? who.R : 0);
         a.part[i] = part;
         part += p.slots * a.slot_floats[i];
-        if (i == 0) a.blocks0 = (calls[0].C + 127) / 128;
-        blocks += (calls[i].C + 127) / 128;
+        const int mine = (calls[i].C + 127) / 128, groups = few ? (mine + kFewWaves - 1) / kFewWaves : mine;
+        if (i == 0) a.groups0 = groups;
+        blocks += groups;
         joins += (int)((a.slot_floats[i] + 1023) / 1024);
         if (i == 0) joins0 = joins;
     }
@@ -497,7 +497,7 @@ static int weight_grad(const TokenSets& who, int kind, const TokenPlan* plan, co
     if (products_of(who.R) == 1) f32 ? grad_go<1, true>(a, kind, blocks, entries, few, s) : grad_go<1, false>(a, kind, blocks, entries, few, s);
     else f32 ? grad_go<2, true>(a, kind, blocks, entries, few, s) : grad_go<2, false>(a, kind, blocks, entries, few, s);
     if (p.slots) {
-        a.blocks0 = joins0;
+        a.groups0 = joins0;
         hipLaunchKernelGGL(weight_grad_join_kernel, dim3((unsigned)joins, (unsigned)who.n), dim3(256), 0, s, a, (int)chunks);
     }
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
