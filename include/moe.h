@@ -689,8 +689,8 @@ typedef struct moe_adapters {
  * NaN and codes 0: all of them read as NaN.
  *   q      int8 [rows][K], 16-byte aligned
  *   scale  float32 [rows][K/128], 4-byte aligned
- * Limits: 0 <= rows <= 4194304; K a multiple of 128, 128 <= K <= 32768.  The
- * struct is a host object, read during the call only. */
+ * Limits: 0 <= rows <= 4194304; K a multiple of 128, 128 <= K <= 32768; rows * K
+ * <= 2^36.  The struct is a host object, read during the call only. */
 typedef struct moe_checkpoint {
     int8_t* q;
     float* scale;

@@ -15,19 +15,26 @@ struct TokenSets {
 
 // The tokens in order of their adapters, made once a call where there are too many for every
 // workgroup to look through the ids itself; tokens without an adapter come last, as set -1.
+constexpr int kPlanTile = 64;
+struct PlanTileEntry {
+    int32_t set, rows;        // rows 0: an empty entry
+    int32_t pad[2];
+    int32_t token[kPlanTile]; // (past the rows: anything)
+};
 struct TokenPlan {
     int32_t* order;           // [T]
-    int4* tiles;              // [T / kPlanTile + n + 1]: (set, first place in order, tokens up to kPlanTile or 0)
+    PlanTileEntry* tiles;     // [T / kPlanTile + n + 1]
     int4* chunks;             // [T / chunk + n]: (set or -1 for an empty entry, first place, tokens, slot), each adapter's
                               // tokens by up to `chunk`, one entry where it has none; slot: where an adapter with
                               // several has its partial sums, else -1
     int2* joins;              // [n]: an adapter's first slot and their number (0: it has none)
     int chunk;
 };
-constexpr int kPlanTile = 64;
 constexpr int kScanTile = 16;
 
-// Up to this many tokens every workgroup looks through the ids itself.
+// Up to this many tokens every workgroup looks through the ids itself (4096 x 4096, rank 16, us by
+// scans and by the plan: 128 tokens of 4 adapters 8.8 and 14.0, 384 13.6 and 15.0, 512 16.8 and 16.0; 512 of
+// 256 adapters 27.3 and 33.3).
 constexpr int kScanTokens = 512;
 
 inline int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }

@@ -21,7 +21,6 @@
 #include <type_traits>
 
 #include "adapters.h"
-#include "launch_util.h"
 #include "token_tiles.h"
 
 namespace moe {
@@ -68,12 +67,15 @@ __device__ __forceinline__ int my_tile(const TokenSets& who, const TokenPlan& pl
     constexpr int TOK = PLAN ? kPlanTile / SUBS : kScanTile;
     const int tid = threadIdx.x;
     if constexpr (PLAN) {
-        const int4 e = plan.tiles[idx / SUBS];
+        const PlanTileEntry& e = plan.tiles[idx / SUBS];
         const int sub = idx % SUBS * TOK;
-        set = __builtin_amdgcn_readfirstlane(e.x);
-        const int rows = min(__builtin_amdgcn_readfirstlane(e.z) - sub, TOK);
+        const int token = e.token[sub + min(tid, TOK - 1)];
+        const int2 head = *reinterpret_cast<const int2*>(&e);
+        set = __builtin_amdgcn_readfirstlane(head.x);
+        const int rows = min(__builtin_amdgcn_readfirstlane(head.y) - sub, TOK);
         if (rows <= 0) return 0;
-        if (tid < TOK) list[tid] = plan.order[e.y + sub + min(tid, rows - 1)];
+        const int last = __shfl(token, rows - 1, kWave);               // (of the first wave, which has them all)
+        if (tid < TOK) list[tid] = tid < rows ? token : last;
         __syncthreads();
         return rows;
     } else {
@@ -93,7 +95,8 @@ template <int RT, bool F32, bool PLAN>
 __global__ __launch_bounds__(64 * kWaves) void adapter_shrink_kernel(ShrinkArgs a) {
     constexpr int NT = PLAN ? kPlanTile / 16 : 1, PARTS = F32 ? 3 : 1;
     __shared__ int list[16 * NT];
-    __shared__ __attribute__((aligned(16))) float sums[kWaves][16][16 * RT + 4];
+    constexpr int AT_ONCE = RT <= 2 ? NT : 1;              // groups of 16 tokens whose sums meet at once
+    __shared__ __attribute__((aligned(16))) float sums[kWaves][16 * AT_ONCE][16 * RT + 4];
     int set;
     const int rows = my_tile<PLAN>(a.who, a.plan, (int)blockIdx.y, set, list);
     if (rows == 0 || set < 0) return;
@@ -162,23 +165,25 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_shrink_kernel(ShrinkArgs 
             for (int p = 0; p < 4; ++p) step(c0 + 32 * p, std::true_type{});
         }
     }
-    // the waves' sums, 16 tokens at a time; ranks past the adapter's are 0
+    // the waves' sums; ranks past the adapter's are 0
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        if (16 * nt >= rows) break;
-        if (nt) __syncthreads();
+    for (int n0 = 0; n0 < NT; n0 += AT_ONCE) {
+        if (16 * n0 >= rows) break;
+        if (n0) __syncthreads();
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) *reinterpret_cast<floatx4_t*>(&sums[wid][c][16 * rt + 4 * q]) = acc[nt][rt];
+        for (int k = 0; k < AT_ONCE; ++k)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) *reinterpret_cast<floatx4_t*>(&sums[wid][16 * k + c][16 * rt + 4 * q]) = acc[n0 + k][rt];
         __syncthreads();
-        for (int e = tid; e < 16 * 4 * RT; e += 64 * kWaves) {
+        for (int e = tid; e < 16 * AT_ONCE * 4 * RT; e += 64 * kWaves) {
             const int row = e / (4 * RT), r = 4 * (e % (4 * RT));
-            if (16 * nt + row >= rows) break;
+            if (16 * n0 + row >= rows) break;
             floatx4_t v = *reinterpret_cast<const floatx4_t*>(&sums[0][row][r]);
 #pragma unroll
             for (int k = 1; k < kWaves; ++k) v += *reinterpret_cast<const floatx4_t*>(&sums[k][row][r]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.f;
-            *reinterpret_cast<floatx4_t*>(a.part + ((int64_t)blockIdx.x * a.who.T + list[16 * nt + row]) * (16 * RT) + r) = v;
+            *reinterpret_cast<floatx4_t*>(a.part + ((int64_t)blockIdx.x * a.who.T + list[16 * n0 + row]) * (16 * RT) + r) = v;
         }
     }
 }
@@ -449,7 +454,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapter_plan_kernel(TokenSets
     // the lists' entries
     const int tile0 = less / kPlanTile + set, tile1 = (less + mine) / kPlanTile + set + 1;
     for (int k = tid; k < tile1 - tile0; k += 64 * kPlanWaves)
-        plan.tiles[tile0 + k] = make_int4(set < n ? set : -1, less + k * kPlanTile, max(min(kPlanTile, mine - k * kPlanTile), 0), 0);
+        *reinterpret_cast<int2*>(&plan.tiles[tile0 + k]) = make_int2(set < n ? set : -1, max(min(kPlanTile, mine - k * kPlanTile), 0));
     const int chunks = set < n ? max(1, (mine + plan.chunk - 1) / plan.chunk) : 0, slot0 = 2 * less / plan.chunk;
     const int chunk0 = less / plan.chunk + set, chunk1 = set < n ? (less + mine) / plan.chunk + set + 1 : who.T / plan.chunk + n;
     for (int k = tid; k < chunk1 - chunk0; k += 64 * kPlanWaves)
@@ -486,7 +491,11 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapter_plan_kernel(TokenSets
         }
 #pragma unroll
         for (int j = 0; j < kPlanPer; ++j)
-            if (v[j] == set) plan.order[next + place++] = base + kPlanPer * tid + j;
+            if (v[j] == set) {
+                const int token = base + kPlanPer * tid + j, at = next + place++ - less;      // its place among the set's
+                plan.order[less + at] = token;
+                plan.tiles[tile0 + at / kPlanTile].token[at % kPlanTile] = token;
+            }
         next += all;
     }
 }
@@ -530,7 +539,7 @@ Space space(const moe_adapters& m, int T, bool grad, const WeightGradPlan& p, vo
     if (planned(T)) {
         const int tiles = T / kPlanTile + m.n + 1, chunk = grad ? p.chunk : T;
         sp.plan.order = reinterpret_cast<int32_t*>(take((size_t)T * 4));
-        sp.plan.tiles = reinterpret_cast<int4*>(take((size_t)tiles * 16));
+        sp.plan.tiles = reinterpret_cast<PlanTileEntry*>(take((size_t)tiles * sizeof(PlanTileEntry)));
         sp.plan.chunks = reinterpret_cast<int4*>(take((size_t)(T / kLeastChunk + m.n) * 16));
         sp.plan.joins = reinterpret_cast<int2*>(take((size_t)m.n * 8));
         sp.plan.chunk = chunk;
@@ -592,7 +601,10 @@ void expand(const TokenSets& who, const Space& sp, int splits, const float* scal
     else f32 ? expand_go<true, false>(a, grid, s) : expand_go<false, false>(a, grid, s);
 }
 
-// Few tokens in one launch, every workgroup with all of its tile's sums.
+// Few tokens in one launch, every workgroup with all of its tile's sums, where a's rows are 64 KB at most:
+// past that a workgroup's own stream of them is longer than the second launch (us by two launches and
+// by one: 1 token 2048 x 2048 at rank 8 6.8 and 5.5, 64 of 16 adapters 1024 x 1024 at 16 7.6 and
+// 6.0; 1 token 4096 x 4096 at 16 7.4 and 8.2, 128 of 64 adapters 12.1 and 15.6).
 int self_blocks(const moe_adapters& m) { return (m.N + kSelfWaves * kUnitCols - 1) / (kSelfWaves * kUnitCols); }
 bool one_launch(const moe_adapters& m, int T) { return !planned(T) && m.R <= 32 && m.R * m.K <= 32768; }
 

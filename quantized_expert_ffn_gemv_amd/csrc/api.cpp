@@ -245,6 +245,8 @@ int check_checkpoint(const char* fn, const char* name, const moe_checkpoint* c, 
     if (c->K < 128 || c->K > 32768 || c->K % 128 != 0)
         return fail(MOE_ERR_UNSUPPORTED, "%s: K = %d of %s must be a multiple of 128 in [128, 32768]", fn, c->K, name);
     if (c->rows < 0 || c->rows > 4194304) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %d of %s outside [0, 4194304]", fn, c->rows, name);
+    if ((int64_t)c->rows * c->K > ((int64_t)1 << 36))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %s has %lld codes, more than 2^36", fn, name, (long long)c->rows * c->K);
     if (K > 0 && c->K != K) return fail(MOE_ERR_INVALID_ARG, "%s: %s has rows of %d, %d needed", fn, name, c->K, K);
     if (c->rows < rows) return fail(MOE_ERR_INVALID_ARG, "%s: %s has %d rows, %lld needed", fn, name, c->rows, (long long)rows);
     if (c->rows == 0) return MOE_OK;

@@ -149,7 +149,7 @@ def test_logprobs_grad_refusals(kw, status, word):
     assert word in moe.last_error()
 
 
-@pytest.mark.parametrize("kw,status", [(dict(K=100), 2), (dict(K=0), 2), (dict(K=65536), 2), (dict(rows=-1), 2), (dict(rows=4194305), 2),
+@pytest.mark.parametrize("kw,status", [(dict(K=100), 2), (dict(K=0), 2), (dict(K=65536), 2), (dict(rows=-1), 2), (dict(rows=4194305), 2), (dict(rows=4194304, K=32768), 2),
                                        (dict(q=None), 1), (dict(scale=None), 1), (dict(q=FAKE + 4), 1), (dict(scale=FAKE + 2), 1)])
 def test_checkpoint_refusals(kw, status):
     c = checkpoint(**kw)
