@@ -84,7 +84,7 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
     const uint32_t gcol = r_at(c);
     const char* x = static_cast<const char*>(w.x);
     const int64_t xlane = ((int64_t)(8 * q) * w.ldx + col) * ES;            // (kAll: rows are a constant stride apart)
-    const uint32_t ldg = (uint32_t)w.ldg, ngs = (uint32_t)C / 128;
+    const uint32_t ldg = (uint32_t)w.ldg, glane = 4 * (8 * q * ldg + gcol), ngs = (uint32_t)C / 128;
     // 32 tokens; with TAIL (kAll) some of them past the end: the last again, their g 0
     auto load_x = [&](XFrag<XT>& f, int step, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
@@ -121,10 +121,21 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
     auto load_g = [&](float (&g)[RTW][8], int step, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
         const int k0 = kStep * step;
+        if constexpr (LIST == kAll && !TAIL) {
+            const float* row = w.g + (int64_t)(first + k0) * w.ldg;            // (rows by scalars)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float gv[RTW];
+                __builtin_memcpy(gv, reinterpret_cast<const char*>(row + (int64_t)i * w.ldg) + glane, 4 * RTW);
+#pragma unroll
+                for (int rt = 0; rt < RTW; ++rt) g[rt][i] = gv[rt];
+            }
+            return;
+        }
         uint32_t tok[8];
         if constexpr (LIST == kAll) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tok[i] = first + (TAIL ? min(k0 + 8 * q + i, cnt - 1) : k0 + 8 * q + i);
+            for (int i = 0; i < 8; ++i) tok[i] = first + min(k0 + 8 * q + i, cnt - 1);
         } else {
             *reinterpret_cast<uint4*>(tok) = *reinterpret_cast<const uint4*>(&list.token[k0 + 8 * q]);
             *reinterpret_cast<uint4*>(tok + 4) = *reinterpret_cast<const uint4*>(&list.token[k0 + 8 * q + 4]);
