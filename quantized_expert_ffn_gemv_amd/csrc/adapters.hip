@@ -28,6 +28,7 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kMostSplits = 16;           // workgroups that share a tile's columns in shrink
 constexpr int kUnitCols = 128;            // columns of a wave's step in shrink, of a wave in expand
 
 struct ShrinkArgs {
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(64 * (SELF ? kSelfWaves : kWaves)) void adapter_exp
         for (int rt = 0; rt < RT; ++rt) *reinterpret_cast<floatx4_t*>(&sums[wid][c][16 * rt + 4 * q]) = acc[rt];
         __syncthreads();
     }
-    // the sums of the tile's tokens: the splits' parts, four at a time, or the waves'
+    // the sums of the tile's tokens: the splits' parts, four at a time or (few tokens) all at once, or the waves'
     for (int e = tid; e < TOK * (RP / 4); e += 64 * NW) {
         const int row = e / (RP / 4), r = 4 * (e % (RP / 4));
         floatx4_t v{0.f, 0.f, 0.f, 0.f};
@@ -296,14 +297,17 @@ __global__ __launch_bounds__(64 * (SELF ? kSelfWaves : kWaves)) void adapter_exp
                 for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.f;
             } else {
                 const float* p = a.part + (int64_t)list[row] * RP + r;
-                for (int k = 0; k < a.splits; k += 4) {
-                    floatx4_t o[4];
+                auto add = [&](int k, auto number) {
+                    constexpr int N = decltype(number)::value;
+                    floatx4_t o[N];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < N; ++u)
                         o[u] = *reinterpret_cast<const floatx4_t*>(p + (int64_t)min(k + u, a.splits - 1) * a.who.T * RP);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) v += k + u < a.splits ? o[u] : floatx4_t{0.f, 0.f, 0.f, 0.f};
-                }
+                    for (int u = 0; u < N; ++u) v += k + u < a.splits ? o[u] : floatx4_t{0.f, 0.f, 0.f, 0.f};
+                };
+                if (!PLAN && RT <= 2 && a.splits > 4) add(0, std::integral_constant<int, kMostSplits>{});
+                else for (int k = 0; k < a.splits; k += 4) add(k, std::integral_constant<int, 4>{});
             }
         }
         if (a.h && xblock == 0 && row < rows)
@@ -507,7 +511,7 @@ bool planned(int T) { return T > kScanTokens; }
 
 // Workgroups' worth of tiles, and how the columns of a shrink are split: workgroups twice the
 // CUs where there are columns for it, four waves each with a unit at least.
-constexpr int kMostSplits = 16, kShrinkBlocks = 512;
+constexpr int kShrinkBlocks = 512;
 int shrink_splits(int T, int n, int C) {
     const int sets = std::max(1, std::min(n, T));
     const int tiles = planned(T) ? (T + kPlanTile - 1) / kPlanTile + sets / 2 : sets;
