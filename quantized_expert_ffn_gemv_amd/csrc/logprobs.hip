@@ -393,7 +393,9 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobArgs a) {
     }
     const bool some = sum.m > -INFINITY || sum.s != sum.s;
     const float base = sum.m > -INFINITY ? sum.m : 0.f;
-    const float log_s = some ? logf(sum.s) : -INFINITY;
+    // (lane 0's sum: the lanes add in different orders, and any of them may have an alternative)
+    const float whole = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(sum.s)));
+    const float log_s = some ? logf(whole) : -INFINITY;
     if (tid == 0) {
         a.stats[2 * (int64_t)t] = sum.m;
         a.stats[2 * (int64_t)t + 1] = log_s;

@@ -298,6 +298,18 @@ def test_captured_streams_and_shared_buffers(T, V):
     assert int(buf.sync.abs().sum()) == 0
 
 
+@pytest.mark.parametrize("T,V,n", [(40, 9000, 64), (300, 1500, 20), (3, 50001, 64), (700, 3001, 40)])
+def test_alternatives_are_relative_to_the_same_sum(T, V, n):
+    """top_logp is (logit - maximum) - log S in float32 of the very statistics that are returned, whichever
+    thread wrote it, so that equal calls give equal bits."""
+    rng = np.random.default_rng(33)
+    L = (3 * rng.standard_normal((T, V))).astype(np.float32)
+    r = run(L, rng.integers(0, V, T), True, n)
+    m, log_s = r["stats"].astype(np.float32).T
+    want = (np.take_along_axis(L, r["ids"], 1) - m[:, None]) - log_s[:, None]
+    assert np.array_equal(r["top"].astype(np.float32), want)
+
+
 def test_far_rows():
     """Rows more than 2^31 elements from the first."""
     rng = np.random.default_rng(9)
