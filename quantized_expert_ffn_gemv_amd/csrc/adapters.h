@@ -39,20 +39,6 @@ constexpr int kScanTokens = 512;
 
 inline int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
-struct AdapterCall {
-    moe_adapters m;
-    TokenSets who;
-    const void* x;            // x (bf16) or dy
-    int64_t ldx;
-    int x_type;
-    const void* base;         // or NULL
-    int64_t ldbase;
-    void* y;                  // or NULL
-    int64_t ldy;
-    int y_type;               // base's too
-    float* h;                 // [T][R] or NULL
-};
-
 // The factors' gradients: d[i][r][c] = scale[i] sum over adapter i's tokens of g[t][r] x[t][c].
 struct WeightGradCall {
     const float* g;           // [T][ldg]

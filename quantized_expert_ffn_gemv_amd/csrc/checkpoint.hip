@@ -8,7 +8,10 @@
 // therefore lies on a tie where the exact one does, and on its side where not.
 //
 // All three kernels are bound by memory: 3 bytes an element saving or restoring, 1 (and
-// dout, once a token) for the gates' gradient.
+// dout, once a token) for the gates' gradient.  32768 x 2048 saved and restored: 82 us, 5.0 TB/s,
+// a large copy's rate; the gates of 4096 tokens x 8 picks x 2048: 18.1 us, 4.8 TB/s.  Groups go four to
+// 16 lanes, so that a lane has 64 bytes in flight; a token's picks are neighbouring waves, which
+// share its dout through the caches.
 #include "common.h"
 #include "row_ops.h"
 
@@ -155,10 +158,10 @@ __device__ __forceinline__ float gates_row(const uint16_t* dout, const int8_t* y
 
 }  // namespace
 
-// LP lanes a pair: 16 .. 64, or the whole workgroup's 256.
+// LP lanes a pair, as many as have a piece.  (Few pairs by a workgroup each were no faster: 8 tokens x 8 picks x
+// 2048 4.7 to 5.9 us both, 64 x 5120 5.2 to 5.5, 16 x 8192 4.9 to 5.3 against 5.8.)
 template <bool DY, int LP>
 __global__ __launch_bounds__(256) void gates_saved_kernel(GatesSavedArgs a) {
-    __shared__ float part[4];
     const int p = ((int)blockIdx.x * 256 + (int)threadIdx.x) / LP, sub = threadIdx.x % LP;
     const bool in = p < a.P;
     const int pc = in ? p : a.P - 1, t = pc / a.k, row = a.p2r[pc];
@@ -166,12 +169,7 @@ __global__ __launch_bounds__(256) void gates_saved_kernel(GatesSavedArgs a) {
     if (in && row >= 0 && row < a.P)
         dot = gates_row<DY>(a.dout + (size_t)t * a.H, a.q + (size_t)row * a.H, a.scale + (size_t)row * (a.H / 128),
                             DY ? a.dy + (size_t)row * a.H : nullptr, DY ? a.gates[pc] : 0.f, a.H / 8, sub, LP);
-    dot = row_sum<(LP < 64 ? LP : 64)>(dot);
-    if constexpr (LP == 256) {
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-        __syncthreads();
-        dot = (part[0] + part[1]) + (part[2] + part[3]);
-    }
+    dot = row_sum<LP>(dot);
     if (in && sub == 0) a.dgates[p] = dot;
 }
 
@@ -204,8 +202,7 @@ int launch_combine_backward_saved(const moe_dims& d, const uint16_t* dout, const
                                   const float* gates, float* dgates, uint16_t* dy, hipStream_t s) {
     const GatesSavedArgs a{dout, y.q, y.scale, p2r, gates, dgates, dy, d.T * d.k, d.H, d.k};
     if (a.P == 0) return MOE_OK;
-    if (a.P <= 512) gates_go<256>(a, s);
-    else if (a.H <= 128) gates_go<16>(a, s);
+    if (a.H <= 128) gates_go<16>(a, s);
     else if (a.H <= 256) gates_go<32>(a, s);
     else gates_go<64>(a, s);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;

@@ -17,6 +17,11 @@
 // several share one and the last to arrive joins them.  The gradient
 //   p ( -w - u (log p + entropy) ) + w [v = token]
 // is one pass more, a row's pieces spread over workgroups.
+//
+// Many rows are bound by memory: 4096 x 49999 bf16 with 5 alternatives 88 us (4.6 TB/s), the gradient, padding
+// left unread, 136 us.  A single row is bound by latency: 49999 float32 logits over 13 workgroups
+// 6.2 us, with 20 alternatives 9 to 12, two selections of 2 to 3 us each; handing on whole
+// sorted lists took twice that.
 #include <algorithm>
 #include <cmath>
 
@@ -499,7 +504,9 @@ __global__ __launch_bounds__(NT) void logprobs_grad_kernel(LogprobGradArgs a, un
 
 namespace {
 
-// Rows of up to this many elements have a wave each.
+// Rows of up to this many elements have a wave each (us by a wave and by four: 4096 x 2048 float32 9.6 and 12.0, with 5
+// alternatives 12.1 and 18.1, 16384 x 1000 14.3 and 30.0; the few rows of 4 x 2048 7.4 and 6.5 with
+// alternatives, 5.3 and 5.1 without).
 constexpr int kShortRow = 2048;
 
 // Workgroups that share a row: 512 in all, each with a step's pieces at least; their candidates

@@ -14,6 +14,13 @@
 // A workgroup's waves share its tokens and meet in LDS (many tokens), or have 128 columns each
 // (few).  Where columns and r give too few workgroups, tokens are split in chunks, whose sums a
 // second kernel adds in order.  No atomics: equal calls give equal bits.
+//
+// What it costs: both factors of 4 adapters, 4096 tokens, 2048 (codes) and 8192 (bf16) columns at rank 16
+// 18.6 us, 4.1 TB/s of x and dy, and 4.7 for the join; the router's weight, 8192 tokens x 128 x 2048 from codes,
+// 21.7 us and 6.  There the vector ALUs are the bound, 300 instructions a step to prepare the operands of 48 products,
+// at 1.65 us a step and SIMD (bf16 x: 1.4), beside 8 us for the launch, the first loads and the sums' way out.
+// 64 r a wave would halve the turning of x for twice the accumulators (20.5 us and 6.1; no gain), loads two
+// steps ahead changed nothing.
 #include <algorithm>
 #include <type_traits>
 
@@ -485,8 +492,13 @@ WeightGradPlan weight_grad_plan(int T, int n, int R, int C0, int C1) { return pl
 static int weight_grad(const TokenSets& who, int kind, const TokenPlan* plan, const float* scale, const WeightGradPlan& p,
                        const WeightGradCall* calls, int n_calls, float* part, hipStream_t s) {
     const unsigned chunks = who.T > p.chunk ? (unsigned)((who.T + p.chunk - 1) / p.chunk) : 1u;
-    // few tokens a set: a wave has them all
-    const bool few = kind != kAll && who.T <= 64 * who.n;
+    // Few tokens a set: a wave has them all, where workgroups that share them would be more than the card has at
+    // once (us of all gradients by waves and by workgroups, 4096 x 4096 at rank 16: 64 tokens of 16 adapters 14.2 and
+    // 17.3, 512 of 16 27.6 and 28.9; 2048 x 2048, 1024 of 64 32.7 and 37.8; but 4096 x 4096, 128 of 4 15.2
+    // and 14.0, and 64 of one 2048 x 2048 at rank 32 15.7 and 13.9).
+    int all_blocks = 0;
+    for (int i = 0; i < n_calls; ++i) all_blocks += (calls[i].C + 127) / 128;
+    const bool few = kind != kAll && who.T <= 64 * who.n && all_blocks * groups_of(who.R) * who.n > 512;
     GradArgs a{};
     a.who = who;
     if (plan) a.plan = *plan;
