@@ -782,7 +782,8 @@ int moe_logprobs_grad(int32_t T, int32_t V, const void* logits, int64_t ld, int 
 
 /* ------------------------------------------------- activations kept in 8 bits
  * moe_checkpoint_save writes a checkpoint of bf16 rows (ldx >= K elements apart, 2-byte
- * aligned); moe_checkpoint_restore writes bf16(q scale) to such rows. */
+ * aligned); moe_checkpoint_restore writes bf16(q scale) to such rows.  Rows that lie in the
+ * checkpoint's own memory are refused. */
 int moe_checkpoint_save(const moe_checkpoint* checkpoint, const uint16_t* x, int64_t ldx, void* stream);
 int moe_checkpoint_restore(const moe_checkpoint* checkpoint, uint16_t* x, int64_t ldx, void* stream);
 

@@ -256,6 +256,13 @@ int check_checkpoint(const char* fn, const char* name, const moe_checkpoint* c, 
     return MOE_OK;
 }
 
+// Whether rows of c->K bf16 values meet the checkpoint's own memory.
+bool meets_checkpoint(const moe_checkpoint* c, const void* x, int64_t ldx, int32_t rows) {
+    if (rows == 0 || c->rows == 0) return false;
+    const int64_t codes = (int64_t)c->rows * c->K, span = 2 * ((rows - 1) * ldx + c->K);
+    return rows_meet(x, span, span, c->q, codes, codes, 1) || rows_meet(x, span, span, c->scale, codes / 32, codes / 32, 1);
+}
+
 int check_linear_workspace(const char* fn, const moe_qmatrix* w, int32_t T, int type, bool grad, const void* ws,
                            size_t ws_bytes) {
     return check_scratch(fn, moe::linear_workspace_bytes(*w, T, type, grad), ws, ws_bytes);
@@ -1044,6 +1051,7 @@ int moe_checkpoint_save(const moe_checkpoint* c, const uint16_t* x, int64_t ldx,
     if (c->rows == 0) return ok();
     st = check_rows(fn, "x", x, ldx, c->K, 2);
     if (st) return st;
+    if (meets_checkpoint(c, x, ldx, c->rows)) return fail(MOE_ERR_INVALID_ARG, "%s: the checkpoint overlaps x", fn);
     st = moe::launch_checkpoint_save(*c, x, ldx, as_stream(stream));
     if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
     return ok();
@@ -1056,6 +1064,7 @@ int moe_checkpoint_restore(const moe_checkpoint* c, uint16_t* x, int64_t ldx, vo
     if (c->rows == 0) return ok();
     st = check_rows(fn, "x", x, ldx, c->K, 2);
     if (st) return st;
+    if (meets_checkpoint(c, x, ldx, c->rows)) return fail(MOE_ERR_INVALID_ARG, "%s: x overlaps the checkpoint", fn);
     st = moe::launch_checkpoint_restore(*c, x, ldx, as_stream(stream));
     if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));
     return ok();
@@ -1075,7 +1084,10 @@ int moe_combine_backward_saved(const moe_dims* d, const uint16_t* out_grad, cons
     if (y_rows_grad) {
         REQUIRE_PTR(y_rows_grad, 16);
         REQUIRE_PTR(topk_w, 4);
-        if (y_rows_grad == out_grad) return fail(MOE_ERR_INVALID_ARG, "%s: y_rows_grad is one of the inputs", fn);
+        const int64_t wide = 2 * (int64_t)d->H;
+        if (meets_checkpoint(y_rows, y_rows_grad, d->H, d->T * d->k) ||
+            rows_meet(y_rows_grad, d->T * d->k * wide, d->T * d->k * wide, out_grad, d->T * wide, d->T * wide, 1))
+            return fail(MOE_ERR_INVALID_ARG, "%s: y_rows_grad is one of the inputs", fn);
     }
     st = moe::launch_combine_backward_saved(*d, out_grad, *y_rows, pair_to_row, topk_w, topk_w_grad, y_rows_grad, as_stream(stream));
     if (st) return fail(st, "%s: kernel launch failed: %s", fn, hipGetErrorString(hipGetLastError()));

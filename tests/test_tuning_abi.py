@@ -180,6 +180,22 @@ def test_saved_gates_and_router_weight_refusals():
     assert weight(d=moe.dims(4, 8320, 128, 8, 2)) == moe.ERR_UNSUPPORTED
 
 
+def test_checkpoints_in_the_rows_own_memory_are_refused():
+    bad = moe.ERR_INVALID_ARG
+    # 4 rows of 256: 1024 bytes of codes, 32 of scales; the rows span 2048 bytes (3 ld + 256 elements)
+    for c, x, ld in ((checkpoint(q=FAKE, scale=FAR), FAKE, 256), (checkpoint(q=FAKE, scale=FAR), FAKE - 2046, 256),
+                     (checkpoint(q=FAKE, scale=FAR), FAKE + 1022, 256), (checkpoint(q=FAKE, scale=FAR), FAKE - 2560, 512),
+                     (checkpoint(q=FAR, scale=FAKE), FAKE + 30, 256), (checkpoint(q=FAR, scale=FAKE), FAKE - 2046, 256)):
+        assert lib().moe_checkpoint_save(by(c), x, ld, None) == bad
+        assert lib().moe_checkpoint_restore(by(c), x, ld, None) == bad
+        assert b"overlaps" in lib().moe_last_error()
+    d = moe.dims(4, 256, 128, 8, 2)
+    y = checkpoint(q=FAKE, scale=FAKE + 65536, rows=8)
+    for dy in (FAKE - 4080, FAKE + 2032, FAKE + 65536 + 48, FAKE + 65536 - 4080, FAR + 2032, FAR - 4080):
+        assert lib().moe_combine_backward_saved(by(d), FAR, by(y), FAR, FAR, FAR, dy, None) == bad
+        assert b"one of the inputs" in lib().moe_last_error()
+
+
 def test_binding_refuses_wrong_tensors():
     bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     a, b, s = torch.zeros(3, 4, 256, dtype=bf), torch.zeros(3, 4, 64, dtype=bf), torch.zeros(3)
