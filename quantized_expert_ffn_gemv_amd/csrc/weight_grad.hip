@@ -69,7 +69,6 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
                                                   int set, int first, int cnt, int slot, const Listed<LIST>& list,
                                                   float (*sums)[16][132]) {
     constexpr int ES = XT == MOE_F32 ? 4 : XT == kCodes ? 1 : 2;
-    constexpr bool EARLY = RTW < 4 || XT == kCodes;     // (64 r and a bf16 x: no registers for the next step's x)
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int R = a.who.R, C = w.C;
@@ -253,10 +252,9 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
                 multiply(gp, 0, b, 3);
                 __builtin_amdgcn_sched_barrier(0);
                 prepare_x(f, 1, b);
-                if constexpr (EARLY) load_x(f, next, full);
+                load_x(f, next, full);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(gp, 1, b, 3);
-                if constexpr (!EARLY) load_x(f, next, full);
             }
         }
         if (LIST == kAll && cnt % kStep && wid == steps % WT) {
