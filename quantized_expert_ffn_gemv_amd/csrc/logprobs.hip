@@ -359,7 +359,19 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobArgs a) {
         int handed = 0;
         if constexpr (TOP) {
             __syncthreads();
-            const int c = min(L.count, kList);
+            int c = min(L.count, kList);
+            if (c > kKeep && c <= NT) {
+                // without earlier stretches' entries that the last bound shuts out, so that they need no order yet (64 x 49999
+                // with 20 alternatives 19.0 -> 17.6 us, 64 x 150000 26.1 -> 23.6)
+                const float v = L.v[min(tid, c - 1)];
+                const int i = L.i[min(tid, c - 1)];
+                __syncthreads();
+                if (tid == 0) L.count = 0;
+                __syncthreads();
+                if (tid < c && v >= bound) append(L, v, i);
+                __syncthreads();
+                c = L.count;
+            }
             handed = c <= kKeep ? c : n;
             if (c <= kKeep) {
                 if (tid < c) {
