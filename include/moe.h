@@ -661,8 +661,8 @@ int moe_combine_backward(const moe_dims* dims, const uint16_t* out_grad, const u
  * other), the projection frozen: token t uses adapter i = ids[t], or none where
  * that is outside [0, n).  Both factors are stored by rank:
  *   a      bf16 [n][R][K]
- *   b      bf16 [n][R] rows of ldb elements, of which the first N are used; ldb a
- *          multiple of 8
+ *   b      bf16 [n][R] rows of ldb elements, of which only the first N are read (the
+ *          last row may end with them); ldb a multiple of 8
  *   scale  float32 [n]
  *   rank   int32 [n] or NULL (R for all): ranks rank[i] and up of adapter i are
  *          left out and not read (values outside [0, R] count as the nearer end)

@@ -751,9 +751,9 @@ def router_weight_grad(d: Dims, logits_grad, x, w_router_grad, buffers: RouterWe
 @dataclass(frozen=True, eq=False)
 class Adapters:
     """Low-rank adapters of many requests (struct moe_adapters): a bfloat16 [n, R, K],
-    b bfloat16 [n, R, N] whose rows may be the first N columns of a wider buffer
-    [n, R, ldb] (ldb a multiple of 8; pack() makes one), scale float32 [n], rank int32
-    [n] or None (R for all)."""
+    b bfloat16 [n, R, N] whose rows may be N columns of a wider buffer [n, R, ldb] (ldb
+    and the first of them multiples of 8; pack() makes one), scale float32 [n], rank
+    int32 [n] or None (R for all)."""
     a: torch.Tensor
     b: torch.Tensor
     scale: torch.Tensor
@@ -770,8 +770,10 @@ class Adapters:
         ldb = b.stride(1) if R > 1 else b.stride(0) if n > 1 else (N + 7) // 8 * 8
         if (N > 1 and b.stride(2) != 1) or ldb < N or ldb % 8 or (n > 1 and b.stride(0) != R * ldb):
             raise ValueError("b's rows need one stride, a multiple of 8 elements (Adapters.pack() lays them out)")
-        if b.storage_offset() + n * R * ldb > b.untyped_storage().nbytes() // b.element_size():
-            raise ValueError("b's last row ends before its stride (Adapters.pack() lays them out)")
+        # (only a row's N elements are read; a last row without a whole last piece begins between 16-byte borders)
+        end = b.storage_offset() + (n * R - 1) * ldb + (N if n * R == 1 else (N + 7) // 8 * 8)
+        if end > b.untyped_storage().nbytes() // b.element_size():
+            raise ValueError("b's last row ends before a whole 16-byte piece (Adapters.pack() lays them out)")
         c = AdaptersC(at, b.data_ptr(), ldb, _want("scale", self.scale, dev, _F32S, (n,)),
                       None if self.rank is None else _want("rank", self.rank, dev, _I32S, (n,)), n, R, K, N)
         for name, v in (("n", n), ("R", R), ("K", K), ("N", N), ("_c", c), ("_ref", ctypes.byref(c))):

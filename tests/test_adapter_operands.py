@@ -1,0 +1,61 @@
+"""Where the adapters' operands may lie: column slices of wider buffers are taken, results
+over memory that the call still reads are refused before anything is written."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_expert_ffn_gemv_amd as moe
+import tuning_ref as ref
+from weights_ref import bf16_round
+
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("first,N,cols", [(8, 64, 72), (8, 59, 72), (16, 40, 72), (64, 8, 72), (8, 67, 80)])
+def test_factor_rows_in_the_middle_of_a_buffer(first, N, cols):
+    """b as columns first .. first + N - 1 of a wider buffer, up to its end."""
+    a, wide, s = torch.zeros(3, 4, 256, dtype=BF), torch.zeros(3, 4, cols, dtype=BF), torch.zeros(3)
+    b = wide[:, :, first:first + N]
+    m = moe.Adapters(a, b, s)
+    assert (m.N, m._c.ldb, m._c.b) == (N, cols, wide.data_ptr() + 2 * first)
+
+
+def test_one_row_needs_no_stride():
+    b = torch.zeros(1, 1, 67, dtype=BF)
+    assert moe.Adapters(torch.zeros(1, 1, 128, dtype=BF), b, torch.zeros(1))._c.ldb == 72
+
+
+def test_rows_between_16_byte_borders_are_refused():
+    wide = torch.zeros(3, 4, 72, dtype=BF)
+    with pytest.raises(ValueError, match="16-byte"):
+        moe.Adapters(torch.zeros(3, 4, 256, dtype=BF), wide[:, :, 12:], torch.zeros(3))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 600])
+@pytest.mark.parametrize("R,K", [(8, 256), (40, 1024)])
+def test_results_from_the_middle_of_a_buffer(T, R, K):
+    """The last columns of a buffer of NaNs, whose last row ends with it: the bits of a copy's results."""
+    rng = np.random.default_rng(T + R)
+    n, N, first = 3, 131, 24
+    f = ref.Factors(rng, n, R, K, N)
+    wide = torch.full((n, R, first + 136), float("nan"), dtype=BF, device="cuda")
+    wide[:, :, first:first + N] = torch.from_numpy(f.b).to("cuda", BF)
+    a, s = torch.from_numpy(f.a).to("cuda", BF), torch.from_numpy(f.scale).cuda()
+    packed = torch.zeros(n, R, 136, dtype=BF, device="cuda")
+    packed[:, :, :N] = wide[:, :, first:first + N]
+    ids = torch.from_numpy(rng.integers(-1, n, T).astype(np.int32)).cuda()
+    x, dy = (torch.from_numpy(bf16_round(rng.standard_normal((T, c)).astype(np.float32))).to("cuda", BF) for c in (K, N))
+    got = []
+    for b in (wide[:, :, first:first + N], packed[:, :, :N]):
+        m = moe.Adapters(a, b, s)
+        y, h, dx = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, R, device="cuda"), torch.empty(T, K, dtype=BF, device="cuda")
+        da, db = torch.empty(n, R, K, device="cuda"), torch.empty(n, R, N, device="cuda")
+        moe.adapter(m, ids, x, y, moe.AdapterBuffers.allocate(m, T), h=h)
+        moe.adapter_grad(m, ids, dy, x, h, moe.AdapterBuffers.allocate(m, T, grad=True), dx=dx, da=da, db=db)
+        got.append((y, h, dx, da, db))
+    assert all(torch.equal(p, q) for p, q in zip(*got)) and all(bool(torch.isfinite(p).all()) for p in got[0])
+    wy, wh, yb, _ = ref.adapter(f, ids.cpu().numpy(), x.float().cpu().numpy())
+    assert np.all(np.abs(got[0][0].double().cpu().numpy() - wy) <= ref.rounded(wy, yb, False))
