@@ -734,8 +734,8 @@ int moe_adapter(const moe_adapters* adapters, int32_t T, const int32_t* ids, con
  *            flows into dx (moe_linear_grad's result), may be dx itself, or NULL (0).
  *   da       float32 [n][R][K] or NULL;  db  float32 [n][R][N] or NULL
  *   workspace  moe_adapter_workspace_bytes(adapters, T, 1), 256-byte aligned
- * dx, da and db overlap no input (refused for dx with dy, x and dx_base).  Sums in
- * float32 in a fixed order; with float32 dy, 2^-24 of a product of db is left out. */
+ * dx, da and db overlap no input (refused for dx with dy, x, x_saved, h and dx_base).  Sums
+ * in float32 in a fixed order; with float32 dy, 2^-24 of a product of db is left out. */
 int moe_adapter_grad(const moe_adapters* adapters, int32_t T, const int32_t* ids, const void* dy, int64_t lddy,
                      int dy_type, const uint16_t* x, int64_t ldx, const moe_checkpoint* x_saved, const float* h,
                      const uint16_t* dx_base, int64_t lddx_base, uint16_t* dx, int64_t lddx, float* da, float* db,

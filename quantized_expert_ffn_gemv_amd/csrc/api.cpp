@@ -962,6 +962,9 @@ int moe_adapter_grad(const moe_adapters* m, int32_t T, const int32_t* ids, const
         const int64_t wx = 2 * (int64_t)m->K;
         if (dx && (rows_meet(dx, 2 * lddx, wx, dy, e * lddy, (int64_t)e * m->N, T) ||
                    (da && x && rows_meet(dx, 2 * lddx, wx, x, 2 * ldx, wx, T)) ||
+                   (da && x_saved && meets_checkpoint(x_saved, dx, lddx, T)) ||
+                   (db && rows_meet(dx, 2 * ((T - 1) * lddx + m->K), 2 * ((T - 1) * lddx + m->K), h, 4 * (int64_t)T * m->R,
+                                    4 * (int64_t)T * m->R, 1)) ||
                    (a.dx_base && a.dx_base != dx && rows_meet(dx, 2 * lddx, wx, dx_base, 2 * lddx_base, wx, T))))
             return fail(MOE_ERR_INVALID_ARG, "%s: dx overlaps an input", fn);
     }

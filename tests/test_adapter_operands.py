@@ -59,3 +59,26 @@ def test_results_from_the_middle_of_a_buffer(T, R, K):
     assert all(torch.equal(p, q) for p, q in zip(*got)) and all(bool(torch.isfinite(p).all()) for p in got[0])
     wy, wh, yb, _ = ref.adapter(f, ids.cpu().numpy(), x.float().cpu().numpy())
     assert np.all(np.abs(got[0][0].double().cpu().numpy() - wy) <= ref.rounded(wy, yb, False))
+
+
+# ---------------------------------------------------------------- overlaps
+
+A, FAR = 0x10000000, 0x7000000000
+
+
+def _grad(dx, saved=None, x=None, h=FAR, da=FAR + (1 << 30), db=FAR + (1 << 31), T=4, lddx=256):
+    m = moe.AdaptersC(FAR, FAR, 64, FAR, None, 4, 16, 256, 64)
+    return moe.lib().moe_adapter_grad(ctypes.byref(m), T, FAR, FAR, 64, moe.BF16, x, 256, None if saved is None else ctypes.byref(saved), h,
+                                      None, 0, dx, lddx, da, db, 0x100, 1 << 42, None)
+
+
+@pytest.mark.parametrize("kw", [
+    # 4 rows of 256 columns: dx 2048 bytes (512 apart: 2 (3 512 + 256) = 3584), the checkpoint 1024 of codes and 32 of scales, h 256
+    dict(dx=A, saved=moe.CheckpointC(A, FAR, 4, 256)), dict(dx=A, saved=moe.CheckpointC(A + 2032, FAR, 4, 256)),
+    dict(dx=A + 1022, saved=moe.CheckpointC(A, FAR, 4, 256)), dict(dx=A, saved=moe.CheckpointC(FAR, A + 2044, 4, 256)),
+    dict(dx=A + 30, saved=moe.CheckpointC(FAR, A, 4, 256)), dict(dx=A, saved=moe.CheckpointC(A + 3568, FAR, 4, 256), lddx=512),
+    dict(dx=A, x=FAR, h=A + 2044), dict(dx=A + 254, x=FAR, h=A), dict(dx=A, da=None, h=A),
+])
+def test_dx_over_what_the_factors_gradients_read_is_refused(kw):
+    assert _grad(**kw) == moe.ERR_INVALID_ARG
+    assert "dx overlaps" in moe.last_error()
