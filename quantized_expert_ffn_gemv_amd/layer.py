@@ -316,15 +316,31 @@ def adapted_linear(w: QMatrix, adapters: Adapters, ids, x, y, buffers: AdaptedBu
     adapter(adapters, ids, x, y, buffers.adapter, base=y, h=h, stream=stream)
 
 
+def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the rows of a and b share memory: rows of one stride exactly, others by their extents."""
+    if not a.numel() or not b.numel() or a.dim() != 2 or b.dim() != 2:     # (other shapes are refused by the calls)
+        return False
+    (ra, ca), (rb, cb) = ((t.stride(0) * t.element_size(), t.shape[1] * t.element_size()) for t in (a, b))
+    off = b.data_ptr() - a.data_ptr()
+    if off >= (a.shape[0] - 1) * ra + ca or -off >= (b.shape[0] - 1) * rb + cb:
+        return False
+    return ra != rb or ra == 0 or min(a.shape[0], b.shape[0]) == 1 or off % ra < ca or off % ra + cb > ra
+
+
 def adapted_linear_backward(w: QMatrix, adapters: Adapters, ids, dy, x, h, buffers: AdaptedBuffers, dx=None, da=None,
                             db=None, stream=None) -> None:
     """The way back through adapted_linear(): dx = dy W + the adapters' part (linear_grad(),
     then adapter_grad() on it in place), da and db the factors' gradients, each if given.  x:
-    the input or a Checkpoint of it (for da), h adapted_linear()'s (for db).  (The residual's
-    gradient is dy.)"""
+    the input or a Checkpoint of it (for da), h adapted_linear()'s (for db), neither of them in
+    dx's memory.  (The residual's gradient is dy.)"""
     _beside(w, adapters)
     if buffers.adapter_back is None:
         raise ValueError("buffers allocated without grad")
+    # (adapter_grad() refuses these too, but after linear_grad() has written dx)
+    if dx is not None:
+        read = () if da is None or x is None else (x.q, x.scale) if isinstance(x, Checkpoint) else (x,)
+        if any(_meet(dx, t) for t in read + (() if db is None or h is None else (h,))):
+            raise ValueError("dx overlaps what the factors' gradients read")
     if dx is not None:
         linear_grad(w, dy, dx, buffers.linear_back, stream)
     adapter_grad(adapters, ids, dy, x, h, buffers.adapter_back, dx=dx, dx_base=dx, da=da, db=db, stream=stream)

@@ -82,3 +82,36 @@ def _grad(dx, saved=None, x=None, h=FAR, da=FAR + (1 << 30), db=FAR + (1 << 31),
 def test_dx_over_what_the_factors_gradients_read_is_refused(kw):
     assert _grad(**kw) == moe.ERR_INVALID_ARG
     assert "dx overlaps" in moe.last_error()
+
+
+def _projection(N=64, K=256):
+    return moe.QMatrix(4, 128, torch.zeros(K // 128, N, 64, dtype=torch.uint8), *(torch.zeros(N, K // 128, dtype=torch.float16) for _ in range(2)))
+
+
+def test_adapted_backward_refuses_before_it_writes(monkeypatch):
+    """dx over what adapter_grad() would read: refused before linear_grad() has written it."""
+    from quantized_expert_ffn_gemv_amd import layer
+
+    called = []
+    monkeypatch.setattr(layer, "linear_grad", lambda *a, **k: called.append("linear_grad"))
+    monkeypatch.setattr(layer, "adapter_grad", lambda *a, **k: called.append("adapter_grad"))
+    w, n, R, T, K, N = _projection(), 3, 4, 5, 256, 64
+    m = moe.Adapters(torch.zeros(n, R, K, dtype=BF), torch.zeros(n, R, N, dtype=BF), torch.zeros(n))
+    buf = layer.AdaptedBuffers(None, None, None, moe.AdapterBuffers.allocate(m, T, grad=True))
+    ids, dy, h = torch.zeros(T, dtype=torch.int32), torch.zeros(T, N, dtype=BF), torch.zeros(T, R)
+    da, db = torch.zeros(n, R, K), torch.zeros(n, R, N)
+    x, wide = torch.zeros(T, K, dtype=BF), torch.zeros(T, 2 * K, dtype=BF)
+    kept = moe.Checkpoint.allocate(2 * T, K, device="cpu")
+    over_codes = kept.q.view(-1).view(BF)[:T * K].view(T, K)
+    five = moe.Checkpoint(kept.q[:T], kept.scale[:T])
+    over_h = torch.zeros(T * K, dtype=BF)
+    for kw in (dict(dx=x, x=x, da=da), dict(dx=wide[:, 8:K + 8], x=wide[:, :K], da=da), dict(dx=over_codes, x=five, da=da),
+               dict(dx=over_h.view(T, K), x=x, h=over_h.view(torch.float32)[:T * R].view(T, R), db=db)):
+        args = dict(dict(h=h, da=None, db=None), **kw)
+        with pytest.raises(ValueError, match="dx overlaps"):
+            moe.adapted_linear_backward(w, m, ids, dy, args["x"], args["h"], buf, dx=args["dx"], da=args["da"], db=args["db"])
+    assert not called
+    # x is not read without da, and column slices of one buffer share nothing
+    moe.adapted_linear_backward(w, m, ids, dy, x, h, buf, dx=x, db=db)
+    moe.adapted_linear_backward(w, m, ids, dy, wide[:, :K], h, buf, dx=wide[:, K:], da=da, db=db)
+    assert called == ["linear_grad", "adapter_grad"] * 2
