@@ -812,11 +812,8 @@ class AdapterBuffers:
                                           device=adapters.a.device))
 
 
-def adapter(adapters: Adapters, ids, x, y, buffers: AdapterBuffers, base=None, h=None, stream=None):
-    """moe_adapter: y = base + scale h b, h = a x of each token's adapter.  ids int32 [T]
-    (outside [0, n): none); x bfloat16 [T, K]; y bfloat16 or float32 [T, N]; base like y
-    (may be y itself) or None (0); rows contiguous, any row strides; h float32 [T, R] or
-    None: receives h for adapter_grad()."""
+def _adapter_call(adapters: Adapters, ids, x, y, buffers: AdapterBuffers, base, h):
+    """moe_adapter's arguments up to the stream, checked."""
     dev, T = adapters.a.device, x.shape[0]
     ldx = _want_rows("x", x, dev, _BITS16, T, adapters.K)
     ldy = _want_rows("y", y, dev, _VALUES, T, adapters.N)
@@ -825,9 +822,17 @@ def adapter(adapters: Adapters, ids, x, y, buffers: AdapterBuffers, base=None, h
     if base is not None and _element_type(base.dtype) != kind:
         raise ValueError(f"base holds {base.dtype}, y {y.dtype}")
     ws, nbytes = _scratch(buffers, dev)
-    _enqueue(lib().moe_adapter, dev, stream, adapters._ref, T, _want("ids", ids, dev, _I32S, (T,)), x.data_ptr(), ldx,
-             None if base is None else base.data_ptr(), ldb, y.data_ptr(), ldy, kind,
-             None if h is None else _want("h", h, dev, _F32S, (T, adapters.R)), ws, nbytes)
+    return (adapters._ref, T, _want("ids", ids, dev, _I32S, (T,)), x.data_ptr(), ldx,
+            None if base is None else base.data_ptr(), ldb, y.data_ptr(), ldy, kind,
+            None if h is None else _want("h", h, dev, _F32S, (T, adapters.R)), ws, nbytes)
+
+
+def adapter(adapters: Adapters, ids, x, y, buffers: AdapterBuffers, base=None, h=None, stream=None):
+    """moe_adapter: y = base + scale h b, h = a x of each token's adapter.  ids int32 [T]
+    (outside [0, n): none); x bfloat16 [T, K]; y bfloat16 or float32 [T, N]; base like y
+    (may be y itself) or None (0); rows contiguous, any row strides; h float32 [T, R] or
+    None: receives h for adapter_grad()."""
+    _enqueue(lib().moe_adapter, adapters.a.device, stream, *_adapter_call(adapters, ids, x, y, buffers, base, h))
 
 
 def adapter_grad(adapters: Adapters, ids, dy, x, h, buffers: AdapterBuffers, dx=None, dx_base=None, da=None, db=None,

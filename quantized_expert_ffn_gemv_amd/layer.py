@@ -49,10 +49,10 @@ import torch
 
 from . import (ALGO_AUTO, DISPATCH_SYNC_INTS, FFN_SYNC_INTS, OP_FFN, RESIDENCY_LISTS, WORK_ENTRY_INTS, Dims,
                AdapterBuffers, Adapters, BalanceBuffers, Checkpoint, LinearBuffers, QMatrix, QWeights, RouterWeightBuffers,
-               adapter, adapter_grad, balance_loss, combine, combine_backward, combine_shared, dims, expert_copy,
-               expert_ffn_fused, expert_ffn_fused_shared, expert_ffn_q2, expert_ffn_q4, linear, linear_grad, permute,
-               residency_plan, route_backward, route_counts, route_dispatch, route_topk, router_weight_grad, slot_lookup,
-               work_list_capacity, workspace_bytes)
+               _adapter_call, _enqueue, adapter_grad, adapter_workspace_bytes, balance_loss, combine, combine_backward,
+               combine_shared, dims, expert_copy, expert_ffn_fused, expert_ffn_fused_shared, expert_ffn_q2, expert_ffn_q4,
+               lib, linear, linear_grad, permute, residency_plan, route_backward, route_counts, route_dispatch, route_topk,
+               router_weight_grad, slot_lookup, work_list_capacity, workspace_bytes)
 
 
 @dataclass
@@ -312,8 +312,12 @@ def adapted_linear(w: QMatrix, adapters: Adapters, ids, x, y, buffers: AdaptedBu
     on y in place (a bfloat16 y is rounded by both).  ids int32 [T]; h: float32 [T, R] or
     None, for adapted_linear_backward()."""
     _beside(w, adapters)
+    # (adapter()'s checks, before linear() writes y, which may be the residual)
+    call = _adapter_call(adapters, ids, x, y, buffers.adapter, y, h)
+    if residual is not None and adapter_workspace_bytes(adapters, x.shape[0]) > buffers.adapter.workspace.numel():
+        raise ValueError(f"buffers.adapter.workspace is too small for {x.shape[0]} tokens")
     linear(w, x, y, buffers.linear, row_bias, residual, stream)
-    adapter(adapters, ids, x, y, buffers.adapter, base=y, h=h, stream=stream)
+    _enqueue(lib().moe_adapter, adapters.a.device, stream, *call)
 
 
 def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:

@@ -115,3 +115,22 @@ def test_adapted_backward_refuses_before_it_writes(monkeypatch):
     moe.adapted_linear_backward(w, m, ids, dy, x, h, buf, dx=x, db=db)
     moe.adapted_linear_backward(w, m, ids, dy, wide[:, :K], h, buf, dx=wide[:, K:], da=da, db=db)
     assert called == ["linear_grad", "adapter_grad"] * 2
+
+
+def test_adapted_linear_refuses_before_it_writes(monkeypatch):
+    """A residual in place is lost once linear() has run: what adapter() refuses is refused before."""
+    from quantized_expert_ffn_gemv_amd import layer
+
+    called = []
+    monkeypatch.setattr(layer, "linear", lambda *a, **k: called.append("linear"))
+    w, n, R, T, K, N = _projection(), 3, 4, 5, 256, 64
+    m = moe.Adapters(torch.zeros(n, R, K, dtype=BF), torch.zeros(n, R, N, dtype=BF), torch.zeros(n))
+    buf = layer.AdaptedBuffers(None, moe.AdapterBuffers.allocate(m, T))
+    ids, x, y, h = torch.zeros(T, dtype=torch.int32), torch.zeros(T, K, dtype=BF), torch.zeros(T, N, dtype=BF), torch.zeros(T, R)
+    small = layer.AdaptedBuffers(None, moe.AdapterBuffers(torch.zeros(256, dtype=torch.uint8)))
+    for kw, word in ((dict(ids=ids.long()), "ids holds"), (dict(ids=ids[:4]), "ids has shape"), (dict(h=h[:4]), "h has shape"),
+                     (dict(x=x.float()), "x holds"), (dict(y=y.half()), "y holds"), (dict(buf=small), "workspace")):
+        a = dict(dict(ids=ids, x=x, y=y, h=h, buf=buf), **kw)
+        with pytest.raises(ValueError, match=word):
+            moe.adapted_linear(w, m, a["ids"], a["x"], a["y"], a["buf"], residual=a["y"], h=a["h"])
+    assert not called
