@@ -1,0 +1,61 @@
+"""Every kernel form of the adapters and of the router's weight gradient, at the sizes of
+adapter_forms.py, within the bounds of tuning_ref.py."""
+import numpy as np
+import pytest
+import torch
+
+import adapter_forms as forms
+import quantized_expert_ffn_gemv_amd as moe
+import test_gpu_adapters as gpu
+import tuning_ref as ref
+from weights_ref import U32, bf16_round
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("case", forms.CASES, ids=str)
+def test_dense(case):
+    T, n, R, K, N, f32 = case
+    rng = np.random.default_rng(T + n + R)
+    f = ref.Factors(rng, n, R, K, N, ragged=n > 2)
+    m = gpu.upload(f, 1)
+    ids = gpu.make_ids(rng, T, n, none=True, skew=n == 3)
+    x = bf16_round(rng.standard_normal((T, K)).astype(np.float32))
+    base = rng.standard_normal((T, N)).astype(np.float32)
+    base = base if f32 else bf16_round(base)
+    y, h = gpu.run_forward(f, m, ids, x, base, f32, 3, in_place=True)
+    wy, wh, yb, hb = ref.adapter(f, ids, x, base)
+    gpu.check(h, wh, hb, "h")
+    gpu.check(y, wy, ref.rounded(wy, yb, f32), "y")
+    dy = (1e-3 * np.exp(2 * rng.standard_normal((T, 1))) * rng.standard_normal((T, N))).astype(np.float32)
+    dy = dy if f32 else bf16_round(dy)
+    hv = rng.standard_normal((T, R)).astype(np.float32)
+    xs = ref.restored(*ref.save(x))
+    for saved in (False, True):
+        dx, da, db = gpu.run_grad(f, m, ids, dy, x, hv, None, f32, 5, saved=saved)
+        wx, wa, wb, xb, ab, bb = ref.adapter_grad(f, ids, dy, xs if saved else x, hv)
+        gpu.check(dx, wx, ref.rounded(wx, xb, False), "dx")
+        gpu.check(da, wa, ab, f"da saved={saved}")
+        gpu.check(db, wb, bb, "db")
+
+
+@pytest.mark.parametrize("T,E,H", forms.ROUTER)
+@pytest.mark.parametrize("saved", [False, True])
+def test_router_weight(T, E, H, saved):
+    rng = np.random.default_rng(T + H)
+    d = moe.dims(T, H, 128, E, 1)
+    buf = moe.RouterWeightBuffers.allocate(d)
+    dense = (1e-3 * np.exp(2 * rng.standard_normal((T, 1))) * rng.standard_normal((T, E))).astype(np.float32)
+    rows = bf16_round(rng.standard_normal((T, H)).astype(np.float32))
+    for dl, x, step in ((dense, rows, (T + 64) * ref.SUM),):
+        kept, X = gpu.dev(x), x.astype(np.float64)
+        if saved:
+            c = moe.Checkpoint.allocate(T, H)
+            moe.checkpoint_save(kept, c)
+            kept, X = c, ref.restored(*ref.save(x))
+        buf.workspace.fill_(0xFF)
+        dw, db = torch.full((E, H), float("nan"), device="cuda"), torch.full((E,), float("nan"), device="cuda")
+        moe.router_weight_grad(d, gpu.dev(dl, torch.float32), kept, dw, buf, bias_grad=db)
+        D = dl.astype(np.float64)
+        gpu.check(dw, D.T @ X, step * (np.abs(D).T @ np.abs(X)) + ref.TINY, "weight")
+        gpu.check(db, D.sum(0), (T + 16) * U32 * np.abs(D).sum(0) + ref.TINY, "bias")
