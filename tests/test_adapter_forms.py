@@ -1,10 +1,13 @@
-"""Host-only: the sizes of adapter_forms.py reach every kernel form of the adapters."""
+"""Host-only: the sizes of adapter_forms.py reach every kernel form of the adapters, and
+their bounds show a form that has lost a part of its float32 operands."""
 import ctypes
 
+import numpy as np
 import pytest
 
 import adapter_forms as forms
 import quantized_expert_ffn_gemv_amd as moe
+import tuning_ref as ref
 
 
 def test_every_form_is_reached():
@@ -42,3 +45,31 @@ def test_workspaces_hold_what_the_rules_take(case):
             chunk, chunks = forms.grad_chunk(T, R, C)
             need += 4 * T * R + (4 * R * (K + N) * (chunks if n == 1 else 2 * T // chunk) if forms.planned(T) and T > chunk else 0)
         assert out.value >= need
+
+
+def test_three_parts_are_all_of_a_float32():
+    rng = np.random.default_rng(0)
+    v = (rng.standard_normal(10000) * np.exp(12 * rng.standard_normal(10000))).astype(np.float32)
+    assert np.array_equal(forms.cut(v, 3), v.astype(np.float64))
+    off = np.abs(forms.cut(v, 2) - v) / np.abs(v)
+    assert 2.0 ** -17 < off.max() < 2.0 ** -15
+
+
+@pytest.mark.parametrize("case", forms.CASES, ids=str)
+def test_the_bounds_show_a_lost_part(case):
+    """The mistake is planted here, in the reference: two parts instead of three of h, of g and of dy."""
+    s = forms.Sparse(*case)
+    _, h, *_ = ref.adapter(s.f, s.ids, s.x_dense)
+    h = h.astype(np.float32)
+    want, bound = s.y(h)
+    assert np.max(np.abs(s.y(h, 2)[0] - want) / bound) > 1.5
+    full, lost = s.gradients(s.x), s.gradients(s.x, 2)
+    for k, name in enumerate(("dx", "da", "db")):
+        assert np.max(np.abs(lost[k] - full[k]) / full[3 + k]) > 1.5, name
+
+
+def test_the_router_bound_shows_a_lost_part():
+    for T, E, H in forms.ROUTER[:1]:
+        dl, x, steps = forms.router_operands(T, E, H)
+        want, size = dl.astype(np.float64).T @ x, np.abs(dl).astype(np.float64).T @ np.abs(x)
+        assert np.max(np.abs(forms.cut(dl, 2).T @ x - want) / (steps * size + ref.TINY)) > 1.5

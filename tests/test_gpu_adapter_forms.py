@@ -1,5 +1,6 @@
 """Every kernel form of the adapters and of the router's weight gradient, at the sizes of
-adapter_forms.py, within the bounds of tuning_ref.py."""
+adapter_forms.py: dense operands within the bounds of tuning_ref.py, and operands few of which are
+not zero, whose results show all 24 bits of h, g and a float32 dy."""
 import numpy as np
 import pytest
 import torch
@@ -39,15 +40,37 @@ def test_dense(case):
         gpu.check(db, wb, bb, "db")
 
 
+@pytest.mark.parametrize("case", forms.CASES, ids=str)
+def test_every_bit(case):
+    f32 = case[-1]
+    s = forms.Sparse(*case)
+    m = gpu.upload(s.f)
+    _, h = gpu.run_forward(s.f, m, s.ids, s.x_dense, None, f32)
+    part, bound = s.y(h.cpu().numpy())
+    # a bf16 y: what the adapters' part nearly cancels, so that rounding hides little of it
+    base = np.zeros_like(part, np.float32) if f32 else bf16_round(-part.astype(np.float32))
+    y, again = gpu.run_forward(s.f, m, s.ids, s.x_dense, base, f32)
+    assert torch.equal(h, again)
+    want = base + part
+    gpu.check(y, want, ref.rounded(want, bound + 2 * U32 * (np.abs(base) + np.abs(want)), f32), "y")
+    for saved in (False, True):
+        dx, da, db = gpu.run_grad(s.f, m, s.ids, s.dy, s.x, s.h, s.base, f32, saved=saved)
+        wx, wa, wb, xb, ab, bb = s.gradients(ref.restored(*ref.save(s.x)) if saved else s.x.astype(np.float64))
+        gpu.check(dx, wx, xb, "dx")
+        gpu.check(da, wa, ab, f"da saved={saved}")
+        gpu.check(db, wb, bb, "db")
+
+
 @pytest.mark.parametrize("T,E,H", forms.ROUTER)
 @pytest.mark.parametrize("saved", [False, True])
 def test_router_weight(T, E, H, saved):
     rng = np.random.default_rng(T + H)
     d = moe.dims(T, H, 128, E, 1)
     buf = moe.RouterWeightBuffers.allocate(d)
+    sparse, some, steps = forms.router_operands(T, E, H)
     dense = (1e-3 * np.exp(2 * rng.standard_normal((T, 1))) * rng.standard_normal((T, E))).astype(np.float32)
     rows = bf16_round(rng.standard_normal((T, H)).astype(np.float32))
-    for dl, x, step in ((dense, rows, (T + 64) * ref.SUM),):
+    for dl, x, step in ((dense, rows, (T + 64) * ref.SUM), (sparse, some, steps)):
         kept, X = gpu.dev(x), x.astype(np.float64)
         if saved:
             c = moe.Checkpoint.allocate(T, H)
