@@ -715,7 +715,9 @@ int moe_adapter_workspace_bytes(const moe_adapters* adapters, int32_t T, int gra
  *   h          float32 [T][R] or NULL: receives h, for moe_adapter_grad
  *   workspace  moe_adapter_workspace_bytes(adapters, T, 0), 256-byte aligned
  * Rows are aligned to their elements.  A row of x with an infinity or NaN changes no
- * other row.  Sums are taken in a fixed order: equal calls give equal bits. */
+ * other row.  An infinite h makes its row of y NaN, also where the formula would be
+ * infinite (h is multiplied in three bf16 parts, and those of an infinity are no
+ * numbers).  Sums are taken in a fixed order: equal calls give equal bits. */
 int moe_adapter(const moe_adapters* adapters, int32_t T, const int32_t* ids, const uint16_t* x, int64_t ldx,
                 const void* base, int64_t ldbase, void* y, int64_t ldy, int y_type, float* h, void* workspace,
                 size_t workspace_bytes, void* stream);
@@ -735,7 +737,9 @@ int moe_adapter(const moe_adapters* adapters, int32_t T, const int32_t* ids, con
  *   da       float32 [n][R][K] or NULL;  db  float32 [n][R][N] or NULL
  *   workspace  moe_adapter_workspace_bytes(adapters, T, 1), 256-byte aligned
  * dx, da and db overlap no input (refused for dx with dy, x, x_saved, h and dx_base).  Sums
- * in float32 in a fixed order; with float32 dy, 2^-24 of a product of db is left out. */
+ * in float32 in a fixed order; with float32 dy, 2^-24 of a product of db is left out.  An
+ * infinite g, h or float32 dy makes what it enters NaN, an infinite x or bf16 dy infinite or NaN;
+ * other tokens' dx and other adapters' da and db do not change. */
 int moe_adapter_grad(const moe_adapters* adapters, int32_t T, const int32_t* ids, const void* dy, int64_t lddy,
                      int dy_type, const uint16_t* x, int64_t ldx, const moe_checkpoint* x_saved, const float* h,
                      const uint16_t* dx_base, int64_t lddx_base, uint16_t* dx, int64_t lddx, float* da, float* db,
@@ -753,7 +757,8 @@ int moe_adapter_grad(const moe_adapters* adapters, int32_t T, const int32_t* ids
  *            first, equal ones (also -0 and +0) by the lower index, and their d_v - log S.
  *            NaNs and logits of -inf are not taken: -1 and -inf where there are no more.
  *            n_top 0 .. 64; not used where it is 0.
- * A NaN or +inf in a row makes its stats[1], logp, entropy and top_logp NaN; no other row changes.
+ * A NaN or +inf in a row makes its stats[1], entropy, logp (of a token that is scored) and top_logp
+ * (of alternatives that there are) NaN; no other row changes.
  *   tokens     int32 [T]
  *   workspace  moe_logprobs_workspace_bytes(T, V, n_top), 256-byte aligned (NULL where 0)
  *   sync       int32 [MOE_LOGPROBS_SYNC_INTS] device memory, 256-byte aligned, zeros before the
@@ -798,7 +803,9 @@ int moe_combine_backward_saved(const moe_dims* dims, const uint16_t* out_grad, c
  *   router_bias_grad[e]  = sum_t logits_grad[t][e]           (float32 [E], or NULL)
  * x: bf16 [T] rows of H elements, ldx >= H apart, or NULL with x_saved, a checkpoint of T rows
  * of H.  With T = 0 all are 0.  workspace: moe_router_weight_workspace_bytes(dims), 256-byte
- * aligned (NULL where 0).  Only T, E and H of dims are used (k and group_size are checked). */
+ * aligned (NULL where 0).  Only T, E and H of dims are used (k and group_size are checked).
+ * An infinite logits_grad[t][e] makes row e of w_router_grad NaN, an infinite x its column infinite
+ * or NaN. */
 int moe_router_weight_workspace_bytes(const moe_dims* dims, size_t* bytes);
 int moe_router_weight_grad(const moe_dims* dims, const float* logits_grad, const uint16_t* x, int64_t ldx,
                            const moe_checkpoint* x_saved, float* w_router_grad, float* router_bias_grad,

@@ -82,3 +82,44 @@ def test_router_weight(T, E, H, saved):
         D = dl.astype(np.float64)
         gpu.check(dw, D.T @ X, step * (np.abs(D).T @ np.abs(X)) + ref.TINY, "weight")
         gpu.check(db, D.sum(0), (T + 16) * U32 * np.abs(D).sum(0) + ref.TINY, "bias")
+
+
+@pytest.mark.parametrize("T", [30, 600])
+@pytest.mark.parametrize("f32", [False, True])
+def test_infinities_are_nan_where_they_enter(T, f32):
+    """As the header says: an infinite h, g or float32 dy is three parts that are no numbers, an infinite
+    bf16 operand may give either; everything else keeps its bits."""
+    rng = np.random.default_rng(T)
+    f = ref.Factors(rng, 3, 8, 128, 24)
+    m = gpu.upload(f)
+    ids = gpu.make_ids(rng, T, 3)
+    t, i = 5, int(ids[5])
+    x, dy = (bf16_round(rng.standard_normal((T, c)).astype(np.float32)) for c in (128, 24))
+    hv = rng.standard_normal((T, 8)).astype(np.float32)
+    others, rest = [k for k in range(3) if k != i], torch.arange(T, device="cuda") != t
+    good = gpu.run_forward(f, m, ids, x, None, f32), gpu.run_grad(f, m, ids, dy, x, hv, None, f32)
+    bad = x.copy()
+    bad[t, 9] = np.inf
+    y, h = gpu.run_forward(f, m, ids, bad, None, f32)
+    assert bool(torch.isinf(h[t]).all()) and bool(torch.isnan(y[t]).all())
+    assert torch.equal(y[rest], good[0][0][rest]) and torch.equal(h[rest], good[0][1][rest])
+    dx, da, db = gpu.run_grad(f, m, ids, dy, bad, hv, None, f32)
+    assert torch.equal(dx, good[1][0]) and torch.equal(db, good[1][2]) and torch.equal(da[others], good[1][1][others])
+    keep = torch.arange(128, device="cuda") != 9
+    assert not bool(torch.isfinite(da[i, :, 9]).any()) and torch.equal(da[i][:, keep], good[1][1][i][:, keep])
+    bad = dy.copy()
+    bad[t, 3] = -np.inf
+    dx, da, db = gpu.run_grad(f, m, ids, bad, x, hv, None, f32)
+    assert bool(torch.isnan(dx[t]).all()) and torch.equal(dx[rest], good[1][0][rest])
+    assert bool(torch.isnan(da[i]).all()) and torch.equal(da[others], good[1][1][others])
+    keep = torch.arange(24, device="cuda") != 3
+    assert not bool(torch.isfinite(db[i, :, 3]).any()) and torch.equal(db[:, :, keep], good[1][2][:, :, keep])
+    assert torch.equal(db[others], good[1][2][others])
+    d = moe.dims(T, 128, 128, 8, 1)
+    buf, dl = moe.RouterWeightBuffers.allocate(d), gpu.dev(hv, torch.float32)
+    a, b = torch.empty(8, 128, device="cuda"), torch.empty(8, 128, device="cuda")
+    moe.router_weight_grad(d, dl, gpu.dev(x), a, buf)
+    dl[t, 2] = float("inf")
+    moe.router_weight_grad(d, dl, gpu.dev(x), b, buf)
+    rows = torch.arange(8, device="cuda") != 2
+    assert bool(torch.isnan(b[2]).all()) and torch.equal(a[rows], b[rows])
