@@ -612,12 +612,25 @@ void expand(const TokenSets& who, const Space& sp, int splits, const float* scal
     else f32 ? expand_go<true, false>(a, grid, s) : expand_go<false, false>(a, grid, s);
 }
 
-// Few tokens in one launch, every workgroup with all of its tile's sums, where a's rows are 64 KB at most:
-// past that a workgroup's own stream of them is longer than the second launch (us by two launches and
-// by one: 1 token 2048 x 2048 at rank 8 6.8 and 5.5, 64 of 16 adapters 1024 x 1024 at 16 7.6 and
-// 6.0; 1 token 4096 x 4096 at 16 7.4 and 8.2, 128 of 64 adapters 12.1 and 15.6).
+// Few tokens in one launch, every workgroup with all of its tile's sums: where a's rows are 64 KB at most, K is 2048 at
+// most (less than 4096 with no more tokens than adapters), and the workgroups of an XCD find room at once: all of a tile's
+// sit on one, and each takes the sums anew (K columns each, and what 512 more would take, up to 64 x 2048).  us by two
+// launches and by one:
+//   rank 8, K 2048, N 4096:   1 token 6.2 and 5.3, 40 of 40 adapters 6.7 and 5.6, 128 of 64 8.1 and 8.7
+//   rank 16, K 1024:          1 token x N 16384 6.1 and 4.9, x 100000 6.1 and 12.3; 128 of 64 x 4096 9.0 and 8.4,
+//                             x 16384 15.7 and 21.9, x 100000 66 and 119
+//   rank 16, K 2048, N 4096:  64 tokens of 4 7.2 and 7.8; rank 32: 1 token 7.1 and 8.1 (a's rows 128 KB)
+//   rank 4, K 3200, N 4096:   40 tokens of 40 7.2 and 6.0; K 4096: 1 token 6.3 and 6.2, 64 of 4, whose tiles have 16 rows
+//                             of x, 7.4 and 9.3; K 8192: 1 token 6.3 and 8.6.
+// Over 1344 sizes (K 256 to 4096, rank 4 to 32, N 1024 to 49152, 1 to 512 tokens) the choice costs 1 % beside
+// the better side, the limit on a's rows alone 10 %, two launches throughout 8 %.
+constexpr int kSelfColumns = 64 * 2048;
 int self_blocks(const moe_adapters& m) { return (m.N + kSelfWaves * kUnitCols - 1) / (kSelfWaves * kUnitCols); }
-bool one_launch(const moe_adapters& m, int T) { return !planned(T) && m.R <= 32 && m.R * m.K <= 32768; }
+bool one_launch(const moe_adapters& m, int T) {
+    if (planned(T) || m.R > 32 || m.R * m.K > 32768 || m.K >= (T > m.n ? 2176 : 4096)) return false;
+    const int tiles = std::min(T, std::min(m.n, T) + T / kScanTile), an_xcd = (tiles + 7) / 8 * self_blocks(m);
+    return (int64_t)an_xcd * (m.K + 512) <= kSelfColumns;
+}
 
 void make_plan(const TokenSets& who, const TokenPlan& plan, hipStream_t s) {
     hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)who.n + 1), dim3(64 * kPlanWaves), 0, s, who, plan);

@@ -15,6 +15,7 @@ from weights_ref import U32, bf16_round
 # T, n, R, K, N, float32 y and dy
 CASES = [(T, n, R, K, N, f32) for T, n, R, K, N in [
     (9, 2, 8, 256, 72), (9, 2, 24, 256, 1100),                     # one launch
+    (30, 3, 8, 1024, 100001), (20, 3, 4, 2304, 200),               # two: wide rows, many columns
     (20, 3, 16, 2176, 300), (30, 3, 32, 2176, 136),                # two, with more than four splits
     (40, 2, 64, 640, 200), (40, 2, 96, 384, 250),
     (200, 64, 8, 512, 700), (200, 64, 24, 512, 700),               # factors' gradients by waves
@@ -65,7 +66,8 @@ def grad_chunk(T, R, C, ids=True):
 def forward(T, n, R, K, N, f32):
     """Kernel forms of moe_adapter: (kernel, template arguments)."""
     rt, plan = rank_tiles(R), planned(T)
-    if not plan and R <= 32 and R * K <= 32768:
+    workgroups = up(min(T, min(n, T) + T // 16), 8) * up(N, 1024)          # of an XCD
+    if not plan and R <= 32 and R * K <= 32768 and K < (2176 if T > n else 4096) and workgroups * (K + 512) <= 64 * 2048:
         return [("expand", rt, f32, False, True)]
     return [("shrink", rt, False, plan), ("expand", rt, f32, plan, False)]
 
