@@ -22,6 +22,7 @@
 // 64 r a wave would halve the turning of x for twice the accumulators (20.5 us and 6.1; no gain), loads two
 // steps ahead changed nothing.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "adapters.h"
@@ -468,6 +469,17 @@ void grad_go(const GradArgs& a, int kind, int blocks, unsigned entries, bool few
 }  // namespace
 
 // ids: tokens up to kScanTokens are one chunk (every workgroup finds its own).
+//
+// How many tokens a chunk has: as many workgroups as the card holds at once, 256 of eight waves (R <= 16) or 512 of
+// four.  us so, with twice the workgroups and with half: the factors of 4 adapters, 4096 tokens, 2048 and 8192 columns at rank
+// 16 60.9, 60.9 and 61.2 (whole calls); rank 64, 2048 x 2048 52.5, 58.0, 50.9; the router's weight, 8192 tokens x 128 x
+// 2048 26.7, 31.7, 28.9; 4096 x 256 x 4096 38.4, 41.1, 43.7.
+// At most kMostChunk where the tokens are listed in LDS (the first of these 65.2 with 256, 62.3 with 512, 60.9 with 1024).
+// At least kLeastChunk (1024 tokens, one adapter of 1024 x 1024 at rank 16 22.8 us, with 512 23.7; 600 x 32 x 512 9.3, with 512
+// 11.0).  Over all tokens the chunks' sums are joined one after the other, so that a narrow matrix wants chunks that grow with
+// the root of the tokens (chunks of 256, 512, 1024, 2048: 4096 x 32 x 512 13.7, 13.0, 16.0, 23.6; 16384 x 32 x 512
+// 36.0, 26.1, 23.9, 29.9; 65536 x 8 x 128 128.7, 59.8, 36.3, 28.5).  Adapters' chunks of 256 cost
+// 6 % at most there (65536 tokens of one, 128 x 128 108.7, with 1024 102.3).
 static WeightGradPlan plan_of(int T, int n, int R, int C0, int C1, bool ids) {
     WeightGradPlan p{};
     if (ids && T <= kScanTokens) {
@@ -475,9 +487,10 @@ static WeightGradPlan plan_of(int T, int n, int R, int C0, int C1, bool ids) {
         return p;
     }
     const int wgs = groups_of(R) * ((C0 + 127) / 128 + (C1 + 127) / 128);
+    auto up = [](double v) { return (int)std::ceil(v / kLeastChunk) * kLeastChunk; };
     const int want = ((R > 16 ? 512 : 256) + wgs - 1) / wgs;
-    const int even = ((T + want - 1) / want + kLeastChunk - 1) / kLeastChunk * kLeastChunk;
-    p.chunk = std::max(kLeastChunk, ids ? std::min(even, kMostChunk) : even);
+    const int even = up((T + want - 1) / want), least = ids ? kLeastChunk : up(8 * std::sqrt((double)T));
+    p.chunk = std::max(least, ids ? std::min(even, kMostChunk) : even);
     // a set in several chunks has more than `chunk` tokens, and one chunk at most is not full
     if (T > p.chunk) p.slots = n == 1 ? (T + p.chunk - 1) / p.chunk : 2 * T / p.chunk;
     const size_t most = T <= kLeastChunk ? 0 : ids ? 2 * std::max<size_t>(want, (T + kMostChunk - 1) / kMostChunk) : want;

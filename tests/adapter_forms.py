@@ -7,6 +7,8 @@ zero), each taken as three bf16 parts, a matrix-core sum makes 3 live additions 
 step of 2 U32 each of the terms' absolute sum; additions of zeros are exact.  Eight steps more are for
 scales, the joins of waves, splits and chunks, and what precedes the sum.  A form that kept two
 parts would be off by up to 2^-15 of a term."""
+import math
+
 import numpy as np
 
 import tuning_ref as ref
@@ -30,7 +32,7 @@ CASES = [(T, n, R, K, N, f32) for T, n, R, K, N in [
 ]
 
 # T, E, H of the router's weight gradient: whole calls and chunks of 256, 512 and more tokens
-ROUTER = [(4200, 128, 1024), (9000, 40, 4096), (2100, 1024, 2048), (5000, 8, 8192), (3000, 16, 128), (700, 130, 256), (65536, 3, 128)]
+ROUTER = [(4200, 128, 1024), (9000, 40, 4096), (2100, 1024, 2048), (5000, 8, 8192), (3000, 16, 128), (700, 130, 256), (65536, 3, 128), (1100, 40, 384)]
 
 
 # ------------------------------------------------------------ launch rules
@@ -59,7 +61,7 @@ def grad_chunk(T, R, C, ids=True):
         return T, 1
     wgs = up(R, 16 if R <= 16 else 32) * sum(up(c, 128) for c in C)
     even = up(up(T, up(512 if R > 16 else 256, wgs)), 256) * 256
-    chunk = max(256, min(even, 1024) if ids else even)
+    chunk = min(max(256, even), 1024) if ids else max(256 * math.ceil(8 * math.sqrt(T) / 256), even)
     return chunk, up(T, chunk)
 
 

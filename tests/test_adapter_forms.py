@@ -30,7 +30,7 @@ def test_splits_rounds_and_chunks_are_reached():
     chunks = {(1 if R <= 16 else 2, forms.grad_chunk(T, R, (K, N))[0]) for T, n, R, K, N, _ in plans}
     assert {c for _, c in chunks} == {256, 512, 768, 1024} and {(1, 1024), (2, 1024)} <= chunks
     assert {forms.grad_chunk(T, E, (H,), False) for T, E, H in forms.ROUTER} == {
-        (512, 9), (1280, 8), (2304, 1), (1280, 4), (256, 12), (256, 3), (256, 256)}
+        (768, 6), (1280, 8), (2304, 1), (1280, 4), (512, 6), (256, 3), (2048, 32), (512, 3)}
 
 
 @pytest.mark.parametrize("case", forms.CASES, ids=str)
