@@ -6,8 +6,8 @@
 // so two kernels serve both directions: `shrink` (sums along the rows) and `expand` (sums over
 // the ranks).  The factors' gradients are weight_grad.hip's.
 //
-// A workgroup has up to 16 or 64 tokens of one adapter, so that an adapter's rows are read once
-// for them.  Few tokens (decode): a workgroup finds its tile by looking through the ids; more: a
+// A workgroup has up to 16 tokens of one adapter, or 64 (expand: 32) where tokens are planned, so that
+// an adapter's rows are read once for them.  Few tokens (decode): a workgroup finds its tile by looking through the ids; more: a
 // first kernel puts the tokens in order.  Sums along the rows are split over workgroups where tiles
 // are few; expand adds the parts.
 //

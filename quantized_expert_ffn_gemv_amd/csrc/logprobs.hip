@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * NW) void logprobs_kernel(LogprobArgs a) {
         if constexpr (ENT) sum.w += w[0] + w[1];
         if constexpr (TOP) {
             // the bound after the 1st, 2nd, 4th, ... stretch
-            if ((step & (step + 1)) == 0 || step == 0) bound = fmaxf(bound, bound_of<NW>(L, m, n));
+            if ((step & (step + 1)) == 0) bound = fmaxf(bound, bound_of<NW>(L, m, n));
             if (step == 0) {
                 if constexpr (NW == 1) __syncthreads();
                 if (first > -INFINITY && first >= bound) append(L, first, edge);

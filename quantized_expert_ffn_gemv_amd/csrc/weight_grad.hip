@@ -35,8 +35,8 @@ namespace {
 constexpr int kGradWaves = 8;
 constexpr int kStep = 32;                 // tokens a product
 enum ListKind { kAll = 0, kScan = 1, kPlan = 2 };
-// Waves a SIMD that the registers are held to: with 16 r two workgroups a CU hide each other's
-// loads; with 32 one fits, whose waves have the next step's loads in flight instead.
+// Waves a SIMD that the registers are held to: four with 16 r (128 VGPRs, two workgroups of eight waves a CU, which
+// hide each other's loads), three with 32 (168, three workgroups of four), two with float32 x (up to 202).
 template <int RTW, int WT, bool F32> constexpr int kGradResident = F32 ? 2 : RTW > 1 ? 3 : WT > 1 ? 4 : 3;
 
 struct GradArgs {
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(GradArgs a, int n
 
 namespace {
 
-// r's of 16 a wave, the most that is not past R by more than a product
+// Products of 16 r a wave.  (Rows past R take the last r's again and store nothing: of R = 33 the second group has one.)
 int products_of(int R) { return R <= 16 ? 1 : 2; }
 int groups_of(int R) { return (R + 16 * products_of(R) - 1) / (16 * products_of(R)); }
 
