@@ -334,8 +334,8 @@ def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:
 def adapted_linear_backward(w: QMatrix, adapters: Adapters, ids, dy, x, h, buffers: AdaptedBuffers, dx=None, da=None,
                             db=None, stream=None) -> None:
     """The way back through adapted_linear(): dx = dy W + the adapters' part (linear_grad(),
-    then adapter_grad() on it in place), da and db the factors' gradients, each if given.  x:
-    the input or a Checkpoint of it (for da), h adapted_linear()'s (for db), neither of them in
+    then adapter_grad() on it in place; both round it to bfloat16), da and db the factors'
+    gradients, each if given.  x: the input or a Checkpoint of it (for da), h adapted_linear()'s (for db), neither of them in
     dx's memory.  (The residual's gradient is dy.)"""
     _beside(w, adapters)
     if buffers.adapter_back is None:
