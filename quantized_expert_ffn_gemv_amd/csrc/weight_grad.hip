@@ -270,7 +270,7 @@ __device__ __forceinline__ void weight_grad_block(const GradArgs& a, const Weigh
             }
         }
     }
-    const float s = slot < 0 && a.scale ? ld_scalar(a.scale, set) : 1.f;
+    const float s = slot < 0 && a.scale && cnt > 0 ? ld_scalar(a.scale, set) : 1.f;      // (a set without a token: 0, whatever its scale)
     float* out = slot < 0 ? w.out + (int64_t)set * R * C : part + (int64_t)slot * slot_floats;
     float* bias = slot < 0 ? w.bias : part + (int64_t)slot * slot_floats + (int64_t)R * C;
     // By way of LDS, so that a store has whole rows of 512 bytes (from the products' layout, 8 columns a

@@ -123,3 +123,22 @@ def test_infinities_are_nan_where_they_enter(T, f32):
     moe.router_weight_grad(d, dl, gpu.dev(x), b, buf)
     rows = torch.arange(8, device="cuda") != 2
     assert bool(torch.isnan(b[2]).all()) and torch.equal(a[rows], b[rows])
+
+
+@pytest.mark.parametrize("T,n,R", [(3, 5, 8), (40, 200, 8), (40, 200, 24), (700, 7, 8), (700, 7, 40), (600, 150, 8)])
+def test_adapters_without_a_token_may_hold_anything(T, n, R):
+    """An empty slot of a set: its factors' gradients are 0 whatever its scale, rank and factors are."""
+    rng = np.random.default_rng(T + R)
+    f = ref.Factors(rng, n, R, 384, 264)
+    used = rng.choice(n, max(1, n // 3), False)
+    ids = used[rng.integers(0, len(used), T)].astype(np.int32)
+    empty = np.setdiff1d(np.arange(n), ids)
+    x, dy = (bf16_round(rng.standard_normal((T, c)).astype(np.float32)) for c in (384, 264))
+    h = rng.standard_normal((T, R)).astype(np.float32)
+    want = gpu.run_grad(f, gpu.upload(f), ids, dy, x, h, None, False)
+    f.rank = np.full(n, R, np.int32)
+    f.scale[empty] = rng.choice(np.array([np.nan, np.inf, -np.inf], np.float32), len(empty))
+    f.a[empty], f.b[empty], f.rank[empty] = np.nan, np.inf, rng.integers(-3, 2 * R, len(empty))
+    got = gpu.run_grad(f, gpu.upload(f), ids, dy, x, h, None, False)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    assert bool((got[1][empty] == 0).all()) and bool((got[2][empty] == 0).all())
