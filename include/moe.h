@@ -727,7 +727,8 @@ int moe_adapter(const moe_adapters* adapters, int32_t T, const int32_t* ids, con
  *   da[i][r][k] = sum over adapter i's tokens of g[t][r] x[t][k]        (float32)
  *   db[i][r][n] = scale[i] sum over its tokens of h[t][r] dy[t][n]      (float32)
  * Every element of da and db is written: 0 for adapters without a token (whatever
- * their scale, rank and factors hold) and past the rank.  (base's gradient is dy; scale is a constant.)
+ * their scale, rank and factors hold) and past the rank.  (base's gradient is dy;
+ * scale is a constant.)
  *   dy       bf16 or float32 (dy_type) rows of N elements, lddy >= N apart
  *   x        bf16 rows of K elements, ldx >= K apart, or NULL with x_saved: a
  *            checkpoint of T rows of K.  Neither is used without da.
@@ -804,8 +805,8 @@ int moe_combine_backward_saved(const moe_dims* dims, const uint16_t* out_grad, c
  * x: bf16 [T] rows of H elements, ldx >= H apart, or NULL with x_saved, a checkpoint of T rows
  * of H.  With T = 0 all are 0.  workspace: moe_router_weight_workspace_bytes(dims), 256-byte
  * aligned (NULL where 0).  Only T, E and H of dims are used (k and group_size are checked).
- * The results overlap no input.  An infinite logits_grad[t][e] makes row e of w_router_grad NaN, an infinite x its column infinite
- * or NaN. */
+ * The results overlap no input.  An infinite logits_grad[t][e] makes row e of w_router_grad
+ * NaN, an infinite x its column infinite or NaN. */
 int moe_router_weight_workspace_bytes(const moe_dims* dims, size_t* bytes);
 int moe_router_weight_grad(const moe_dims* dims, const float* logits_grad, const uint16_t* x, int64_t ldx,
                            const moe_checkpoint* x_saved, float* w_router_grad, float* router_bias_grad,

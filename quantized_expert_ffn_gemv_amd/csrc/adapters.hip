@@ -7,9 +7,9 @@
 // the ranks).  The factors' gradients are weight_grad.hip's.
 //
 // A workgroup has up to 16 tokens of one adapter, or 64 (expand: 32) where tokens are planned, so that
-// an adapter's rows are read once for them.  Few tokens (decode): a workgroup finds its tile by looking through the ids; more: a
-// first kernel puts the tokens in order.  Sums along the rows are split over workgroups where tiles
-// are few; expand adds the parts.
+// an adapter's rows are read once for them.  Few tokens (decode): a workgroup finds its tile by
+// looking through the ids; more: a first kernel puts the tokens in order.  Sums along the rows are
+// split over workgroups where tiles are few; expand adds the parts.
 //
 // Operands of v_mfma_f32_16x16x32_bf16 straight from memory.  shrink: both run along the sum,
 // 16 bytes a lane.  expand: the factor's rows run across the sum; a lane takes 8 columns of 8
@@ -520,7 +520,7 @@ bool planned(int T) { return T > kScanTokens; }
 // CUs where there are columns for it, four waves each with a unit at least.
 // (Whole calls with 256, 512 and 1024 workgroups wanted, 8 adapters, 2048 and 8192 columns: gradients of 4096 tokens at rank 16 65.8,
 // 60.9 and 58.7 us, rank 64 91.5, 90.5 and 93.8, rank 128, where the registers leave a wave a SIMD, 164, 156 and 167;
-// of 1024 at rank 128 75.2, 77.5 and 77.3.  Forwards 4 splits are all the columns that 2048 have: no difference.)
+// of 1024 at rank 128 75.2, 77.5 and 77.3.  Forwards 2048 columns have no more than 4 splits: no difference.)
 constexpr int kShrinkBlocks = 512;
 int shrink_splits(int T, int n, int C) {
     const int sets = std::max(1, std::min(n, T));

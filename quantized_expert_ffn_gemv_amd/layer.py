@@ -335,8 +335,9 @@ def adapted_linear_backward(w: QMatrix, adapters: Adapters, ids, dy, x, h, buffe
                             db=None, stream=None) -> None:
     """The way back through adapted_linear(): dx = dy W + the adapters' part (linear_grad(),
     then adapter_grad() on it in place; both round it to bfloat16), da and db the factors'
-    gradients, each if given.  x: the input or a Checkpoint of it (for da), h adapted_linear()'s (for db), neither of them in
-    dx's memory.  (The residual's gradient is dy.)"""
+    gradients, each if given.  x: the input or a Checkpoint of it (for da), h
+    adapted_linear()'s (for db), neither of them in dx's memory.  (The residual's gradient
+    is dy.)"""
     _beside(w, adapters)
     if buffers.adapter_back is None:
         raise ValueError("buffers allocated without grad")
